@@ -7,7 +7,12 @@ PyTorch fallback; if the library is missing every call raises.
 """
 from .binding import (  # noqa: F401
     CODEBOOKS,
+    KV_FORMATS,
     Exl3Error,
+    KVCache,
+    attention_paged,
+    attention_paged_workspace_bytes,
+    attention_prompt,
     autotune_entries,
     clear_autotune,
     device_status,
@@ -15,12 +20,16 @@ from .binding import (  # noqa: F401
     gemm_splitk,
     input_transform,
     input_transform_swiglu,
+    kv_read,
+    kv_write,
     lib,
     linear,
     set_autotune,
     moe_combine,
     moe_gemm,
     moe_input_transform,
+    rope,
+    rope_phases,
     splitk_parts,
     splitk_workspace_bytes,
     status_string,

@@ -21,6 +21,21 @@ _F16, _BF16 = 0, 1
 _STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported", 3: "split-k workspace too small", 4: "CUDA error"}
 
 
+class _Heads(ctypes.Structure):  # exl3_heads_t
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class _Rope(ctypes.Structure):  # exl3_rope_t
+    _fields_ = [("phases", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("rot_dim", ctypes.c_int32),
+                ("layout", ctypes.c_int), ("amplitude", ctypes.c_float)]
+
+
+class _Cache(ctypes.Structure):  # exl3_kv_cache_t
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("format", ctypes.c_int)]
+
+
 class Exl3Error(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -81,6 +96,21 @@ def lib() -> ctypes.CDLL:
     L.exl3_device_status.restype = ctypes.c_int
     L.exl3_last_error.argtypes = []
     L.exl3_last_error.restype = ctypes.c_char_p
+    heads, cache, rope_p, f32 = ctypes.POINTER(_Heads), ctypes.POINTER(_Cache), ctypes.POINTER(_Rope), ctypes.c_float
+    f64 = ctypes.c_double
+    L.exl3_rope_phases.argtypes = [i32, f64, ctypes.c_int, f64, f64, f64, f64, vp, ctypes.POINTER(f32)]
+    L.exl3_rope.argtypes = [heads, ctypes.c_int, i64, i32, i32, rope_p, vp, i64, i64, vp]
+    L.exl3_kv_write.argtypes = [cache, heads, heads, ctypes.c_int, i64, vp, rope_p, heads, i32, vp, i64, i64, vp]
+    L.exl3_kv_read.argtypes = [cache, vp, i64, ctypes.c_int, vp, vp, vp]
+    L.exl3_attention_prompt.argtypes = [heads, heads, heads, ctypes.c_int, i64, i32, i32, i32, vp, i32, i32, f32, vp,
+                                        i64, i64, vp]
+    L.exl3_attention_paged_workspace_bytes.argtypes = [i64, i32, i32, i32, i32, i32, i32]
+    L.exl3_attention_paged_workspace_bytes.restype = sz
+    L.exl3_attention_paged.argtypes = [heads, ctypes.c_int, i64, i32, cache, vp, i32, vp, vp, i32, i32, i32, i32, f32,
+                                       vp, i64, i64, vp, sz, vp]
+    for name in ("exl3_rope_phases", "exl3_rope", "exl3_kv_write", "exl3_kv_read", "exl3_attention_prompt",
+                 "exl3_attention_paged"):
+        getattr(L, name).restype = ctypes.c_int
     for name in ("exl3_input_transform", "exl3_gemm", "exl3_gemm_splitk", "exl3_test_codebook", "exl3_test_unpack"):
         getattr(L, name).restype = ctypes.c_int
     _lib = L
@@ -393,4 +423,269 @@ def test_unpack(trellis: torch.Tensor, bits: int, cb) -> torch.Tensor:
     cbid = CODEBOOKS[cb] if isinstance(cb, str) else int(cb)
     st = lib().exl3_test_unpack(_ptr(trellis), bits, cbid, 16 * kt, 16 * nt, _ptr(out), _stream(trellis))
     _check(st, "exl3_test_unpack")
+    return out
+
+
+# --------------------------------------------------------------------------------------------------
+# rotary positions, the paged cache and attention
+
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3}
+KV_FORMATS = {"f16": 0, "bf16": 1, "int8": 2, "int4": 3}
+_KV_DTYPES = {"f16": torch.float16, "bf16": torch.bfloat16, "int8": torch.uint8, "int4": torch.uint8}
+
+
+def _type(t: torch.Tensor, name: str) -> int:
+    if t.dtype is torch.bfloat16:
+        return _BF16
+    if t.dtype is torch.float16:
+        return _F16
+    raise ValueError(f"{name} must be bf16 or fp16, got {t.dtype}")
+
+
+def _heads(t: torch.Tensor, dtype, name: str) -> _Heads:
+    """exl3_heads_t of a [tokens, heads, head_dim] view whose last axis is contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim]")
+    ts, hs, ds = t.stride()
+    tokens, heads, d = t.shape
+    if ds != 1 and d != 1:
+        raise ValueError(f"{name} must be contiguous along head_dim")
+    # the stride of an axis of one (or no) element says nothing
+    return _Heads(t.data_ptr(), ts if tokens > 1 else heads * d or 8, hs if heads > 1 else d)
+
+
+def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
+    """Whether the memory that two views span overlaps."""
+    def span(t):
+        last = sum((n - 1) * st for n, st in zip(t.shape, t.stride()))
+        return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
+
+    if a.numel() == 0 or b.numel() == 0:
+        return False
+    (a0, a1), (b0, b1) = span(a), span(b)
+    return a0 < b1 and b0 < a1
+
+
+def _alike(t: torch.Tensor, dtype, shape, name: str) -> None:
+    _need(t, dtype, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def rope_phases(rot_dim: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0, fast: float = 32.0,
+                slow: float = 1.0, original_len: float = 4096.0, device="cuda"):
+    """(phases, amplitude) for rope and kv_write: int64 [rot_dim / 2] on ``device``, turns per position in 2^-64.
+
+    scaling: "plain", "linear" (positions / factor), "ntk" (larger base) or "yarn" (slow frequencies / factor,
+    fast ones kept, a ramp between ``slow`` and ``fast`` turns over ``original_len`` positions).
+    """
+    out = torch.empty(max(0, int(rot_dim)) // 2, dtype=torch.int64)
+    amplitude = ctypes.c_float(0.0)
+    st = lib().exl3_rope_phases(int(rot_dim), float(base), ROPE_SCALINGS[scaling], float(factor), float(fast),
+                                float(slow), float(original_len), _ptr(out), ctypes.byref(amplitude))
+    _check(st, "exl3_rope_phases")
+    return out.to(device), float(amplitude.value)
+
+
+def _rope_args(positions: torch.Tensor, phases: torch.Tensor, layout: str, amplitude: float, tokens: int) -> _Rope:
+    _alike(positions, torch.int32, (tokens,), "positions")
+    _need(phases, torch.int64, "phases")
+    return _Rope(phases.data_ptr(), positions.data_ptr(), 2 * phases.numel(), ROPE_LAYOUTS[layout], float(amplitude))
+
+
+def rope(x: torch.Tensor, positions: torch.Tensor, phases: torch.Tensor, layout: str = "half", amplitude: float = 1.0,
+         out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Rotary positions on the heads of x [tokens, heads, head_dim] (a view of a fused projection will do).
+
+    The first 2 * phases.numel() values of every head turn.  ``out`` may be x itself.
+    """
+    dt = _type(x, "x")
+    xh = _heads(x, x.dtype, "x")
+    tokens, heads, d = x.shape
+    r = _rope_args(positions, phases, layout, amplitude, tokens)
+    if out is None:
+        out = torch.empty((tokens, heads, d), dtype=x.dtype, device=x.device)
+    if out.shape != x.shape:
+        raise ValueError("out must have x's shape")
+    oh = _heads(out, x.dtype, "out")
+    if oh.data != xh.data and _overlap(x, out):
+        raise ValueError("out overlaps x without being x")
+    st = lib().exl3_rope(xh, dt, tokens, heads, d, r, oh.data, oh.token_stride, oh.head_stride, _stream(x))
+    _check(st, "exl3_rope")
+    return out
+
+
+class KVCache:
+    """A paged cache: k and v [pages, kv_heads, page_size, row] (row: head_dim values in 16 bits, head_dim bytes for
+    "int8", head_dim / 2 for "int4"), and for the quantised formats bf16 scales [pages, kv_heads, page_size]."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: Optional[torch.Tensor],
+                 v_scale: Optional[torch.Tensor], fmt: str):
+        if fmt not in KV_FORMATS:
+            raise ValueError(f"cache format must be one of {sorted(KV_FORMATS)}")
+        dtype = _KV_DTYPES[fmt]
+        _need(k, dtype, "k")
+        if k.dim() != 4:
+            raise ValueError("k must be [pages, kv_heads, page_size, row]")
+        _alike(v, dtype, k.shape, "v")
+        pages, heads, page, row = k.shape
+        if fmt in ("int8", "int4"):
+            if k_scale is None or v_scale is None:
+                raise ValueError(f"an {fmt} cache needs scales")
+            _alike(k_scale, torch.bfloat16, (pages, heads, page), "k_scale")
+            _alike(v_scale, torch.bfloat16, (pages, heads, page), "v_scale")
+        self.k, self.v, self.k_scale, self.v_scale, self.fmt = k, v, k_scale, v_scale, fmt
+        self.num_pages, self.kv_heads, self.page_size = pages, heads, page
+        self.head_dim = 2 * row if fmt == "int4" else row
+        self.args = _Cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if k_scale is not None else None,
+                           v_scale.data_ptr() if v_scale is not None else None, pages, page, heads, self.head_dim,
+                           KV_FORMATS[fmt])
+
+    @classmethod
+    def empty(cls, num_pages: int, page_size: int, kv_heads: int, head_dim: int, fmt: str, device="cuda") -> "KVCache":
+        """A cache of rows not yet written."""
+        if fmt not in KV_FORMATS:
+            raise ValueError(f"cache format must be one of {sorted(KV_FORMATS)}")
+        shape = (num_pages, kv_heads, page_size, head_dim // 2 if fmt == "int4" else head_dim)
+        k, v = (torch.zeros(shape, dtype=_KV_DTYPES[fmt], device=device) for _ in range(2))
+        scales = [None, None]
+        if fmt in ("int8", "int4"):
+            scales = [torch.ones(shape[:3], dtype=torch.bfloat16, device=device) for _ in range(2)]
+        return cls(k, v, scales[0], scales[1], fmt)
+
+
+def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, q: Optional[torch.Tensor] = None,
+             positions: Optional[torch.Tensor] = None, phases: Optional[torch.Tensor] = None, layout: str = "half",
+             amplitude: float = 1.0, q_out: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
+    """Write k and v [tokens, kv_heads, head_dim] into the cache rows ``slots`` (int64; page * page_size + row,
+    anything outside the cache writes nothing).
+
+    With positions and phases the keys are rotated first, and so is q [tokens, heads, head_dim] when given: the
+    rotated q (q_out, a new tensor unless given) is returned, else None.
+    """
+    dt = _type(k, "k")
+    tokens = k.shape[0]
+    kh, vh = _heads(k, k.dtype, "k"), _heads(v, k.dtype, "v")
+    if tuple(k.shape) != (tokens, cache.kv_heads, cache.head_dim) or v.shape != k.shape:
+        raise ValueError("k and v must be [tokens, kv_heads, head_dim] of the cache")
+    _alike(slots, torch.int64, (tokens,), "slots")
+    r = qh = None
+    heads, qo = 0, (None, 0, 0)
+    if phases is not None:
+        if positions is None:
+            raise ValueError("phases need positions")
+        r = _rope_args(positions, phases, layout, amplitude, tokens)
+    if q is not None:
+        if r is None:
+            raise ValueError("q is only taken to be rotated: it needs positions and phases")
+        if q.dim() != 3 or q.shape[0] != tokens or q.shape[2] != cache.head_dim:
+            raise ValueError("q must be [tokens, heads, head_dim]")
+        qh, heads = _heads(q, k.dtype, "q"), q.shape[1]
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+        oh = _heads(q_out, k.dtype, "q_out")
+        if oh.data != qh.data and _overlap(q, q_out):
+            raise ValueError("q_out overlaps q without being q")
+        qo = (oh.data, oh.token_stride, oh.head_stride)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    st = lib().exl3_kv_write(cache.args, kh, vh, dt, tokens, _ptr(slots), r, qh, heads, *qo, _stream(k))
+    _check(st, "exl3_kv_write")
+    return q_out
+
+
+def kv_read(cache: KVCache, slots: torch.Tensor, dtype=torch.bfloat16, k: Optional[torch.Tensor] = None,
+            v: Optional[torch.Tensor] = None):
+    """(k, v) [tokens, kv_heads, head_dim] of the cache rows ``slots``; zeros for a slot outside the cache."""
+    _need(slots, torch.int64, "slots")
+    if slots.dim() != 1:
+        raise ValueError("slots must be [tokens]")
+    shape = (slots.numel(), cache.kv_heads, cache.head_dim)
+    k = torch.empty(shape, dtype=dtype, device=slots.device) if k is None else k
+    v = torch.empty(shape, dtype=dtype, device=slots.device) if v is None else v
+    _alike(k, dtype, shape, "k")
+    _alike(v, dtype, shape, "v")
+    st = lib().exl3_kv_read(cache.args, _ptr(slots), shape[0], _type(k, "k"), _ptr(k), _ptr(v), _stream(slots))
+    _check(st, "exl3_kv_read")
+    return k, v
+
+
+def _out_like(q: torch.Tensor, out: Optional[torch.Tensor]):
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    return out, _heads(out, q.dtype, "out")
+
+
+def attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, max_len: int = 0,
+                     scale: Optional[float] = None, window: int = 0,
+                     out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Causal attention over packed prompts: q [total, heads, head_dim], k and v [total, kv_heads, head_dim],
+    sequence b the tokens cu_seqlens[b] .. cu_seqlens[b + 1] (int32).
+
+    scale: 1 / sqrt(head_dim) unless given.  window > 0: a query sees its own and the window - 1 keys before.
+    max_len is accepted for symmetry with attention_paged; the split does not need it.
+    """
+    dt = _type(q, "q")
+    qh, kh, vh = _heads(q, q.dtype, "q"), _heads(k, q.dtype, "k"), _heads(v, q.dtype, "v")
+    total, heads, d = q.shape
+    if k.shape[0] != total or k.shape[2] != d or v.shape != k.shape:
+        raise ValueError("k and v must be [total, kv_heads, head_dim]")
+    _need(cu_seqlens, torch.int32, "cu_seqlens")
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must be [batch + 1]")
+    out, oh = _out_like(q, out)
+    st = lib().exl3_attention_prompt(qh, kh, vh, dt, total, heads, k.shape[1], d, _ptr(cu_seqlens),
+                                     cu_seqlens.numel() - 1, int(window), d ** -0.5 if scale is None else float(scale),
+                                     oh.data, oh.token_stride, oh.head_stride, _stream(q))
+    _check(st, "exl3_attention_prompt")
+    return out
+
+
+def attention_paged_workspace_bytes(total_q: int, batch: int, heads: int, kv_heads: int, head_dim: int, max_q: int,
+                                    max_kv: int) -> int:
+    return int(lib().exl3_attention_paged_workspace_bytes(total_q, batch, heads, kv_heads, head_dim, max_q, max_kv))
+
+
+def attention_paged(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, cu_q: torch.Tensor,
+                    kv_lens: torch.Tensor, max_q: int, max_kv: int, scale: Optional[float] = None, window: int = 0,
+                    out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Attention of each sequence's last tokens over the cache, their own rows already written.
+
+    q [total_q, heads, head_dim], packed by cu_q (int32 [batch + 1]); block_table int32 [batch, width]; kv_lens int32
+    [batch]; max_q and max_kv: the largest of the sequences' query and cached tokens (max_q must not be too small).
+    ``workspace``: uint8, at least attention_paged_workspace_bytes (allocated when not given).
+    """
+    dt = _type(q, "q")
+    qh = _heads(q, q.dtype, "q")
+    total, heads, d = q.shape
+    if d != cache.head_dim:
+        raise ValueError("q and the cache differ in head_dim")
+    _need(cu_q, torch.int32, "cu_q")
+    if cu_q.dim() != 1 or cu_q.numel() < 1:
+        raise ValueError("cu_q must be [batch + 1]")
+    batch = cu_q.numel() - 1
+    _alike(kv_lens, torch.int32, (batch,), "kv_lens")
+    _need(block_table, torch.int32, "block_table")
+    if block_table.dim() != 2 or block_table.shape[0] != batch:
+        raise ValueError("block_table must be [batch, width]")
+    out, oh = _out_like(q, out)
+    L = lib()
+    need = int(L.exl3_attention_paged_workspace_bytes(total, batch, heads, cache.kv_heads, d, int(max_q), int(max_kv)))
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    _need(workspace, torch.uint8, "workspace")
+    st = L.exl3_attention_paged(qh, dt, total, heads, cache.args, _ptr(block_table), block_table.shape[1],
+                                _ptr(cu_q), _ptr(kv_lens), batch, int(max_q), int(max_kv), int(window),
+                                d ** -0.5 if scale is None else float(scale), oh.data, oh.token_stride,
+                                oh.head_stride, _ptr(workspace), workspace.numel(), _stream(q))
+    _check(st, "exl3_attention_paged")
     return out

@@ -5,6 +5,7 @@
 #include <string.h>
 
 #include "../../include/exl3.h"
+#include "exl3_attn.h"
 #include "exl3_launch.h"
 
 namespace {
@@ -72,6 +73,10 @@ exl3_status_t check_gemm(const uint16_t* xh, int64_t m, int64_t k, const int16_t
 }
 
 }  // namespace
+
+namespace exl3 {
+exl3_status_t api_status(cudaError_t e, const char* where) { return cuda_status(e, where); }
+}  // namespace exl3
 
 extern "C" {
 

@@ -6,6 +6,7 @@
 #include <map>
 #include <mutex>
 
+#include "exl3_attn.h"
 #include "exl3_launch.h"
 
 namespace exl3 {
@@ -669,9 +670,9 @@ cudaError_t launch_moe_gemm_tc(const GemmArgs& a, int bits, int cb, int block, c
 cudaError_t take_device_errors(uint32_t* flags) {
   *flags = 0;
   cudaError_t e = cudaSuccess;
-  cudaError_t (*fns[8])(uint32_t*) = {take_device_error_tc<1>, take_device_error_tc<2>, take_device_error_tc<3>,
+  cudaError_t (*fns[9])(uint32_t*) = {take_device_error_tc<1>, take_device_error_tc<2>, take_device_error_tc<3>,
                                       take_device_error_tc<4>, take_device_error_tc<5>, take_device_error_tc<6>,
-                                      take_device_error_tc<7>, take_device_error_tc<8>};
+                                      take_device_error_tc<7>, take_device_error_tc<8>, take_device_error_attn};
   for (auto f : fns) {
     cudaError_t r = f(flags);
     if (r != cudaSuccess) e = r;

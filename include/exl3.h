@@ -253,6 +253,175 @@ exl3_status_t exl3_moe_combine(const void* y, exl3_dtype_t y_dtype, int64_t rows
                                int32_t* pair_rows, void* out, exl3_dtype_t out_dtype, void* stream);
 
 /*
+ * Attention around the quantised layers: rotary positions, a paged key / value
+ * cache in 16, 8 or 4 bits, attention over whole prompts and over the cache.
+ * The pages have no counterpart to these calls: their layers run inside an
+ * engine that brings its own.  Arithmetic, layouts and limits are this
+ * library's own and are stated here.
+ *
+ * Heads of packed tokens are described by exl3_heads_t: element (t, h, d) at
+ * data[t * token_stride + h * head_stride + d], strides in elements, positive
+ * multiples of 8, data 16-byte aligned (so a call reads the heads it wants
+ * straight from a fused projection's output).  head_dim is 64 or 128 (others:
+ * EXL3_EUNSUPPORTED).  q_heads is a multiple of kv_heads; query head h uses key
+ * head h / (q_heads / kv_heads).
+ */
+typedef struct {
+  const void* data;
+  int64_t token_stride, head_stride;
+} exl3_heads_t;
+
+/*
+ * Rotary positions.  Pair i of a head turns by the angle position * f_i:
+ *     (a, b) -> amplitude * (a cos - b sin, b cos + a sin)
+ * The pairs are (x[i], x[i + rot_dim/2]) for EXL3_ROPE_HALF and
+ * (x[2i], x[2i + 1]) for EXL3_ROPE_INTERLEAVED, i < rot_dim / 2; values from
+ * rot_dim on stay.  f_i is given as a phase: turns per position in units of
+ * 2^-64 (f_i / 2 pi * 2^64), so that position * phase modulo 2^64 is the exact
+ * angle at every 32-bit position; its upper 32 bits, signed, times pi / 2^31 are
+ * the angle in fp32.  Products and sums are fp32, rounded one by one, then once
+ * to the type.
+ *   phases     device, uint64 [rot_dim / 2]
+ *   positions  device, int32 [tokens]
+ *   rot_dim    multiple of 16, at most head_dim
+ */
+typedef enum { EXL3_ROPE_HALF = 0, EXL3_ROPE_INTERLEAVED = 1 } exl3_rope_layout_t;
+typedef struct {
+  const uint64_t* phases;
+  const int32_t* positions;
+  int32_t rot_dim;
+  exl3_rope_layout_t layout;
+  float amplitude;
+} exl3_rope_t;
+
+/*
+ * exl3_rope_phases -- phases and amplitude of the usual frequencies
+ * f_i = base^(-2i / rot_dim), scaled for long contexts (pure host function, 64
+ * bits):
+ *   EXL3_ROPE_PLAIN   f_i, amplitude 1
+ *   EXL3_ROPE_LINEAR  f_i / factor, amplitude 1
+ *   EXL3_ROPE_NTK     base * factor^(rot_dim / (rot_dim - 2)) in place of base, amplitude 1
+ *   EXL3_ROPE_YARN    r_i = original_len * f_i / 2 pi turns over the original
+ *                     context; g_i = clamp((r_i - slow) / (fast - slow), 0, 1);
+ *                     f_i * (g_i + (1 - g_i) / factor), amplitude 0.1 ln(factor) + 1
+ *                     (Peng et al., "YaRN: Efficient Context Window Extension of
+ *                     Large Language Models")
+ * factor >= 1, base > 1; fast > slow > 0 and original_len > 0 are read for YARN only.
+ *   phases  HOST, uint64 [rot_dim / 2] (output);  amplitude  HOST (output)
+ */
+typedef enum { EXL3_ROPE_PLAIN = 0, EXL3_ROPE_LINEAR = 1, EXL3_ROPE_NTK = 2, EXL3_ROPE_YARN = 3 } exl3_rope_scaling_t;
+exl3_status_t exl3_rope_phases(int32_t rot_dim, double base, exl3_rope_scaling_t scaling, double factor,
+                               double fast, double slow, double original_len, uint64_t* phases,
+                               float* amplitude);
+
+/*
+ * exl3_rope -- rotate `heads` heads of every token.  out may be x itself (same
+ * strides): in place.  Out-of-place, out may not overlap x.
+ *   out  device, strides as for exl3_heads_t
+ */
+exl3_status_t exl3_rope(const exl3_heads_t* x, exl3_dtype_t dtype, int64_t tokens, int32_t heads,
+                        int32_t head_dim, const exl3_rope_t* rope, void* out, int64_t out_token_stride,
+                        int64_t out_head_stride, void* stream);
+
+/*
+ * The paged cache.  Slot s is row s % page_size of page s / page_size.
+ *   k, v              device, [num_pages][kv_heads][page_size][row bytes]
+ *   k_scale, v_scale  device, bf16 [num_pages][kv_heads][page_size]; NULL for the 16-bit formats
+ *   page_size         16, 32, 64, 128 or 256;  num_pages * kv_heads * page_size below 2^31
+ * Formats, for a row x of head_dim values (H the head_dim-point Hadamard
+ * transform, adds in strides 1, 2, 4, ... in fp32):
+ *   EXL3_KV_F16, EXL3_KV_BF16  x itself
+ *   EXL3_KV_INT8   y = H x / 8;  scale = max|y| / 127 in fp32 (times the rounded reciprocal), rounded
+ *                  up to bf16, at least 2^-100, 1 for a row of zeros;  code = rint(y * (1 / scale)),
+ *                  stored as code + 128 in a byte
+ *   EXL3_KV_INT4   the same with 7 in place of 127, code + 8 in a nibble, even values low
+ * A row with a NaN or an infinity gets zero codes and a NaN scale and reads back as NaN.  The values read back are
+ * H(codes) * scale * 8 / head_dim.  Attention works on the rotated rows: it
+ * rotates q and its output instead.  Over a quantised cache its operands are fp16
+ * in that basis, so rotated keys, values and queries must stay below 65504 (entries below 8000 always do).
+ */
+typedef enum { EXL3_KV_F16 = 0, EXL3_KV_BF16 = 1, EXL3_KV_INT8 = 2, EXL3_KV_INT4 = 3 } exl3_kv_format_t;
+typedef struct {
+  void* k;
+  void* v;
+  uint16_t* k_scale;
+  uint16_t* v_scale;
+  int64_t num_pages;
+  int32_t page_size, kv_heads, head_dim;
+  exl3_kv_format_t format;
+} exl3_kv_cache_t;
+
+/*
+ * exl3_kv_write -- write the key and value rows of `tokens` tokens into their
+ * slots; with `rope`, keys are rotated on the way (rounded to the type, then
+ * quantised), and so are the q_heads heads of q, into q_out: one launch for a
+ * decode step.  rope NULL: nothing is rotated, and q, q_out are not used
+ * (q_heads 0).  A 16-bit cache's format must be the rows' type.
+ *   slots  device, int64 [tokens]: a slot outside the cache (a padding token's -1) writes nothing;
+ *          no two tokens of a call share a slot
+ *   q_out  device, may be q's own data (in place); may not overlap k or v
+ */
+exl3_status_t exl3_kv_write(const exl3_kv_cache_t* cache, const exl3_heads_t* k, const exl3_heads_t* v,
+                            exl3_dtype_t dtype, int64_t tokens, const int64_t* slots, const exl3_rope_t* rope,
+                            const exl3_heads_t* q, int32_t q_heads, void* q_out, int64_t q_out_token_stride,
+                            int64_t q_out_head_stride, void* stream);
+
+/*
+ * exl3_kv_read -- the rows of `tokens` slots, as `dtype` (each one rounding of
+ * the value read back).  A slot outside the cache reads as zeros.
+ *   k, v  device, [tokens][kv_heads][head_dim] (outputs)
+ */
+exl3_status_t exl3_kv_read(const exl3_kv_cache_t* cache, const int64_t* slots, int64_t tokens,
+                           exl3_dtype_t dtype, void* k, void* v, void* stream);
+
+/*
+ * exl3_attention_prompt -- causal attention over whole prompts, packed one
+ * after the other:
+ *     out[i] = sum_j p_ij v[j] / sum_j p_ij,  p_ij = exp(scale * q[i] . k[j])
+ * over the keys j <= i of i's own sequence and, with window > 0, j > i - window.
+ * Scores, softmax statistics and sums are fp32; the weights round to the type
+ * before they meet v.
+ *   q, k, v    [total] tokens of `dtype`;  scale  positive and finite
+ *   cu_seqlens device, int32 [batch + 1]: sequence b is tokens [cu[b], cu[b + 1]); tokens of no
+ *              sequence keep their output
+ *   out        device, [total] tokens of q_heads heads
+ */
+exl3_status_t exl3_attention_prompt(const exl3_heads_t* q, const exl3_heads_t* k, const exl3_heads_t* v,
+                                    exl3_dtype_t dtype, int64_t total, int32_t q_heads, int32_t kv_heads,
+                                    int32_t head_dim, const int32_t* cu_seqlens, int32_t batch, int32_t window,
+                                    float scale, void* out, int64_t out_token_stride, int64_t out_head_stride,
+                                    void* stream);
+
+/*
+ * exl3_attention_paged -- the same over the cache, for the last tokens of each
+ * sequence (one, a few drafted ones, or a chunk of a prompt), whose keys and
+ * values are already written.  Query i of sequence b stands at position
+ * kv_lens[b] - (cu_q[b + 1] - cu_q[b]) + i and sees the keys up to its own; a
+ * query that sees none (a negative position, an empty sequence) gives zeros.
+ *   q           [total_q] tokens of `dtype` (a 16-bit cache's format must be the same)
+ *   block_table device, int32 [batch][table_width]: pages of a sequence in order.  Entries past the
+ *               length are not followed; with a window neither are those of pages wholly before it.  An entry
+ *               outside the cache is not followed either (its keys count as zeros)
+ *   cu_q        device, int32 [batch + 1]: query tokens of sequence b, as cu_seqlens above
+ *   kv_lens     device, int32 [batch]: cached tokens, the new ones among them; at most table_width * page_size
+ *   max_q       HOST: no sequence has more query tokens (a sequence's tokens past it keep their output)
+ *   max_kv      HOST: about the longest length; it only steers how the work is split
+ *   workspace   device, 16-byte aligned, at least exl3_attention_paged_workspace_bytes of the same sizes
+ *               (0 bytes: may be NULL), any contents.  Calls that share it must be ordered on one stream.
+ * Values (and value scales) of keys that one query of a call may not see but another of the same sequence
+ * does must be finite: a weight of zero still multiplies them.  Rows past a length may hold anything.
+ * If a kernel gives up on a bounded wait (exl3_device_status reports it), out is undefined.
+ */
+size_t exl3_attention_paged_workspace_bytes(int64_t total_q, int32_t batch, int32_t q_heads, int32_t kv_heads,
+                                            int32_t head_dim, int32_t max_q, int32_t max_kv);
+exl3_status_t exl3_attention_paged(const exl3_heads_t* q, exl3_dtype_t dtype, int64_t total_q, int32_t q_heads,
+                                   const exl3_kv_cache_t* cache, const int32_t* block_table, int32_t table_width,
+                                   const int32_t* cu_q, const int32_t* kv_lens, int32_t batch, int32_t max_q,
+                                   int32_t max_kv, int32_t window, float scale, void* out,
+                                   int64_t out_token_stride, int64_t out_head_stride, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
+/*
  * exl3_gemm_splitk_noalloc -- the split-k GEMM for callers that cannot allocate.
  *
  * The pages have no counterpart to this call; it exists for callers that have
