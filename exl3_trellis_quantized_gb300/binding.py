@@ -7,6 +7,7 @@ stream to the C ABI.  All arithmetic happens in the library's kernels.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Sequence
 
@@ -435,6 +436,9 @@ KV_FORMATS = {"f16": 0, "bf16": 1, "int8": 2, "int4": 3}
 _KV_DTYPES = {"f16": torch.float16, "bf16": torch.bfloat16, "int8": torch.uint8, "int4": torch.uint8}
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's handle, without a Stream object
+
+
 def _type(t: torch.Tensor, name: str) -> int:
     if t.dtype is torch.bfloat16:
         return _BF16
@@ -453,7 +457,7 @@ def _heads(t: torch.Tensor, dtype, name: str) -> _Heads:
         raise ValueError(f"{name} must be [tokens, heads, head_dim]")
     ts, hs, ds = t.stride()
     tokens, heads, d = t.shape
-    if ds != 1 and d != 1:
+    if ds != 1 and d > 1:
         raise ValueError(f"{name} must be contiguous along head_dim")
     # the stride of an axis of one (or no) element says nothing
     return _Heads(t.data_ptr(), ts if tokens > 1 else heads * d or 8, hs if heads > 1 else d)
@@ -469,6 +473,20 @@ def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
         return False
     (a0, a1), (b0, b1) = span(a), span(b)
     return a0 < b1 and b0 < a1
+
+
+def _out_like(x: torch.Tensor, out: Optional[torch.Tensor], name: str):
+    """The output of rows like x's and its exl3_heads_t; one that the caller gave is x itself or lies apart from it."""
+    if out is None:
+        out = x.new_empty(x.shape)
+        _, heads, d = x.shape
+        return out, _Heads(out.data_ptr(), heads * d or 8, d)
+    if out.shape != x.shape:
+        raise ValueError(f"{name} must have the input's shape")
+    oh = _heads(out, x.dtype, name)
+    if oh.data != x.data_ptr() and _overlap(x, out):
+        raise ValueError(f"{name} overlaps the input without being it")
+    return out, oh
 
 
 def _alike(t: torch.Tensor, dtype, shape, name: str) -> None:
@@ -487,7 +505,7 @@ def rope_phases(rot_dim: int, base: float = 10000.0, scaling: str = "plain", fac
     out = torch.empty(max(0, int(rot_dim)) // 2, dtype=torch.int64)
     amplitude = ctypes.c_float(0.0)
     st = lib().exl3_rope_phases(int(rot_dim), float(base), ROPE_SCALINGS[scaling], float(factor), float(fast),
-                                float(slow), float(original_len), _ptr(out), ctypes.byref(amplitude))
+                                float(slow), float(original_len), out.data_ptr(), ctypes.byref(amplitude))
     _check(st, "exl3_rope_phases")
     return out.to(device), float(amplitude.value)
 
@@ -508,14 +526,8 @@ def rope(x: torch.Tensor, positions: torch.Tensor, phases: torch.Tensor, layout:
     xh = _heads(x, x.dtype, "x")
     tokens, heads, d = x.shape
     r = _rope_args(positions, phases, layout, amplitude, tokens)
-    if out is None:
-        out = torch.empty((tokens, heads, d), dtype=x.dtype, device=x.device)
-    if out.shape != x.shape:
-        raise ValueError("out must have x's shape")
-    oh = _heads(out, x.dtype, "out")
-    if oh.data != xh.data and _overlap(x, out):
-        raise ValueError("out overlaps x without being x")
-    st = lib().exl3_rope(xh, dt, tokens, heads, d, r, oh.data, oh.token_stride, oh.head_stride, _stream(x))
+    out, oh = _out_like(x, out, "out")
+    st = lib().exl3_rope(xh, dt, tokens, heads, d, r, oh.data, oh.token_stride, oh.head_stride, _raw_stream(x.device.index))
     _check(st, "exl3_rope")
     return out
 
@@ -586,17 +598,11 @@ def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tens
         if q.dim() != 3 or q.shape[0] != tokens or q.shape[2] != cache.head_dim:
             raise ValueError("q must be [tokens, heads, head_dim]")
         qh, heads = _heads(q, k.dtype, "q"), q.shape[1]
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if q_out.shape != q.shape:
-            raise ValueError("q_out must have q's shape")
-        oh = _heads(q_out, k.dtype, "q_out")
-        if oh.data != qh.data and _overlap(q, q_out):
-            raise ValueError("q_out overlaps q without being q")
+        q_out, oh = _out_like(q, q_out, "q_out")
         qo = (oh.data, oh.token_stride, oh.head_stride)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    st = lib().exl3_kv_write(cache.args, kh, vh, dt, tokens, _ptr(slots), r, qh, heads, *qo, _stream(k))
+    st = lib().exl3_kv_write(cache.args, kh, vh, dt, tokens, slots.data_ptr(), r, qh, heads, *qo, _raw_stream(k.device.index))
     _check(st, "exl3_kv_write")
     return q_out
 
@@ -612,17 +618,9 @@ def kv_read(cache: KVCache, slots: torch.Tensor, dtype=torch.bfloat16, k: Option
     v = torch.empty(shape, dtype=dtype, device=slots.device) if v is None else v
     _alike(k, dtype, shape, "k")
     _alike(v, dtype, shape, "v")
-    st = lib().exl3_kv_read(cache.args, _ptr(slots), shape[0], _type(k, "k"), _ptr(k), _ptr(v), _stream(slots))
+    st = lib().exl3_kv_read(cache.args, slots.data_ptr(), shape[0], _type(k, "k"), k.data_ptr(), v.data_ptr(), _raw_stream(slots.device.index))
     _check(st, "exl3_kv_read")
     return k, v
-
-
-def _out_like(q: torch.Tensor, out: Optional[torch.Tensor]):
-    if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    if out.shape != q.shape:
-        raise ValueError("out must have q's shape")
-    return out, _heads(out, q.dtype, "out")
 
 
 def attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, max_len: int = 0,
@@ -642,17 +640,22 @@ def attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     _need(cu_seqlens, torch.int32, "cu_seqlens")
     if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
         raise ValueError("cu_seqlens must be [batch + 1]")
-    out, oh = _out_like(q, out)
-    st = lib().exl3_attention_prompt(qh, kh, vh, dt, total, heads, k.shape[1], d, _ptr(cu_seqlens),
+    out, oh = _out_like(q, out, "out")
+    st = lib().exl3_attention_prompt(qh, kh, vh, dt, total, heads, k.shape[1], d, cu_seqlens.data_ptr(),
                                      cu_seqlens.numel() - 1, int(window), d ** -0.5 if scale is None else float(scale),
-                                     oh.data, oh.token_stride, oh.head_stride, _stream(q))
+                                     oh.data, oh.token_stride, oh.head_stride, _raw_stream(q.device.index))
     _check(st, "exl3_attention_prompt")
     return out
 
 
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(*sizes) -> int:
+    return int(lib().exl3_attention_paged_workspace_bytes(*sizes))
+
+
 def attention_paged_workspace_bytes(total_q: int, batch: int, heads: int, kv_heads: int, head_dim: int, max_q: int,
                                     max_kv: int) -> int:
-    return int(lib().exl3_attention_paged_workspace_bytes(total_q, batch, heads, kv_heads, head_dim, max_q, max_kv))
+    return _workspace_bytes(total_q, batch, heads, kv_heads, head_dim, max_q, max_kv)
 
 
 def attention_paged(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, cu_q: torch.Tensor,
@@ -677,15 +680,15 @@ def attention_paged(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, 
     _need(block_table, torch.int32, "block_table")
     if block_table.dim() != 2 or block_table.shape[0] != batch:
         raise ValueError("block_table must be [batch, width]")
-    out, oh = _out_like(q, out)
-    L = lib()
-    need = int(L.exl3_attention_paged_workspace_bytes(total, batch, heads, cache.kv_heads, d, int(max_q), int(max_kv)))
+    out, oh = _out_like(q, out, "out")
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    _need(workspace, torch.uint8, "workspace")
-    st = L.exl3_attention_paged(qh, dt, total, heads, cache.args, _ptr(block_table), block_table.shape[1],
-                                _ptr(cu_q), _ptr(kv_lens), batch, int(max_q), int(max_kv), int(window),
+        need = _workspace_bytes(total, batch, heads, cache.kv_heads, d, int(max_q), int(max_kv))
+        workspace = q.new_empty(need, dtype=torch.uint8)
+    else:
+        _need(workspace, torch.uint8, "workspace")
+    st = lib().exl3_attention_paged(qh, dt, total, heads, cache.args, block_table.data_ptr(), block_table.shape[1],
+                                cu_q.data_ptr(), kv_lens.data_ptr(), batch, int(max_q), int(max_kv), int(window),
                                 d ** -0.5 if scale is None else float(scale), oh.data, oh.token_stride,
-                                oh.head_stride, _ptr(workspace), workspace.numel(), _stream(q))
+                                oh.head_stride, workspace.data_ptr(), workspace.numel(), _raw_stream(q.device.index))
     _check(st, "exl3_attention_paged")
     return out

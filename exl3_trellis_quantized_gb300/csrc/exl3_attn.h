@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/exl3.h"
 
 namespace exl3 {
@@ -90,12 +92,33 @@ struct AttnArgs {
 };
 // Rows (query tokens x heads of a group) one item of the token kernel holds.
 constexpr int kTokenRows = 16;
+// CTAs of the token kernel an SM holds, by the rows it is compiled for (8 or 16).
+constexpr int token_ctas_per_sm(int rows) { return rows <= 8 ? 3 : 2; }
 // Keys per scheduling unit of the token kernel.
 constexpr int kTokenUnit = 64;
 // Few query rows a sequence (max_q * group <= kTokenRows) over a paged cache.
 cudaError_t launch_attn_token(const AttnArgs& a, cudaStream_t stream);
 // Query rows in tiles of 256, prompt (k, v) or paged.
 cudaError_t launch_attn_tile(const AttnArgs& a, bool paged, cudaStream_t stream);
+// Lets KERNEL use `bytes` of dynamic shared memory and, with regs > 0, checks that it was built for `regs` registers a
+// thread: asked of the runtime once a kernel and device.
+template <auto* KERNEL>
+cudaError_t allow_smem(int bytes, int regs = 0) {
+  static std::atomic<uint64_t> done{0};  // bit: device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && (done.load(std::memory_order_relaxed) >> dev & 1u)) return cudaSuccess;
+  if (regs > 0) {
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, KERNEL);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs != regs) return cudaErrorInvalidConfiguration;
+  }
+  e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+  return e;
+}
 // A CUDA result as a status; keeps an error's text for exl3_last_error.
 exl3_status_t api_status(cudaError_t e, const char* where);
 // Wait-timeout flag of the tile kernel's translation unit.

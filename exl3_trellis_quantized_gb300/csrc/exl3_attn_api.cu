@@ -18,6 +18,10 @@ bool valid_strides(int64_t token, int64_t head) {
 bool valid_heads(const exl3_heads_t* h) {
   return h != nullptr && aligned16(h->data) && valid_strides(h->token_stride, h->head_stride);
 }
+// An output of rows like x's: aligned, and where it is x itself, element by element.
+bool valid_out(const exl3_heads_t* x, const void* out, int64_t token, int64_t head) {
+  return aligned16(out) && (out != x->data || (token == x->token_stride && head == x->head_stride));
+}
 // A group's query heads are rows of one tile.
 bool valid_head_counts(int32_t q_heads, int32_t kv_heads) {
   return kv_heads >= 1 && q_heads >= 1 && q_heads % kv_heads == 0 && q_heads / kv_heads <= 128 && q_heads <= 65536;
@@ -73,9 +77,10 @@ PagedPlan paged_plan(int64_t total_q, int64_t batch, int64_t q_heads, int64_t kv
   p.splits = 1;
   p.token = max_q * group <= exl3::kTokenRows;
   if (p.token) {
-    // two CTAs an SM; no more than there are units of keys
-    const int64_t units = batch * kv_heads * ((max_kv + exl3::kTokenUnit - 1) / exl3::kTokenUnit + 1);
-    p.ctas = (int)(units < 2 * kSms ? units : 2 * kSms);
+    // as many CTAs as the SMs hold, but at least two units of keys each
+    const int64_t pairs = batch * kv_heads * ((max_kv + 2 * exl3::kTokenUnit - 1) / (2 * exl3::kTokenUnit) + 1);
+    const int64_t most = kSms * exl3::token_ctas_per_sm((int)(max_q * group));
+    p.ctas = (int)(pairs < most ? pairs : most);
     p.o_bytes = (size_t)2 * p.ctas * exl3::kTokenRows * head_dim * sizeof(float);
     p.ml_bytes = (size_t)2 * p.ctas * exl3::kTokenRows * 2 * sizeof(float);
     return p;
@@ -135,9 +140,7 @@ exl3_status_t exl3_rope(const exl3_heads_t* x, exl3_dtype_t dtype, int64_t token
   if (st != EXL3_OK) return st;
   if (!valid_strides(out_token_stride, out_head_stride)) return EXL3_EINVAL;
   if (tokens == 0) return EXL3_OK;
-  if (!valid_heads(x) || !aligned16(out)) return EXL3_EINVAL;
-  // in place means element by element
-  if (out == x->data && (out_token_stride != x->token_stride || out_head_stride != x->head_stride)) return EXL3_EINVAL;
+  if (!valid_heads(x) || !valid_out(x, out, out_token_stride, out_head_stride)) return EXL3_EINVAL;
   a.x = view(x);
   a.x_heads = heads;
   a.out = out;
@@ -168,8 +171,7 @@ exl3_status_t exl3_kv_write(const exl3_kv_cache_t* cache, const exl3_heads_t* k,
   if (!valid_heads(k) || !valid_heads(v)) return EXL3_EINVAL;
   if (slots == nullptr || (reinterpret_cast<uintptr_t>(slots) & 7u) != 0) return EXL3_EINVAL;
   if (q_heads > 0) {
-    if (!valid_heads(q) || !aligned16(q_out)) return EXL3_EINVAL;
-    if (q_out == q->data && (q_out_token_stride != q->token_stride || q_out_head_stride != q->head_stride)) return EXL3_EINVAL;
+    if (!valid_heads(q) || !valid_out(q, q_out, q_out_token_stride, q_out_head_stride)) return EXL3_EINVAL;
     a.x = view(q);
     a.out = q_out;
     a.out_token_stride = q_out_token_stride;
@@ -211,7 +213,7 @@ exl3_status_t exl3_attention_prompt(const exl3_heads_t* q, const exl3_heads_t* k
   if (st != EXL3_OK) return st;
   if (window < 0 || !(scale > 0.0f) || !isfinite(scale) || !valid_strides(out_token_stride, out_head_stride)) return EXL3_EINVAL;
   if (total == 0 || batch == 0) return EXL3_OK;
-  if (!valid_heads(q) || !valid_heads(k) || !valid_heads(v) || !aligned16(out)) return EXL3_EINVAL;
+  if (!valid_heads(q) || !valid_heads(k) || !valid_heads(v) || !valid_out(q, out, out_token_stride, out_head_stride)) return EXL3_EINVAL;
   if (cu_seqlens == nullptr || (reinterpret_cast<uintptr_t>(cu_seqlens) & 3u) != 0) return EXL3_EINVAL;
   exl3::AttnArgs a = {};
   a.q = view(q);
@@ -255,7 +257,7 @@ exl3_status_t exl3_attention_paged(const exl3_heads_t* q, exl3_dtype_t dtype, in
   if (max_q < 1 || max_kv < 0 || window < 0 || !(scale > 0.0f) || !isfinite(scale)) return EXL3_EINVAL;
   if (!valid_strides(out_token_stride, out_head_stride)) return EXL3_EINVAL;
   if (total_q == 0 || batch == 0) return EXL3_OK;
-  if (!valid_heads(q) || !aligned16(out)) return EXL3_EINVAL;
+  if (!valid_heads(q) || !valid_out(q, out, out_token_stride, out_head_stride)) return EXL3_EINVAL;
   const void* ints[3] = {block_table, cu_q, kv_lens};
   for (const void* p : ints)
     if (p == nullptr || (reinterpret_cast<uintptr_t>(p) & 3u) != 0) return EXL3_EINVAL;

@@ -891,13 +891,9 @@ cudaError_t launch_tile(const AttnArgs& a, cudaStream_t stream) {
     if (e == cudaSuccess) e = make_map(&maps.v, a.cache.v, D, 1, rows, D, D, box);
   }
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(attn_tile_kernel<D, SRC, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-  if (e != cudaSuccess) return e;
   // the register split waits for registers that a launch with fewer would never have
-  cudaFuncAttributes fa;
-  e = cudaFuncGetAttributes(&fa, attn_tile_kernel<D, SRC, BF16>);
+  e = allow_smem<attn_tile_kernel<D, SRC, BF16>>(C::kSmem, C::kLaunchRegs);
   if (e != cudaSuccess) return e;
-  if (fa.numRegs != C::kLaunchRegs) return cudaErrorInvalidConfiguration;
   // row tiles: no more than all rows' and one partly filled for each sequence
   const int64_t group = a.heads / a.kv_heads;
   const int64_t tiles = a.total_q * group / kItemRows + (a.total_q < a.batch ? a.total_q : a.batch);

@@ -2,24 +2,31 @@
 // drafted tokens) over the paged cache, and the join of split results.
 //
 // One item is a sequence and a key head; its rows are the query tokens times
-// the group's query heads (at most 16, the M of mma.m16n8k16).  Scores, the
-// running maximum and sum, and the output accumulate in one pass over the keys:
+// the group's query heads (at most 16).  Scores, the running maximum and sum, and
+// the output accumulate in one pass over the keys:
 //     m' = max(m, s),  l' = l 2^(m - m') + sum 2^(s - m'),  o' = o 2^(m - m') + sum 2^(s - m') v.
 // Every cached byte is read once and meets 2 * 16 multiply-adds a value at the
-// most, so DRAM bounds it: the tensor work is far below even the warp-level
-// MMA rate, whose fragments let the quantised formats go from shared memory to
-// operands in registers without a 16-bit copy.
+// most, so DRAM bounds it, and after that the instructions that turn codes into
+// operands.  The keys and values are the M = 16 operand of mma.m16n8k16 and the
+// rows the N = 8 one (S' = K Q', O' = V' P'): with up to eight rows, the usual
+// decode step, no multiply-add, exponential or register goes to rows that are not
+// there (with the rows as M = 16, 8-bit keys took 640 instructions a warp and 32
+// keys, against 470).  The codes go from shared memory to operands in
+// registers without a 16-bit copy in between.
 //
 // Split.  The work is the list of all items' units of 64 keys, cut into one
 // equal range a CTA (whatever the sequences' lengths are), so a range may begin
-// and end inside items.  Each CTA works the cuts out from kv_lens by itself.  An
-// item inside one range is finished there; one that is cut leaves (m, l, o) of
-// its parts in the workspace, which attn_token_join_kernel joins in order.
-// Inside a CTA four warps take turns at the range's steps, each with its own
-// ring of asynchronous copies and its own (m, l, o), joined at the item's end.
+// and end inside items; an item counts a few units more than it has, for what
+// beginning and ending one costs.  Each CTA works the cuts out from kv_lens by
+// itself.  An item inside one range is finished there; one that is cut leaves
+// (m, l, o) of its parts in the workspace, which attn_token_join_kernel joins in
+// order.  Inside a CTA four warps take turns at the range's steps, each with its
+// own ring of asynchronous copies and its own (m, l, o), joined at the item's end.
 //
 // Quantised rows stay in the rotated basis (see exl3_rope_cache.cu): q is
-// rotated by the D-point Hadamard transform times 8/D once, the output once.
+// rotated by the D-point Hadamard transform times 8/D once, the output once.  The
+// rotated q is not exact in fp16: it goes in as two fp16 terms (22 bits), since
+// one alone moved the outputs of fp16 queries by 1.7 times their own rounding.
 // A key's scale multiplies its score in fp32.  A value's scale goes into the
 // exponent: the weight 2^(s + log2 scale - m), with m the maximum of the same sum,
 // is at most 2^8 whatever the scales are, so rounding it to fp16 loses nothing by
@@ -40,6 +47,8 @@ constexpr float kNegInf = -__builtin_huge_valf();
 // The reference of the exponents moves only when the maximum has grown by more
 // than this (log2), so most steps rescale nothing; weights stay below 2^8.
 constexpr float kSlack = 8.0f;
+// What an item's beginning and end cost, in units of keys (for the cuts).
+constexpr int kItemUnits = 4;
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -122,6 +131,28 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
+// Transpose of an 8x8 matrix of 16-bit values held as fragments.
+__device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+// The larger, or NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float lds_bf16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+  return __uint_as_float((uint32_t)v << 16);
+}
 // Two bytes (offset codes) widened by the pattern of 1024: {1024 + c0, 1024 + c1} - 1152.
 __device__ __forceinline__ uint32_t bytes_to_h2(uint32_t w, uint32_t sel) {
   return hsub2(__byte_perm(w, 0x64646464u, sel), 0x64806480u);
@@ -139,6 +170,8 @@ struct Seq {
   int first;  // first key that any row sees
   int lo;     // first key of the first unit
   int units;  // 0: no query tokens
+  // units that the cuts count for one of its items: kItemUnits, then the units
+  __device__ __forceinline__ int weight() const { return units == 0 ? 0 : units + kItemUnits; }
 };
 __device__ __forceinline__ Seq load_seq(const AttnArgs& a, int b) {
   Seq s;
@@ -161,7 +194,7 @@ __device__ __forceinline__ Seq load_seq(const AttnArgs& a, int b) {
 // All units of the call (one warp; every lane gets the sum).
 __device__ int64_t total_units(const AttnArgs& a, int lane) {
   int64_t sum = 0;
-  for (int b = lane; b < a.batch; b += 32) sum += load_seq(a, b).units;
+  for (int b = lane; b < a.batch; b += 32) sum += load_seq(a, b).weight();
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   return sum * a.kv_heads;
@@ -170,7 +203,7 @@ __device__ int64_t total_units(const AttnArgs& a, int lane) {
 __device__ int find_seq(const AttnArgs& a, int lane, int64_t u, int64_t* before) {
   int64_t base = 0;
   for (int b0 = 0; b0 < a.batch; b0 += 32) {
-    int64_t n = b0 + lane < a.batch ? (int64_t)load_seq(a, b0 + lane).units * a.kv_heads : 0;
+    int64_t n = b0 + lane < a.batch ? (int64_t)load_seq(a, b0 + lane).weight() * a.kv_heads : 0;
     int64_t inc = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -189,24 +222,49 @@ __device__ int find_seq(const AttnArgs& a, int lane, int64_t u, int64_t* before)
   return a.batch;
 }
 
-// FMT: KvFormat.  BF16: operand type of the MMAs (fp16 for the quantised formats).
-template <int FMT, int D>
+// FMT: KvFormat.  NR: tiles of eight rows.
+template <int FMT, int D, int NR>
 struct TokenCfg {
   static constexpr bool kQuant = kv_quantised(FMT);
-  static constexpr bool kBf16 = FMT == kKvBf16;
+  static constexpr bool kBf16 = FMT == kKvBf16;  // operand type of the MMAs (fp16 for the quantised formats)
+  static constexpr int kRows = 8 * NR;
+  static constexpr int kCtas = token_ctas_per_sm(kRows);
   static constexpr int kRow = kv_row_bytes(FMT, D);
   static constexpr int kStep = kRow >= 256 ? 16 : 32;  // keys a warp takes at a time
   static constexpr int kSide = kStep * kRow;           // bytes of a step's keys (or values)
   static constexpr int kScales = kQuant ? 4 * kStep : 0;
   static constexpr int kStage = 2 * kSide + kScales;
-  static constexpr int kStages = kSide >= 4096 ? 3 : 5;
-  static constexpr int kRing = kStages * kStage;                    // a warp's
-  static constexpr int kJoin = kTokenRows * D * 4 + kTokenRows * 8;  // a warp's (o, m, l) at an item's end
+  static constexpr int kStages = kSide >= 4096 ? 2 : 4;
+  static constexpr int kRing = kStages * kStage;           // a warp's
+  static constexpr int kJoin = kRows * D * 4 + kRows * 8;  // a warp's (o, m, l) at an item's end
   static constexpr int kWarpBytes = ((kRing > kJoin ? kRing : kJoin) + 127) / 128 * 128;
-  static constexpr int kQBytes = kQuant ? kTokenRows * D * 2 : 0;
+  static constexpr int kQBytes = kQuant ? 2 * kRows * D * 2 : 0;  // two fp16 terms of the rotated q
   static constexpr int kSmem = kWarps * kWarpBytes + kQBytes;
   static constexpr int kChunks = kRow / 16;  // 16-byte chunks of a row
+  static constexpr int kTpr = kThreads / kRows;  // threads of a row where the CTA works on whole rows
+  static constexpr int kPer = D / kTpr;          // and values of each
+  static_assert(kCtas * (kSmem + 1024) <= 228 * 1024, "shared memory");
 };
+// Hadamard transform of a row held as PER consecutive values by TPR neighbouring threads.
+template <int PER, int TPR>
+__device__ __forceinline__ void hadamard_threads(float (&v)[PER], int part) {
+#pragma unroll
+  for (int st = 1; st < PER; st *= 2)
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (!(i & st)) {
+        const float x = v[i], y = v[i + st];
+        v[i] = x + y;
+        v[i + st] = x - y;
+      }
+#pragma unroll
+  for (int st = 1; st < TPR; st *= 2)
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const float x = __shfl_xor_sync(0xffffffffu, v[i], st);
+      v[i] = (part & st) ? x - v[i] : v[i] + x;
+    }
+}
 
 // Byte offset of chunk c of row r of a step's keys or values.  The permutations
 // keep the eight or sixteen lanes of one shared-memory access on different
@@ -221,13 +279,13 @@ __device__ __forceinline__ uint32_t ring_offset(int r, int c) {
   return (uint32_t)(r * ROW + (c << 4));
 }
 
-template <int FMT, int D>
-__global__ void __launch_bounds__(kThreads, 2) attn_token_kernel(const AttnArgs a) {
-  using C = TokenCfg<FMT, D>;
+template <int FMT, int D, int NR>
+__global__ void __launch_bounds__(kThreads, token_ctas_per_sm(8 * NR)) attn_token_kernel(const AttnArgs a) {
+  using C = TokenCfg<FMT, D, NR>;
   constexpr bool BF16 = C::kBf16;
-  constexpr int KS = D / 16;       // k16 steps of the scores
-  constexpr int NT = C::kStep / 8;  // 8-key tiles of a step
-  constexpr int ND = D / 8;        // 8-column tiles of the output
+  constexpr int KS = D / 16;        // k16 steps of the scores
+  constexpr int NK = C::kStep / 16;  // 16-key tiles of a step
+  constexpr int ND = D / 16;        // 16-row tiles of the output (transposed)
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, q = lane & 3;
@@ -246,16 +304,24 @@ __global__ void __launch_bounds__(kThreads, 2) attn_token_kernel(const AttnArgs 
   while (u < u_end) {
     Seq s = load_seq(a, b);
     while (s.units == 0) s = load_seq(a, ++b);  // there is a unit left, so a sequence that has it
+    const int weight = s.weight();
     const int64_t in_seq = u - before;
-    const int h = (int)(in_seq / s.units);
-    const int unit0 = (int)(in_seq - (int64_t)h * s.units);
+    const int h = (int)(in_seq / weight);
+    const int at0 = (int)(in_seq - (int64_t)h * weight);
     const int64_t room = u_end - u;
-    const int unit1 = room < s.units - unit0 ? unit0 + (int)room : s.units;
+    const int at1 = room < weight - at0 ? at0 + (int)room : weight;
+    const int32_t* pages = a.table + (int64_t)b * a.table_width;
+    u += at1 - at0;
+    if (at1 == weight && h == a.kv_heads - 1) {
+      before += (int64_t)weight * a.kv_heads;
+      ++b;
+    }
+    const int unit0 = max(0, at0 - kItemUnits), unit1 = max(0, at1 - kItemUnits);
+    if (unit0 == unit1) continue;  // nothing but what the item's beginning counts
     const int rows = s.q_len * group;
     const int t0 = s.lo + unit0 * kTokenUnit;
     const int t1 = min(s.kv_len, s.lo + unit1 * kTokenUnit);
     const int steps = t1 > t0 ? (t1 - t0 + C::kStep - 1) / C::kStep : 0;
-    const int32_t* pages = a.table + (int64_t)b * a.table_width;
 
     // ---- page ids of this warp's next 32 steps, one step a lane
     constexpr int PG = C::kStep / 16;  // a step's 16-key groups, each inside one page
@@ -272,6 +338,41 @@ __global__ void __launch_bounds__(kThreads, 2) attn_token_kernel(const AttnArgs 
     const int mine = steps > warp ? (steps - warp + kWarps - 1) / kWarps : 0;
     int pid_base = 0;
     load_pids(0);
+
+    // ---- the query rows' loads, in flight with the page ids'
+    uint32_t qb[NR][KS][2];  // B fragments: row 8n + g, values 16k + 2q, + 1 and + 8, + 9; zeros past the last row
+    constexpr int QW = C::kQuant ? C::kPer / 2 : 1;
+    uint32_t qraw[QW];
+    const int jr = threadIdx.x / C::kTpr, part = threadIdx.x % C::kTpr;  // row and part where the CTA works on rows
+    if constexpr (!C::kQuant) {
+#pragma unroll
+      for (int n = 0; n < NR; ++n) {
+        const int r = 8 * n + g;
+        const uint16_t* src = nullptr;
+        if (r < rows) {
+          const int tok = r / group;
+          src = static_cast<const uint16_t*>(a.q.data) + (s.q0 + tok) * a.q.token_stride +
+                (int64_t)(h * group + r - tok * group) * a.q.head_stride;
+        }
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          qb[n][k][0] = src ? *reinterpret_cast<const uint32_t*>(src + 16 * k + 2 * q) : 0u;
+          qb[n][k][1] = src ? *reinterpret_cast<const uint32_t*>(src + 16 * k + 8 + 2 * q) : 0u;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < QW; ++i) qraw[i] = 0u;
+      if (jr < rows) {
+        const int tok = jr / group;
+        const uint32_t* src = reinterpret_cast<const uint32_t*>(
+            static_cast<const uint16_t*>(a.q.data) + (s.q0 + tok) * a.q.token_stride +
+            (int64_t)(h * group + jr - tok * group) * a.q.head_stride + part * C::kPer);
+#pragma unroll
+        for (int i = 0; i < QW; ++i) qraw[i] = src[i];
+      }
+    }
+
     auto issue = [&](int i) {  // copies of this warp's step i into slot i % stages
       if (i < mine) {
         if (i - pid_base >= 32) {
@@ -295,8 +396,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_token_kernel(const AttnArgs 
           const int r = idx / C::kChunks, c = idx % C::kChunks;
           const int p = PG == 1 ? 0 : r >> 4;
           // rows outside the keys seen come as zeros, so no weight ever meets what a page holds there
-          const bool there = (PG == 1 ? ok[0] : p ? ok[PG - 1] : ok[0]) && t + r < t1 && t + r >= s.first;
-          const int64_t row = (PG == 1 || p == 0 ? base[0] : base[PG - 1]) + (there ? (r & 15) : 0);
+          const bool there = (p ? ok[PG - 1] : ok[0]) && t + r < t1 && t + r >= s.first;
+          const int64_t row = (p ? base[PG - 1] : base[0]) + (there ? (r & 15) : 0);
           const uint32_t off = ring_offset<C::kRow>(r, c);
           cp_async16(dst + off, a.cache.k + row * C::kRow + 16 * c, there);
           cp_async16(dst + C::kSide + off, a.cache.v + row * C::kRow + 16 * c, there);
@@ -315,103 +416,70 @@ __global__ void __launch_bounds__(kThreads, 2) attn_token_kernel(const AttnArgs 
 #pragma unroll
     for (int i = 0; i < C::kStages - 1; ++i) issue(i);
 
-    // ---- the query rows as A fragments; the rows past the last are zeros
-    uint32_t qa[KS][4];
-    if constexpr (!C::kQuant) {
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int r = g + 8 * half;
-        const uint16_t* src = nullptr;
-        if (r < rows) {
-          const int tok = r / group;
-          src = static_cast<const uint16_t*>(a.q.data) + (s.q0 + tok) * a.q.token_stride +
-                (int64_t)(h * group + r - tok * group) * a.q.head_stride;
-        }
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          qa[k][half] = src ? *reinterpret_cast<const uint32_t*>(src + 16 * k + 2 * q) : 0u;
-          qa[k][half + 2] = src ? *reinterpret_cast<const uint32_t*>(src + 16 * k + 8 + 2 * q) : 0u;
-        }
-      }
-    } else {
-      // eight threads a row, D/8 values each: rotate, times 8/D, to fp16 in shared memory
-      constexpr int PER = D / 8;
+    uint32_t ql[C::kQuant ? NR : 1][KS][2];  // the second term of the rotated q
+    if constexpr (C::kQuant) {
+      // rotate, times 8/D, to two fp16 terms in shared memory
       uint16_t* qs = reinterpret_cast<uint16_t*>(smem + kWarps * C::kWarpBytes);
-      const int r = threadIdx.x >> 3, part = threadIdx.x & 7;
-      float v[PER];
+      float v[C::kPer];
 #pragma unroll
-      for (int i = 0; i < PER; ++i) v[i] = 0.0f;
-      if (r < rows) {
-        const int tok = r / group;
-        const uint16_t* src = static_cast<const uint16_t*>(a.q.data) + (s.q0 + tok) * a.q.token_stride +
-                              (int64_t)(h * group + r - tok * group) * a.q.head_stride + part * PER;
-#pragma unroll
-        for (int i = 0; i < PER; i += 8) {
-          const uint4 w = *reinterpret_cast<const uint4*>(src + i);
-          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            v[i + 2 * j] = to_f32((uint16_t)(ww[j] & 0xFFFFu), a.bf16 != 0);
-            v[i + 2 * j + 1] = to_f32((uint16_t)(ww[j] >> 16), a.bf16 != 0);
-          }
-        }
+      for (int i = 0; i < QW; ++i) {
+        v[2 * i] = to_f32((uint16_t)(qraw[i] & 0xFFFFu), a.bf16 != 0);
+        v[2 * i + 1] = to_f32((uint16_t)(qraw[i] >> 16), a.bf16 != 0);
       }
+      hadamard_threads<C::kPer, C::kTpr>(v, part);
 #pragma unroll
-      for (int st = 1; st < PER; st *= 2)
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-          if (!(i & st)) {
-            const float x = v[i], y = v[i + st];
-            v[i] = x + y;
-            v[i + st] = x - y;
-          }
-#pragma unroll
-      for (int st = 1; st < 8; st *= 2)
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-          const float o = __shfl_xor_sync(0xffffffffu, v[i], st);
-          v[i] = (part & st) ? o - v[i] : v[i] + o;
-        }
-#pragma unroll
-      for (int i = 0; i < PER; i += 2)
-        *reinterpret_cast<uint32_t*>(qs + r * D + part * PER + i) = pack2<false>(v[i] * (8.0f / D), v[i + 1] * (8.0f / D));
+      for (int i = 0; i < C::kPer; i += 2) {
+        const float x = v[i] * (8.0f / D), y = v[i + 1] * (8.0f / D);
+        const uint32_t hi = pack2<false>(x, y);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+        *reinterpret_cast<uint32_t*>(qs + jr * D + part * C::kPer + i) = hi;
+        *reinterpret_cast<uint32_t*>(qs + (C::kRows + jr) * D + part * C::kPer + i) = pack2<false>(x - f.x, y - f.y);
+      }
       __syncthreads();
       // fragments in the order in which the codes come out of their words
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const uint16_t* src = qs + (g + 8 * half) * D;
+      for (int n = 0; n < 2 * NR; ++n) {
+        const uint16_t* src = qs + (8 * n + g) * D;
+        uint32_t(&dst)[KS][2] = n < NR ? qb[n % NR] : ql[n % NR];
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
           if constexpr (FMT == kKvInt8) {
             // lane q holds values 16q .. 16q + 15 (of each 64), four a k16 step
-            const int d = (k >> 2) * 64 + 16 * q + 4 * (k & 3);
-            qa[k][half] = *reinterpret_cast<const uint32_t*>(src + d);
-            qa[k][half + 2] = *reinterpret_cast<const uint32_t*>(src + d + 2);
+            const uint32_t* w = reinterpret_cast<const uint32_t*>(src + (k >> 2) * 64 + 16 * q + 4 * (k & 3));
+            dst[k][0] = w[0];
+            dst[k][1] = w[1];
           } else {
             // lane q holds values (D/4)q .. , eight a word, pairs (0, 4) (1, 5) then (2, 6) (3, 7)
             const int d = (D / 4) * q + 8 * (k >> 1) + 2 * (k & 1);
-            qa[k][half] = (uint32_t)src[d] | (uint32_t)src[d + 4] << 16;
-            qa[k][half + 2] = (uint32_t)src[d + 1] | (uint32_t)src[d + 5] << 16;
+            dst[k][0] = (uint32_t)src[d] | (uint32_t)src[d + 4] << 16;
+            dst[k][1] = (uint32_t)src[d + 1] | (uint32_t)src[d + 5] << 16;
           }
         }
       }
     }
 
-    // ---- the two rows of this lane: what they see, and their running softmax
-    int lim[2], low[2];
+    // ---- this lane's rows 8n + 2q, + 1: what they see, and their running softmax
+    int lim[NR][2], low[NR][2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = min(g + 8 * i, rows - 1);
-      const int pos = s.kv_len - s.q_len + r / group;
-      lim[i] = min(pos, t1 - 1);
-      low[i] = a.window > 0 ? max(0, pos - a.window + 1) : 0;
-    }
+    for (int n = 0; n < NR; ++n)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = min(8 * n + 2 * q + i, rows - 1);
+        const int pos = s.kv_len - s.q_len + r / group;
+        lim[n][i] = min(pos, t1 - 1);
+        low[n][i] = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+      }
     const int lim_all = min(s.kv_len - s.q_len, t1 - 1);  // keys up to here are seen by every row
     const int low_all = a.window > 0 ? max(0, s.kv_len - a.window) : 0;
-    float m[2] = {kNegInf, kNegInf}, l[2] = {0.0f, 0.0f};
-    float o[ND][4];
+    float m[NR][2], l[NR][2];
+    float o[NR][ND][4];  // rows of the output's tile j: values (see the write below), columns: rows 2q, 2q + 1
 #pragma unroll
-    for (int j = 0; j < ND; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
+    for (int n = 0; n < NR; ++n) {
+      m[n][0] = m[n][1] = kNegInf;
+      l[n][0] = l[n][1] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < ND; ++j) o[n][j][0] = o[n][j][1] = o[n][j][2] = o[n][j][3] = 0.0f;
+    }
 
     for (int i = 0; i < mine; ++i) {
       issue(i + C::kStages - 1);
@@ -421,163 +489,187 @@ __global__ void __launch_bounds__(kThreads, 2) attn_token_kernel(const AttnArgs 
       const uint32_t vb = kb + C::kSide;
       const int t = t0 + (warp + kWarps * i) * C::kStep;
 
-      // ---- scores
-      float sc[NT][4];
+      // ---- scores of keys 16x + g (elements 0, 1) and 16x + g + 8 (2, 3)
+      float sc[NK][NR][4];
 #pragma unroll
-      for (int j = 0; j < NT; ++j) sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.0f;
-      if constexpr (!C::kQuant) {
+      for (int x = 0; x < NK; ++x) {
 #pragma unroll
-        for (int j = 0; j < NT; j += 2)
+        for (int n = 0; n < NR; ++n) sc[x][n][0] = sc[x][n][1] = sc[x][n][2] = sc[x][n][3] = 0.0f;
+        if constexpr (!C::kQuant) {
 #pragma unroll
           for (int k = 0; k < KS; ++k) {
             uint32_t r[4];
-            const int row = 8 * j + (lane & 7) + ((lane >> 4) << 3);
-            ldmatrix_x4(kb + ring_offset<C::kRow>(row, 2 * k + ((lane >> 3) & 1)), r);
-            mma16816<BF16>(sc[j], qa[k], r[0], r[1]);
-            mma16816<BF16>(sc[j + 1], qa[k], r[2], r[3]);
+            ldmatrix_x4(kb + ring_offset<C::kRow>(16 * x + (lane & 15), 2 * k + (lane >> 4)), r);
+#pragma unroll
+            for (int n = 0; n < NR; ++n) mma16816<BF16>(sc[x][n], r, qb[n][k][0], qb[n][k][1]);
           }
-      } else {
+        } else if constexpr (FMT == kKvInt8) {
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          const int row = 8 * j + g;
-          if constexpr (FMT == kKvInt8) {
+          for (int k4 = 0; k4 < KS / 4; ++k4) {
+            const uint4 w0 = lds128(kb + ring_offset<C::kRow>(16 * x + g, 4 * k4 + q));
+            const uint4 w1 = lds128(kb + ring_offset<C::kRow>(16 * x + g + 8, 4 * k4 + q));
+            const uint32_t u0[4] = {w0.x, w0.y, w0.z, w0.w}, u1[4] = {w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-            for (int k4 = 0; k4 < KS / 4; ++k4) {
-              const uint4 w = lds128(kb + ring_offset<C::kRow>(row, 4 * k4 + q));
-              const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t r[4] = {bytes_to_h2(u0[k], 0x4140), bytes_to_h2(u1[k], 0x4140), bytes_to_h2(u0[k], 0x4342),
+                                     bytes_to_h2(u1[k], 0x4342)};
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                mma16816<false>(sc[j], qa[4 * k4 + k], bytes_to_h2(ww[k], 0x4140),
-                                bytes_to_h2(ww[k], 0x4342));
+              for (int n = 0; n < NR; ++n) {
+                mma16816<false>(sc[x][n], r, qb[n][4 * k4 + k][0], qb[n][4 * k4 + k][1]);
+                mma16816<false>(sc[x][n], r, ql[n][4 * k4 + k][0], ql[n][4 * k4 + k][1]);
+              }
             }
+          }
+        } else {
+          uint32_t u0[D / 32], u1[D / 32];
+          if constexpr (D == 128) {
+            const uint4 w0 = lds128(kb + ring_offset<C::kRow>(16 * x + g, q));
+            const uint4 w1 = lds128(kb + ring_offset<C::kRow>(16 * x + g + 8, q));
+            u0[0] = w0.x, u0[1] = w0.y, u0[2] = w0.z, u0[3] = w0.w;
+            u1[0] = w1.x, u1[1] = w1.y, u1[2] = w1.z, u1[3] = w1.w;
           } else {
-            uint32_t ww[D / 32];
-            if constexpr (D == 128) {
-              const uint4 w = lds128(kb + ring_offset<C::kRow>(row, q));
-              ww[0] = w.x, ww[1] = w.y, ww[2] = w.z, ww[3] = w.w;
-            } else {
-              const uint2 w = lds64(kb + ring_offset<C::kRow>(row, q >> 1) + 8 * (q & 1));
-              ww[0] = w.x, ww[1] = w.y;
-            }
+            const uint2 w0 = lds64(kb + ring_offset<C::kRow>(16 * x + g, q >> 1) + 8 * (q & 1));
+            const uint2 w1 = lds64(kb + ring_offset<C::kRow>(16 * x + g + 8, q >> 1) + 8 * (q & 1));
+            u0[0] = w0.x, u0[1] = w0.y;
+            u1[0] = w1.x, u1[1] = w1.y;
+          }
 #pragma unroll
-            for (int k = 0; k < D / 32; ++k) {
-              mma16816<false>(sc[j], qa[2 * k], nib_lo(ww[k]), nib_hi(ww[k]));
-              mma16816<false>(sc[j], qa[2 * k + 1], nib_lo(ww[k] >> 8), nib_hi(ww[k] >> 8));
+          for (int k = 0; k < KS; ++k) {
+            const uint32_t x0 = u0[k >> 1] >> (8 * (k & 1)), x1 = u1[k >> 1] >> (8 * (k & 1));
+            const uint32_t r[4] = {nib_lo(x0), nib_lo(x1), nib_hi(x0), nib_hi(x1)};
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
+              mma16816<false>(sc[x][n], r, qb[n][k][0], qb[n][k][1]);
+              mma16816<false>(sc[x][n], r, ql[n][k][0], ql[n][k][1]);
             }
           }
         }
       }
 
       // ---- scale, mask, running maximum
-      float rv[NT][2];  // quantised: 1 / value scale of this lane's keys
+      float rv[NK][2];  // quantised: 1 / value scale of this lane's keys
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
+      for (int x = 0; x < NK; ++x) {
         if constexpr (C::kQuant) {
-          const uint32_t ks = lds32(kb + 2 * C::kSide + 2 * (8 * j + 2 * q));
-          const uint32_t vs = lds32(kb + 2 * C::kSide + 2 * C::kStep + 2 * (8 * j + 2 * q));
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const float kc = __uint_as_float(c ? ks & 0xFFFF0000u : ks << 16) * a.scale_log2;
-            const float vc = fmaxf(__uint_as_float(c ? vs & 0xFFFF0000u : vs << 16), 7.888609052210118e-31f);
-            // fmaxf drops a NaN scale (a row that reads back as NaN); the sum with the raw scale keeps it
-            const float nan = __uint_as_float(c ? vs & 0xFFFF0000u : vs << 16) * 0.0f;
-            const float lv = lg2(vc) + nan;
-            rv[j][c] = __frcp_rn(vc);
-            sc[j][c] = fmaf(sc[j][c], kc, lv);
-            sc[j][c + 2] = fmaf(sc[j][c + 2], kc, lv);
+          for (int y = 0; y < 2; ++y) {
+            const uint32_t at = kb + 2 * C::kSide + 2 * (16 * x + 8 * y + g);
+            const float kc = lds_bf16(at) * a.scale_log2;
+            // a NaN scale (a row that reads back as NaN) stays one
+            const float vc = max_nan(lds_bf16(at + 2 * C::kStep), 7.888609052210118e-31f);
+            const float lv = lg2(vc);
+            rv[x][y] = rcp(vc);
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
+              sc[x][n][2 * y] = fmaf(sc[x][n][2 * y], kc, lv);
+              sc[x][n][2 * y + 1] = fmaf(sc[x][n][2 * y + 1], kc, lv);
+            }
           }
         } else {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) sc[j][c] *= a.scale_log2;
+          for (int n = 0; n < NR; ++n)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) sc[x][n][c] *= a.scale_log2;
         }
       }
       if (t + C::kStep - 1 > lim_all || t < low_all) {
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+        for (int x = 0; x < NK; ++x)
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const int key = t + 8 * j + 2 * q + (c & 1);
-            if (key > lim[c >> 1] || key < low[c >> 1]) sc[j][c] = kNegInf;
+            const int key = t + 16 * x + g + 8 * (c >> 1);
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
+              if (key > lim[n][c & 1] || key < low[n][c & 1]) {
+                sc[x][n][c] = kNegInf;
+              }
+            if constexpr (C::kQuant) {
+              // seen by no row: its scale may be anything
+              if (key > lim_all + s.q_len - 1 || key < s.first) rv[x][c >> 1] = 0.0f;
+            }
           }
       }
-      float top[2] = {kNegInf, kNegInf};
+      float top[NR][2];
+      bool up = false;
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        top[0] = fmaxf(top[0], fmaxf(sc[j][0], sc[j][1]));
-        top[1] = fmaxf(top[1], fmaxf(sc[j][2], sc[j][3]));
-      }
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
-        top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
-      }
-      const bool up0 = top[0] > m[0] + kSlack, up1 = top[1] > m[1] + kSlack;
-      if (__any_sync(0xffffffffu, up0 || up1)) {
-        const float f0 = up0 ? ex2(m[0] - top[0]) : 1.0f, f1 = up1 ? ex2(m[1] - top[1]) : 1.0f;
-        m[0] = up0 ? top[0] : m[0];
-        m[1] = up1 ? top[1] : m[1];
-        l[0] *= f0;
-        l[1] *= f1;
-#pragma unroll
-        for (int j = 0; j < ND; ++j) {
-          o[j][0] *= f0;
-          o[j][1] *= f0;
-          o[j][2] *= f1;
-          o[j][3] *= f1;
-        }
-      }
-      // a row that has seen nothing yet has only -inf scores; any finite reference gives it zero weights
-      const float ref0 = m[0] == kNegInf ? 0.0f : m[0], ref1 = m[1] == kNegInf ? 0.0f : m[1];
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
+      for (int n = 0; n < NR; ++n)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          sc[j][c] = ex2(sc[j][c] - ref0);
-          sc[j][c + 2] = ex2(sc[j][c + 2] - ref1);
-          if constexpr (C::kQuant) {
-            l[0] = fmaf(sc[j][c], rv[j][c], l[0]);
-            l[1] = fmaf(sc[j][c + 2], rv[j][c], l[1]);
-          } else {
-            l[0] += sc[j][c];
-            l[1] += sc[j][c + 2];
+          float v = kNegInf;
+#pragma unroll
+          for (int x = 0; x < NK; ++x) v = fmaxf(v, fmaxf(sc[x][n][c], sc[x][n][c + 2]));
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+          top[n][c] = v;
+          up = up || v > m[n][c] + kSlack;
+        }
+      if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+          float f[2];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const bool u1 = top[n][c] > m[n][c] + kSlack;
+            f[c] = u1 ? ex2(m[n][c] - top[n][c]) : 1.0f;
+            m[n][c] = u1 ? top[n][c] : m[n][c];
+            l[n][c] *= f[c];
+          }
+#pragma unroll
+          for (int j = 0; j < ND; ++j) {
+            o[n][j][0] *= f[0];
+            o[n][j][1] *= f[1];
+            o[n][j][2] *= f[0];
+            o[n][j][3] *= f[1];
           }
         }
       }
 
-      // ---- weights times values
+      // ---- weights, and weights times values
 #pragma unroll
-      for (int k = 0; k < C::kStep / 16; ++k) {
-        const uint32_t pa[4] = {pack2<BF16>(sc[2 * k][0], sc[2 * k][1]), pack2<BF16>(sc[2 * k][2], sc[2 * k][3]),
-                                pack2<BF16>(sc[2 * k + 1][0], sc[2 * k + 1][1]),
-                                pack2<BF16>(sc[2 * k + 1][2], sc[2 * k + 1][3])};
+      for (int x = 0; x < NK; ++x) {
+        uint32_t pb[NR][2];
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            // a row that has seen nothing yet has only -inf scores; any finite reference gives it zero weights
+            const float ref = m[n][c & 1] == kNegInf ? 0.0f : m[n][c & 1];
+            sc[x][n][c] = ex2(sc[x][n][c] - ref);
+            l[n][c & 1] = C::kQuant ? fmaf(sc[x][n][c], rv[x][c >> 1], l[n][c & 1]) : l[n][c & 1] + sc[x][n][c];
+          }
+          pb[n][0] = movmatrix(pack2<BF16>(sc[x][n][0], sc[x][n][1]));
+          pb[n][1] = movmatrix(pack2<BF16>(sc[x][n][2], sc[x][n][3]));
+        }
         if constexpr (!C::kQuant) {
 #pragma unroll
-          for (int j = 0; j < ND; j += 2) {
+          for (int j = 0; j < ND; ++j) {
             uint32_t r[4];
-            const int row = 16 * k + (lane & 15);
-            ldmatrix_x4_trans(vb + ring_offset<C::kRow>(row, j + (lane >> 4)), r);
-            mma16816<BF16>(o[j], pa, r[0], r[1]);
-            mma16816<BF16>(o[j + 1], pa, r[2], r[3]);
+            const int row = 16 * x + (lane & 7) + ((lane >> 4) << 3);
+            ldmatrix_x4_trans(vb + ring_offset<C::kRow>(row, 2 * j + ((lane >> 3) & 1)), r);
+#pragma unroll
+            for (int n = 0; n < NR; ++n) mma16816<BF16>(o[n][j], r, pb[n][0], pb[n][1]);
           }
         } else {
           // this lane's keys 2q, 2q + 1, 2q + 8, 2q + 9 of the sixteen, its D/8 values from (D/8) g on
           constexpr int VB = C::kRow / 8;  // bytes a lane takes of a row
           uint32_t w[4][VB / 4];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int row = 16 * k + 2 * q + (x & 1) + 8 * (x >> 1);
+          for (int y = 0; y < 4; ++y) {
+            const int row = 16 * x + 2 * q + (y & 1) + 8 * (y >> 1);
             const int at = VB * g;
             const uint32_t addr = vb + ring_offset<C::kRow>(row, at >> 4) + (at & 15);
             if constexpr (VB == 16) {
               const uint4 v = lds128(addr);
-              w[x][0] = v.x, w[x][1] = v.y, w[x][2] = v.z, w[x][3] = v.w;
+              w[y][0] = v.x, w[y][1] = v.y, w[y][2] = v.z, w[y][3] = v.w;
             } else if constexpr (VB == 8) {
               const uint2 v = lds64(addr);
-              w[x][0] = v.x, w[x][1] = v.y;
+              w[y][0] = v.x, w[y][1] = v.y;
             } else {
-              w[x][0] = lds32(addr);
+              w[y][0] = lds32(addr);
             }
           }
+          // tile j's rows g and g + 8 are this lane's values 2j and 2j + 1
 #pragma unroll
           for (int y = 0; y < VB / 4; ++y) {
             if constexpr (FMT == kKvInt8) {
@@ -586,8 +678,10 @@ __global__ void __launch_bounds__(kThreads, 2) attn_token_kernel(const AttnArgs 
                 // {a, b, a', b'} of two neighbouring values, then each pair widened
                 const uint32_t lo = __byte_perm(w[0][y], w[1][y], z ? 0x7362 : 0x5140);
                 const uint32_t hi = __byte_perm(w[2][y], w[3][y], z ? 0x7362 : 0x5140);
-                mma16816<false>(o[4 * y + 2 * z], pa, bytes_to_h2(lo, 0x4140), bytes_to_h2(hi, 0x4140));
-                mma16816<false>(o[4 * y + 2 * z + 1], pa, bytes_to_h2(lo, 0x4342), bytes_to_h2(hi, 0x4342));
+                const uint32_t r[4] = {bytes_to_h2(lo, 0x4140), bytes_to_h2(lo, 0x4342), bytes_to_h2(hi, 0x4140),
+                                       bytes_to_h2(hi, 0x4342)};
+#pragma unroll
+                for (int n = 0; n < NR; ++n) mma16816<false>(o[n][2 * y + z], r, pb[n][0], pb[n][1]);
               }
             } else {
 #pragma unroll
@@ -595,10 +689,13 @@ __global__ void __launch_bounds__(kThreads, 2) attn_token_kernel(const AttnArgs 
                 // four values of key a below the same four of key b
                 const uint32_t lo = __byte_perm(w[0][y], w[1][y], z ? 0x7632 : 0x5410);
                 const uint32_t hi = __byte_perm(w[2][y], w[3][y], z ? 0x7632 : 0x5410);
-                mma16816<false>(o[8 * y + 4 * z], pa, nib_lo(lo), nib_lo(hi));
-                mma16816<false>(o[8 * y + 4 * z + 1], pa, nib_hi(lo), nib_hi(hi));
-                mma16816<false>(o[8 * y + 4 * z + 2], pa, nib_lo(lo >> 8), nib_lo(hi >> 8));
-                mma16816<false>(o[8 * y + 4 * z + 3], pa, nib_hi(lo >> 8), nib_hi(hi >> 8));
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const uint32_t r[4] = {nib_lo(lo >> (8 * e)), nib_hi(lo >> (8 * e)), nib_lo(hi >> (8 * e)),
+                                         nib_hi(hi >> (8 * e))};
+#pragma unroll
+                  for (int n = 0; n < NR; ++n) mma16816<false>(o[n][4 * y + 2 * z + e], r, pb[n][0], pb[n][1]);
+                }
               }
             }
           }
@@ -610,36 +707,40 @@ __global__ void __launch_bounds__(kThreads, 2) attn_token_kernel(const AttnArgs 
 
     // ---- join the warps' results
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-    }
+    for (int n = 0; n < NR; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        l[n][c] += __shfl_xor_sync(0xffffffffu, l[n][c], 4);
+        l[n][c] += __shfl_xor_sync(0xffffffffu, l[n][c], 8);
+        l[n][c] += __shfl_xor_sync(0xffffffffu, l[n][c], 16);
+      }
     __syncthreads();
     {
       float* wo = reinterpret_cast<float*>(smem + warp * C::kWarpBytes);
-      float2* wml = reinterpret_cast<float2*>(wo + kTokenRows * D);
+      float2* wml = reinterpret_cast<float2*>(wo + C::kRows * D);
 #pragma unroll
-      for (int j = 0; j < ND; ++j)
+      for (int n = 0; n < NR; ++n) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int n = 2 * q + (c & 1);
-          const int d = C::kQuant ? (D / 8) * n + j : 8 * j + n;
-          wo[(g + 8 * (c >> 1)) * D + d] = o[j][c];
+        for (int j = 0; j < ND; ++j)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int d = C::kQuant ? (D / 8) * g + 2 * j + (c >> 1) : 16 * j + g + 8 * (c >> 1);
+            wo[(8 * n + 2 * q + (c & 1)) * D + d] = o[n][j][c];
+          }
+        if (g == 0) {
+          wml[8 * n + 2 * q] = make_float2(m[n][0], l[n][0]);
+          wml[8 * n + 2 * q + 1] = make_float2(m[n][1], l[n][1]);
         }
-      if (q == 0) {
-        wml[g] = make_float2(m[0], l[0]);
-        wml[g + 8] = make_float2(m[1], l[1]);
       }
     }
     __syncthreads();
     {
-      constexpr int PER = D / 8;
-      const int r = threadIdx.x >> 3, part = threadIdx.x & 7;
+      constexpr int PER = C::kPer;
       float2 ml[kWarps];
       float top = kNegInf, sum = 0.0f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        ml[w] = reinterpret_cast<const float2*>(smem + w * C::kWarpBytes + kTokenRows * D * 4)[r];
+        ml[w] = reinterpret_cast<const float2*>(smem + w * C::kWarpBytes + C::kRows * D * 4)[jr];
         top = fmaxf(top, ml[w].x);
       }
       float v[PER];
@@ -647,9 +748,10 @@ __global__ void __launch_bounds__(kThreads, 2) attn_token_kernel(const AttnArgs 
       for (int i = 0; i < PER; ++i) v[i] = 0.0f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float f = ml[w].x == kNegInf ? 0.0f : ex2(ml[w].x - top);
+        // a warp without a maximum saw nothing (its sum is 0) or nothing but NaN (its sum is NaN)
+        const float f = ml[w].x == kNegInf ? (ml[w].y == 0.0f ? 0.0f : ml[w].y) : ex2(ml[w].x - top);
         sum = fmaf(ml[w].y, f, sum);
-        const float4* wo = reinterpret_cast<const float4*>(smem + w * C::kWarpBytes + (r * D + part * PER) * 4);
+        const float4* wo = reinterpret_cast<const float4*>(smem + w * C::kWarpBytes + (jr * D + part * PER) * 4);
 #pragma unroll
         for (int i = 0; i < PER / 4; ++i) {
           const float4 x = wo[i];
@@ -662,80 +764,58 @@ __global__ void __launch_bounds__(kThreads, 2) attn_token_kernel(const AttnArgs 
       if (unit0 == 0 && unit1 == s.units) {
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
         if constexpr (C::kQuant) {
-#pragma unroll
-          for (int st = 1; st < PER; st *= 2)
-#pragma unroll
-            for (int i = 0; i < PER; ++i)
-              if (!(i & st)) {
-                const float x = v[i], y = v[i + st];
-                v[i] = x + y;
-                v[i + st] = x - y;
-              }
-#pragma unroll
-          for (int st = 1; st < 8; st *= 2)
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-              const float x = __shfl_xor_sync(0xffffffffu, v[i], st);
-              v[i] = ((part & st) ? x - v[i] : v[i] + x);
-            }
+          hadamard_threads<PER, C::kTpr>(v, part);
 #pragma unroll
           for (int i = 0; i < PER; ++i) v[i] *= 8.0f / D;
         }
-        if (r < rows) {
-          const int tok = r / group;
+        if (jr < rows) {
+          const int tok = jr / group;
           uint16_t* dst = static_cast<uint16_t*>(a.out) + (s.q0 + tok) * a.out_token_stride +
-                          (int64_t)(h * group + r - tok * group) * a.out_head_stride + part * PER;
+                          (int64_t)(h * group + jr - tok * group) * a.out_head_stride + part * PER;
 #pragma unroll
-          for (int i = 0; i < PER; i += 8) {
-            uint32_t w[4];
+          for (int i = 0; i < PER; i += 4) {
+            uint32_t w[2];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < 2; ++j) {
               const float x = v[i + 2 * j] * inv, y = v[i + 2 * j + 1] * inv;
               w[j] = a.bf16 ? pack2<true>(x, y) : pack2<false>(x, y);
             }
-            *reinterpret_cast<uint4*>(dst + i) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint2*>(dst + i) = make_uint2(w[0], w[1]);
           }
         }
-      } else if (r < rows) {
+      } else if (jr < rows) {
         // a range begins inside at most one item and ends inside at most one
         const int64_t slot = 2 * (int64_t)blockIdx.x + (unit0 == 0 ? 1 : 0);
-        float4* dst = reinterpret_cast<float4*>(a.part_o + (slot * kTokenRows + r) * D + part * PER);
+        float4* dst = reinterpret_cast<float4*>(a.part_o + (slot * kTokenRows + jr) * D + part * PER);
 #pragma unroll
         for (int i = 0; i < PER / 4; ++i) dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-        if (part == 0) a.part_ml[slot * kTokenRows + r] = make_float2(top, sum);
+        if (part == 0) a.part_ml[slot * kTokenRows + jr] = make_float2(top, sum);
       }
     }
     __syncthreads();  // the next item's copies refill what was read here
-    u += unit1 - unit0;
-    if (unit1 == s.units && h == a.kv_heads - 1) {
-      before += (int64_t)s.units * a.kv_heads;
-      ++b;
-    }
   }
 }
 
-// Joins the parts of the items that were cut: one block an item and row, its
-// warps take the parts in turn (all their loads in flight), then one joins the
-// warps in order.  The order is fixed by the lengths, so results repeat.
-constexpr int kJoinWarps = 4;
+// Joins the parts of the items that were cut: one block an item and row; its
+// warps take the parts in turn, four loads at a time, then one joins the warps in
+// order.  The order is fixed by the lengths, so results repeat.
+constexpr int kJoinWarps = 8;
 template <int D, bool QUANT>
 __global__ void __launch_bounds__(32 * kJoinWarps) attn_token_join_kernel(const AttnArgs a) {
   constexpr int PER = D / 32;
+  constexpr int AHEAD = 4;
   __shared__ float so[kJoinWarps][D];
   __shared__ float2 sml[kJoinWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int group = a.heads / a.kv_heads;
   const int r = blockIdx.y;
-  // every block waits, cut item or not: the end of this grid then stands for the end of both
-  pdl_wait();
   const int b = blockIdx.x / a.kv_heads, h = blockIdx.x % a.kv_heads;
   const Seq s = load_seq(a, b);
   const int rows = s.q_len * group;
-  if (r >= rows) return;
   // units before this sequence, and of the call
   int64_t total = 0, before = 0;
   for (int i = lane; i < a.batch; i += 32) {
-    const int n = load_seq(a, i).units;
+    const int n = load_seq(a, i).weight();
     total += n;
     before += i < b ? n : 0;
   }
@@ -745,30 +825,49 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_token_join_kernel(const 
     before += __shfl_xor_sync(0xffffffffu, before, o);
   }
   total *= a.kv_heads;
-  const int64_t first = before * a.kv_heads + (int64_t)h * s.units, last = first + s.units - 1;
+  const int64_t first = before * a.kv_heads + (int64_t)h * s.weight() + kItemUnits, last = first + s.units - 1;
   const int64_t grid = a.ctas;
   // the CTA of a unit is the last whose range begins at or before it
-  const int64_t c0 = ((first + 1) * grid - 1) / total, c1 = ((last + 1) * grid - 1) / total;
-  if (c0 == c1) return;  // not cut
+  int64_t c0 = 0, c1 = 0;
+  if (r < rows) {
+    c0 = ((first + 1) * grid - 1) / total;
+    c1 = ((last + 1) * grid - 1) / total;
+  }
+  // every block waits, cut item or not: the end of this grid then stands for the end of both
+  pdl_wait();
+  if (c0 == c1) return;  // no such row, or not cut
   float m = kNegInf, l = 0.0f, o[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) o[i] = 0.0f;
-  for (int64_t c = c0 + warp; c <= c1; c += kJoinWarps) {
-    const int64_t begin = total * c / grid, end = total * (c + 1) / grid;
-    if (begin == end) continue;
-    const int64_t slot = 2 * c + (begin <= first ? 1 : 0);
-    const float2 ml = a.part_ml[slot * kTokenRows + r];
-    float v[PER];
-    const float* src = a.part_o + (slot * kTokenRows + r) * D + PER * lane;
+  for (int64_t c = c0 + warp; c <= c1; c += kJoinWarps * AHEAD) {
+    float2 ml[AHEAD];
+    float v[AHEAD][PER];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) v[i] = src[i];
-    if (ml.x == kNegInf) continue;
-    const float top = fmaxf(m, ml.x);
-    const float f = m == kNegInf ? 0.0f : ex2(m - top), f1 = ex2(ml.x - top);
-    l = l * f + ml.y * f1;
+    for (int x = 0; x < AHEAD; ++x) {
+      const int64_t cc = c + x * kJoinWarps;
+      const int64_t begin = total * cc / grid, end = total * (cc + 1) / grid;
+      ml[x] = make_float2(kNegInf, 0.0f);
+      if (cc <= c1 && begin < end) {
+        const int64_t slot = 2 * cc + (begin <= first ? 1 : 0);
+        ml[x] = a.part_ml[slot * kTokenRows + r];
+        const float* src = a.part_o + (slot * kTokenRows + r) * D + PER * lane;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) o[i] = o[i] * f + v[i] * f1;
-    m = top;
+        for (int i = 0; i < PER; ++i) v[x][i] = src[i];
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < AHEAD; ++x) {
+      if (ml[x].x == kNegInf) {
+        l += ml[x].y;  // 0, or NaN
+        continue;
+      }
+      const float top = fmaxf(m, ml[x].x);
+      const float f = m == kNegInf ? 0.0f : ex2(m - top), f1 = ex2(ml[x].x - top);
+      l = (m == kNegInf ? l : l * f) + ml[x].y * f1;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) o[i] = o[i] * f + v[x][i] * f1;
+      m = top;
+    }
   }
 #pragma unroll
   for (int i = 0; i < PER; ++i) so[warp][PER * lane + i] = o[i];
@@ -782,29 +881,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_token_join_kernel(const 
   for (int i = 0; i < PER; ++i) o[i] = 0.0f;
 #pragma unroll
   for (int w = 0; w < kJoinWarps; ++w) {
-    const float f = sml[w].x == kNegInf ? 0.0f : ex2(sml[w].x - top);
+    const float f = sml[w].x == kNegInf ? (sml[w].y == 0.0f ? 0.0f : sml[w].y) : ex2(sml[w].x - top);
     sum = fmaf(sml[w].y, f, sum);
 #pragma unroll
     for (int i = 0; i < PER; ++i) o[i] = fmaf(so[w][PER * lane + i], f, o[i]);
   }
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
   if constexpr (QUANT) {
-#pragma unroll
-    for (int st = 1; st < PER; st *= 2)
-#pragma unroll
-      for (int i = 0; i < PER; ++i)
-        if (!(i & st)) {
-          const float x = o[i], y = o[i + st];
-          o[i] = x + y;
-          o[i + st] = x - y;
-        }
-#pragma unroll
-    for (int st = 1; st < 32; st *= 2)
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const float x = __shfl_xor_sync(0xffffffffu, o[i], st);
-        o[i] = (lane & st) ? x - o[i] : o[i] + x;
-      }
+    hadamard_threads<PER, 32>(o, lane);
 #pragma unroll
     for (int i = 0; i < PER; ++i) o[i] *= 8.0f / D;
   }
@@ -818,12 +902,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_token_join_kernel(const 
   }
 }
 
-template <int FMT, int D>
+template <int FMT, int D, int NR>
 cudaError_t launch_token(const AttnArgs& a, cudaStream_t stream) {
-  using C = TokenCfg<FMT, D>;
-  cudaError_t e = cudaFuncSetAttribute(attn_token_kernel<FMT, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  using C = TokenCfg<FMT, D, NR>;
+  cudaError_t e = allow_smem<attn_token_kernel<FMT, D, NR>>(C::kSmem);
   if (e != cudaSuccess) return e;
-  attn_token_kernel<FMT, D><<<(unsigned)a.ctas, kThreads, C::kSmem, stream>>>(a);
+  attn_token_kernel<FMT, D, NR><<<(unsigned)a.ctas, kThreads, C::kSmem, stream>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -838,20 +922,23 @@ cudaError_t launch_token(const AttnArgs& a, cudaStream_t stream) {
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, attn_token_join_kernel<D, C::kQuant>, a);
 }
+template <int FMT>
+cudaError_t launch_token_fmt(const AttnArgs& a, cudaStream_t stream) {
+  const bool small = a.max_q * (a.heads / a.kv_heads) <= 8;
+  if (a.head_dim == 64) return small ? launch_token<FMT, 64, 1>(a, stream) : launch_token<FMT, 64, 2>(a, stream);
+  return small ? launch_token<FMT, 128, 1>(a, stream) : launch_token<FMT, 128, 2>(a, stream);
+}
 
 }  // namespace
 
 cudaError_t launch_attn_token(const AttnArgs& a, cudaStream_t stream) {
-#define EXL3_TOKEN(F)                                            \
-  case F: return a.head_dim == 64 ? launch_token<F, 64>(a, stream) : launch_token<F, 128>(a, stream);
   switch (a.cache.format) {
-    EXL3_TOKEN(kKvF16)
-    EXL3_TOKEN(kKvBf16)
-    EXL3_TOKEN(kKvInt8)
-    EXL3_TOKEN(kKvInt4)
+    case kKvF16: return launch_token_fmt<kKvF16>(a, stream);
+    case kKvBf16: return launch_token_fmt<kKvBf16>(a, stream);
+    case kKvInt8: return launch_token_fmt<kKvInt8>(a, stream);
+    case kKvInt4: return launch_token_fmt<kKvInt4>(a, stream);
     default: return cudaErrorInvalidValue;
   }
-#undef EXL3_TOKEN
 }
 
 }  // namespace exl3

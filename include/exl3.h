@@ -384,7 +384,8 @@ exl3_status_t exl3_kv_read(const exl3_kv_cache_t* cache, const int64_t* slots, i
  *   q, k, v    [total] tokens of `dtype`;  scale  positive and finite
  *   cu_seqlens device, int32 [batch + 1]: sequence b is tokens [cu[b], cu[b + 1]); tokens of no
  *              sequence keep their output
- *   out        device, [total] tokens of q_heads heads
+ *   out        device, [total] tokens of q_heads heads; may be q itself (same strides), else it overlaps
+ *              no input
  */
 exl3_status_t exl3_attention_prompt(const exl3_heads_t* q, const exl3_heads_t* k, const exl3_heads_t* v,
                                     exl3_dtype_t dtype, int64_t total, int32_t q_heads, int32_t kv_heads,
@@ -404,6 +405,7 @@ exl3_status_t exl3_attention_prompt(const exl3_heads_t* q, const exl3_heads_t* k
  *               outside the cache is not followed either (its keys count as zeros)
  *   cu_q        device, int32 [batch + 1]: query tokens of sequence b, as cu_seqlens above
  *   kv_lens     device, int32 [batch]: cached tokens, the new ones among them; at most table_width * page_size
+ *   out         as for exl3_attention_prompt
  *   max_q       HOST: no sequence has more query tokens (a sequence's tokens past it keep their output)
  *   max_kv      HOST: about the longest length; it only steers how the work is split
  *   workspace   device, 16-byte aligned, at least exl3_attention_paged_workspace_bytes of the same sizes
