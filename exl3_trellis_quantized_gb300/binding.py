@@ -478,7 +478,7 @@ def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
 def _out_like(x: torch.Tensor, out: Optional[torch.Tensor], name: str):
     """The output of rows like x's and its exl3_heads_t; one that the caller gave is x itself or lies apart from it."""
     if out is None:
-        out = x.new_empty(x.shape)
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
         _, heads, d = x.shape
         return out, _Heads(out.data_ptr(), heads * d or 8, d)
     if out.shape != x.shape:
@@ -683,7 +683,7 @@ def attention_paged(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, 
     out, oh = _out_like(q, out, "out")
     if workspace is None:
         need = _workspace_bytes(total, batch, heads, cache.kv_heads, d, int(max_q), int(max_kv))
-        workspace = q.new_empty(need, dtype=torch.uint8)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     else:
         _need(workspace, torch.uint8, "workspace")
     st = lib().exl3_attention_paged(qh, dt, total, heads, cache.args, block_table.data_ptr(), block_table.shape[1],

@@ -6,7 +6,7 @@
 // CTA takes 256 of them (two tiles of 128, the M of the MMA) whatever the group
 // size, and reads each key and value once for all of them.
 //
-// Per tile of 128 keys and 128 rows:
+// Per block of 64 keys and 128 rows:
 //     S = Q K^T            tcgen05.mma, both operands in shared memory, S in tensor memory
 //     m' = max(m, S c),  P = 2^(S c - m'),  l += sum P    (c = scale * log2 e; one thread a row)
 //     O += P V             tcgen05.mma, P from tensor memory (written over S), V from shared memory
@@ -15,21 +15,33 @@
 // in fp32, and O in tensor memory needs no rescaling.  P rounds to the operand
 // type; l sums the unrounded values in fp32.
 //
-// What bounds it: the tensor core (4 * 128 * 128 * D operations a tile) once there
-// are a few hundred rows a sequence.  The two row tiles take turns: while one's
-// softmax runs the tensor core works for the other.  A CTA with no more than 128
-// rows gives both halves the same rows and every other key tile each, and joins
-// them at the end.  With few row tiles the keys are also split over CTAs, and
-// attn_tile_join_kernel joins the parts.
+// What bounds it: the tensor core (4 * 128 * 64 * D operations a block) once there
+// are a few hundred rows a sequence.  Each row tile has two buffers of scores, so
+// the products of the next block run under a block's softmax, and a warp of its
+// own issues them.  (Blocks of 128 keys have products that read less shared memory,
+// but leave room for one buffer a tile: then each tile's products and softmax wait
+// for one another, and 16384 tokens of 32 heads took 1529 us.)
 //
-// Roles: warps 0-3 and 4-7 softmax of row tiles 0 and 1 (a thread a row), warp 8
-// issues the MMAs, warp 9 issues the tensor copies of keys and values into a
-// ring of slots; for the quantised cache formats warps 12-15 load the codes and
-// write them as fp16 rows into the same ring.  Quantised rows stay in the
-// rotated basis (see exl3_rope_cache.cu): q is rotated on its way into shared
-// memory and the output on its way out, each a transform within a thread.
+// A CTA with no more than 128 rows gives both halves the same rows and every
+// other block of keys each, and joins them at the end.  With few row tiles the keys are
+// also split over CTAs, and attn_tile_join_kernel joins the parts.
 //
-// Tensor memory: S of both tiles at columns 0 and 128, O at 256 and 384.
+// The grid has a CTA an item, but one CTA an SM takes item after item: when its
+// loader has issued an item's last copies it cancels a CTA that has not started
+// (clusterlaunchcontrol) and takes its item, so the copies and first scores of the
+// next item run under the last softmax and the output of the one before, and the
+// order of the items stays the hardware's.
+//
+// Roles: warps 0-3 and 4-7 softmax of row tiles 0 and 1 (a thread a row), warps 8
+// and 10 issue their MMAs, warp 9 takes the items and issues the copies of keys and values
+// into a ring of slots; for the quantised cache formats it copies the codes and
+// scales into a ring of their own, and warps 12-15 turn them into fp16 rows.
+// Quantised rows stay in the rotated basis (see exl3_rope_cache.cu): q is rotated
+// on its way into shared memory and the output on its way out, each a transform
+// within a thread.  Keys, values and q round to fp16 there, 2^-11 of each entry,
+// below the codes' own steps.
+//
+// Tensor memory: S of row tile i at columns 128 i and 128 i + 64, O at 256 + 128 i.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cudaTypedefs.h>
@@ -43,7 +55,8 @@ namespace exl3 {
 namespace {
 
 enum Source { kPacked = 0, kPaged16 = 1, kPaged8 = 2, kPaged4 = 3 };
-constexpr int kKeys = 128;      // keys of a tile
+constexpr int kKeys = 128;      // keys of a copy (a tile)
+constexpr int kBlock = 64;      // keys of a step
 constexpr int kTileRows = 128;  // rows of a tile; a CTA has two tiles
 constexpr int kItemRows = 2 * kTileRows;
 constexpr float kNegInf = -__builtin_huge_valf();
@@ -52,32 +65,53 @@ constexpr float kSlack = 8.0f;
 template <int D, int SRC>
 struct TileCfg {
   static constexpr bool kQuant = SRC >= kPaged8;
-  static constexpr int kLoaders = kQuant ? 4 : 1;
-  static constexpr int kFirstLoader = kQuant ? 12 : 9;
+  static constexpr int kConverters = kQuant ? 4 : 0;   // warps 12-15
   static constexpr int kThreads = kQuant ? 512 : 384;  // whole groups of four warps, for the register split
   // Registers a thread of each group of four warps.  The kernel is launched with 168 (384 threads) or 128 (512); what
   // the softmax warps gain is what the others give up.
   static constexpr int kLaunchRegs = kQuant ? 128 : 168;
   static constexpr int kSoftmaxRegs = kQuant ? 192 : 208;
-  static constexpr int kIssueRegs = kQuant ? 40 : 88;
-  static constexpr int kLoaderRegs = 88;
-  static_assert(256 * kSoftmaxRegs + 128 * kIssueRegs + (kQuant ? 128 * kLoaderRegs : 0) <= kLaunchRegs * kThreads,
+  static constexpr int kIssueRegs = kQuant ? 72 : 88;
+  static constexpr int kConvertRegs = 56;
+  static_assert(256 * kSoftmaxRegs + 128 * kIssueRegs + (kQuant ? 128 * kConvertRegs : 0) <= kLaunchRegs * kThreads,
                 "the split draws on the registers of the launch");
   static constexpr int kSlot = kKeys * D * 2;
-  static constexpr int kSlots = D == 128 ? 5 : 8;
+  static constexpr int kSlots = D == 64 ? 8 : kQuant ? 4 : 5;
+  // codes and scales of 128 keys or values as they lie in the cache
+  static constexpr int kRowBytes = SRC == kPaged8 ? D : D / 2;
+  static constexpr int kCodes = kKeys * kRowBytes;
+  static constexpr int kRaw = kCodes + kKeys * 2;
+  static constexpr int kRaws = !kQuant ? 0 : kRaw > 16 * 1024 ? 2 : 3;
   static constexpr int kQ = 0;
   static constexpr int kRing = 2 * kTileRows * D * 2;
-  static constexpr int kCtrl = 1024;
-  static constexpr int kSmem = 1024 + kCtrl + kRing + kSlots * kSlot;
+  static constexpr int kRawRing = kRing + kSlots * kSlot;
+  static constexpr int kCtrl = kRawRing + kRaws * kRaw;  // barriers, items, a joint item's exponents
+  static constexpr int kSmem = 1024 + kCtrl + 1280;
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(kSmem > 114 * 1024, "one CTA an SM: each allocates all of tensor memory");
-  static_assert(kSlots * kSlot >= kTileRows * D * 4 + kTileRows * 8, "the ring holds a tile's output for the join");
+  static_assert(kRing >= kTileRows * D * 4, "q's room holds a tile's output for the join");
 };
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// mbar_wait in few instructions: the many waits of this kernel are code that its warps walk through once a tile.
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity) {
+  const uint32_t b = smem_u32(bar);
+  uint64_t t0 = 0;
+#pragma unroll 1
+  for (uint32_t tries = 0; !mbar_try_wait(b, parity); ++tries) {
+    if ((tries & 255u) != 0) continue;
+    const uint64_t t = globaltimer_ns();
+    if (t0 == 0) t0 = t;
+    if (t - t0 > kWaitTimeoutNs) {
+      atomicOr(&g_device_error, kErrWaitTimeout);
+      return false;
+    }
+  }
+  return true;
 }
 // Two fp32 multiply-adds / adds in one instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
@@ -95,6 +129,29 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "=f"(d.x), "=f"(d.y)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// Ask for a CTA of this grid that has not started: 16 bytes of answer at `answer`, completing on `bar`.
+__device__ __forceinline__ void cancel_cta(uint32_t answer, uint64_t* bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(answer),
+               "r"(smem_u32(bar))
+               : "memory");
+}
+// Its index, or -1 when there is none left.
+__device__ __forceinline__ int cancelled_cta(uint32_t answer) {
+  int x;
+  asm volatile(
+      "{\n .reg .b128 h;\n .reg .pred p;\n ld.shared.b128 h, [%1];\n"
+      " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n mov.b32 %0, -1;\n"
+      " @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, h;\n}\n"
+      : "=r"(x)
+      : "r"(answer)
+      : "memory");
+  return x;
 }
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -173,31 +230,45 @@ struct TileMaps {
   CUtensorMap k, v;
 };
 
-// What one CTA works on.
+// What a CTA works on at a time.
+struct Span {  // blocks of one half: b0, b0 + step, ... below b1 (b1 <= b0: none)
+  int b0, b1, step;
+};
 struct Item {
   int64_t q0;        // first packed query token of the sequence
   int kvh, first;    // key head; position of the sequence's first query token
   int row0, rows;    // rows of the item within the sequence and head
   int kv_len;
-  int base;          // first key of key tile 0
-  int j0, j1;        // key tiles of this CTA
-  bool joint;        // both halves on the same rows, key tiles in turn
+  int base;          // first key of block 0
   int b, split;
+  int joint;         // both halves on the same rows, blocks in turn
+  Span span[2];
+  int jlo, jhi;      // key tiles (two blocks each) that a half uses
+  int tail;          // the key tile that the length ends in, where its value rows past the end must be made zeros; or -1
+  int done;          // no item
 };
 
-struct Span {  // key tiles of one half: j0, j0 + step, ... below j1 (j1 <= j0: none)
-  int j0, j1, step;
-  __device__ __forceinline__ bool has(int j) const { return j >= j0 && j < j1 && (step == 1 || ((j - j0) & 1) == 0); }
-};
-
-template <int SRC>
-__device__ bool find_item(const AttnArgs& a, int lane, Item* it) {
+// Blocks of n0 .. n1 that half i of the item uses.
+__device__ Span half_span(const AttnArgs& a, const Item& it, int n0, int n1, int i) {
+  if (it.joint) return Span{min(n0 + ((n0 & 1) ^ i), n1), n1, 2};  // half 0 the even blocks
   const int group = a.heads / a.kv_heads;
-  int64_t idx = blockIdx.x;
+  const int r0 = it.row0 + i * kTileRows;
+  const int r1 = min(r0 + kTileRows, it.row0 + it.rows) - 1;
+  const int p0 = it.first + r0 / group, p1 = it.first + r1 / group;
+  const int lo = a.window > 0 ? max(0, p0 - a.window + 1) : 0;
+  if (r1 < r0 || p1 < lo) return Span{n0, n0, 1};
+  const int s0 = max(n0, (lo - it.base) / kBlock), s1 = min(n1, (p1 - it.base) / kBlock + 1);
+  return s0 < s1 ? Span{s0, s1, 1} : Span{n0, n0, 1};
+}
+
+// The item of CTA index idx (a whole warp); false past the last row tile.
+template <int SRC>
+__device__ bool find_item(const AttnArgs& a, int lane, int64_t idx, Item* it) {
+  const int group = a.heads / a.kv_heads;
   it->split = (int)(idx % a.splits);
   idx /= a.splits;
   it->kvh = (int)(idx % a.kv_heads);
-  int64_t tile = idx / a.kv_heads;
+  const int64_t tile = idx / a.kv_heads;
   // the sequence that holds row tile `tile`
   int64_t base = 0;
   for (int b0 = 0; b0 < a.batch; b0 += 32) {
@@ -246,27 +317,25 @@ __device__ bool find_item(const AttnArgs& a, int lane, Item* it) {
         lo &= ~(align - 1);
       }
       it->base = lo;
-      const int tiles_k = p1 >= lo ? (p1 - lo) / kKeys + 1 : 0;
-      it->j0 = (int)((int64_t)tiles_k * it->split / a.splits);
-      it->j1 = (int)((int64_t)tiles_k * (it->split + 1) / a.splits);
+      const int blocks = p1 >= lo ? (p1 - lo) / kBlock + 1 : 0;
+      const int n0 = (int)((int64_t)blocks * it->split / a.splits);
+      const int n1 = (int)((int64_t)blocks * (it->split + 1) / a.splits);
+      it->span[0] = half_span(a, *it, n0, n1, 0);
+      it->span[1] = half_span(a, *it, n0, n1, 1);
+      // the spans of two non-empty halves overlap or touch
+      const Span s0 = it->span[0], s1 = it->span[1];
+      const bool use0 = s0.b0 < s0.b1, use1 = s1.b0 < s1.b1;
+      it->jlo = (use0 && use1 ? min(s0.b0, s1.b0) : use0 ? s0.b0 : use1 ? s1.b0 : 0) >> 1;
+      it->jhi = ((use0 && use1 ? max(s0.b1, s1.b1) : use0 ? s0.b1 : use1 ? s1.b1 : 0) + 1) >> 1;
+      // a weight of zero times what a page or the next sequence holds past the length need not be zero
+      const int over = it->kv_len - lo;
+      it->tail = (over & 15) != 0 && over / kKeys >= it->jlo && over / kKeys < it->jhi ? over / kKeys : -1;
+      it->done = 0;
       return true;
     }
     base += __shfl_sync(0xffffffffu, inc, 31);
   }
   return false;
-}
-
-// Key tiles of half i of the item.
-__device__ Span half_span(const AttnArgs& a, const Item& it, int i) {
-  if (it.joint) return Span{min(it.j0 + i, it.j1), it.j1, 2};
-  const int group = a.heads / a.kv_heads;
-  const int r0 = it.row0 + i * kTileRows;
-  const int r1 = min(r0 + kTileRows, it.row0 + it.rows) - 1;
-  const int p0 = it.first + r0 / group, p1 = it.first + r1 / group;
-  const int lo = a.window > 0 ? max(0, p0 - a.window + 1) : 0;
-  if (r1 < r0 || p1 < lo) return Span{it.j0, it.j0, 1};
-  const int s0 = max(it.j0, (lo - it.base) / kKeys), s1 = min(it.j1, (p1 - it.base) / kKeys + 1);
-  return s0 < s1 ? Span{s0, s1, 1} : Span{it.j0, it.j0, 1};
 }
 
 // D: head size.  BF16: operand type (fp16 for the quantised formats).
@@ -276,37 +345,57 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
   using C = TileCfg<D, SRC>;
   constexpr int NS = C::kSlots;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint64_t* kvfull = reinterpret_cast<uint64_t*>(base);  // slot filled
-  uint64_t* kvempty = kvfull + NS;                       // slot read by the MMAs
-  uint64_t* qfull = kvempty + NS;                        // [2] a row tile's q in shared memory
-  uint64_t* sfull = qfull + 2;                           // [2] scores in tensor memory
-  uint64_t* pfull = sfull + 2;                           // [2] weights in tensor memory, O rescaled
-  uint64_t* ofull = pfull + 2;                           // [2] every MMA of a tile done
-  uint64_t* vfix = ofull + 2;                            // the last value slot's rows past the length are zeros
-  uint64_t* mdrain = vfix + 1;                           // MMAs issued before a wait gave up
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mdrain + 1);
-  uint8_t* data = base + C::kCtrl;
+  uint8_t* data = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* base = data + C::kCtrl;
+  uint64_t* kvfull = reinterpret_cast<uint64_t*>(base);  // [NS] slot filled
+  uint64_t* kvempty = kvfull + 8;                        // [NS] slot read by the MMAs
+  uint64_t* rawfull = kvempty + 8;                       // [kRaws] codes and scales landed
+  uint64_t* rawempty = rawfull + 4;                      // [kRaws] converted
+  uint64_t* qfull = rawempty + 4;                        // [2] a half's q in shared memory
+  uint64_t* sfull = qfull + 2;                           // [2][2] a half's scores in a buffer of tensor memory
+  uint64_t* pfull = sfull + 4;                           // [2][2] weights in tensor memory, O rescaled
+  uint64_t* pvdone = pfull + 4;                          // [2] a block's weights times values added to O
+  uint64_t* ofull = pvdone + 2;                          // [2] every MMA of a half's item done
+  uint64_t* ifull = ofull + 2;                           // [2] item published
+  uint64_t* iempty = ifull + 2;                          // [2] and read by every warp
+  uint64_t* jfull = iempty + 2;                          // joint item: half 1's output in shared memory
+  uint64_t* jfree = jfull + 1;                           // and read by half 0
+  uint64_t* vfix = jfree + 1;                            // [NS] a tail's value rows past the length are zeros
+  uint64_t* clc = vfix + 8;                              // answer to a cancel request
+  uint64_t* mdrain = clc + 1;                            // [2] MMAs issued before a wait gave up
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mdrain + 2);
+  uint8_t* answer = base + 448;                          // 16 bytes
+  Item* items = reinterpret_cast<Item*>(base + 464);     // [2]
+  float* jlse = reinterpret_cast<float*>(base + 768);    // [128] joint item: log2 of half 1's sums
+  static_assert((2 * 8 + 2 * 4 + 31) * 8 + 4 <= 448 && 464 + 2 * sizeof(Item) <= 768, "control area");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if constexpr (SRC != kPacked) pdl_launch_dependents();  // the join may be scheduled; it waits for this grid
-  Item it;
-  if (!find_item<SRC>(a, lane, &it)) return;  // the whole block: past the last row tile
   const int group = a.heads / a.kv_heads;
-
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
-      mbar_init(&kvfull[s], C::kQuant ? C::kLoaders : 1);
-      mbar_init(&kvempty[s], 1);
+      mbar_init(&kvfull[s], C::kQuant ? C::kConverters : 1);
+      mbar_init(&kvempty[s], 2);
+      mbar_init(&vfix[s], 1);
+    }
+    for (int s = 0; s < C::kRaws; ++s) {
+      mbar_init(&rawfull[s], 1);
+      mbar_init(&rawempty[s], C::kConverters);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&qfull[i], 4);
-      mbar_init(&sfull[i], 1);
-      mbar_init(&pfull[i], 4);
+      mbar_init(&sfull[2 * i], 1);
+      mbar_init(&sfull[2 * i + 1], 1);
+      mbar_init(&pvdone[i], 1);
+      mbar_init(&pfull[2 * i], 4);
+      mbar_init(&pfull[2 * i + 1], 4);
       mbar_init(&ofull[i], 1);
+      mbar_init(&ifull[i], 1);
+      mbar_init(&iempty[i], 10 + C::kConverters);
+      mbar_init(&mdrain[i], 1);
     }
-    mbar_init(vfix, 1);
-    mbar_init(mdrain, 1);
+    mbar_init(jfull, 4);
+    mbar_init(jfree, 4);
+    mbar_init(clc, 1);
     fence_mbar_init();
   }
   if (warp == 8) {
@@ -317,198 +406,191 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const Span sp0 = half_span(a, it, 0), sp1 = half_span(a, it, 1);
-  // the tiles that a half uses; the spans of two non-empty halves overlap or touch
-  const bool use0 = sp0.j0 < sp0.j1, use1 = sp1.j0 < sp1.j1;
-  const int jlo = use0 && use1 ? min(sp0.j0, sp1.j0) : use0 ? sp0.j0 : use1 ? sp1.j0 : 0;
-  const int jhi = use0 && use1 ? max(sp0.j1, sp1.j1) : use0 ? sp0.j1 : use1 ? sp1.j1 : 0;
-  // the length ends inside key tile `tail`: its value rows past the end must be zeros (a weight of zero times what a
-  // page or the next sequence holds there need not be zero)
-  const int tail = (it.kv_len - it.base) % kKeys != 0 ? (it.kv_len - it.base) / kKeys : -1;
-  const bool fix = !C::kQuant && tail >= jlo && tail < jhi && (it.kv_len & 15) != ((it.base & 15));
+
+  // The n-th item, as every warp but the loader reads it; false when there is none (or a wait gave up).
+  auto read_item = [&](uint32_t n, Item* it) {
+    if (!bar_wait(&ifull[n & 1], (n >> 1) & 1u)) return false;
+    *it = items[n & 1];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&iempty[n & 1]);
+    return it->done == 0;
+  };
 
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
     // ---------------- softmax: a thread a row ----------------
     const int i = warp >> 2;
-    const Span sp = i ? sp1 : sp0;
     const int r = 32 * (warp & 3) + lane;  // row of the tile, lane of tensor memory
-    const int row = (it.joint ? 0 : i * kTileRows) + r;
-    const bool there = row < it.rows;
-    const int tok = (it.row0 + (there ? row : it.rows - 1)) / group;
-    const int head = it.kvh * group + (it.row0 + (there ? row : it.rows - 1)) - tok * group;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t s_col = tmem + lanes + 128 * i;
+    const uint32_t s_col = tmem + lanes + 128 * i;  // buffer 0
     const uint32_t o_col = tmem + lanes + 256 + 128 * i;
-    bool ok = true;
-
-    {  // q into shared memory
+    const float c = a.scale_log2;
+    // query token (in the sequence) and head of this thread's row; the last row's where there is none
+    auto row_of = [&](const Item& it, int* tok, int* head) {
+      const int row = (it.joint ? 0 : i * kTileRows) + r;
+      const int rr = it.row0 + (row < it.rows ? row : it.rows - 1);
+      *tok = rr / group;
+      *head = it.kvh * group + rr - *tok * group;
+      return row < it.rows;
+    };
+    auto load_q = [&](const Item& it) {
+      int tok, head;
+      const bool there = row_of(it, &tok, &head);
       const uint16_t* src =
           static_cast<const uint16_t*>(a.q.data) + (it.q0 + tok) * a.q.token_stride + (int64_t)head * a.q.head_stride;
       const uint32_t dst = smem_u32(data + C::kQ) + (uint32_t)i * (kTileRows * D * 2);
       if constexpr (!C::kQuant) {
         uint4 w[D / 8];
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) w[c] = there ? *reinterpret_cast<const uint4*>(src + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
+        for (int x = 0; x < D / 8; ++x) w[x] = there ? *reinterpret_cast<const uint4*>(src + 8 * x) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) sts128(dst + row_chunk(r, c), w[c].x, w[c].y, w[c].z, w[c].w);
+        for (int x = 0; x < D / 8; ++x) sts128(dst + row_chunk(r, x), w[x].x, w[x].y, w[x].z, w[x].w);
       } else {
         float v[D];
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 w = there ? *reinterpret_cast<const uint4*>(src + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
+        for (int x = 0; x < D / 8; ++x) {
+          const uint4 w = there ? *reinterpret_cast<const uint4*>(src + 8 * x) : make_uint4(0u, 0u, 0u, 0u);
           const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
+          for (int y = 0; y < 4; ++y) {
             if (a.bf16) {
-              v[8 * c + 2 * x] = __uint_as_float(ww[x] << 16);
-              v[8 * c + 2 * x + 1] = __uint_as_float(ww[x] & 0xFFFF0000u);
+              v[8 * x + 2 * y] = __uint_as_float(ww[y] << 16);
+              v[8 * x + 2 * y + 1] = __uint_as_float(ww[y] & 0xFFFF0000u);
             } else {
-              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&ww[x]));
-              v[8 * c + 2 * x] = f.x;
-              v[8 * c + 2 * x + 1] = f.y;
+              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&ww[y]));
+              v[8 * x + 2 * y] = f.x;
+              v[8 * x + 2 * y + 1] = f.y;
             }
           }
         }
         hadamard_row<D>(v);
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
+        for (int x = 0; x < D / 8; ++x) {
           uint32_t w[4];
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            w[x] = pack2<false>(v[column_value<SRC>(8 * c + 2 * x)] * (8.0f / D),
-                                v[column_value<SRC>(8 * c + 2 * x + 1)] * (8.0f / D));
-          sts128(dst + row_chunk(r, c), w[0], w[1], w[2], w[3]);
+          for (int y = 0; y < 4; ++y)
+            w[y] = pack2<false>(v[column_value<SRC>(8 * x + 2 * y)] * (8.0f / D),
+                                v[column_value<SRC>(8 * x + 2 * y + 1)] * (8.0f / D));
+          sts128(dst + row_chunk(r, x), w[0], w[1], w[2], w[3]);
         }
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&qfull[i]);
-    }
+    };
 
-    const int pos = it.first + tok;
-    const int lim = pos - it.base;                                             // last key it sees, from the item's first key
-    const int low = a.window > 0 ? max(0, pos - a.window + 1) - it.base : 0;   // first
-    const float c = a.scale_log2;
-    float m = kNegInf;
-    float2 l0 = make_float2(0.0f, 0.0f), l1 = make_float2(0.0f, 0.0f);
-    uint32_t phase = 0;
-    bool any = false;
-    for (int j = sp.j0; ok && j < sp.j1; j += sp.step) {
-      ok = mbar_wait(&sfull[i], phase);
-      phase ^= 1u;
-      if (!ok) break;
-      tc_fence_after();
-      float s[kKeys];
+    Item it;
+    uint32_t n = 0, jphase = 0;
+    uint32_t blocks = 0;  // of this half so far: the buffers and their phases
+    uint32_t oph = 0;     // phases of the halves' outputs (a bit a half; an item without blocks of a half has none)
+    bool have = read_item(n, &it);
+    auto used = [&](const Item& x) { return i ? x.span[1].b0 < x.span[1].b1 : x.span[0].b0 < x.span[0].b1; };
+    if (have && used(it)) load_q(it);
+    while (have) {
+      bool ok = true;
+      int tok, head;
+      const bool there = row_of(it, &tok, &head);
+      const Span sp = i ? it.span[1] : it.span[0];
+      const int pos = it.first + tok;
+      const int lim = pos - it.base;                                            // last key it sees, from the item's first key
+      const int low = a.window > 0 ? max(0, pos - a.window + 1) - it.base : 0;  // first
+      float m = kNegInf;
+      float2 l0 = make_float2(0.0f, 0.0f), l1 = make_float2(0.0f, 0.0f);
+      bool any = false;
+#pragma unroll 1
+      for (int b = sp.b0; b < sp.b1; b += sp.step, ++blocks) {
+        const uint32_t buf = blocks & 1u;
+        ok = bar_wait(&sfull[2 * i + buf], blocks >> 1 & 1u);
+        if (!ok) break;
+        tc_fence_after();
+        float s[kBlock];
+        const uint32_t col = s_col + kBlock * buf;
 #pragma unroll
-      for (int x = 0; x < kKeys; x += 32) tmem_ld_32x32b_x32(s_col + x, *reinterpret_cast<uint32_t(*)[32]>(&s[x]));
-      tmem_ld_wait();
-      const int k0 = j * kKeys;
-      if (__any_sync(0xffffffffu, k0 + kKeys - 1 > lim || k0 < low)) {
-        const int hi = lim - k0, lo = low - k0;
+        for (int x = 0; x < kBlock; x += 32) tmem_ld_32x32b_x32(col + x, *reinterpret_cast<uint32_t(*)[32]>(&s[x]));
+        tmem_ld_wait();
+        const int k0 = b * kBlock;
+        if (__any_sync(0xffffffffu, k0 + kBlock - 1 > lim || k0 < low)) {
+          const int hi = lim - k0, lo = low - k0;
 #pragma unroll
-        for (int x = 0; x < kKeys; ++x)
-          if (x > hi || x < lo) s[x] = kNegInf;
-      }
-      float t0 = s[0], t1 = s[1], t2 = s[2], t3 = s[3];
+          for (int x = 0; x < kBlock; ++x)
+            if (x > hi || x < lo) s[x] = kNegInf;
+        }
+        float t[4];
 #pragma unroll
-      for (int x = 4; x < kKeys; x += 4) {
-        t0 = fmaxf(t0, s[x]);
-        t1 = fmaxf(t1, s[x + 1]);
-        t2 = fmaxf(t2, s[x + 2]);
-        t3 = fmaxf(t3, s[x + 3]);
-      }
-      const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * c;
-      const bool up = top > m + kSlack;
-      if (__any_sync(0xffffffffu, up)) {
-        const float f = up ? ex2(m - top) : 1.0f;
-        m = up ? top : m;
-        l0.x *= f, l0.y *= f, l1.x *= f, l1.y *= f;
-        if (any) {
-          // the scores' barrier also stands for the previous tile's P V, so O is complete
+        for (int x = 0; x < 4; ++x) t[x] = max3(s[x], s[x + 4], s[x + 8]);
 #pragma unroll
-          for (int x = 0; x < D; x += 32) {
-            uint32_t w[32];
-            tmem_ld_32x32b_x32(o_col + x, w);
-            tmem_ld_wait();
+        for (int x = 12; x < 60; x += 8)
 #pragma unroll
-            for (int y = 0; y < 32; ++y) w[y] = __float_as_uint(__uint_as_float(w[y]) * f);
-            tmem_st_x32(o_col + x, w);
+          for (int y = 0; y < 4; ++y) t[y] = max3(t[y], s[x + y], s[x + y + 4]);
+        const float top = fmaxf(max3(t[0], t[1], t[2]), max3(max3(t[3], s[60], s[61]), s[62], s[63])) * c;
+        const bool up = top > m + kSlack;
+        if (__any_sync(0xffffffffu, up)) {
+          const float f = up ? ex2(m - top) : 1.0f;
+          m = up ? top : m;
+          l0.x *= f, l0.y *= f, l1.x *= f, l1.y *= f;
+          if (any) {
+            ok = bar_wait(&pvdone[i], (blocks & 1u) ^ 1u);  // the block before this one is in O
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int x = 0; x < D; x += 32) {
+              uint32_t o[32];
+              tmem_ld_32x32b_x32(o_col + x, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+              tmem_st_x32(o_col + x, o);
+            }
           }
         }
-      }
-      any = true;
-      const float ref = m == kNegInf ? 0.0f : m;  // nothing seen yet: all scores are -inf, any finite reference does
-      const float2 cc = make_float2(c, c), mm = make_float2(-ref, -ref);
-#pragma unroll
-      for (int x = 0; x < kKeys; x += 64) {
+        any = true;
+        // nothing seen yet: all scores are -inf, any finite reference does
+        const float ref = m == kNegInf ? 0.0f : m;
+        const float2 cc = make_float2(c, c), mm = make_float2(-ref, -ref);
         uint32_t w[32];
 #pragma unroll
         for (int y = 0; y < 32; y += 2) {
-          float2 p = fma2(make_float2(s[x + 2 * y], s[x + 2 * y + 1]), cc, mm);
-          float2 n = fma2(make_float2(s[x + 2 * y + 2], s[x + 2 * y + 3]), cc, mm);
-          p.x = ex2(p.x), p.y = ex2(p.y), n.x = ex2(n.x), n.y = ex2(n.y);
+          const float* x = s + 2 * y;
+          float2 p = fma2(make_float2(x[0], x[1]), cc, mm), q = fma2(make_float2(x[2], x[3]), cc, mm);
+          p.x = ex2(p.x), p.y = ex2(p.y), q.x = ex2(q.x), q.y = ex2(q.y);
           l0 = add2(l0, p);
-          l1 = add2(l1, n);
+          l1 = add2(l1, q);
           w[y] = pack2<BF16>(p.x, p.y);
-          w[y + 1] = pack2<BF16>(n.x, n.y);
+          w[y + 1] = pack2<BF16>(q.x, q.y);
         }
-        tmem_st_x32(s_col + x / 2, w);
+        tmem_st_x32(col, w);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pfull[2 * i + buf]);
       }
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&pfull[i]);
-    }
 
-    // ---- the row's output
-    float l = (l0.x + l0.y) + (l1.x + l1.y);
-    float o[D];
+      // The next item's q goes in before this item's output is waited for, so that its scores can be computed meanwhile;
+      // after a joint item it goes in last (q's room is its meeting place).
+      float l = (l0.x + l0.y) + (l1.x + l1.y);
+      Item next;
+      have = ok && read_item(n + 1, &next);
+#pragma unroll 1
+      for (int pass = 0; pass < 2; ++pass) {
+        if (have && ok && it.joint == pass && used(next)) load_q(next);
+        if (pass == 1 || !ok) continue;
+        // ---- the row's output
+        float o[D];
 #pragma unroll
-    for (int x = 0; x < D; ++x) o[x] = 0.0f;
-    // in a joint item the other half's MMAs still read the ring that the join writes
-    if (ok && jhi > jlo) {
-      if (sp.j1 > sp.j0 || it.joint) ok = mbar_wait(&ofull[i], 0u);
-      if (ok && it.joint) ok = mbar_wait(&ofull[i ^ 1], 0u);
-    }
-    if (ok && any) {
-      tc_fence_after();
+        for (int x = 0; x < D; ++x) o[x] = 0.0f;
+        // a joint item's meeting place is q's room, of both halves
 #pragma unroll
-      for (int x = 0; x < D; x += 32) tmem_ld_32x32b_x32(o_col + x, *reinterpret_cast<uint32_t(*)[32]>(&o[x]));
-      tmem_ld_wait();
-    }
-    if (it.joint) {
-      float* jo = reinterpret_cast<float*>(data + C::kRing);  // [D][128]: a thread a column, no bank conflicts
-      float2* jml = reinterpret_cast<float2*>(jo + D * kTileRows);
-      if (i == 1 && ok) {
-#pragma unroll
-        for (int x = 0; x < D; ++x) jo[x * kTileRows + r] = o[x];
-        jml[r] = make_float2(m, l);
-      }
-      named_barrier(1, 256);  // both halves come here, also after a wait gave up
-      if (i == 0 && ok) {
-        const float2 other = jml[r];
-        const float both = fmaxf(m, other.x);
-        const float f0 = m == kNegInf ? 0.0f : ex2(m - both), f1 = other.x == kNegInf ? 0.0f : ex2(other.x - both);
-        l = l * f0 + other.y * f1;
-#pragma unroll
-        for (int x = 0; x < D; ++x) o[x] = o[x] * f0 + jo[x * kTileRows + r] * f1;
-        m = both;
-      }
-    }
-    if (ok && there && !(it.joint && i == 1)) {
-      const int64_t grow = (it.q0 + tok) * a.heads + head;
-      if (a.splits > 1) {
-        const int64_t prow = (int64_t)it.split * a.total_q * a.heads + grow;
-        a.part_ml[prow] = make_float2(m, l);
-        if (m != kNegInf) {
-          float4* dst = reinterpret_cast<float4*>(a.part_o + prow * D);
-#pragma unroll
-          for (int x = 0; x < D / 4; ++x) dst[x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+        for (int h = 0; h < 2; ++h) {
+          if (it.span[h].b0 >= it.span[h].b1) continue;
+          if (ok && (h == i || it.joint)) ok = bar_wait(&ofull[h], oph >> h & 1u);
+          oph ^= 1u << h;
         }
-      } else {
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // a row that saw no key gives zeros
-        uint16_t* dst = static_cast<uint16_t*>(a.out) + (it.q0 + tok) * a.out_token_stride + (int64_t)head * a.out_head_stride;
+        if (ok && any) {
+          tc_fence_after();
+#pragma unroll
+          for (int x = 0; x < D; x += 32) tmem_ld_32x32b_x32(o_col + x, *reinterpret_cast<uint32_t(*)[32]>(&o[x]));
+          tmem_ld_wait();
+        }
         if constexpr (C::kQuant) {
           float v[D];
 #pragma unroll
@@ -517,254 +599,385 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
 #pragma unroll
           for (int x = 0; x < D; ++x) o[x] = v[x] * (8.0f / D);
         }
+        if (ok && it.joint) {
+          float* jo = reinterpret_cast<float*>(data + C::kQ);  // [D][128]: a thread a column, no bank conflicts
+          if (i == 1) {
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
-        for (int x = 0; x < D; x += 8) {
-          uint32_t w[4];
+            for (int x = 0; x < D; ++x) jo[x * kTileRows + r] = o[x] * inv;
+            jlse[r] = m + log2f(l);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(jfull);
+          } else {
+            ok = bar_wait(jfull, jphase);
+            if (ok) {
+              const float other = jlse[r];
+              const float both = fmaxf(m, other);
+              // a half without a maximum saw nothing (its sum is 0) or nothing but NaN (its sum is NaN)
+              const float f0 = m == kNegInf ? (l == 0.0f ? 0.0f : l) : ex2(m - both);
+              const float f1 = other == kNegInf ? 0.0f : ex2(other - both);
+              l = l * f0 + f1;
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const float p = o[x + 2 * y] * inv, n = o[x + 2 * y + 1] * inv;
-            w[y] = (C::kQuant ? a.bf16 != 0 : BF16) ? pack2<true>(p, n) : pack2<false>(p, n);
+              for (int x = 0; x < D; ++x) o[x] = o[x] * f0 + jo[x * kTileRows + r] * f1;
+              m = both;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(jfree);
           }
-          *reinterpret_cast<uint4*>(dst + x) = make_uint4(w[0], w[1], w[2], w[3]);
+          if (ok) ok = bar_wait(jfree, jphase);
+          jphase ^= 1u;
         }
+        if (ok && there && !(it.joint && i == 1)) {
+          if (a.splits > 1) {
+            const int64_t prow = ((int64_t)it.split * a.total_q + it.q0 + tok) * a.heads + head;
+            a.part_ml[prow] = make_float2(m, l);
+            if (m != kNegInf) {
+              float4* dst = reinterpret_cast<float4*>(a.part_o + prow * D);
+#pragma unroll
+              for (int x = 0; x < D / 4; ++x) dst[x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+            }
+          } else {
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // a row that saw no key gives zeros
+            uint16_t* dst = static_cast<uint16_t*>(a.out) + (it.q0 + tok) * a.out_token_stride + (int64_t)head * a.out_head_stride;
+#pragma unroll
+            for (int x = 0; x < D; x += 8) {
+              uint32_t w[4];
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const float p = o[x + 2 * y] * inv, q = o[x + 2 * y + 1] * inv;
+                w[y] = (C::kQuant ? a.bf16 != 0 : BF16) ? pack2<true>(p, q) : pack2<false>(p, q);
+              }
+              *reinterpret_cast<uint4*>(dst + x) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+        tc_fence_before();
       }
+      have = have && ok;
+      it = next;
+      ++n;
     }
-    tc_fence_before();
   } else if (warp < 12) {
-   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kIssueRegs));
-   if (warp == 8) {
-    // ---------------- MMA issue ----------------
-    constexpr uint32_t kIdS = idesc(BF16, 128, 128, false);
-    constexpr uint32_t kIdO = idesc(BF16, 128, D, true);
-    const uint32_t qaddr = smem_u32(data + C::kQ), ring = smem_u32(data + C::kRing);
-    bool ok = true;
-    int pend[2] = {-1, -1};     // key tile whose P V is due
-    uint32_t pph[2] = {0u, 0u};
-    bool started[2] = {false, false};
-    const uint32_t one = elect_one();
-    // slots are filled in the order K(jlo), V(jlo), K(jlo + 1), ...
-    auto slot_of = [&](int j, int value) { return (2 * (j - jlo) + value) % NS; };
-    auto phase_of = [&](int j, int value) { return (uint32_t)((2 * (j - jlo) + value) / NS) & 1u; };
-    auto values = [&](int i) {  // P V of half i's pending tile
-      const int j = pend[i];
-      const int s = slot_of(j, 1);
-      if (!mbar_wait(&kvfull[s], phase_of(j, 1))) return false;
-      if (fix && j == tail && !mbar_wait(vfix, 0u)) return false;
-      if (!mbar_wait(&pfull[i], pph[i])) return false;
-      pph[i] ^= 1u;
-      tc_fence_after();
-      // keys past the length take no part: whole steps of 16 are left out
-      const int keys = min(kKeys, it.kv_len - it.base - j * kKeys);
-      const int steps = (keys + 15) >> 4;
-      const uint64_t vd = sdesc_n_major(ring + (uint32_t)s * C::kSlot, kKeys * 128);
-      for (int k = 0; k < steps; ++k) {
-        if (one)
-          tc_mma_f16_ta(tmem + 256 + 128 * i, tmem + 128 * i + 8 * k, vd + (uint64_t)(k * (2048 >> 4)), kIdO,
-                        started[i] || k > 0);
-      }
-      started[i] = true;
-      pend[i] = -1;
-      const Span& other = i ? sp0 : sp1;
-      // the slot is free once every half that uses it has read it; half 1 comes after half 0
-      if (i == 1 || !other.has(j)) {
-        if (one) tc_commit(&kvempty[s]);
-      }
-      return true;
-    };
-    for (int j = jlo; ok && j < jhi; ++j) {
-      const int s = slot_of(j, 0);
-      ok = mbar_wait(&kvfull[s], phase_of(j, 0));
-      for (int i = 0; ok && i < 2; ++i) {
-        const Span& sp = i ? sp1 : sp0;
-        if (!sp.has(j)) {
-          // past this half's last tile: its values go before the other half's release their slot
-          if (pend[i] >= 0 && j >= sp.j1) ok = values(i);
-          continue;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kIssueRegs));
+    if (warp == 8 || warp == 10) {
+      // ---------------- MMA issue: a warp a half ----------------
+      // The MMAs' descriptors are taken from uniform registers.  What comes out of shared memory is the same in every
+      // lane but not known to be: it goes through a warp reduction, whose result is.
+      constexpr uint32_t kIdS = idesc(BF16, 128, kBlock, false);
+      constexpr uint32_t kIdO = idesc(BF16, 128, D, true);
+      auto uni = [](int x) { return (int)__reduce_or_sync(0xffffffffu, (unsigned)x); };
+      const int i = uni(warp == 10);
+      const uint64_t qd = sdesc_sw128(smem_u32(data + C::kQ)) + (uint64_t)(i * (kTileRows * D * 2 >> 4));
+      const uint64_t kd0 = sdesc_sw128(smem_u32(data + C::kRing));
+      const uint64_t vd0 = sdesc_n_major(smem_u32(data + C::kRing), kKeys * 128);
+      const uint32_t tm = (uint32_t)uni((int)tmem) + 128 * i;  // this half's scores and weights; its output 256 columns on
+      const uint32_t one = elect_one();
+      bool ok = true;
+      uint32_t n = 0, qph = 0, blocks = 0;
+      uint32_t fph = 0;  // phases of the slots' tails (a bit a slot)
+      // The ring holds K(jlo), V(jlo), K(jlo + 1), ... of each item: where the next tile's keys and values lie.
+      uint32_t slot[2] = {0u, 1u}, sph[2] = {0u, 0u};
+      auto next_slot = [&](int value) {
+        slot[value] += 2;
+        if (slot[value] >= NS) {
+          slot[value] -= NS;
+          sph[value] ^= 1u;
         }
-        if (pend[i] >= 0) ok = values(i);
-        else ok = mbar_wait(&qfull[i], 0u);
-        if (!ok) break;
-        tc_fence_after();
-        const uint64_t qd = sdesc_sw128(qaddr + (uint32_t)i * (kTileRows * D * 2));
-        const uint64_t kd = sdesc_sw128(ring + (uint32_t)s * C::kSlot);
+      };
+      while (ok) {
+        Item it;
+        if (!__all_sync(0xffffffffu, read_item(n, &it))) break;
+        ++n;
+        const int b0 = uni(i ? it.span[1].b0 : it.span[0].b0), b1 = uni(i ? it.span[1].b1 : it.span[0].b1), step = uni(it.joint) + 1;
+        const int jlo = uni(it.jlo), jhi = uni(it.jhi), tail = uni(it.tail), keys = uni(it.kv_len - it.base);
+        int kt = jlo, vt = jlo;  // tiles whose keys / values come next
+        // Tiles that this half does not use, before its first and after its last: released once they are filled, so that
+        // releases stay in step with fills, and in the ring's order.
+        auto skip = [&](int upto) {
+#pragma unroll 1
+          for (; ok && kt < upto; ++kt, ++vt) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint64_t off = (uint64_t)(((k >> 2) * (kKeys * 128) + (k & 3) * 32) >> 4);
-          if (one) tc_mma_f16(tmem + 128 * i, qd + off, kd + off, kIdS, k > 0);
+            for (int value = 0; value < 2; ++value) {
+              ok = bar_wait(&kvfull[slot[value]], sph[value]) && ok;
+              if (one) mbar_arrive(&kvempty[slot[value]]);
+              if (value && vt == tail) fph ^= 1u << slot[1];
+              next_slot(value);
+            }
+            ok = __all_sync(0xffffffffu, ok);
+          }
+        };
+        skip(b0 < b1 ? b0 >> 1 : jhi);
+        if (b0 < b1) {
+          ok = bar_wait(&qfull[i], qph) && ok;
+          qph ^= 1u;
         }
-        if (one) tc_commit(&sfull[i]);
-        pend[i] = j;
-      }
-      if (ok && one) tc_commit(&kvempty[s]);
-    }
-    for (int i = 0; ok && i < 2; ++i)
-      if (pend[i] >= 0) ok = values(i);
-    if (ok) {
-      if (one) {
-        tc_commit(&ofull[0]);
-        tc_commit(&ofull[1]);
-      }
-    } else {
-      // what was issued must be done before the CTA's memory goes
-      if (one) tc_commit(mdrain);
-      mbar_wait(mdrain, 0u);
-    }
-    tc_fence_before();
-   } else if (!C::kQuant && warp == C::kFirstLoader) {
-    // ---------------- tensor copies of keys and values ----------------
-    bool ok = true;
-    int64_t n = 0;
-    int page_rows = kKeys;  // keys of one copy
-    if constexpr (SRC == kPaged16) page_rows = min(kKeys, 1 << a.cache.page_shift);
-    if (lane == 0) {
-      prefetch_tensormap(&maps.k);
-      prefetch_tensormap(&maps.v);
-    }
-    for (int j = jlo; ok && j < jhi; ++j) {
-      const int t = it.base + j * kKeys;
-      int64_t row = 0;  // cache row of this lane's copy (paged)
-      int copies = 1;
-      if constexpr (SRC == kPaged16) {
-        copies = (min(kKeys, it.kv_len - t) + page_rows - 1) / page_rows;
-        if (lane < copies) {
-          const int key = t + lane * page_rows;
-          const int id = a.table[(int64_t)it.b * a.table_width + (key >> a.cache.page_shift)];
-          // an id outside the cache reads as zeros (past the map's last row)
-          row = id >= 0 && id < a.cache.num_pages
-                    ? (((int64_t)id * a.kv_heads + it.kvh) << a.cache.page_shift) + (key & ((1 << a.cache.page_shift) - 1))
-                    : (a.cache.num_pages * a.kv_heads) << a.cache.page_shift;
-        }
-      }
-      for (int value = 0; value < 2; ++value, ++n) {
-        const int s = (int)(n % NS);
-        ok = mbar_wait(&kvempty[s], ((uint32_t)(n / NS) & 1u) ^ 1u);
-        if (!ok) break;
-        uint8_t* dst = data + C::kRing + s * C::kSlot;
-        const CUtensorMap* map = value ? &maps.v : &maps.k;
-        if (lane == 0) mbar_arrive_expect_tx(&kvfull[s], (uint32_t)(copies * page_rows * D * 2));
-        __syncwarp();
-        if (lane < copies) {
+        // Scores run a block ahead of weights times values: turn b has the scores of block b and the values of the one
+        // before.
+#pragma unroll 1
+        for (int b = b0; b < b1 + step && b0 < b1; b += step) {
+          if (b < b1) {
+            const uint32_t s = slot[0], buf = blocks & 1u;
+            ok = bar_wait(&kvfull[s], sph[0]) && ok;
+            tc_fence_after();
+            const uint64_t kd = kd0 + (uint64_t)(s * (C::kSlot >> 4) + (b & 1) * (kBlock * 128 >> 4));
 #pragma unroll
-          for (int h = 0; h < D / 64; ++h) {
-            if constexpr (SRC == kPacked)
-              tma_tile3d_g2s(dst + h * (kKeys * 128), map, 64 * h, it.kvh, (int)(it.q0 + t), &kvfull[s]);
-            else
-              tma_tile3d_g2s(dst + h * (kKeys * 128) + lane * page_rows * 128, map, 64 * h, 0, (int)row, &kvfull[s]);
+            for (int k = 0; k < D / 16; ++k) {
+              if (one)
+                tc_mma_f16(tm + kBlock * buf, qd + (uint64_t)(((k >> 2) * (kTileRows * 128) + (k & 3) * 32) >> 4),
+                           kd + (uint64_t)(((k >> 2) * (kKeys * 128) + (k & 3) * 32) >> 4), kIdS, k > 0);
+              __syncwarp();
+            }
+            if (one) tc_commit(&sfull[2 * i + buf]);
+            if (b + step >= b1 || (b + step) >> 1 != b >> 1) {  // the tile's last scores
+              if (one) tc_commit(&kvempty[s]);
+              next_slot(0);
+              ++kt;
+            }
+            __syncwarp();
           }
+          if (b > b0) {
+            const int pb = b - step;
+            const uint32_t s = slot[1], g = blocks - 1, buf = g & 1u;
+            ok = bar_wait(&kvfull[s], sph[1]) && ok;
+            if (!C::kQuant && vt == tail) ok = bar_wait(&vfix[s], fph >> s & 1u) && ok;
+            // keys past the length take no part: whole steps of 16 are left out
+            const int steps = (min(kBlock, keys - pb * kBlock) + 15) >> 4;
+            const uint64_t vd = vd0 + (uint64_t)(s * (C::kSlot >> 4) + (pb & 1) * (kBlock * 128 >> 4));
+            const uint32_t pd = tm + kBlock * buf;
+            const bool held = pb > b0;
+            ok = bar_wait(&pfull[2 * i + buf], g >> 1 & 1u) && ok;
+            tc_fence_after();
+            if (steps == 4) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                if (one) tc_mma_f16_ta(tm + 256, pd + 8 * k, vd + (uint64_t)(k * (2048 >> 4)), kIdO, held || k > 0);
+                __syncwarp();
+              }
+            } else {
+#pragma unroll 1
+              for (int k = 0; k < steps; ++k) {
+                if (one) tc_mma_f16_ta(tm + 256, pd + 8 * k, vd + (uint64_t)(k * (2048 >> 4)), kIdO, held || k > 0);
+                __syncwarp();
+              }
+            }
+            if (one) tc_commit(&pvdone[i]);
+            if (b >= b1 || b >> 1 != pb >> 1) {  // the tile's last values
+              if (one) tc_commit(&kvempty[s]);
+              if (vt == tail) fph ^= 1u << s;
+              next_slot(1);
+              ++vt;
+            }
+            __syncwarp();
+          }
+          ++blocks;
+          if (!__all_sync(0xffffffffu, ok)) break;
         }
-        __syncwarp();
-        if (fix && value && j == tail) {
-          // zeros from the length to the next multiple of 16 keys of the tile
-          ok = mbar_wait(&kvfull[s], (uint32_t)(n / NS) & 1u);
-          if (!ok) {
-            ++n;
-            break;
-          }
-          const int keys = it.kv_len - t, upto = (keys + 15) & ~15;
-          const uint32_t d32 = smem_u32(dst);
-          for (int x = lane; x < (upto - keys) * (D / 8); x += 32) {
-            const int rr = keys + x / (D / 8), cc = x % (D / 8);
-            sts128(d32 + row_chunk(rr, cc), 0u, 0u, 0u, 0u);
-          }
-          fence_proxy_async_smem();
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (b0 < b1) {
+          --blocks;  // the last turn had values only
+          if (one) tc_commit(&ofull[i]);
           __syncwarp();
-          if (lane == 0) mbar_arrive(vfix);
         }
+        skip(jhi);
       }
-    }
-    drain_ring(kvfull, NS, n);
-   }
-  } else if constexpr (C::kQuant) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kLoaderRegs));
-    // ---------------- codes to fp16 rows ----------------
-    constexpr int RB = SRC == kPaged8 ? D : D / 2;   // bytes of a cached row
-    constexpr int LPR = RB / 16;                     // lanes of a row
-    constexpr int RPP = 32 / LPR;                    // rows a warp loads at a time
-    constexpr int NP = 32 / RPP;                     // such loads for the warp's 32 rows
-    const int lw = warp - C::kFirstLoader;
-    bool ok = true;
-    int64_t n = 0;
-    const int sub = lane % LPR;
-    auto page_of = [&](int j) {  // page of the 16-key group lane & 7 of tile j
-      const int key = it.base + j * kKeys + 16 * (lane & 7);
-      int id = -1;
-      if (j < jhi && key < it.kv_len) id = a.table[(int64_t)it.b * a.table_width + (key >> a.cache.page_shift)];
-      return id < a.cache.num_pages ? id : -1;
-    };
-    uint4 code[NP];
-    uint32_t scale[NP];  // both halves: the row's scale as fp16, 0 past the length
-    auto fetch = [&](int j, int value, int pid) {
-      const uint8_t* src = value ? a.cache.v : a.cache.k;
-      const uint16_t* ss = value ? a.cache.v_scale : a.cache.k_scale;
+      if (!ok) {
+        // what was issued must be done before the CTA's memory goes
+        if (one) tc_commit(&mdrain[i]);
+        __syncwarp();
+        bar_wait(&mdrain[i], 0u);
+      }
+      tc_fence_before();
+    } else if (warp == 9) {
+      // ---------------- items, and copies of keys and values ----------------
+      constexpr int NR = C::kQuant ? C::kRaws : NS;
+      uint64_t* full = C::kQuant ? rawfull : kvfull;
+      uint64_t* empty = C::kQuant ? rawempty : kvempty;
+      bool ok = true, more = true;
+      uint32_t n = 0, asks = 0;
+      int64_t filled = 0;
+      int idx = (int)blockIdx.x;
+      int page_rows = kKeys;  // keys of one copy
+      if constexpr (SRC != kPacked) page_rows = min(kKeys, 1 << a.cache.page_shift);
+      if (!C::kQuant && lane == 0) {
+        prefetch_tensormap(&maps.k);
+        prefetch_tensormap(&maps.v);
+      }
+      while (ok && more) {
+        Item it;
+        const bool valid = find_item<SRC>(a, lane, idx, &it);
+        if (valid) {
+          ok = bar_wait(&iempty[n & 1], ((n >> 1) & 1u) ^ 1u);
+          if (!ok) break;
+          if (lane == 0) {
+            items[n & 1] = it;
+            mbar_arrive(&ifull[n & 1]);
+          }
+          __syncwarp();
+          ++n;
+          for (int j = it.jlo; ok && j < it.jhi; ++j) {
+            const int t = it.base + j * kKeys;
+            int64_t row = 0;  // cache row of this lane's copy (paged)
+            int copies = 1;
+            bool page_ok = true;
+            if constexpr (SRC != kPacked) {
+              copies = (min(kKeys, it.kv_len - t) + page_rows - 1) / page_rows;
+              if (lane < copies) {
+                const int key = t + lane * page_rows;
+                const int id = a.table[(int64_t)it.b * a.table_width + (key >> a.cache.page_shift)];
+                page_ok = id >= 0 && id < a.cache.num_pages;
+                // an id outside the cache: past the map's last row, which reads as zeros (16 bits); page 0 in its
+                // place (the codes count for something, but nothing outside the cache is read)
+                row = page_ok ? (((int64_t)id * a.kv_heads + it.kvh) << a.cache.page_shift) +
+                                    (key & ((1 << a.cache.page_shift) - 1))
+                              : C::kQuant ? 0 : (a.cache.num_pages * a.kv_heads) << a.cache.page_shift;
+              }
+            }
 #pragma unroll
-      for (int p = 0; p < NP; ++p) {
-        const int rr = 32 * lw + p * RPP + lane / LPR;
-        const int id = __shfl_sync(0xffffffffu, pid, rr >> 4);
-        const int key = it.base + j * kKeys + rr;
-        code[p] = make_uint4(0u, 0u, 0u, 0u);
-        scale[p] = 0u;
-        if (id >= 0 && key < it.kv_len && j < jhi) {
-          const int64_t row = (((int64_t)id * a.kv_heads + it.kvh) << a.cache.page_shift) + (key & ((1 << a.cache.page_shift) - 1));
-          code[p] = __ldg(reinterpret_cast<const uint4*>(src + row * RB + 16 * sub));
-          scale[p] = (uint32_t)__ldg(ss + row) << 16;
+            for (int value = 0; value < 2; ++value) {
+              if (!ok) break;
+              const int s = (int)(filled % NR);
+              const uint32_t ph = (uint32_t)(filled / NR) & 1u;
+              ok = bar_wait(&empty[s], ph ^ 1u);
+              if (!ok) break;
+              ++filled;
+              if constexpr (!C::kQuant) {
+                uint8_t* dst = data + C::kRing + s * C::kSlot;
+                const CUtensorMap* map = value ? &maps.v : &maps.k;
+                if (lane == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)(copies * page_rows * D * 2));
+                __syncwarp();
+                if (lane < copies) {
+#pragma unroll
+                  for (int h = 0; h < D / 64; ++h) {
+                    if constexpr (SRC == kPacked)
+                      tma_tile3d_g2s(dst + h * (kKeys * 128), map, 64 * h, it.kvh, (int)(it.q0 + t), &full[s]);
+                    else
+                      tma_tile3d_g2s(dst + h * (kKeys * 128) + lane * page_rows * 128, map, 64 * h, 0, (int)row, &full[s]);
+                  }
+                }
+                __syncwarp();
+                if (value && j == it.tail) {
+                  // zeros from the length to the next multiple of 16 keys of the tile
+                  ok = bar_wait(&full[s], ph);
+                  if (!ok) break;
+                  const int keys = it.kv_len - t, upto = (keys + 15) & ~15;
+                  const uint32_t d32 = smem_u32(dst);
+                  for (int x = lane; x < (upto - keys) * (D / 8); x += 32)
+                    sts128(d32 + row_chunk(keys + x / (D / 8), x % (D / 8)), 0u, 0u, 0u, 0u);
+                  fence_proxy_async_smem();
+                  __syncwarp();
+                  if (lane == 0) mbar_arrive(&vfix[s]);
+                }
+              } else {
+                uint8_t* dst = data + C::kRawRing + s * C::kRaw;
+                if (lane == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)(copies * page_rows * (C::kRowBytes + 2)));
+                __syncwarp();
+                if (lane < copies) {
+                  tma_bulk_g2s(dst + lane * page_rows * C::kRowBytes, (value ? a.cache.v : a.cache.k) + row * C::kRowBytes,
+                               (uint32_t)(page_rows * C::kRowBytes), &full[s]);
+                  tma_bulk_g2s(dst + C::kCodes + lane * page_rows * 2, (value ? a.cache.v_scale : a.cache.k_scale) + row,
+                               (uint32_t)(page_rows * 2), &full[s]);
+                }
+                __syncwarp();
+              }
+            }
+          }
         }
-      }
-    };
-    int pid = page_of(jlo), pid_next = page_of(jlo + 1);
-    fetch(jlo, 0, pid);
-    for (int j = jlo; ok && j < jhi; ++j) {
-      for (int value = 0; value < 2; ++value, ++n) {
-        const int s = (int)(n % NS);
-        ok = mbar_wait(&kvempty[s], ((uint32_t)(n / NS) & 1u) ^ 1u);
         if (!ok) break;
-        const uint32_t dst = smem_u32(data + C::kRing) + (uint32_t)s * C::kSlot;
+        // the next item: a CTA that has not started yet
+        if (lane == 0) {
+          fence_proxy_async_smem();  // the last answer has been read before this one is written
+          mbar_arrive_expect_tx(clc, 16u);
+          cancel_cta(smem_u32(answer), clc);
+        }
+        __syncwarp();
+        ok = bar_wait(clc, asks & 1u);
+        ++asks;
+        if (!ok) break;
+        idx = cancelled_cta(smem_u32(answer));
+        __syncwarp();
+        more = idx >= 0;
+      }
+      // no item left (after a wait that gave up, the readers' own waits give up)
+      if (ok && bar_wait(&iempty[n & 1], ((n >> 1) & 1u) ^ 1u)) {
+        if (lane == 0) {
+          items[n & 1].done = 1;
+          mbar_arrive(&ifull[n & 1]);
+        }
+        __syncwarp();
+      }
+      drain_ring(full, NR, filled);
+    }
+  } else if constexpr (C::kQuant) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kConvertRegs));
+    // ---------------- codes to fp16 rows ----------------
+    constexpr int LPR = C::kRowBytes / 16;  // lanes of a row
+    constexpr int RPP = 32 / LPR;           // rows a warp takes at a time
+    constexpr int NP = 32 / RPP;            // passes over the warp's 32 rows
+    const int lw = warp - 12, sub = lane % LPR;
+    bool ok = true;
+    Item it;
+    uint32_t n = 0, raw = 0, filled = 0;
+    while (ok && read_item(n, &it)) {
+      for (int x = 0; ok && x < 2 * (it.jhi - it.jlo); ++x, ++raw, ++filled) {
+        const uint32_t rs = raw % C::kRaws, s = filled % NS;
+        ok = bar_wait(&rawfull[rs], raw / C::kRaws & 1u) && bar_wait(&kvempty[s], (filled / NS & 1u) ^ 1u);
+        if (!ok) break;
+        const int left = it.kv_len - it.base - (it.jlo + (x >> 1)) * kKeys;  // keys before the length
+        const uint32_t src = smem_u32(data + C::kRawRing) + rs * C::kRaw;
+        const uint32_t dst = smem_u32(data + C::kRing) + s * C::kSlot;
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
           const int rr = 32 * lw + p * RPP + lane / LPR;
-          const uint32_t ww[4] = {code[p].x, code[p].y, code[p].z, code[p].w};
-          const bool none = scale[p] == 0u;  // past the length or no page: zeros
-          const float sf = __uint_as_float(scale[p]);
+          uint32_t ww[4], sb;
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(ww[0]), "=r"(ww[1]), "=r"(ww[2]), "=r"(ww[3])
+                       : "r"(src + rr * C::kRowBytes + 16 * sub)
+                       : "memory");
+          {
+            uint16_t s16;
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(s16) : "r"(src + C::kCodes + 2 * rr) : "memory");
+            sb = (uint32_t)s16 << 16;
+          }
+          const bool none = rr >= left;  // past the length: zeros
+          const float sf = __uint_as_float(sb);
           const uint32_t sh = pack2<false>(sf, sf);
           if constexpr (SRC == kPaged8) {
             uint32_t h[8];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              h[2 * x] = hmul2(hsub2(__byte_perm(ww[x], 0x64646464u, 0x4140), 0x64806480u), sh);
-              h[2 * x + 1] = hmul2(hsub2(__byte_perm(ww[x], 0x64646464u, 0x4342), 0x64806480u), sh);
+            for (int y = 0; y < 4; ++y) {
+              h[2 * y] = hmul2(hsub2(__byte_perm(ww[y], 0x64646464u, 0x4140), 0x64806480u), sh);
+              h[2 * y + 1] = hmul2(hsub2(__byte_perm(ww[y], 0x64646464u, 0x4342), 0x64806480u), sh);
             }
             if (none) {
 #pragma unroll
-              for (int x = 0; x < 8; ++x) h[x] = 0u;
+              for (int y = 0; y < 8; ++y) h[y] = 0u;
             }
             sts128(dst + row_chunk(rr, 2 * sub), h[0], h[1], h[2], h[3]);
             sts128(dst + row_chunk(rr, 2 * sub + 1), h[4], h[5], h[6], h[7]);
           } else {
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
+            for (int y = 0; y < 4; ++y) {
               uint32_t h[4];
 #pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                const uint32_t w = ww[x] >> (8 * y);
-                h[2 * y] = hmul2(hsub2((w & 0x000F000Fu) | 0x64006400u, 0x64086408u), sh);
-                h[2 * y + 1] = hmul2(hfma2((w & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u), sh);
+              for (int z = 0; z < 2; ++z) {
+                const uint32_t w = ww[y] >> (8 * z);
+                h[2 * z] = hmul2(hsub2((w & 0x000F000Fu) | 0x64006400u, 0x64086408u), sh);
+                h[2 * z + 1] = hmul2(hfma2((w & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u), sh);
               }
               if (none) h[0] = h[1] = h[2] = h[3] = 0u;
-              sts128(dst + row_chunk(rr, 4 * sub + x), h[0], h[1], h[2], h[3]);
+              sts128(dst + row_chunk(rr, 4 * sub + y), h[0], h[1], h[2], h[3]);
             }
           }
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&kvfull[s]);
-        // the next rows' loads are in flight while the next slot is waited for
-        if (value == 0) {
-          fetch(j, 1, pid);
-        } else {
-          pid = pid_next;
-          pid_next = page_of(j + 2);
-          fetch(j + 1, 0, pid);
+        if (lane == 0) {
+          mbar_arrive(&kvfull[s]);
+          mbar_arrive(&rawempty[rs]);
         }
       }
+      ++n;
     }
   }
   __syncthreads();
@@ -774,9 +987,8 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
 
 // Joins the parts of split key ranges: a warp a row, parts in order.
 template <int D>
-__global__ void __launch_bounds__(256) attn_tile_join_kernel(const AttnArgs a, int quant) {
+__global__ void __launch_bounds__(256) attn_tile_join_kernel(const AttnArgs a) {
   constexpr int PER = D / 32;
-  pdl_wait();
   const int lane = threadIdx.x & 31;
   const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int64_t n = a.total_q * a.heads;
@@ -809,37 +1021,6 @@ __global__ void __launch_bounds__(256) attn_tile_join_kernel(const AttnArgs a, i
     for (int i = 0; i < PER; ++i) o[i] = fmaf(src[i], f, o[i]);
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  if (quant) {
-    // lane `lane` holds columns PER * lane ..; put the values of 4-bit rows back in order
-    __shared__ float sv[8][D];
-    float* v = sv[threadIdx.x >> 5];
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int c = PER * lane + i;
-      v[quant == kPaged4 ? column_value<kPaged4>(c) : c] = o[i];
-    }
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < PER; ++i) o[i] = v[PER * lane + i];
-#pragma unroll
-    for (int st = 1; st < PER; st *= 2)
-#pragma unroll
-      for (int i = 0; i < PER; ++i)
-        if (!(i & st)) {
-          const float x = o[i], y = o[i + st];
-          o[i] = x + y;
-          o[i + st] = x - y;
-        }
-#pragma unroll
-    for (int st = 1; st < 32; st *= 2)
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const float x = __shfl_xor_sync(0xffffffffu, o[i], st);
-        o[i] = (lane & st) ? x - o[i] : o[i] + x;
-      }
-#pragma unroll
-    for (int i = 0; i < PER; ++i) o[i] *= 8.0f / D;
-  }
   uint16_t* dst = static_cast<uint16_t*>(a.out) + tok * a.out_token_stride +
                   (row - tok * a.heads) * a.out_head_stride + PER * lane;
 #pragma unroll
@@ -902,16 +1083,8 @@ cudaError_t launch_tile(const AttnArgs& a, cudaStream_t stream) {
   attn_tile_kernel<D, SRC, BF16><<<(unsigned)blocks, C::kThreads, C::kSmem, stream>>>(maps, a);
   e = cudaGetLastError();
   if (e != cudaSuccess || a.splits == 1) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((a.total_q * a.heads + 7) / 8), 1u, 1u);
-  cfg.blockDim = dim3(256u, 1u, 1u);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_tile_join_kernel<D>, a, C::kQuant ? SRC : 0);
+  attn_tile_join_kernel<D><<<(unsigned)((a.total_q * a.heads + 7) / 8), 256, 0, stream>>>(a);
+  return cudaGetLastError();
 }
 
 template <int D>
