@@ -105,7 +105,7 @@ def lib() -> ctypes.CDLL:
     L.exl3_kv_read.argtypes = [cache, vp, i64, ctypes.c_int, vp, vp, vp]
     L.exl3_attention_prompt.argtypes = [heads, heads, heads, ctypes.c_int, i64, i32, i32, i32, vp, i32, i32, f32, vp,
                                         i64, i64, vp]
-    L.exl3_attention_paged_workspace_bytes.argtypes = [i64, i32, i32, i32, i32, i32, i32]
+    L.exl3_attention_paged_workspace_bytes.argtypes = [i64, i32, i32, i32, i32, i32, i32, i32]
     L.exl3_attention_paged_workspace_bytes.restype = sz
     L.exl3_attention_paged.argtypes = [heads, ctypes.c_int, i64, i32, cache, vp, i32, vp, vp, i32, i32, i32, i32, f32,
                                        vp, i64, i64, vp, sz, vp]
@@ -654,8 +654,8 @@ def _workspace_bytes(*sizes) -> int:
 
 
 def attention_paged_workspace_bytes(total_q: int, batch: int, heads: int, kv_heads: int, head_dim: int, max_q: int,
-                                    max_kv: int) -> int:
-    return _workspace_bytes(total_q, batch, heads, kv_heads, head_dim, max_q, max_kv)
+                                    max_kv: int, window: int = 0) -> int:
+    return _workspace_bytes(total_q, batch, heads, kv_heads, head_dim, max_q, max_kv, window)
 
 
 def attention_paged(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, cu_q: torch.Tensor,
@@ -682,7 +682,7 @@ def attention_paged(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, 
         raise ValueError("block_table must be [batch, width]")
     out, oh = _out_like(q, out, "out")
     if workspace is None:
-        need = _workspace_bytes(total, batch, heads, cache.kv_heads, d, int(max_q), int(max_kv))
+        need = _workspace_bytes(total, batch, heads, cache.kv_heads, d, int(max_q), int(max_kv), int(window))
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     else:
         _need(workspace, torch.uint8, "workspace")

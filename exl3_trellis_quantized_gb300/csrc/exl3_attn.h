@@ -85,7 +85,8 @@ struct AttnArgs {
   int window;             // 0: none
   float scale_log2;       // softmax scale * log2(e)
   int bf16;               // type of q and out
-  int splits;             // parts of each row tile's keys (tile kernel)
+  int splits;             // parts of each item's keys (tile kernel)
+  int tile_tokens;        // query tokens of a row tile (tile kernel)
   int ctas;               // grid of the token kernel
   float* part_o;
   float2* part_ml;
@@ -98,7 +99,9 @@ constexpr int token_ctas_per_sm(int rows) { return rows <= 8 ? 3 : 2; }
 constexpr int kTokenUnit = 64;
 // Few query rows a sequence (max_q * group <= kTokenRows) over a paged cache.
 cudaError_t launch_attn_token(const AttnArgs& a, cudaStream_t stream);
-// Query rows in tiles of 256, prompt (k, v) or paged.
+// Rows of a row tile of the tile kernel: it holds kTileTokenRows / group whole query tokens.
+constexpr int kTileTokenRows = 128;
+// Query rows in row tiles, prompt (k, v) or paged.
 cudaError_t launch_attn_tile(const AttnArgs& a, bool paged, cudaStream_t stream);
 // Lets KERNEL use `bytes` of dynamic shared memory and, with regs > 0, checks that it was built for `regs` registers a
 // thread: asked of the runtime once a kernel and device.

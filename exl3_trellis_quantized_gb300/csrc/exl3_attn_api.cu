@@ -71,7 +71,7 @@ struct PagedPlan {
   size_t o_bytes, ml_bytes;
 };
 PagedPlan paged_plan(int64_t total_q, int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t max_q,
-                     int64_t max_kv) {
+                     int64_t max_kv, int64_t window) {
   PagedPlan p = {};
   const int64_t group = q_heads / kv_heads;
   p.splits = 1;
@@ -85,14 +85,25 @@ PagedPlan paged_plan(int64_t total_q, int64_t batch, int64_t q_heads, int64_t kv
     p.ml_bytes = (size_t)2 * p.ctas * exl3::kTokenRows * 2 * sizeof(float);
     return p;
   }
-  // row tiles of 256 rows; while they leave SMs idle, each one's keys go to as
-  // many CTAs as there is room for, of at least four tiles of 128 keys
-  const int64_t tiles = batch == 1 ? (total_q * group + 255) / 256 : total_q * group / 256 + (total_q < batch ? total_q : batch);
+  // Row tiles, two an item.  The keys of each item may go to several CTAs: the number of parts is the one that a simple
+  // model of the time likes best, waves of items, each as long as its blocks of 64 keys (about 0.85 us each) and the
+  // beginning and end of an item (about 4 us), and what the parts cost to write and join.
+  const int64_t per = 2 * (exl3::kTileTokenRows / group);
+  const int64_t tiles = batch == 1 ? (total_q + per - 1) / per : total_q / per + (total_q < batch ? total_q : batch);
   const int64_t items = tiles * kv_heads;
-  int64_t splits = items > 0 ? kSms / items : 1;
-  const int64_t most = max_kv / 512;
-  if (splits > most) splits = most;
-  if (splits > 32) splits = 32;
+  const int64_t seen = window > 0 && window + per < max_kv ? window + per : max_kv;  // keys of an item
+  const double blocks = (double)(seen > 64 ? seen : 64) / 64.0;
+  double best = 0.0;
+  int64_t splits = 1;
+  for (int64_t s = 1; s <= 16 && blocks / s >= 8.0 && (s == 1 || items <= kSms); ++s) {
+    const double waves = (double)((items * s + kSms - 1) / kSms);
+    const double join = s > 1 ? 4.0 + (double)s * total_q * q_heads * head_dim * 8.0 / 4.0e6 : 0.0;
+    const double us = waves * (blocks / s * 0.85 + 4.0) + join;
+    if (s == 1 || us < 0.97 * best) {
+      best = us;
+      splits = s;
+    }
+  }
   if (splits > 1) {
     p.splits = (int)splits;
     p.o_bytes = (size_t)splits * total_q * q_heads * head_dim * sizeof(float);
@@ -232,14 +243,15 @@ exl3_status_t exl3_attention_prompt(const exl3_heads_t* q, const exl3_heads_t* k
   a.scale_log2 = scale * 1.4426950408889634f;
   a.bf16 = dtype == EXL3_BF16;
   a.splits = 1;
+  a.tile_tokens = exl3::kTileTokenRows / (q_heads / kv_heads);
   return exl3::api_status(exl3::launch_attn_tile(a, false, static_cast<cudaStream_t>(stream)), "exl3_attention_prompt");
 }
 
 size_t exl3_attention_paged_workspace_bytes(int64_t total_q, int32_t batch, int32_t q_heads, int32_t kv_heads,
-                                            int32_t head_dim, int32_t max_q, int32_t max_kv) {
+                                            int32_t head_dim, int32_t max_q, int32_t max_kv, int32_t window) {
   if (!valid_rows(total_q) || !valid_rows(batch) || !valid_head_counts(q_heads, kv_heads)) return 0;
-  if (check_head_dim(head_dim) != EXL3_OK || max_q < 1 || max_kv < 0 || total_q == 0 || batch == 0) return 0;
-  const PagedPlan p = paged_plan(total_q, batch, q_heads, kv_heads, head_dim, max_q, max_kv);
+  if (check_head_dim(head_dim) != EXL3_OK || max_q < 1 || max_kv < 0 || window < 0 || total_q == 0 || batch == 0) return 0;
+  const PagedPlan p = paged_plan(total_q, batch, q_heads, kv_heads, head_dim, max_q, max_kv, window);
   return p.o_bytes + p.ml_bytes;
 }
 
@@ -261,7 +273,7 @@ exl3_status_t exl3_attention_paged(const exl3_heads_t* q, exl3_dtype_t dtype, in
   const void* ints[3] = {block_table, cu_q, kv_lens};
   for (const void* p : ints)
     if (p == nullptr || (reinterpret_cast<uintptr_t>(p) & 3u) != 0) return EXL3_EINVAL;
-  const PagedPlan plan = paged_plan(total_q, batch, q_heads, a.cache.kv_heads, a.cache.head_dim, max_q, max_kv);
+  const PagedPlan plan = paged_plan(total_q, batch, q_heads, a.cache.kv_heads, a.cache.head_dim, max_q, max_kv, window);
   if (plan.o_bytes > 0 && !aligned16(workspace)) return EXL3_EINVAL;
   if (workspace_bytes < plan.o_bytes + plan.ml_bytes) return EXL3_EWORKSPACE;
   a.q = view(q);
@@ -282,6 +294,7 @@ exl3_status_t exl3_attention_paged(const exl3_heads_t* q, exl3_dtype_t dtype, in
   a.scale_log2 = scale * 1.4426950408889634f;
   a.bf16 = dtype == EXL3_BF16;
   a.splits = plan.splits;
+  a.tile_tokens = exl3::kTileTokenRows / (q_heads / a.kv_heads);
   a.ctas = plan.ctas;
   a.part_o = static_cast<float*>(workspace);
   a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + plan.o_bytes);

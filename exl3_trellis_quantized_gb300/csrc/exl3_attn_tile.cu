@@ -3,8 +3,10 @@
 //
 // Rows.  The query heads of a group share their keys, so the rows of a sequence
 // and key head are its query tokens times the group's heads, token major: one
-// CTA takes 256 of them (two tiles of 128, the M of the MMA) whatever the group
-// size, and reads each key and value once for all of them.
+// CTA takes two tiles of 128 (the M of the MMA), as many whole tokens as fit into
+// each, and reads each key and value once for all of them.  (Whole tokens make a
+// row tile one box of a tensor copy: with a thread loading and storing a row, the
+// two took 10000 cycles an item, half of a 512-token prompt's time.)
 //
 // Per block of 64 keys and 128 rows:
 //     S = Q K^T            tcgen05.mma, both operands in shared memory, S in tensor memory
@@ -34,7 +36,7 @@
 //
 // Roles: warps 0-3 and 4-7 softmax of row tiles 0 and 1 (a thread a row), warps 8
 // and 10 issue their MMAs, warp 9 takes the items and issues the copies of keys and values
-// into a ring of slots; for the quantised cache formats it copies the codes and
+// into a ring of slots, warp 11 those of q; for the quantised cache formats it copies the codes and
 // scales into a ring of their own, and warps 12-15 turn them into fp16 rows.
 // Quantised rows stay in the rotated basis (see exl3_rope_cache.cu): q is rotated
 // on its way into shared memory and the output on its way out, each a transform
@@ -58,7 +60,6 @@ enum Source { kPacked = 0, kPaged16 = 1, kPaged8 = 2, kPaged4 = 3 };
 constexpr int kKeys = 128;      // keys of a copy (a tile)
 constexpr int kBlock = 64;      // keys of a step
 constexpr int kTileRows = 128;  // rows of a tile; a CTA has two tiles
-constexpr int kItemRows = 2 * kTileRows;
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kSlack = 8.0f;
 
@@ -97,12 +98,33 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// mbar_wait in few instructions: the many waits of this kernel are code that its warps walk through once a tile.
+// One look at a barrier's phase: SPIN answers at once, else after as long as the hardware holds a waiting thread.
+// (With a suspend-time hint waiting warps woke late: 16384 tokens of 32 heads took 1600 us instead of 1411.)
+template <bool SPIN>
+__device__ __forceinline__ bool bar_poll(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  if constexpr (SPIN) {
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+  }
+  return ok != 0;
+}
+// mbar_wait in few instructions: the many waits of this kernel are code that its warps walk through once a block.
+template <bool SPIN = false>
 __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity) {
   const uint32_t b = smem_u32(bar);
   uint64_t t0 = 0;
 #pragma unroll 1
-  for (uint32_t tries = 0; !mbar_try_wait(b, parity); ++tries) {
+  for (uint32_t tries = 0; !bar_poll<SPIN>(b, parity); ++tries) {
     if ((tries & 255u) != 0) continue;
     const uint64_t t = globaltimer_ns();
     if (t0 == 0) t0 = t;
@@ -190,6 +212,14 @@ __device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t* r) {
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+// Sixteen lanes of tensor memory, eight 32-bit columns a piece: lane t gets columns 2 (t % 4), + 1 of rows t / 4 (first
+// two registers of a piece) and t / 4 + 8.
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+               : "r"(taddr)
+               : "memory");
+}
 // Instruction descriptor, kind::f16 with fp32 accumulators: operand types at bits 7 and 10 (1: bf16), B transposed
 // (N contiguous in shared memory) at bit 16.
 __host__ __device__ constexpr uint32_t idesc(bool bf16, int m, int n, bool b_n_major) {
@@ -227,7 +257,7 @@ __device__ __forceinline__ void hadamard_row(float (&v)[D]) {
 }
 
 struct TileMaps {
-  CUtensorMap k, v;
+  CUtensorMap q, k, v;
 };
 
 // What a CTA works on at a time.
@@ -237,7 +267,7 @@ struct Span {  // blocks of one half: b0, b0 + step, ... below b1 (b1 <= b0: non
 struct Item {
   int64_t q0;        // first packed query token of the sequence
   int kvh, first;    // key head; position of the sequence's first query token
-  int row0, rows;    // rows of the item within the sequence and head
+  int tok0, toks;    // query tokens of the item within the sequence
   int kv_len;
   int base;          // first key of block 0
   int b, split;
@@ -251,20 +281,18 @@ struct Item {
 // Blocks of n0 .. n1 that half i of the item uses.
 __device__ Span half_span(const AttnArgs& a, const Item& it, int n0, int n1, int i) {
   if (it.joint) return Span{min(n0 + ((n0 & 1) ^ i), n1), n1, 2};  // half 0 the even blocks
-  const int group = a.heads / a.kv_heads;
-  const int r0 = it.row0 + i * kTileRows;
-  const int r1 = min(r0 + kTileRows, it.row0 + it.rows) - 1;
-  const int p0 = it.first + r0 / group, p1 = it.first + r1 / group;
-  const int lo = a.window > 0 ? max(0, p0 - a.window + 1) : 0;
-  if (r1 < r0 || p1 < lo) return Span{n0, n0, 1};
-  const int s0 = max(n0, (lo - it.base) / kBlock), s1 = min(n1, (p1 - it.base) / kBlock + 1);
+  const int t0 = it.tok0 + i * a.tile_tokens;
+  const int t1 = min(t0 + a.tile_tokens, it.tok0 + it.toks) - 1;
+  const int lo = a.window > 0 ? max(0, it.first + t0 - a.window + 1) : 0;
+  if (t1 < t0 || it.first + t1 < lo) return Span{n0, n0, 1};
+  const int s0 = max(n0, (lo - it.base) / kBlock), s1 = min(n1, (it.first + t1 - it.base) / kBlock + 1);
   return s0 < s1 ? Span{s0, s1, 1} : Span{n0, n0, 1};
 }
 
 // The item of CTA index idx (a whole warp); false past the last row tile.
 template <int SRC>
 __device__ bool find_item(const AttnArgs& a, int lane, int64_t idx, Item* it) {
-  const int group = a.heads / a.kv_heads;
+  const int per = 2 * a.tile_tokens;  // tokens of an item
   it->split = (int)(idx % a.splits);
   idx /= a.splits;
   it->kvh = (int)(idx % a.kv_heads);
@@ -280,7 +308,7 @@ __device__ bool find_item(const AttnArgs& a, int lane, int64_t idx, Item* it) {
       const int64_t c1 = a.cu_q[b + 1] > a.total_q ? a.total_q : a.cu_q[b + 1];
       n = c1 > c0 ? c1 - c0 : 0;
     }
-    const int64_t tiles = (n * group + kItemRows - 1) / kItemRows;
+    const int tiles = ((int)n + per - 1) / per;
     int64_t inc = tiles;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -291,15 +319,13 @@ __device__ bool find_item(const AttnArgs& a, int lane, int64_t idx, Item* it) {
     if (hit) {
       const int at = __ffs(hit) - 1;
       const int64_t before = base + __shfl_sync(0xffffffffu, inc - tiles, at);
-      const int64_t count = __shfl_sync(0xffffffffu, tiles, at);
+      const int count = __shfl_sync(0xffffffffu, tiles, at);
       const int q_len = (int)__shfl_sync(0xffffffffu, n, at);
       it->q0 = __shfl_sync(0xffffffffu, c0, at);
       it->b = b0 + at;
       // a sequence's last row tiles see the most keys and go first
-      const int64_t t = count - 1 - (tile - before);
-      it->row0 = (int)(t * kItemRows);
-      const int64_t left = (int64_t)q_len * group - it->row0;
-      it->rows = left < kItemRows ? (int)left : kItemRows;
+      it->tok0 = (count - 1 - (int)(tile - before)) * per;
+      it->toks = min(per, q_len - it->tok0);
       it->kv_len = q_len;
       if constexpr (SRC != kPacked) {
         const int64_t room = (int64_t)a.table_width << a.cache.page_shift;
@@ -307,9 +333,9 @@ __device__ bool find_item(const AttnArgs& a, int lane, int64_t idx, Item* it) {
         it->kv_len = (int)(kl < 0 ? 0 : kl > room ? room : kl);
       }
       it->first = it->kv_len - q_len;
-      it->joint = it->rows <= kTileRows;
-      // keys that the item's first row sees first, and that its last row sees last
-      const int p0 = it->first + it->row0 / group, p1 = it->first + (it->row0 + it->rows - 1) / group;
+      it->joint = it->toks <= a.tile_tokens;
+      // positions of the item's first and last token
+      const int p0 = it->first + it->tok0, p1 = p0 + it->toks - 1;
       int lo = a.window > 0 && p0 - a.window + 1 > 0 ? p0 - a.window + 1 : 0;
       if constexpr (SRC != kPacked) {
         // whole pages (or 128 keys of a larger one), so that a page is never cut by a tile's first key
@@ -361,13 +387,15 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
   uint64_t* jfull = iempty + 2;                          // joint item: half 1's output in shared memory
   uint64_t* jfree = jfull + 1;                           // and read by half 0
   uint64_t* vfix = jfree + 1;                            // [NS] a tail's value rows past the length are zeros
-  uint64_t* clc = vfix + 8;                              // answer to a cancel request
+  uint64_t* qraw = vfix + 8;                             // [2] a half's q as it is (quantised formats: still to be rotated)
+  uint64_t* qempty = qraw + 2;                           // [2] a half's scores of an item are done
+  uint64_t* clc = qempty + 2;                              // answer to a cancel request
   uint64_t* mdrain = clc + 1;                            // [2] MMAs issued before a wait gave up
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mdrain + 2);
-  uint8_t* answer = base + 448;                          // 16 bytes
-  Item* items = reinterpret_cast<Item*>(base + 464);     // [2]
+  uint8_t* answer = base + 480;                          // 16 bytes
+  Item* items = reinterpret_cast<Item*>(base + 496);     // [2]
   float* jlse = reinterpret_cast<float*>(base + 768);    // [128] joint item: log2 of half 1's sums
-  static_assert((2 * 8 + 2 * 4 + 31) * 8 + 4 <= 448 && 464 + 2 * sizeof(Item) <= 768, "control area");
+  static_assert((2 * 8 + 2 * 4 + 35) * 8 + 4 <= 480 && 496 + 2 * sizeof(Item) <= 768, "control area");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int group = a.heads / a.kv_heads;
@@ -382,7 +410,9 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
       mbar_init(&rawempty[s], C::kConverters);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&qfull[i], 4);
+      mbar_init(&qfull[i], C::kQuant ? 4 : 1);
+      mbar_init(&qraw[i], 1);
+      mbar_init(&qempty[i], 1);
       mbar_init(&sfull[2 * i], 1);
       mbar_init(&sfull[2 * i + 1], 1);
       mbar_init(&pvdone[i], 1);
@@ -390,7 +420,7 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
       mbar_init(&pfull[2 * i + 1], 4);
       mbar_init(&ofull[i], 1);
       mbar_init(&ifull[i], 1);
-      mbar_init(&iempty[i], 10 + C::kConverters);
+      mbar_init(&iempty[i], 11 + C::kConverters);
       mbar_init(&mdrain[i], 1);
     }
     mbar_init(jfull, 4);
@@ -425,71 +455,63 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
     const uint32_t s_col = tmem + lanes + 128 * i;  // buffer 0
     const uint32_t o_col = tmem + lanes + 256 + 128 * i;
     const float c = a.scale_log2;
-    // query token (in the sequence) and head of this thread's row; the last row's where there is none
-    auto row_of = [&](const Item& it, int* tok, int* head) {
-      const int row = (it.joint ? 0 : i * kTileRows) + r;
-      const int rr = it.row0 + (row < it.rows ? row : it.rows - 1);
-      *tok = rr / group;
-      *head = it.kvh * group + rr - *tok * group;
-      return row < it.rows;
-    };
-    auto load_q = [&](const Item& it) {
-      int tok, head;
-      const bool there = row_of(it, &tok, &head);
-      const uint16_t* src =
-          static_cast<const uint16_t*>(a.q.data) + (it.q0 + tok) * a.q.token_stride + (int64_t)head * a.q.head_stride;
-      const uint32_t dst = smem_u32(data + C::kQ) + (uint32_t)i * (kTileRows * D * 2);
-      if constexpr (!C::kQuant) {
-        uint4 w[D / 8];
+    // Rotate the half's q where the copy has put it, a thread a row.
+    auto rotate_q = [&](uint32_t parity) {
+      if (!bar_wait(&qraw[i], parity)) return false;
+      const uint32_t at = smem_u32(data + C::kQ) + (uint32_t)i * (kTileRows * D * 2);
+      float v[D];
 #pragma unroll
-        for (int x = 0; x < D / 8; ++x) w[x] = there ? *reinterpret_cast<const uint4*>(src + 8 * x) : make_uint4(0u, 0u, 0u, 0u);
+      for (int x = 0; x < D / 8; ++x) {
+        uint32_t w[4];
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(at + row_chunk(r, x))
+                     : "memory");
 #pragma unroll
-        for (int x = 0; x < D / 8; ++x) sts128(dst + row_chunk(r, x), w[x].x, w[x].y, w[x].z, w[x].w);
-      } else {
-        float v[D];
-#pragma unroll
-        for (int x = 0; x < D / 8; ++x) {
-          const uint4 w = there ? *reinterpret_cast<const uint4*>(src + 8 * x) : make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            if (a.bf16) {
-              v[8 * x + 2 * y] = __uint_as_float(ww[y] << 16);
-              v[8 * x + 2 * y + 1] = __uint_as_float(ww[y] & 0xFFFF0000u);
-            } else {
-              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&ww[y]));
-              v[8 * x + 2 * y] = f.x;
-              v[8 * x + 2 * y + 1] = f.y;
-            }
+        for (int y = 0; y < 4; ++y) {
+          if (a.bf16) {
+            v[8 * x + 2 * y] = __uint_as_float(w[y] << 16);
+            v[8 * x + 2 * y + 1] = __uint_as_float(w[y] & 0xFFFF0000u);
+          } else {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[y]));
+            v[8 * x + 2 * y] = f.x;
+            v[8 * x + 2 * y + 1] = f.y;
           }
         }
-        hadamard_row<D>(v);
+      }
+      hadamard_row<D>(v);
 #pragma unroll
-        for (int x = 0; x < D / 8; ++x) {
-          uint32_t w[4];
+      for (int x = 0; x < D / 8; ++x) {
+        uint32_t w[4];
 #pragma unroll
-          for (int y = 0; y < 4; ++y)
-            w[y] = pack2<false>(v[column_value<SRC>(8 * x + 2 * y)] * (8.0f / D),
-                                v[column_value<SRC>(8 * x + 2 * y + 1)] * (8.0f / D));
-          sts128(dst + row_chunk(r, x), w[0], w[1], w[2], w[3]);
-        }
+        for (int y = 0; y < 4; ++y)
+          w[y] = pack2<false>(v[column_value<SRC>(8 * x + 2 * y)] * (8.0f / D),
+                              v[column_value<SRC>(8 * x + 2 * y + 1)] * (8.0f / D));
+        sts128(at + row_chunk(r, x), w[0], w[1], w[2], w[3]);
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&qfull[i]);
+      return true;
     };
+    auto used = [&](const Item& x) { return i ? x.span[1].b0 < x.span[1].b1 : x.span[0].b0 < x.span[0].b1; };
 
     Item it;
     uint32_t n = 0, jphase = 0;
     uint32_t blocks = 0;  // of this half so far: the buffers and their phases
     uint32_t oph = 0;     // phases of the halves' outputs (a bit a half; an item without blocks of a half has none)
     bool have = read_item(n, &it);
-    auto used = [&](const Item& x) { return i ? x.span[1].b0 < x.span[1].b1 : x.span[0].b0 < x.span[0].b1; };
-    if (have && used(it)) load_q(it);
+    uint32_t qph = 0;
+    // this thread's row: query token (from the half's first) and head (of the group); none past the tile's whole tokens
+    const int row_tok = r / group, row_head = r - row_tok * group;
+    if (C::kQuant && have && used(it)) {
+      have = rotate_q(qph);
+      qph ^= 1u;
+    }
     while (have) {
       bool ok = true;
-      int tok, head;
-      const bool there = row_of(it, &tok, &head);
+      const int tok = it.tok0 + (it.joint ? 0 : i * a.tile_tokens) + row_tok;  // in the sequence
+      const bool there = row_tok < a.tile_tokens && tok < it.tok0 + it.toks;
       const Span sp = i ? it.span[1] : it.span[0];
       const int pos = it.first + tok;
       const int lim = pos - it.base;                                            // last key it sees, from the item's first key
@@ -565,93 +587,167 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
         if (lane == 0) mbar_arrive(&pfull[2 * i + buf]);
       }
 
-      // The next item's q goes in before this item's output is waited for, so that its scores can be computed meanwhile;
-      // after a joint item it goes in last (q's room is its meeting place).
       float l = (l0.x + l0.y) + (l1.x + l1.y);
       Item next;
       have = ok && read_item(n + 1, &next);
+
+      // ---- the rows' output.  Tensor memory is read sixteen rows at a time, a quad of lanes two of them: of rows
+      // g and g + 8 a lane gets columns 8x + 2q, + 1.
+      const int g = lane >> 2, q = lane & 3;
+      // a joint item's meeting place is q's room, of both halves
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (it.span[h].b0 >= it.span[h].b1) continue;
+        if (ok && (h == i || it.joint)) ok = bar_wait(&ofull[h], oph >> h & 1u);
+        oph ^= 1u << h;
+      }
+      tc_fence_after();
+      // this thread's row: its own part times f0, a joint item's other half's (already divided by its sum) times f1
+      float f0 = 1.0f, f1 = 0.0f;
+      if (ok && it.joint && i == 0) {
+        ok = bar_wait(jfull, jphase);
+        const float other = jlse[r];
+        const float both = fmaxf(m, other);
+        // a half without a maximum saw nothing (its sum is 0) or nothing but NaN (its sum is NaN)
+        f0 = m == kNegInf ? (l == 0.0f ? 0.0f : l) : ex2(m - both);
+        f1 = other == kNegInf ? 0.0f : ex2(other - both);
+        l = l * f0 + f1;
+        m = both;
+      }
+      const bool partial = a.splits > 1 && !(it.joint && i == 1);
+      if (!partial) {
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // a row that saw no key gives zeros
+        f0 *= inv, f1 *= inv;
+      }
+      if (!any) f0 = 0.0f;
+      float* jo = reinterpret_cast<float*>(data + C::kQ) + r;  // [D][128]: a thread a column
+      if (ok && it.joint && i == 1) jlse[r] = m + log2f(l);
+      const int64_t row = (it.q0 + tok) * a.heads + it.kvh * group + row_head;
+      if (ok && partial && there) a.part_ml[(int64_t)it.split * a.total_q * a.heads + row] = make_float2(m, l);
 #pragma unroll 1
-      for (int pass = 0; pass < 2; ++pass) {
-        if (have && ok && it.joint == pass && used(next)) load_q(next);
-        if (pass == 1 || !ok) continue;
-        // ---- the row's output
-        float o[D];
+      for (int h = 0; ok && h < 2; ++h) {
+        float o[D / 2];  // o[4x + 2e + y]: row 16h + 8e + g of the warp, column 8x + 2q + y
+        if (any) {
 #pragma unroll
-        for (int x = 0; x < D; ++x) o[x] = 0.0f;
-        // a joint item's meeting place is q's room, of both halves
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (it.span[h].b0 >= it.span[h].b1) continue;
-          if (ok && (h == i || it.joint)) ok = bar_wait(&ofull[h], oph >> h & 1u);
-          oph ^= 1u << h;
-        }
-        if (ok && any) {
-          tc_fence_after();
-#pragma unroll
-          for (int x = 0; x < D; x += 32) tmem_ld_32x32b_x32(o_col + x, *reinterpret_cast<uint32_t(*)[32]>(&o[x]));
+          for (int x = 0; x < D / 2; x += 16)
+            tmem_ld_16x256b_x4(o_col + ((uint32_t)(16 * h) << 16) + 2 * x, *reinterpret_cast<uint32_t(*)[16]>(&o[x]));
           tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int x = 0; x < D / 2; ++x) o[x] = 0.0f;
         }
         if constexpr (C::kQuant) {
-          float v[D];
+          // Back out of the rotated basis.  Column 8x + 2q + y of the operands holds value 8x + 2q + y, or for the 4-bit
+          // codes' order 8x + 4y + q: its bits are this lane's q, y and x.
 #pragma unroll
-          for (int x = 0; x < D; ++x) v[column_value<SRC>(x)] = o[x];
-          hadamard_row<D>(v);
-#pragma unroll
-          for (int x = 0; x < D; ++x) o[x] = v[x] * (8.0f / D);
-        }
-        if (ok && it.joint) {
-          float* jo = reinterpret_cast<float*>(data + C::kQ);  // [D][128]: a thread a column, no bank conflicts
-          if (i == 1) {
-            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll
-            for (int x = 0; x < D; ++x) jo[x * kTileRows + r] = o[x] * inv;
-            jlse[r] = m + log2f(l);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(jfull);
-          } else {
-            ok = bar_wait(jfull, jphase);
-            if (ok) {
-              const float other = jlse[r];
-              const float both = fmaxf(m, other);
-              // a half without a maximum saw nothing (its sum is 0) or nothing but NaN (its sum is NaN)
-              const float f0 = m == kNegInf ? (l == 0.0f ? 0.0f : l) : ex2(m - both);
-              const float f1 = other == kNegInf ? 0.0f : ex2(other - both);
-              l = l * f0 + f1;
-#pragma unroll
-              for (int x = 0; x < D; ++x) o[x] = o[x] * f0 + jo[x * kTileRows + r] * f1;
-              m = both;
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(jfree);
+          for (int x = 0; x < D / 2; x += 2) {
+            const float u = o[x], v = o[x + 1];
+            o[x] = u + v, o[x + 1] = u - v;
           }
-          if (ok) ok = bar_wait(jfree, jphase);
-          jphase ^= 1u;
-        }
-        if (ok && there && !(it.joint && i == 1)) {
-          if (a.splits > 1) {
-            const int64_t prow = ((int64_t)it.split * a.total_q + it.q0 + tok) * a.heads + head;
-            a.part_ml[prow] = make_float2(m, l);
-            if (m != kNegInf) {
-              float4* dst = reinterpret_cast<float4*>(a.part_o + prow * D);
 #pragma unroll
-              for (int x = 0; x < D / 4; ++x) dst[x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+          for (int st = 1; st < 4; st *= 2)
+#pragma unroll
+            for (int x = 0; x < D / 2; ++x) {
+              const float u = __shfl_xor_sync(0xffffffffu, o[x], st);
+              o[x] = (q & st) ? u - o[x] : o[x] + u;
+            }
+#pragma unroll
+          for (int st = 4; st < D / 2; st *= 2)
+#pragma unroll
+            for (int x = 0; x < D / 2; ++x)
+              if (!(x & st)) {
+                const float u = o[x], v = o[x + st];
+                o[x] = u + v, o[x + st] = u - v;
+              }
+#pragma unroll
+          for (int x = 0; x < D / 2; ++x) o[x] *= 8.0f / D;
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int src = 16 * h + 8 * e + g;  // lane whose row this is
+          const float s0 = __shfl_sync(0xffffffffu, f0, src), s1 = __shfl_sync(0xffffffffu, f1, src);
+          const int rtok = __shfl_sync(0xffffffffu, tok, src), rhead = __shfl_sync(0xffffffffu, row_head, src);
+          const bool rthere = __shfl_sync(0xffffffffu, (int)there, src) != 0;
+#pragma unroll
+          for (int x = 2 * e; x < D / 2; x += 4) o[x] *= s0, o[x + 1] *= s0;
+          if (it.joint) {
+            float* at = jo + h * (D / 2) * kTileRows;
+            if (i == 1) {
+#pragma unroll
+              for (int x = 2 * e; x < D / 2; x += 4) at[x * kTileRows] = o[x], at[(x + 1) * kTileRows] = o[x + 1];
+              continue;
+            }
+#pragma unroll
+            for (int x = 2 * e; x < D / 2; x += 4) {
+              o[x] = fmaf(at[x * kTileRows], s1, o[x]);
+              o[x + 1] = fmaf(at[(x + 1) * kTileRows], s1, o[x + 1]);
+            }
+          }
+          if (partial) {
+            float* dst = a.part_o + (((int64_t)it.split * a.total_q + it.q0 + rtok) * a.heads + it.kvh * group + rhead) * D;
+#pragma unroll
+            for (int x = 0; x < D / 8; ++x) {
+              if (!rthere) continue;
+              if constexpr (SRC == kPaged4) {
+                dst[8 * x + q] = o[4 * x + 2 * e];
+                dst[8 * x + 4 + q] = o[4 * x + 2 * e + 1];
+              } else {
+                *reinterpret_cast<float2*>(dst + 8 * x + 2 * q) = make_float2(o[4 * x + 2 * e], o[4 * x + 2 * e + 1]);
+              }
             }
           } else {
-            const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // a row that saw no key gives zeros
-            uint16_t* dst = static_cast<uint16_t*>(a.out) + (it.q0 + tok) * a.out_token_stride + (int64_t)head * a.out_head_stride;
+            uint16_t* dst = static_cast<uint16_t*>(a.out) + (it.q0 + rtok) * a.out_token_stride +
+                            (int64_t)(it.kvh * group + rhead) * a.out_head_stride;
+            const bool to_bf16 = C::kQuant ? a.bf16 != 0 : BF16;
+            auto two = [&](float u, float v) { return to_bf16 ? pack2<true>(u, v) : pack2<false>(u, v); };
 #pragma unroll
-            for (int x = 0; x < D; x += 8) {
+            for (int x = 0; x < D / 8; x += 4) {
+              // four pieces of eight columns; the quad's transpose gives lane q the whole of piece x + q
               uint32_t w[4];
 #pragma unroll
               for (int y = 0; y < 4; ++y) {
-                const float p = o[x + 2 * y] * inv, q = o[x + 2 * y + 1] * inv;
-                w[y] = (C::kQuant ? a.bf16 != 0 : BF16) ? pack2<true>(p, q) : pack2<false>(p, q);
+                float u = o[4 * (x + y) + 2 * e], v = o[4 * (x + y) + 2 * e + 1];
+                if constexpr (SRC == kPaged4) {
+                  // values q and 4 + q of the piece: swap with the neighbour for two next to each other
+                  const float give = (q & 1) ? u : v;
+                  const float take = __shfl_xor_sync(0xffffffffu, give, 1);
+                  if (q & 1) u = take;  // lane 1, 3: values 4 + q - 1, 4 + q
+                  else v = take;        // lane 0, 2: values q, q + 1
+                }
+                w[y] = two(u, v);
               }
-              *reinterpret_cast<uint4*>(dst + x) = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+              for (int st = 1; st < 4; st *= 2)
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                  if (!(y & st)) {
+                    const uint32_t give = (q & st) ? w[y] : w[y + st];
+                    const uint32_t take = __shfl_xor_sync(0xffffffffu, give, st);
+                    if (q & st) w[y] = take;
+                    else w[y + st] = take;
+                  }
+              // w[y]: what lane y had of piece x + q
+              if constexpr (SRC == kPaged4) {
+                // lanes 0 and 2 had values 0, 1 and 2, 3; lanes 1 and 3 values 4, 5 and 6, 7
+                const uint32_t t = w[1];
+                w[1] = w[2], w[2] = t;
+              }
+              if (rthere) *reinterpret_cast<uint4*>(dst + 8 * (x + q)) = make_uint4(w[0], w[1], w[2], w[3]);
             }
           }
         }
-        tc_fence_before();
+      }
+      if (it.joint) {
+        fence_proxy_async_smem();  // the next q is copied over what was written and read here
+        __syncwarp();
+        if (lane == 0) mbar_arrive(i ? jfull : jfree);
+        if (ok && i == 1) ok = bar_wait(jfree, jphase);
+        jphase ^= 1u;
+      }
+      tc_fence_before();
+      if (C::kQuant && ok && have && used(next)) {
+        ok = rotate_q(qph);
+        qph ^= 1u;
       }
       have = have && ok;
       it = next;
@@ -698,7 +794,7 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
           for (; ok && kt < upto; ++kt, ++vt) {
 #pragma unroll
             for (int value = 0; value < 2; ++value) {
-              ok = bar_wait(&kvfull[slot[value]], sph[value]) && ok;
+              ok = bar_wait<true>(&kvfull[slot[value]], sph[value]) && ok;
               if (one) mbar_arrive(&kvempty[slot[value]]);
               if (value && vt == tail) fph ^= 1u << slot[1];
               next_slot(value);
@@ -708,7 +804,7 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
         };
         skip(b0 < b1 ? b0 >> 1 : jhi);
         if (b0 < b1) {
-          ok = bar_wait(&qfull[i], qph) && ok;
+          ok = bar_wait<true>(&qfull[i], qph) && ok;
           qph ^= 1u;
         }
         // Scores run a block ahead of weights times values: turn b has the scores of block b and the values of the one
@@ -717,7 +813,7 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
         for (int b = b0; b < b1 + step && b0 < b1; b += step) {
           if (b < b1) {
             const uint32_t s = slot[0], buf = blocks & 1u;
-            ok = bar_wait(&kvfull[s], sph[0]) && ok;
+            ok = bar_wait<true>(&kvfull[s], sph[0]) && ok;
             tc_fence_after();
             const uint64_t kd = kd0 + (uint64_t)(s * (C::kSlot >> 4) + (b & 1) * (kBlock * 128 >> 4));
 #pragma unroll
@@ -728,6 +824,7 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
               __syncwarp();
             }
             if (one) tc_commit(&sfull[2 * i + buf]);
+            if (b + step >= b1 && one) tc_commit(&qempty[i]);
             if (b + step >= b1 || (b + step) >> 1 != b >> 1) {  // the tile's last scores
               if (one) tc_commit(&kvempty[s]);
               next_slot(0);
@@ -738,14 +835,14 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
           if (b > b0) {
             const int pb = b - step;
             const uint32_t s = slot[1], g = blocks - 1, buf = g & 1u;
-            ok = bar_wait(&kvfull[s], sph[1]) && ok;
-            if (!C::kQuant && vt == tail) ok = bar_wait(&vfix[s], fph >> s & 1u) && ok;
+            ok = bar_wait<true>(&kvfull[s], sph[1]) && ok;
+            if (!C::kQuant && vt == tail) ok = bar_wait<true>(&vfix[s], fph >> s & 1u) && ok;
             // keys past the length take no part: whole steps of 16 are left out
             const int steps = (min(kBlock, keys - pb * kBlock) + 15) >> 4;
             const uint64_t vd = vd0 + (uint64_t)(s * (C::kSlot >> 4) + (pb & 1) * (kBlock * 128 >> 4));
             const uint32_t pd = tm + kBlock * buf;
             const bool held = pb > b0;
-            ok = bar_wait(&pfull[2 * i + buf], g >> 1 & 1u) && ok;
+            ok = bar_wait<true>(&pfull[2 * i + buf], g >> 1 & 1u) && ok;
             tc_fence_after();
             if (steps == 4) {
 #pragma unroll
@@ -785,7 +882,7 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
         // what was issued must be done before the CTA's memory goes
         if (one) tc_commit(&mdrain[i]);
         __syncwarp();
-        bar_wait(&mdrain[i], 0u);
+        bar_wait<true>(&mdrain[i], 0u);
       }
       tc_fence_before();
     } else if (warp == 9) {
@@ -907,6 +1004,40 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
         __syncwarp();
       }
       drain_ring(full, NR, filled);
+    } else if (warp == 11) {
+      // ---------------- copies of q ----------------
+      uint64_t* landed = C::kQuant ? qraw : qfull;
+      const uint32_t bytes = (uint32_t)(a.tile_tokens * group * D * 2);
+      if (lane == 0) prefetch_tensormap(&maps.q);
+      bool ok = true;
+      Item it;
+      uint32_t n = 0, eph = 3u, jph = 0, filled[2] = {0u, 0u};  // eph: phases of qempty (a bit a half); nothing to wait for at first
+      bool joint = false;                                       // the item before
+      while (ok && read_item(n, &it)) {
+        ++n;
+        if (joint) {
+          ok = bar_wait(jfree, jph);
+          jph ^= 1u;
+        }
+        joint = it.joint != 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (!ok || it.span[i].b0 >= it.span[i].b1) continue;
+          ok = bar_wait(&qempty[i], eph >> i & 1u);
+          eph ^= 1u << i;
+          if (ok && lane == 0) {
+            mbar_arrive_expect_tx(&landed[i], bytes);
+            const int tok = (int)it.q0 + it.tok0 + (it.joint ? 0 : i * a.tile_tokens);
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h)
+              tma_tile3d_g2s(data + C::kQ + i * (kTileRows * D * 2) + h * (kTileRows * 128), &maps.q, 64 * h, it.kvh * group, tok,
+                             &landed[i]);
+          }
+          ++filled[i];
+          __syncwarp();
+        }
+      }
+      for (int i = 0; i < 2; ++i) drain_ring(&landed[i], 1, filled[i]);
     }
   } else if constexpr (C::kQuant) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kConvertRegs));
@@ -1042,14 +1173,14 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// Rows of D 16-bit values as 3-D {D, heads, tokens}; a copy takes 64 columns of box_rows tokens of one head.
+// Rows of D 16-bit values as 3-D {D, heads, tokens}; a copy takes 64 columns of box_tokens tokens of box_heads heads.
 cudaError_t make_map(CUtensorMap* map, const void* data, int d, int64_t heads, int64_t tokens, int64_t head_stride,
-                     int64_t token_stride, int box_rows) {
+                     int64_t token_stride, int box_heads, int box_tokens) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
   if (enc == nullptr) return cudaErrorNotSupported;
   cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)tokens};
   cuuint64_t strides[2] = {(cuuint64_t)head_stride * 2, (cuuint64_t)token_stride * 2};
-  cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows};
+  cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_tokens};
   cuuint32_t estr[3] = {1, 1, 1};
   const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(data), dims, strides, box, estr,
                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -1061,23 +1192,24 @@ template <int D, int SRC, bool BF16>
 cudaError_t launch_tile(const AttnArgs& a, cudaStream_t stream) {
   using C = TileCfg<D, SRC>;
   TileMaps maps = {};
-  cudaError_t e = cudaSuccess;
+  const int group = a.heads / a.kv_heads;
+  cudaError_t e = make_map(&maps.q, a.q.data, D, a.heads, a.total_q, a.q.head_stride, a.q.token_stride, group, a.tile_tokens);
+  if (e != cudaSuccess) return e;
   if constexpr (SRC == kPacked) {
-    e = make_map(&maps.k, a.k.data, D, a.kv_heads, a.total_q, a.k.head_stride, a.k.token_stride, kKeys);
-    if (e == cudaSuccess) e = make_map(&maps.v, a.v.data, D, a.kv_heads, a.total_q, a.v.head_stride, a.v.token_stride, kKeys);
+    e = make_map(&maps.k, a.k.data, D, a.kv_heads, a.total_q, a.k.head_stride, a.k.token_stride, 1, kKeys);
+    if (e == cudaSuccess) e = make_map(&maps.v, a.v.data, D, a.kv_heads, a.total_q, a.v.head_stride, a.v.token_stride, 1, kKeys);
   } else if constexpr (SRC == kPaged16) {
     const int64_t rows = (a.cache.num_pages * a.kv_heads) << a.cache.page_shift;
     const int box = a.cache.page_shift < 7 ? 1 << a.cache.page_shift : kKeys;
-    e = make_map(&maps.k, a.cache.k, D, 1, rows, D, D, box);
-    if (e == cudaSuccess) e = make_map(&maps.v, a.cache.v, D, 1, rows, D, D, box);
+    e = make_map(&maps.k, a.cache.k, D, 1, rows, D, D, 1, box);
+    if (e == cudaSuccess) e = make_map(&maps.v, a.cache.v, D, 1, rows, D, D, 1, box);
   }
   if (e != cudaSuccess) return e;
   // the register split waits for registers that a launch with fewer would never have
   e = allow_smem<attn_tile_kernel<D, SRC, BF16>>(C::kSmem, C::kLaunchRegs);
   if (e != cudaSuccess) return e;
-  // row tiles: no more than all rows' and one partly filled for each sequence
-  const int64_t group = a.heads / a.kv_heads;
-  const int64_t tiles = a.total_q * group / kItemRows + (a.total_q < a.batch ? a.total_q : a.batch);
+  // items: no more than all tokens' and one partly filled for each sequence
+  const int64_t tiles = a.total_q / (2 * a.tile_tokens) + (a.total_q < a.batch ? a.total_q : a.batch);
   const int64_t blocks = tiles * a.kv_heads * a.splits;
   if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   attn_tile_kernel<D, SRC, BF16><<<(unsigned)blocks, C::kThreads, C::kSmem, stream>>>(maps, a);

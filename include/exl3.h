@@ -415,7 +415,7 @@ exl3_status_t exl3_attention_prompt(const exl3_heads_t* q, const exl3_heads_t* k
  * If a kernel gives up on a bounded wait (exl3_device_status reports it), out is undefined.
  */
 size_t exl3_attention_paged_workspace_bytes(int64_t total_q, int32_t batch, int32_t q_heads, int32_t kv_heads,
-                                            int32_t head_dim, int32_t max_q, int32_t max_kv);
+                                            int32_t head_dim, int32_t max_q, int32_t max_kv, int32_t window);
 exl3_status_t exl3_attention_paged(const exl3_heads_t* q, exl3_dtype_t dtype, int64_t total_q, int32_t q_heads,
                                    const exl3_kv_cache_t* cache, const int32_t* block_table, int32_t table_width,
                                    const int32_t* cu_q, const int32_t* kv_lens, int32_t batch, int32_t max_q,

@@ -49,6 +49,20 @@ def test_prompt(dtype, dim, lens, heads, kv):
     prompt(lens, heads, kv, dim, dtype)
 
 
+@pytest.mark.parametrize("dim,heads,kv", [(128, 8, 8), (64, 12, 2)])
+def test_prompt_many_items(dim, heads, kv):
+    """Several row tiles for every SM, of all kinds: whole, half filled, single rows."""
+    prompt([300, 1, 77, 130, 64, 513, 2, 129] * 8, heads, kv, dim, "bf16")
+
+
+@pytest.mark.parametrize("fmt,dtype", [("bf16", "bf16"), ("int8", "bf16"), ("int4", "f16")])
+def test_paged_many_items(fmt, dtype):
+    q_lens = [200, 1, 65, 130, 3, 40] * 8
+    kv_lens = [200, 300, 65, 700, 1, 500] * 8
+    paged(q_lens, kv_lens, 16, 8, 128, 32, fmt, dtype)
+    paged(q_lens, kv_lens, 16, 8, 64, 16, fmt, dtype, window=90)
+
+
 @pytest.mark.parametrize("window", [1, 2, 16, 100, 128, 129, 300, 5000])
 @pytest.mark.parametrize("heads,kv", [(2, 2), (7, 1)])
 def test_prompt_window(window, heads, kv):
