@@ -17,9 +17,14 @@
 // are (only q and the output are rotated).  Read back: H_D(codes) is a sum of
 // integers below 2^24, exact in fp32 in any order, times scale * 8 / D.
 //
-// Bound by DRAM on long calls, by the launch on short ones.  D/8 lanes hold a
-// row (one 16-byte load each), a block one token: its D/2 sines and cosines are
-// computed once and shared by all its heads.
+// Bound by DRAM on long calls, by the launch on short ones; between them the
+// instructions count (a first version spent 300 on a pair of rows in a warp and
+// took 126 us where it now takes 62: 16381 tokens, 32 query and 8 key heads, 4
+// bits).  So: D/8 lanes hold a row, two rows a warp; a block takes one token, whose
+// D/2 sines and cosines are computed once and stay in registers for all its
+// query rows; a lane holds both values of its pairs; a stage of the transform
+// across lanes is a shuffle and a multiply-add by +-1; codes come out of the low
+// bits of a sum with 1.5 * 2^23 and go back the same way.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -77,17 +82,65 @@ __device__ __forceinline__ void hadamard_lanes(float (&v)[8], int lane) {
   }
 #pragma unroll
   for (int s = 1; s < D / 8; s *= 2) {
-    const bool upper = (lane & s) != 0;
+    const float sign = (lane & s) != 0 ? -1.0f : 1.0f;  // exact: the sum or the difference, rounded once
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float o = __shfl_xor_sync(0xffffffffu, v[i], s);
-      v[i] = upper ? o - v[i] : v[i] + o;
-    }
+    for (int i = 0; i < 8; ++i) v[i] = fmaf(v[i], sign, __shfl_xor_sync(0xffffffffu, v[i], s));
   }
+}
+// The larger magnitude, or NaN if either is.
+__device__ __forceinline__ float max_mag(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(fabsf(b)));
+  return y;
+}
+
+// A row's eight values a lane (all lanes of the warp come here) quantised into
+// row `row` of a cache side; nothing is stored where `keep` is false.
+template <int D>
+__device__ __forceinline__ void quantise_row(float (&v)[8], int l, bool int8, uint8_t* dst, uint16_t* scales, int64_t row,
+                                             bool keep) {
+  hadamard_lanes<D>(v, threadIdx.x);
+  float top = fabsf(v[0]);
+#pragma unroll
+  for (int j = 1; j < 8; ++j) top = max_mag(top, v[j]);
+#pragma unroll
+  for (int s = 1; s < D / 8; s *= 2) top = max_mag(top, __shfl_xor_sync(0xffffffffu, top, s));
+  const bool finite = top < __builtin_huge_valf();
+  // y = v / 8: the eighth goes into the maximum and the reciprocal, exactly
+  top *= 0.125f;
+  float scale = __fmul_rn(top, int8 ? 1.0f / 127.0f : 1.0f / 7.0f);
+  scale = __uint_as_float((__float_as_uint(scale) + 0xFFFFu) & 0xFFFF0000u);  // up, so that no code passes the top
+  scale = fmaxf(scale, 7.888609052210118e-31f);                               // 2^-100: its reciprocal is finite
+  if (top == 0.0f) scale = 1.0f;
+  const float inv = __fdiv_rn(1.0f, scale) * 0.125f;
+  // the product, rounded, plus 1.5 * 2^23 (and the offset): rounded to an integer in the low bits
+  const float magic = int8 ? 12582912.0f + 128.0f : 12582912.0f + 8.0f;
+  uint32_t c[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) c[j] = __float_as_uint(__fadd_rn(__fmul_rn(v[j], inv), magic));
+  uint32_t lo = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+  uint32_t hi = __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410);
+  if (!finite) lo = hi = int8 ? 0x80808080u : 0x08080808u;
+  if (!keep) return;
+  if (int8) {
+    *reinterpret_cast<uint2*>(dst + row * D + 8 * l) = make_uint2(lo, hi);
+  } else {
+    lo &= 0x0F0F0F0Fu, hi &= 0x0F0F0F0Fu;
+    *reinterpret_cast<uint32_t*>(dst + row * (D / 2) + 4 * l) = __byte_perm(lo | lo >> 4, hi | hi >> 4, 0x6420);
+  }
+  // a row with a value that is not finite reads back as NaN
+  if (l == 0) scales[row] = finite ? (uint16_t)(__float_as_uint(scale) >> 16) : (uint16_t)0x7FC0u;
+}
+
+// Rotation of the pair (a, b), products and sums rounded one by one.
+__device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
+  const float p = a, q = b;
+  a = __fsub_rn(__fmul_rn(p, c), __fmul_rn(q, s));
+  b = __fadd_rn(__fmul_rn(q, c), __fmul_rn(p, s));
 }
 
 template <int D>
-__global__ void __launch_bounds__(kRopeThreads) rope_write_kernel(const RopeWriteArgs a, int rows_per_block) {
+__global__ void __launch_bounds__(kRopeThreads) rope_write_kernel(const RopeWriteArgs a, int units_per_block) {
   constexpr int LANES = D / 8;
   constexpr int GROUPS = kRopeThreads / LANES;
   __shared__ __align__(16) float cs[D / 2], sn[D / 2];
@@ -96,11 +149,32 @@ __global__ void __launch_bounds__(kRopeThreads) rope_write_kernel(const RopeWrit
   const int group = threadIdx.x / LANES;
   const bool bf16 = a.bf16 != 0;
   const int half = a.rope.rot_dim >> 1;
-  const int rows = a.x_heads + 2 * a.kv_heads;
-  const int row0 = blockIdx.y * rows_per_block;
-  const int row1 = min(rows, row0 + rows_per_block);
+  const bool pairs = a.rope.interleaved != 0 || half == 0;  // a lane's eight values lie next to each other
+  // where the row's values lie that this lane rotates: both of each pair
+  const bool turns = 4 * l < half;
+  const int at0 = !pairs && turns ? 4 * l : 8 * l;
+  const int at1 = !pairs && turns ? half + 4 * l : 8 * l + 4;
 
-  // where the row's key or value goes; nowhere for a negative or too large slot
+  // this block's units of GROUPS rows: of x, then of keys, then of values (a unit is of one kind)
+  const int xu = (a.x_heads + GROUPS - 1) / GROUPS, ku = (a.kv_heads + GROUPS - 1) / GROUPS;
+  const int u0 = blockIdx.y * units_per_block, u1 = min(xu + 2 * ku, u0 + units_per_block);
+
+  const uint16_t* x = static_cast<const uint16_t*>(a.x.data) + t * a.x.token_stride;
+  uint2 raw[kRopeBatch][2];
+  auto load_x = [&](int u) {
+#pragma unroll
+    for (int i = 0; i < kRopeBatch; ++i) {
+      const int r = (u + i) * GROUPS + group;
+      raw[i][0] = raw[i][1] = make_uint2(0u, 0u);
+      if (u + i < min(xu, u1) && r < a.x_heads) {
+        raw[i][0] = *reinterpret_cast<const uint2*>(x + (int64_t)r * a.x.head_stride + at0);
+        raw[i][1] = *reinterpret_cast<const uint2*>(x + (int64_t)r * a.x.head_stride + at1);
+      }
+    }
+  };
+  load_x(u0);
+
+  // where the keys and values go; nowhere for a negative or too large slot
   int64_t page = -1;
   int off = 0;
   if (a.kv_heads > 0) {
@@ -110,202 +184,186 @@ __global__ void __launch_bounds__(kRopeThreads) rope_write_kernel(const RopeWrit
       off = (int)(slot & ((1 << a.cache.page_shift) - 1));
     }
   }
+  // the first keys and values are in flight too while the sines and cosines are computed
+  const int ku0 = max(u0, xu);
+  auto load_kv = [&](int u) {
+    const bool isk = u < xu + ku;
+    const int h = (isk ? u - xu : u - xu - ku) * GROUPS + group;
+    const HeadsView& src = isk ? a.k : a.v;
+    if (u >= u1 || h >= a.kv_heads || page < 0) return make_uint4(0u, 0u, 0u, 0u);
+    return *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(src.data) + t * src.token_stride +
+                                           (int64_t)h * src.head_stride + 8 * l);
+  };
+  uint4 next = load_kv(ku0);
 
-  bool table = half == 0;  // whether the block's sines and cosines are there
-  for (int base = row0; base < row1; base += GROUPS * kRopeBatch) {
-    uint4 raw[kRopeBatch];
+  if ((int)threadIdx.x < half) {
+    const uint64_t turned = (uint64_t)(int64_t)a.rope.positions[t] * a.rope.phases[threadIdx.x];
+    const float angle = __fmul_rn((float)(int32_t)(turned >> 32), 1.46291807926715968e-9f);  // pi / 2^31
+    cs[threadIdx.x] = __fmul_rn(cosf(angle), a.rope.amplitude);
+    sn[threadIdx.x] = __fmul_rn(sinf(angle), a.rope.amplitude);
+  }
+  __syncthreads();
+
+  if (u0 < xu) {
+    float c[4], s[4];
 #pragma unroll
-    for (int i = 0; i < kRopeBatch; ++i) {
-      const int r = base + i * GROUPS + group;
-      raw[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (r < row1) {
-        const bool isx = r < a.x_heads;
-        const bool isk = r < a.x_heads + a.kv_heads;
-        const HeadsView& src = isx ? a.x : isk ? a.k : a.v;
-        const int h = isx ? r : isk ? r - a.x_heads : r - a.x_heads - a.kv_heads;
-        raw[i] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(src.data) + t * src.token_stride +
-                                                 h * src.head_stride + 8 * l);
-      }
-    }
-    if (!table) {
-      // the loads above are in flight while these are computed
-      if ((int)threadIdx.x < half) {
-        const uint64_t turn = (uint64_t)(int64_t)a.rope.positions[t] * a.rope.phases[threadIdx.x];
-        const float angle = __fmul_rn((float)(int32_t)(turn >> 32), 1.46291807926715968e-9f);  // pi / 2^31
-        cs[threadIdx.x] = __fmul_rn(cosf(angle), a.rope.amplitude);
-        sn[threadIdx.x] = __fmul_rn(sinf(angle), a.rope.amplitude);
-      }
-      __syncthreads();
-      table = true;
-    }
+    for (int j = 0; j < 4; ++j) c[j] = turns ? cs[4 * l + j] : 1.0f, s[j] = turns ? sn[4 * l + j] : 0.0f;
+    uint16_t* out = static_cast<uint16_t*>(a.out) + t * a.out_token_stride;
+    for (int u = u0; u < min(xu, u1); u += kRopeBatch) {
+      if (u > u0) load_x(u);
 #pragma unroll
-    for (int i = 0; i < kRopeBatch; ++i) {
-      const int r = base + i * GROUPS + group;
-      if (base + i * GROUPS >= row1) break;  // alike in the whole block
-      const bool there = r < row1;
-      const bool isx = r < a.x_heads;
-      const bool isk = !isx && r < a.x_heads + a.kv_heads;
-      float v[8];
-      unpack8(raw[i], bf16, v);
-      if (half > 0) {
-        // a key or query row's first 2 * half values turn
-        const bool turns = (isx || isk) && 8 * l < 2 * half;
-        if (a.rope.interleaved) {
-          if (turns) {
+      for (int i = 0; i < kRopeBatch; ++i) {
+        const int r = (u + i) * GROUPS + group;
+        if (u + i >= min(xu, u1) || r >= a.x_heads) break;
+        uint4 w = make_uint4(raw[i][0].x, raw[i][0].y, raw[i][1].x, raw[i][1].y);
+        if (turns) {
+          float v[8];
+          unpack8(w, bf16, v);
+          if (pairs) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float c = cs[4 * l + j], s = sn[4 * l + j];
-              const float p = v[2 * j], q = v[2 * j + 1];
-              v[2 * j] = __fsub_rn(__fmul_rn(p, c), __fmul_rn(q, s));
-              v[2 * j + 1] = __fadd_rn(__fmul_rn(q, c), __fmul_rn(p, s));
-            }
+            for (int j = 0; j < 4; ++j) turn(v[2 * j], v[2 * j + 1], c[j], s[j]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) turn(v[j], v[4 + j], c[j], s[j]);
           }
-        } else {
-          const int hl = half >> 3;  // lanes of one half
-          const bool upper = l >= hl;
-          const int lane = threadIdx.x & 31;
-          const int partner = turns ? (upper ? lane - hl : lane + hl) : lane;
-          const int f = 8 * (upper ? l - hl : l);
+          w = pack8(v, bf16);
+        }
+        *reinterpret_cast<uint2*>(out + (int64_t)r * a.out_head_stride + at0) = make_uint2(w.x, w.y);
+        *reinterpret_cast<uint2*>(out + (int64_t)r * a.out_head_stride + at1) = make_uint2(w.z, w.w);
+      }
+    }
+  }
+  if (page < 0) return;  // alike in the whole block
+
+  for (int u = ku0; u < u1; ++u) {
+    uint4 w = next;
+    next = load_kv(u + 1);
+    const bool isk = u < xu + ku;
+    const int h = (isk ? u - xu : u - xu - ku) * GROUPS + group;
+    const bool there = h < a.kv_heads;
+    if (isk && half > 0) {
+      const bool in = 8 * l < 2 * half;
+      float v[8];
+      unpack8(w, bf16, v);
+      if (pairs) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (in) turn(v[2 * j], v[2 * j + 1], cs[4 * l + j], sn[4 * l + j]);
+      } else {
+        const int hl = half >> 3;  // lanes of one half
+        const bool upper = l >= hl;
+        const int lane = threadIdx.x & 31;
+        const int partner = in ? (upper ? lane - hl : lane + hl) : lane;
+        const int f = 8 * (upper ? l - hl : l);
+        float o[8];
+        unpack8(make_uint4(__shfl_sync(0xffffffffu, w.x, partner), __shfl_sync(0xffffffffu, w.y, partner),
+                           __shfl_sync(0xffffffffu, w.z, partner), __shfl_sync(0xffffffffu, w.w, partner)),
+                bf16, o);
+        if (in) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const float o = __shfl_sync(0xffffffffu, v[j], partner);
-            if (turns) {
-              const float c = cs[f + j], s = sn[f + j];
-              v[j] = upper ? __fadd_rn(__fmul_rn(v[j], c), __fmul_rn(o, s))
-                           : __fsub_rn(__fmul_rn(v[j], c), __fmul_rn(o, s));
-            }
+            const float c = cs[f + j], s = sn[f + j];
+            v[j] = upper ? __fadd_rn(__fmul_rn(v[j], c), __fmul_rn(o[j], s)) : __fsub_rn(__fmul_rn(v[j], c), __fmul_rn(o[j], s));
           }
         }
       }
-      // a row that does not turn keeps its bits (a NaN's too)
-      const uint4 packed = half > 0 && (isx || isk) ? pack8(v, bf16) : raw[i];
-      if (there && isx) {
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + t * a.out_token_stride + r * a.out_head_stride +
-                                  8 * l) = packed;
-      }
-      const bool keep = there && !isx && page >= 0;
-      if (!__any_sync(0xffffffffu, keep)) continue;
-      const int h = r - a.x_heads - (isk ? 0 : a.kv_heads);
-      const int64_t row = keep ? ((page * a.kv_heads + h) << a.cache.page_shift) + off : 0;
-      uint8_t* dst = isk ? a.cache.k : a.cache.v;
-      if (!kv_quantised(a.cache.format)) {
-        if (keep) *reinterpret_cast<uint4*>(dst + row * (2 * D) + 16 * l) = packed;
-        continue;
-      }
-      unpack8(packed, bf16, v);  // the row as its type holds it is what gets quantised
-      hadamard_lanes<D>(v, threadIdx.x);
-      uint32_t top = 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        v[j] = __fmul_rn(v[j], 0.125f);
-        top = max(top, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-      }
-#pragma unroll
-      for (int s = 1; s < LANES; s *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, s));
-      const bool int8 = a.cache.format == kKvInt8;
-      const float most = int8 ? 127.0f : 7.0f;
-      float scale = __fmul_rn(__uint_as_float(top), int8 ? 1.0f / 127.0f : 1.0f / 7.0f);
-      scale = __uint_as_float((__float_as_uint(scale) + 0xFFFFu) & 0xFFFF0000u);  // up, so that no code passes the top
-      scale = fmaxf(scale, 7.888609052210118e-31f);                               // 2^-100: its reciprocal is finite
-      if (top == 0u) scale = 1.0f;
-      const bool finite = top < 0x7F800000u;
-      const float inv = __fdiv_rn(1.0f, scale);
-      uint32_t code[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float c = fminf(fmaxf(rintf(__fmul_rn(v[j], inv)), -most), most);
-        code[j] = (uint32_t)((finite ? (int)c : 0) + (int8 ? 128 : 8));
-      }
-      if (keep) {
-        if (int8) {
-          uint2 w;
-          w.x = code[0] | code[1] << 8 | code[2] << 16 | code[3] << 24;
-          w.y = code[4] | code[5] << 8 | code[6] << 16 | code[7] << 24;
-          *reinterpret_cast<uint2*>(dst + row * D + 8 * l) = w;
-        } else {
-          uint32_t w = 0;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) w |= code[j] << (4 * j);
-          *reinterpret_cast<uint32_t*>(dst + row * (D / 2) + 4 * l) = w;
-        }
-        // a row with a value that is not finite reads back as NaN
-        if (l == 0)
-          (isk ? a.cache.k_scale : a.cache.v_scale)[row] =
-              finite ? (uint16_t)(__float_as_uint(scale) >> 16) : (uint16_t)0x7FC0u;
-      }
+      if (in) w = pack8(v, bf16);
+    }
+    const int64_t row = there ? ((page * a.kv_heads + h) << a.cache.page_shift) + off : 0;
+    uint8_t* dst = isk ? a.cache.k : a.cache.v;
+    if (!kv_quantised(a.cache.format)) {
+      if (there) *reinterpret_cast<uint4*>(dst + row * (2 * D) + 16 * l) = w;
+    } else {
+      float v[8];
+      unpack8(w, bf16, v);  // the row as its type holds it is what gets quantised
+      quantise_row<D>(v, l, a.cache.format == kKvInt8, dst, isk ? a.cache.k_scale : a.cache.v_scale, row, there);
     }
   }
 }
 
+// Rows of whole tokens a block: keys, then values of each.
 template <int D>
-__global__ void __launch_bounds__(kRopeThreads) kv_read_kernel(const KvReadArgs a) {
+__global__ void __launch_bounds__(kRopeThreads) kv_read_kernel(const KvReadArgs a, int tokens_per_block) {
   constexpr int LANES = D / 8;
-  const int l = threadIdx.x % LANES;
+  constexpr int GROUPS = kRopeThreads / LANES;
+  const int l = threadIdx.x % LANES, group = threadIdx.x / LANES;
   const bool bf16 = a.bf16 != 0;
   const int kvh = a.cache.kv_heads;
-  const int per = 2 * kvh;  // rows of a token: its keys, then its values
-  const int64_t rows = a.tokens * per;
-  const int64_t groups = (int64_t)gridDim.x * (kRopeThreads / LANES);
+  const int per = 2 * kvh;  // rows of a token
+  const int64_t t0 = (int64_t)blockIdx.x * tokens_per_block;
+  const int rows = (int)min((int64_t)tokens_per_block, a.tokens - t0) * per;
   const int64_t limit = a.cache.num_pages << a.cache.page_shift;
-  const int64_t first = (int64_t)blockIdx.x * (kRopeThreads / LANES);  // a whole block takes the same passes
-  for (int64_t base = first; base < rows; base += groups * kRopeBatch) {
+  const bool int8 = a.cache.format == kKvInt8, quant = kv_quantised(a.cache.format);
+  for (int base = 0; base < rows; base += GROUPS * kRopeBatch) {
     uint4 raw[kRopeBatch];
     float scale[kRopeBatch];
+    bool in[kRopeBatch];
+    int tok[kRopeBatch], which[kRopeBatch];
 #pragma unroll
     for (int i = 0; i < kRopeBatch; ++i) {
-      const int64_t r = base + i * groups + threadIdx.x / LANES;
+      const int r = base + i * GROUPS + group;
       raw[i] = make_uint4(0u, 0u, 0u, 0u);
-      scale[i] = -1.0f;  // no row: zeros
+      scale[i] = 0.0f;
+      in[i] = false;
+      tok[i] = tokens_per_block == 1 ? 0 : r / per;
+      which[i] = r - tok[i] * per;
       if (r < rows) {
-        const int64_t t = r / per;
-        const int w = (int)(r - t * per);
-        const int64_t slot = a.slots[t];
+        const int64_t slot = a.slots[t0 + tok[i]];
         if (slot >= 0 && slot < limit) {
-          const int h = w < kvh ? w : w - kvh;
-          const int64_t row = (((slot >> a.cache.page_shift) * kvh + h) << a.cache.page_shift) +
+          in[i] = true;
+          const bool isk = which[i] < kvh;
+          const int64_t row = (((slot >> a.cache.page_shift) * kvh + (isk ? which[i] : which[i] - kvh)) << a.cache.page_shift) +
                               (slot & ((1 << a.cache.page_shift) - 1));
-          const uint8_t* src = w < kvh ? a.cache.k : a.cache.v;
-          if (a.cache.format == kKvInt8) {
+          const uint8_t* src = isk ? a.cache.k : a.cache.v;
+          if (int8) {
             const uint2 c = *reinterpret_cast<const uint2*>(src + row * D + 8 * l);
             raw[i].x = c.x;
             raw[i].y = c.y;
-          } else if (a.cache.format == kKvInt4) {
+          } else if (quant) {
             raw[i].x = *reinterpret_cast<const uint32_t*>(src + row * (D / 2) + 4 * l);
           } else {
             raw[i] = *reinterpret_cast<const uint4*>(src + row * (2 * D) + 16 * l);
           }
-          scale[i] = 1.0f;
-          if (kv_quantised(a.cache.format))
-            scale[i] = __uint_as_float((uint32_t)(w < kvh ? a.cache.k_scale : a.cache.v_scale)[row] << 16);
+          if (quant) scale[i] = __uint_as_float((uint32_t)(isk ? a.cache.k_scale : a.cache.v_scale)[row] << 16);
         }
       }
     }
 #pragma unroll
     for (int i = 0; i < kRopeBatch; ++i) {
-      if (base + i * groups >= rows) break;  // alike in the whole block
-      const int64_t r = base + i * groups + threadIdx.x / LANES;
-      float v[8];
-      const bool none = scale[i] == -1.0f;
-      if (kv_quantised(a.cache.format)) {
-        const bool int8 = a.cache.format == kKvInt8;
+      if (base + i * GROUPS >= rows) break;  // alike in the whole block
+      uint4 w = raw[i];
+      if (quant) {
+        // a code in the low byte of 2^23, less 2^23 and the offset
+        float v[8];
+        if (int8) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint32_t c = int8 ? ((j < 4 ? raw[i].x : raw[i].y) >> (8 * (j & 3))) & 255u : (raw[i].x >> (4 * j)) & 15u;
-          v[j] = (float)((int)c - (int8 ? 128 : 8));
+          for (int j = 0; j < 4; ++j) {
+            v[j] = __uint_as_float(__byte_perm(w.x, 0x4B000000u, 0x7540 + j)) - (8388608.0f + 128.0f);
+            v[4 + j] = __uint_as_float(__byte_perm(w.y, 0x4B000000u, 0x7540 + j)) - (8388608.0f + 128.0f);
+          }
+        } else {
+          const uint32_t even = w.x & 0x0F0F0F0Fu, odd = w.x >> 4 & 0x0F0F0F0Fu;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            v[2 * j] = __uint_as_float(__byte_perm(even, 0x4B000000u, 0x7540 + j)) - (8388608.0f + 8.0f);
+            v[2 * j + 1] = __uint_as_float(__byte_perm(odd, 0x4B000000u, 0x7540 + j)) - (8388608.0f + 8.0f);
+          }
         }
         hadamard_lanes<D>(v, threadIdx.x);
         const float s = __fmul_rn(scale[i], 8.0f / D);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = none ? 0.0f : __fmul_rn(v[j], s);
-      } else {
-        unpack8(raw[i], a.cache.format == kKvBf16, v);
+        for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], s);
+        w = pack8(v, bf16);
+        if (!in[i]) w = make_uint4(0u, 0u, 0u, 0u);
+      } else if ((a.cache.format == kKvBf16) != bf16) {
+        float v[8];
+        unpack8(w, a.cache.format == kKvBf16, v);
+        w = pack8(v, bf16);
       }
-      if (r < rows) {
-        const int64_t t = r / per;
-        const int w = (int)(r - t * per);
-        const int h = w < kvh ? w : w - kvh;
-        uint16_t* out = static_cast<uint16_t*>(w < kvh ? a.k : a.v);
-        *reinterpret_cast<uint4*>(out + (t * kvh + h) * D + 8 * l) = pack8(v, bf16);
+      if (base + i * GROUPS + group < rows) {
+        const bool isk = which[i] < kvh;
+        uint16_t* out = static_cast<uint16_t*>(isk ? a.k : a.v);
+        *reinterpret_cast<uint4*>(out + ((t0 + tok[i]) * kvh + (isk ? which[i] : which[i] - kvh)) * D + 8 * l) = w;
       }
     }
   }
@@ -315,12 +373,10 @@ __global__ void __launch_bounds__(kRopeThreads) kv_read_kernel(const KvReadArgs 
 
 cudaError_t launch_rope_write(const RopeWriteArgs& a, int head_dim, cudaStream_t stream) {
   const int groups = kRopeThreads / (head_dim / 8);
-  const int rows = a.x_heads + 2 * a.kv_heads;
+  const int units = (a.x_heads + groups - 1) / groups + 2 * ((a.kv_heads + groups - 1) / groups);
   // one block a token, or, while that leaves SMs idle, a token's rows over several blocks
-  int per = groups * kRopeBatch;
-  if (a.tokens >= 152 * 4) per = (rows + per - 1) / per * per;
-  else if (a.tokens < 152) per = groups;
-  const dim3 grid((unsigned)a.tokens, (unsigned)((rows + per - 1) / per));
+  const int per = a.tokens >= 152 * 4 ? units : a.tokens >= 152 ? (units < kRopeBatch ? units : kRopeBatch) : 1;
+  const dim3 grid((unsigned)a.tokens, (unsigned)((units + per - 1) / per));
   if (head_dim == 64)
     rope_write_kernel<64><<<grid, kRopeThreads, 0, stream>>>(a, per);
   else
@@ -330,14 +386,16 @@ cudaError_t launch_rope_write(const RopeWriteArgs& a, int head_dim, cudaStream_t
 
 cudaError_t launch_kv_read(const KvReadArgs& a, cudaStream_t stream) {
   const int groups = kRopeThreads / (a.cache.head_dim / 8);
-  const int64_t rows = a.tokens * a.cache.kv_heads * 2;
-  int64_t blocks = (rows + groups - 1) / groups;
-  if (blocks > 152 * 16) blocks = (rows + groups * kRopeBatch - 1) / (groups * kRopeBatch);
-  if (blocks > (1 << 30)) blocks = 1 << 30;
+  const int64_t per = 2 * a.cache.kv_heads;
+  // a block's passes full, and enough blocks for the SMs: whole tokens, up to kRopeBatch rows a lane group
+  int64_t tokens = groups * kRopeBatch / per;
+  if (tokens < 1) tokens = 1;
+  while (tokens > 1 && a.tokens / tokens < 152 * 4) tokens /= 2;
+  const unsigned blocks = (unsigned)((a.tokens + tokens - 1) / tokens);
   if (a.cache.head_dim == 64)
-    kv_read_kernel<64><<<(unsigned)blocks, kRopeThreads, 0, stream>>>(a);
+    kv_read_kernel<64><<<blocks, kRopeThreads, 0, stream>>>(a, (int)tokens);
   else
-    kv_read_kernel<128><<<(unsigned)blocks, kRopeThreads, 0, stream>>>(a);
+    kv_read_kernel<128><<<blocks, kRopeThreads, 0, stream>>>(a, (int)tokens);
   return cudaGetLastError();
 }
 
