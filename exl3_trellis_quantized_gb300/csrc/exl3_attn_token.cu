@@ -25,8 +25,9 @@
 //
 // Quantised rows stay in the rotated basis (see exl3_rope_cache.cu): q is
 // rotated by the D-point Hadamard transform times 8/D once, the output once.  The
-// rotated q is not exact in fp16: it goes in as two fp16 terms (22 bits), since
-// one alone moved the outputs of fp16 queries by 1.7 times their own rounding.
+// rotated q is not exact in fp16: for fp16 queries it goes in as two fp16 terms
+// (22 bits), since one alone moved the outputs by 1.7 times their own rounding
+// (bf16 outputs round eight times coarser: one term).
 // A key's scale multiplies its score in fp32.  A value's scale goes into the
 // exponent: the weight 2^(s + log2 scale - m), with m the maximum of the same sum,
 // is at most 2^8 whatever the scales are, so rounding it to fp16 loses nothing by
@@ -222,8 +223,8 @@ __device__ int find_seq(const AttnArgs& a, int lane, int64_t u, int64_t* before)
   return a.batch;
 }
 
-// FMT: KvFormat.  NR: tiles of eight rows.
-template <int FMT, int D, int NR>
+// FMT: KvFormat.  NR: tiles of eight rows.  TWO: the rotated q in two terms.
+template <int FMT, int D, int NR, bool TWO>
 struct TokenCfg {
   static constexpr bool kQuant = kv_quantised(FMT);
   static constexpr bool kBf16 = FMT == kKvBf16;  // operand type of the MMAs (fp16 for the quantised formats)
@@ -238,7 +239,7 @@ struct TokenCfg {
   static constexpr int kRing = kStages * kStage;           // a warp's
   static constexpr int kJoin = kRows * D * 4 + kRows * 8;  // a warp's (o, m, l) at an item's end
   static constexpr int kWarpBytes = ((kRing > kJoin ? kRing : kJoin) + 127) / 128 * 128;
-  static constexpr int kQBytes = kQuant ? 2 * kRows * D * 2 : 0;  // two fp16 terms of the rotated q
+  static constexpr int kQBytes = kQuant ? 2 * kRows * D * 2 : 0;  // the rotated q and the fragments of its second term
   static constexpr int kSmem = kWarps * kWarpBytes + kQBytes;
   static constexpr int kChunks = kRow / 16;  // 16-byte chunks of a row
   static constexpr int kTpr = kThreads / kRows;  // threads of a row where the CTA works on whole rows
@@ -279,9 +280,9 @@ __device__ __forceinline__ uint32_t ring_offset(int r, int c) {
   return (uint32_t)(r * ROW + (c << 4));
 }
 
-template <int FMT, int D, int NR>
+template <int FMT, int D, int NR, bool TWO>
 __global__ void __launch_bounds__(kThreads, token_ctas_per_sm(8 * NR)) attn_token_kernel(const AttnArgs a) {
-  using C = TokenCfg<FMT, D, NR>;
+  using C = TokenCfg<FMT, D, NR, TWO>;
   constexpr bool BF16 = C::kBf16;
   constexpr int KS = D / 16;        // k16 steps of the scores
   constexpr int NK = C::kStep / 16;  // 16-key tiles of a step
@@ -416,9 +417,10 @@ __global__ void __launch_bounds__(kThreads, token_ctas_per_sm(8 * NR)) attn_toke
 #pragma unroll
     for (int i = 0; i < C::kStages - 1; ++i) issue(i);
 
-    uint32_t ql[C::kQuant ? NR : 1][KS][2];  // the second term of the rotated q
+    // the second term of the rotated q, only for fp16 queries: [n][k][lane] fragments
+    const uint32_t qlo = smem_u32(smem) + kWarps * C::kWarpBytes + C::kRows * D * 2;
     if constexpr (C::kQuant) {
-      // rotate, times 8/D, to two fp16 terms in shared memory
+      // rotate, times 8/D, to fp16 in shared memory, one term after the other
       uint16_t* qs = reinterpret_cast<uint16_t*>(smem + kWarps * C::kWarpBytes);
       float v[C::kPer];
 #pragma unroll
@@ -428,19 +430,10 @@ __global__ void __launch_bounds__(kThreads, token_ctas_per_sm(8 * NR)) attn_toke
       }
       hadamard_threads<C::kPer, C::kTpr>(v, part);
 #pragma unroll
-      for (int i = 0; i < C::kPer; i += 2) {
-        const float x = v[i] * (8.0f / D), y = v[i + 1] * (8.0f / D);
-        const uint32_t hi = pack2<false>(x, y);
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-        *reinterpret_cast<uint32_t*>(qs + jr * D + part * C::kPer + i) = hi;
-        *reinterpret_cast<uint32_t*>(qs + (C::kRows + jr) * D + part * C::kPer + i) = pack2<false>(x - f.x, y - f.y);
-      }
-      __syncthreads();
+      for (int i = 0; i < C::kPer; ++i) v[i] *= 8.0f / D;
       // fragments in the order in which the codes come out of their words
-#pragma unroll
-      for (int n = 0; n < 2 * NR; ++n) {
+      auto fragments = [&](uint32_t (&dst)[KS][2], int n) {
         const uint16_t* src = qs + (8 * n + g) * D;
-        uint32_t(&dst)[KS][2] = n < NR ? qb[n % NR] : ql[n % NR];
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
           if constexpr (FMT == kKvInt8) {
@@ -455,20 +448,39 @@ __global__ void __launch_bounds__(kThreads, token_ctas_per_sm(8 * NR)) attn_toke
             dst[k][1] = (uint32_t)src[d + 1] | (uint32_t)src[d + 5] << 16;
           }
         }
+      };
+      if constexpr (TWO) {
+#pragma unroll
+        for (int i = 0; i < C::kPer; i += 2) {
+          const uint32_t hi = pack2<false>(v[i], v[i + 1]);
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+          *reinterpret_cast<uint32_t*>(qs + jr * D + part * C::kPer + i) = pack2<false>(v[i] - f.x, v[i + 1] - f.y);
+        }
+        __syncthreads();
+        // warp w makes the fragments of tiles w, w + 4, ...
+        if (warp < NR) {
+          uint32_t tmp[KS][2];
+          fragments(tmp, warp);
+#pragma unroll
+          for (int k = 0; k < KS; ++k)
+            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(qlo + (uint32_t)((warp * KS + k) * 32 + lane) * 8), "r"(tmp[k][0]), "r"(tmp[k][1])
+                         : "memory");
+        }
+        __syncthreads();
       }
+#pragma unroll
+      for (int i = 0; i < C::kPer; i += 2) *reinterpret_cast<uint32_t*>(qs + jr * D + part * C::kPer + i) = pack2<false>(v[i], v[i + 1]);
+      __syncthreads();
+#pragma unroll
+      for (int n = 0; n < NR; ++n) fragments(qb[n], n);
     }
 
     // ---- this lane's rows 8n + 2q, + 1: what they see, and their running softmax
-    int lim[NR][2], low[NR][2];
+    int pos[NR][2];
 #pragma unroll
     for (int n = 0; n < NR; ++n)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = min(8 * n + 2 * q + i, rows - 1);
-        const int pos = s.kv_len - s.q_len + r / group;
-        lim[n][i] = min(pos, t1 - 1);
-        low[n][i] = a.window > 0 ? max(0, pos - a.window + 1) : 0;
-      }
+      for (int i = 0; i < 2; ++i) pos[n][i] = s.kv_len - s.q_len + min(8 * n + 2 * q + i, rows - 1) / group;
     const int lim_all = min(s.kv_len - s.q_len, t1 - 1);  // keys up to here are seen by every row
     const int low_all = a.window > 0 ? max(0, s.kv_len - a.window) : 0;
     float m[NR][2], l[NR][2];
@@ -501,46 +513,53 @@ __global__ void __launch_bounds__(kThreads, token_ctas_per_sm(8 * NR)) attn_toke
             uint32_t r[4];
             ldmatrix_x4(kb + ring_offset<C::kRow>(16 * x + (lane & 15), 2 * k + (lane >> 4)), r);
 #pragma unroll
-            for (int n = 0; n < NR; ++n) mma16816<BF16>(sc[x][n], r, qb[n][k][0], qb[n][k][1]);
-          }
-        } else if constexpr (FMT == kKvInt8) {
-#pragma unroll
-          for (int k4 = 0; k4 < KS / 4; ++k4) {
-            const uint4 w0 = lds128(kb + ring_offset<C::kRow>(16 * x + g, 4 * k4 + q));
-            const uint4 w1 = lds128(kb + ring_offset<C::kRow>(16 * x + g + 8, 4 * k4 + q));
-            const uint32_t u0[4] = {w0.x, w0.y, w0.z, w0.w}, u1[4] = {w1.x, w1.y, w1.z, w1.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t r[4] = {bytes_to_h2(u0[k], 0x4140), bytes_to_h2(u1[k], 0x4140), bytes_to_h2(u0[k], 0x4342),
-                                     bytes_to_h2(u1[k], 0x4342)};
-#pragma unroll
-              for (int n = 0; n < NR; ++n) {
-                mma16816<false>(sc[x][n], r, qb[n][4 * k4 + k][0], qb[n][4 * k4 + k][1]);
-                mma16816<false>(sc[x][n], r, ql[n][4 * k4 + k][0], ql[n][4 * k4 + k][1]);
-              }
+            for (int n = 0; n < NR; ++n) {
+              mma16816<BF16>(sc[x][n], r, qb[n][k][0], qb[n][k][1]);
             }
           }
-        } else {
-          uint32_t u0[D / 32], u1[D / 32];
-          if constexpr (D == 128) {
-            const uint4 w0 = lds128(kb + ring_offset<C::kRow>(16 * x + g, q));
-            const uint4 w1 = lds128(kb + ring_offset<C::kRow>(16 * x + g + 8, q));
-            u0[0] = w0.x, u0[1] = w0.y, u0[2] = w0.z, u0[3] = w0.w;
-            u1[0] = w1.x, u1[1] = w1.y, u1[2] = w1.z, u1[3] = w1.w;
-          } else {
-            const uint2 w0 = lds64(kb + ring_offset<C::kRow>(16 * x + g, q >> 1) + 8 * (q & 1));
-            const uint2 w1 = lds64(kb + ring_offset<C::kRow>(16 * x + g + 8, q >> 1) + 8 * (q & 1));
-            u0[0] = w0.x, u0[1] = w0.y;
-            u1[0] = w1.x, u1[1] = w1.y;
-          }
+        }
+      }
+      if constexpr (C::kQuant) {
+        constexpr int WORDS = FMT == kKvInt8 ? 4 : D / 32;        // words of a row a lane takes at a time
+        constexpr int KW = FMT == kKvInt8 ? 4 : KS;               // k16 steps that they make
 #pragma unroll
-          for (int k = 0; k < KS; ++k) {
-            const uint32_t x0 = u0[k >> 1] >> (8 * (k & 1)), x1 = u1[k >> 1] >> (8 * (k & 1));
-            const uint32_t r[4] = {nib_lo(x0), nib_lo(x1), nib_hi(x0), nib_hi(x1)};
+        for (int k0 = 0; k0 < KS; k0 += KW) {
+          uint32_t w[NK][2][WORDS];
+#pragma unroll
+          for (int x = 0; x < NK; ++x)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const int row = 16 * x + g + 8 * y;
+              if constexpr (WORDS == 4) {
+                const uint4 v = lds128(kb + ring_offset<C::kRow>(row, (FMT == kKvInt8 ? k0 : 0) + q));
+                w[x][y][0] = v.x, w[x][y][1] = v.y, w[x][y][2] = v.z, w[x][y][3] = v.w;
+              } else {
+                const uint2 v = lds64(kb + ring_offset<C::kRow>(row, q >> 1) + 8 * (q & 1));
+                w[x][y][0] = v.x, w[x][y][1] = v.y;
+              }
+            }
+#pragma unroll
+          for (int k = 0; k < KW; ++k) {
+            uint32_t r[NK][4];
+#pragma unroll
+            for (int x = 0; x < NK; ++x) {
+              if constexpr (FMT == kKvInt8) {
+                r[x][0] = bytes_to_h2(w[x][0][k], 0x4140), r[x][1] = bytes_to_h2(w[x][1][k], 0x4140);
+                r[x][2] = bytes_to_h2(w[x][0][k], 0x4342), r[x][3] = bytes_to_h2(w[x][1][k], 0x4342);
+              } else {
+                const uint32_t u0 = w[x][0][k >> 1] >> (8 * (k & 1)), u1 = w[x][1][k >> 1] >> (8 * (k & 1));
+                r[x][0] = nib_lo(u0), r[x][1] = nib_lo(u1), r[x][2] = nib_hi(u0), r[x][3] = nib_hi(u1);
+              }
+            }
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
-              mma16816<false>(sc[x][n], r, qb[n][k][0], qb[n][k][1]);
-              mma16816<false>(sc[x][n], r, ql[n][k][0], ql[n][k][1]);
+#pragma unroll
+              for (int x = 0; x < NK; ++x) mma16816<false>(sc[x][n], r[x], qb[n][k0 + k][0], qb[n][k0 + k][1]);
+              if constexpr (TWO) {
+                const uint2 lo = lds64(qlo + (uint32_t)((n * KS + k0 + k) * 32 + lane) * 8);
+#pragma unroll
+                for (int x = 0; x < NK; ++x) mma16816<false>(sc[x][n], r[x], lo.x, lo.y);
+              }
             }
           }
         }
@@ -580,9 +599,7 @@ __global__ void __launch_bounds__(kThreads, token_ctas_per_sm(8 * NR)) attn_toke
             const int key = t + 16 * x + g + 8 * (c >> 1);
 #pragma unroll
             for (int n = 0; n < NR; ++n)
-              if (key > lim[n][c & 1] || key < low[n][c & 1]) {
-                sc[x][n][c] = kNegInf;
-              }
+              if (key > min(pos[n][c & 1], t1 - 1) || (a.window > 0 && key <= pos[n][c & 1] - a.window)) sc[x][n][c] = kNegInf;
             if constexpr (C::kQuant) {
               // seen by no row: its scale may be anything
               if (key > lim_all + s.q_len - 1 || key < s.first) rv[x][c >> 1] = 0.0f;
@@ -681,7 +698,9 @@ __global__ void __launch_bounds__(kThreads, token_ctas_per_sm(8 * NR)) attn_toke
                 const uint32_t r[4] = {bytes_to_h2(lo, 0x4140), bytes_to_h2(lo, 0x4342), bytes_to_h2(hi, 0x4140),
                                        bytes_to_h2(hi, 0x4342)};
 #pragma unroll
-                for (int n = 0; n < NR; ++n) mma16816<false>(o[n][2 * y + z], r, pb[n][0], pb[n][1]);
+                for (int n = 0; n < NR; ++n) {
+                  mma16816<false>(o[n][2 * y + z], r, pb[n][0], pb[n][1]);
+                }
               }
             } else {
 #pragma unroll
@@ -694,7 +713,9 @@ __global__ void __launch_bounds__(kThreads, token_ctas_per_sm(8 * NR)) attn_toke
                   const uint32_t r[4] = {nib_lo(lo >> (8 * e)), nib_hi(lo >> (8 * e)), nib_lo(hi >> (8 * e)),
                                          nib_hi(hi >> (8 * e))};
 #pragma unroll
-                  for (int n = 0; n < NR; ++n) mma16816<false>(o[n][4 * y + 2 * z + e], r, pb[n][0], pb[n][1]);
+                  for (int n = 0; n < NR; ++n) {
+                    mma16816<false>(o[n][4 * y + 2 * z + e], r, pb[n][0], pb[n][1]);
+                  }
                 }
               }
             }
@@ -902,12 +923,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_token_join_kernel(const 
   }
 }
 
-template <int FMT, int D, int NR>
+template <int FMT, int D, int NR, bool TWO>
 cudaError_t launch_token(const AttnArgs& a, cudaStream_t stream) {
-  using C = TokenCfg<FMT, D, NR>;
-  cudaError_t e = allow_smem<attn_token_kernel<FMT, D, NR>>(C::kSmem);
+  using C = TokenCfg<FMT, D, NR, TWO>;
+  cudaError_t e = allow_smem<attn_token_kernel<FMT, D, NR, TWO>>(C::kSmem);
   if (e != cudaSuccess) return e;
-  attn_token_kernel<FMT, D, NR><<<(unsigned)a.ctas, kThreads, C::kSmem, stream>>>(a);
+  attn_token_kernel<FMT, D, NR, TWO><<<(unsigned)a.ctas, kThreads, C::kSmem, stream>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -922,21 +943,21 @@ cudaError_t launch_token(const AttnArgs& a, cudaStream_t stream) {
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, attn_token_join_kernel<D, C::kQuant>, a);
 }
-template <int FMT>
+template <int FMT, bool TWO>
 cudaError_t launch_token_fmt(const AttnArgs& a, cudaStream_t stream) {
   const bool small = a.max_q * (a.heads / a.kv_heads) <= 8;
-  if (a.head_dim == 64) return small ? launch_token<FMT, 64, 1>(a, stream) : launch_token<FMT, 64, 2>(a, stream);
-  return small ? launch_token<FMT, 128, 1>(a, stream) : launch_token<FMT, 128, 2>(a, stream);
+  if (a.head_dim == 64) return small ? launch_token<FMT, 64, 1, TWO>(a, stream) : launch_token<FMT, 64, 2, TWO>(a, stream);
+  return small ? launch_token<FMT, 128, 1, TWO>(a, stream) : launch_token<FMT, 128, 2, TWO>(a, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_token(const AttnArgs& a, cudaStream_t stream) {
   switch (a.cache.format) {
-    case kKvF16: return launch_token_fmt<kKvF16>(a, stream);
-    case kKvBf16: return launch_token_fmt<kKvBf16>(a, stream);
-    case kKvInt8: return launch_token_fmt<kKvInt8>(a, stream);
-    case kKvInt4: return launch_token_fmt<kKvInt4>(a, stream);
+    case kKvF16: return launch_token_fmt<kKvF16, false>(a, stream);
+    case kKvBf16: return launch_token_fmt<kKvBf16, false>(a, stream);
+    case kKvInt8: return a.bf16 ? launch_token_fmt<kKvInt8, false>(a, stream) : launch_token_fmt<kKvInt8, true>(a, stream);
+    case kKvInt4: return a.bf16 ? launch_token_fmt<kKvInt4, false>(a, stream) : launch_token_fmt<kKvInt4, true>(a, stream);
     default: return cudaErrorInvalidValue;
   }
 }
