@@ -17,14 +17,18 @@
 // are (only q and the output are rotated).  Read back: H_D(codes) is a sum of
 // integers below 2^24, exact in fp32 in any order, times scale * 8 / D.
 //
-// Bound by DRAM on long calls, by the launch on short ones; between them the
-// instructions count (a first version spent 300 on a pair of rows in a warp and
-// took 126 us where it now takes 62: 16381 tokens, 32 query and 8 key heads, 4
-// bits).  So: D/8 lanes hold a row, two rows a warp; a block takes one token, whose
-// D/2 sines and cosines are computed once and stay in registers for all its
-// query rows; a lane holds both values of its pairs; a stage of the transform
-// across lanes is a shuffle and a multiply-add by +-1; codes come out of the low
-// bits of a sum with 1.5 * 2^23 and go back the same way.
+// Bound by DRAM on long calls, by the launch on short ones (one token: 4.2 us).
+// 16381 tokens of 32 query and 8 key heads of 128 in bf16: rotation of the 40
+// heads 61 us (5540 GB/s), the same with keys and values written in 16 bits 71 us
+// (5690 GB/s), in 8 and 4 bits 81 us (4560 and 4350 GB/s: the instructions of the
+// transform count).  So: D/8 lanes hold a row, two rows a warp; a block takes one
+// token, whose D/2 sines and cosines are computed once and stay in registers for
+// all its query rows; a lane holds both values of its pairs; a stage of the
+// transform across lanes is a shuffle and a multiply-add by +-1; codes come out of
+// the low bits of a sum with 1.5 * 2^23.  Four lanes a row need half the
+// instructions for keys and values, but 92 registers instead of 56, and the query
+// rows that share the block want the occupancy: 100 us in 4 bits, and 98 to 125
+// with warps or blocks of their own for keys and values.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -85,6 +89,74 @@ __device__ __forceinline__ void hadamard_lanes(float (&v)[8], int lane) {
     const float sign = (lane & s) != 0 ? -1.0f : 1.0f;  // exact: the sum or the difference, rounded once
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = fmaf(v[i], sign, __shfl_xor_sync(0xffffffffu, v[i], s));
+  }
+}
+// Two fp32 numbers an instruction.
+__device__ __forceinline__ float2 fma2(const float2& a, const float2& b, const float2& c) {
+  float2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(r))
+      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)),
+        "l"(reinterpret_cast<const uint64_t&>(c)));
+  return r;
+}
+__device__ __forceinline__ float2 add2(const float2& a, const float2& b) {
+  float2 r;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(r))
+      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(const float2& a, const float2& b) {
+  float2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(r))
+      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
+  return r;
+}
+__device__ __forceinline__ float2 twice(float x) { return make_float2(x, x); }
+__device__ __forceinline__ void butterfly(float2& a, float2& b) {
+  const float2 p = a;
+  a = add2(p, b);
+  b = fma2(b, twice(-1.0f), p);  // exact product: the difference, rounded once
+}
+
+__device__ __forceinline__ void unpack8(const uint4& w, bool bf16, float2* v) {
+  float f[8];
+  unpack8(w, bf16, f);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = make_float2(f[2 * j], f[2 * j + 1]);
+}
+__device__ __forceinline__ uint4 pack8(const float2* v, bool bf16) {
+  const float f[8] = {v[0].x, v[0].y, v[1].x, v[1].y, v[2].x, v[2].y, v[3].x, v[3].y};
+  return pack8(f, bf16);
+}
+
+// The same for a row held by four lanes, D/32 chunks of eight consecutive
+// values a lane, of integers whose sums are exact: every bit of the place in a
+// lane and of the lane is one stage, in any order.
+template <int D>
+__device__ __forceinline__ void hadamard_quads(float2 (&v)[D / 8], int l) {
+  constexpr int C = D / 32;
+#pragma unroll
+  for (int x = 0; x < D / 8; ++x) v[x] = make_float2(__fadd_rn(v[x].x, v[x].y), __fsub_rn(v[x].x, v[x].y));
+#pragma unroll
+  for (int s = 1; s < 8; s *= 2)  // inside a chunk, then chunks 2 i and 2 i + 1
+#pragma unroll
+    for (int x = 0; x < D / 8; ++x)
+      if (!(x & s)) butterfly(v[x], v[x + s]);
+#pragma unroll
+  for (int s = 1; s < 4; s *= 2) {
+    const float2 sign = twice((l & s) != 0 ? -1.0f : 1.0f);
+#pragma unroll
+    for (int x = 0; x < D / 8; ++x) {
+      const float2 o = make_float2(__shfl_xor_sync(0xffffffffu, v[x].x, s), __shfl_xor_sync(0xffffffffu, v[x].y, s));
+      v[x] = fma2(v[x], sign, o);
+    }
+  }
+  if (C == 4) {
+#pragma unroll
+    for (int x = 0; x < D / 16; ++x) butterfly(v[x], v[x + D / 16]);
   }
 }
 // The larger magnitude, or NaN if either is.
@@ -281,12 +353,17 @@ __global__ void __launch_bounds__(kRopeThreads) rope_write_kernel(const RopeWrit
   }
 }
 
-// Rows of whole tokens a block: keys, then values of each.
+// Rows of whole tokens a block: keys, then values of each; four lanes a row,
+// whose chunk i of lane l is chunk 4 i + l.  At 16381 tokens of 8 heads of 128
+// 30 us in each format (4500 GB/s of 16-bit rows, 2830 of 4-bit ones): the chain
+// slot, row, store of a block is what counts.  Sixteen lanes a row, as writing
+// has them, took 40 (twice the shuffles and adds a row); two rows of four lanes
+// in flight 32.
 template <int D>
 __global__ void __launch_bounds__(kRopeThreads) kv_read_kernel(const KvReadArgs a, int tokens_per_block) {
-  constexpr int LANES = D / 8;
-  constexpr int GROUPS = kRopeThreads / LANES;
-  const int l = threadIdx.x % LANES, group = threadIdx.x / LANES;
+  constexpr int C = D / 32;
+  constexpr int GROUPS = kRopeThreads / 4;
+  const int l = threadIdx.x & 3, group = threadIdx.x >> 2;
   const bool bf16 = a.bf16 != 0;
   const int kvh = a.cache.kv_heads;
   const int per = 2 * kvh;  // rows of a token
@@ -294,77 +371,79 @@ __global__ void __launch_bounds__(kRopeThreads) kv_read_kernel(const KvReadArgs 
   const int rows = (int)min((int64_t)tokens_per_block, a.tokens - t0) * per;
   const int64_t limit = a.cache.num_pages << a.cache.page_shift;
   const bool int8 = a.cache.format == kKvInt8, quant = kv_quantised(a.cache.format);
-  for (int base = 0; base < rows; base += GROUPS * kRopeBatch) {
-    uint4 raw[kRopeBatch];
-    float scale[kRopeBatch];
-    bool in[kRopeBatch];
-    int tok[kRopeBatch], which[kRopeBatch];
+  for (int base = 0; base < rows; base += GROUPS) {
+    const int r = base + group;
+    const int tok = tokens_per_block == 1 ? 0 : r / per, which = r - tok * per;
+    const bool isk = which < kvh;
+    const int head = isk ? which : which - kvh;
+    uint4 raw[C];
 #pragma unroll
-    for (int i = 0; i < kRopeBatch; ++i) {
-      const int r = base + i * GROUPS + group;
-      raw[i] = make_uint4(0u, 0u, 0u, 0u);
-      scale[i] = 0.0f;
-      in[i] = false;
-      tok[i] = tokens_per_block == 1 ? 0 : r / per;
-      which[i] = r - tok[i] * per;
-      if (r < rows) {
-        const int64_t slot = a.slots[t0 + tok[i]];
-        if (slot >= 0 && slot < limit) {
-          in[i] = true;
-          const bool isk = which[i] < kvh;
-          const int64_t row = (((slot >> a.cache.page_shift) * kvh + (isk ? which[i] : which[i] - kvh)) << a.cache.page_shift) +
-                              (slot & ((1 << a.cache.page_shift) - 1));
-          const uint8_t* src = isk ? a.cache.k : a.cache.v;
+    for (int x = 0; x < C; ++x) raw[x] = make_uint4(0u, 0u, 0u, 0u);
+    float scale = 0.0f;
+    bool in = false;
+    if (r < rows) {
+      const int64_t slot = a.slots[t0 + tok];
+      if (slot >= 0 && slot < limit) {
+        in = true;
+        const int64_t row = (((slot >> a.cache.page_shift) * kvh + head) << a.cache.page_shift) +
+                            (slot & ((1 << a.cache.page_shift) - 1));
+        const uint8_t* src = isk ? a.cache.k : a.cache.v;
+#pragma unroll
+        for (int x = 0; x < C; ++x) {
+          const int ch = 4 * x + l;
           if (int8) {
-            const uint2 c = *reinterpret_cast<const uint2*>(src + row * D + 8 * l);
-            raw[i].x = c.x;
-            raw[i].y = c.y;
+            const uint2 c = *reinterpret_cast<const uint2*>(src + row * D + 8 * ch);
+            raw[x].x = c.x;
+            raw[x].y = c.y;
           } else if (quant) {
-            raw[i].x = *reinterpret_cast<const uint32_t*>(src + row * (D / 2) + 4 * l);
+            raw[x].x = *reinterpret_cast<const uint32_t*>(src + row * (D / 2) + 4 * ch);
           } else {
-            raw[i] = *reinterpret_cast<const uint4*>(src + row * (2 * D) + 16 * l);
+            raw[x] = *reinterpret_cast<const uint4*>(src + row * (2 * D) + 16 * ch);
           }
-          if (quant) scale[i] = __uint_as_float((uint32_t)(isk ? a.cache.k_scale : a.cache.v_scale)[row] << 16);
         }
+        if (quant) scale = __uint_as_float((uint32_t)(isk ? a.cache.k_scale : a.cache.v_scale)[row] << 16);
       }
     }
+    if (quant) {
+      // a code in the low byte of 2^23, less 2^23 and the offset
+      float2 v[D / 8];
+      const float2 less = twice(-8388608.0f - (int8 ? 128.0f : 8.0f));
 #pragma unroll
-    for (int i = 0; i < kRopeBatch; ++i) {
-      if (base + i * GROUPS >= rows) break;  // alike in the whole block
-      uint4 w = raw[i];
-      if (quant) {
-        // a code in the low byte of 2^23, less 2^23 and the offset
-        float v[8];
+      for (int x = 0; x < C; ++x) {
+        auto code = [](uint32_t word, int byte) { return __uint_as_float(__byte_perm(word, 0x4B000000u, 0x7540 + byte)); };
+        const uint4& w = raw[x];
         if (int8) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            v[j] = __uint_as_float(__byte_perm(w.x, 0x4B000000u, 0x7540 + j)) - (8388608.0f + 128.0f);
-            v[4 + j] = __uint_as_float(__byte_perm(w.y, 0x4B000000u, 0x7540 + j)) - (8388608.0f + 128.0f);
+          for (int j = 0; j < 2; ++j) {
+            v[4 * x + j] = add2(make_float2(code(w.x, 2 * j), code(w.x, 2 * j + 1)), less);
+            v[4 * x + 2 + j] = add2(make_float2(code(w.y, 2 * j), code(w.y, 2 * j + 1)), less);
           }
         } else {
           const uint32_t even = w.x & 0x0F0F0F0Fu, odd = w.x >> 4 & 0x0F0F0F0Fu;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            v[2 * j] = __uint_as_float(__byte_perm(even, 0x4B000000u, 0x7540 + j)) - (8388608.0f + 8.0f);
-            v[2 * j + 1] = __uint_as_float(__byte_perm(odd, 0x4B000000u, 0x7540 + j)) - (8388608.0f + 8.0f);
-          }
+          for (int j = 0; j < 4; ++j) v[4 * x + j] = add2(make_float2(code(even, j), code(odd, j)), less);
         }
-        hadamard_lanes<D>(v, threadIdx.x);
-        const float s = __fmul_rn(scale[i], 8.0f / D);
+      }
+      hadamard_quads<D>(v, l);
+      const float2 s = twice(__fmul_rn(scale, 8.0f / D));
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], s);
-        w = pack8(v, bf16);
-        if (!in[i]) w = make_uint4(0u, 0u, 0u, 0u);
-      } else if ((a.cache.format == kKvBf16) != bf16) {
-        float v[8];
-        unpack8(w, a.cache.format == kKvBf16, v);
-        w = pack8(v, bf16);
+      for (int x = 0; x < C; ++x) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[4 * x + j] = mul2(v[4 * x + j], s);
+        raw[x] = in ? pack8(v + 4 * x, bf16) : make_uint4(0u, 0u, 0u, 0u);
       }
-      if (base + i * GROUPS + group < rows) {
-        const bool isk = which[i] < kvh;
-        uint16_t* out = static_cast<uint16_t*>(isk ? a.k : a.v);
-        *reinterpret_cast<uint4*>(out + ((t0 + tok[i]) * kvh + (isk ? which[i] : which[i] - kvh)) * D + 8 * l) = w;
+    } else if ((a.cache.format == kKvBf16) != bf16) {
+#pragma unroll
+      for (int x = 0; x < C; ++x) {
+        float2 v[4];
+        unpack8(raw[x], a.cache.format == kKvBf16, v);
+        raw[x] = pack8(v, bf16);
       }
+    }
+    if (r < rows) {
+      uint16_t* out = static_cast<uint16_t*>(isk ? a.k : a.v) + ((t0 + tok) * kvh + head) * D;
+#pragma unroll
+      for (int x = 0; x < C; ++x) *reinterpret_cast<uint4*>(out + 8 * (4 * x + l)) = raw[x];
     }
   }
 }
@@ -385,12 +464,9 @@ cudaError_t launch_rope_write(const RopeWriteArgs& a, int head_dim, cudaStream_t
 }
 
 cudaError_t launch_kv_read(const KvReadArgs& a, cudaStream_t stream) {
-  const int groups = kRopeThreads / (a.cache.head_dim / 8);
+  const int groups = kRopeThreads / 4;
   const int64_t per = 2 * a.cache.kv_heads;
-  // a block's passes full, and enough blocks for the SMs: whole tokens, up to kRopeBatch rows a lane group
-  int64_t tokens = groups * kRopeBatch / per;
-  if (tokens < 1) tokens = 1;
-  while (tokens > 1 && a.tokens / tokens < 152 * 4) tokens /= 2;
+  const int64_t tokens = per < groups ? groups / per : 1;  // one pass a block
   const unsigned blocks = (unsigned)((a.tokens + tokens - 1) / tokens);
   if (a.cache.head_dim == 64)
     kv_read_kernel<64><<<blocks, kRopeThreads, 0, stream>>>(a, (int)tokens);
