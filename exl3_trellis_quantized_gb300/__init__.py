@@ -4,6 +4,10 @@ The compute lives in ``libexl3.so`` (hand-written CUDA behind a C ABI, see
 ``include/exl3.h``).  This package is a thin binding: it marshals torch
 tensors into pointers and sizes and calls the library.  There is no CPU or
 PyTorch fallback; if the library is missing every call raises.
+
+Beside the layer: rotary positions (``rope``), a paged cache of 16, 8 or 4 bits
+(``KVCache``, ``kv_write``, ``kv_read``) and attention over prompts
+(``attention_prompt``) and over the cache (``attention_paged``).
 """
 from .binding import (  # noqa: F401
     CODEBOOKS,
