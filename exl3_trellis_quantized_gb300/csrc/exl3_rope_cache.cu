@@ -19,16 +19,18 @@
 //
 // Bound by DRAM on long calls, by the launch on short ones (one token: 4.2 us).
 // 16381 tokens of 32 query and 8 key heads of 128 in bf16: rotation of the 40
-// heads 61 us (5540 GB/s), the same with keys and values written in 16 bits 71 us
-// (5690 GB/s), in 8 and 4 bits 81 us (4560 and 4350 GB/s: the instructions of the
-// transform count).  So: D/8 lanes hold a row, two rows a warp; a block takes one
-// token, whose D/2 sines and cosines are computed once and stay in registers for
-// all its query rows; a lane holds both values of its pairs; a stage of the
-// transform across lanes is a shuffle and a multiply-add by +-1; codes come out of
-// the low bits of a sum with 1.5 * 2^23.  Four lanes a row need half the
-// instructions for keys and values, but 92 registers instead of 56, and the query
-// rows that share the block want the occupancy: 100 us in 4 bits, and 98 to 125
-// with warps or blocks of their own for keys and values.
+// heads 61 us (5540 GB/s), the same with keys and values written in 16 bits 67 us
+// (6030 GB/s), in 8 and 4 bits 77 us (4800 and 4590 GB/s: the instructions of the
+// transform count); keys and values alone, not rotated, 34 and 42 us.  So: a block
+// takes one token, whose D/2 sines and cosines are computed once and stay in
+// registers for all its query rows, of D/8 lanes each, a lane with both values of
+// its pairs; keys and values have D/16 lanes a row, sums and differences two an
+// instruction, a stage of the transform across lanes is a shuffle and a
+// multiply-add by +-1, and codes come out of the low bits of a sum with 1.5 * 2^23.
+// With D/8 lanes for keys and values too 81 us; four lanes a row need the fewest
+// instructions, but 92 registers instead of 56, and the query rows that share the
+// block want the occupancy: 100 us, and 98 to 125 with warps or blocks of their own
+// for keys and values.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -38,6 +40,7 @@ namespace exl3 {
 namespace {
 
 constexpr int kRopeThreads = 128;
+constexpr int kRopeBlocks = 9;  // blocks an SM: 56 registers a thread (seven blocks of 72: 83 us for 79 below)
 constexpr int kRopeBatch = 4;  // rows a lane group loads before it works on the first
 
 __device__ __forceinline__ void unpack8(const uint4& w, bool bf16, float (&v)[8]) {
@@ -69,28 +72,6 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8], bool bf16) {
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-// D-point Hadamard transform of a row held as eight consecutive values a lane
-// by D/8 neighbouring lanes.
-template <int D>
-__device__ __forceinline__ void hadamard_lanes(float (&v)[8], int lane) {
-#pragma unroll
-  for (int s = 1; s < 8; s *= 2) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (!(i & s)) {
-        const float p = v[i], q = v[i + s];
-        v[i] = p + q;
-        v[i + s] = p - q;
-      }
-    }
-  }
-#pragma unroll
-  for (int s = 1; s < D / 8; s *= 2) {
-    const float sign = (lane & s) != 0 ? -1.0f : 1.0f;  // exact: the sum or the difference, rounded once
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = fmaf(v[i], sign, __shfl_xor_sync(0xffffffffu, v[i], s));
-  }
-}
 // Two fp32 numbers an instruction.
 __device__ __forceinline__ float2 fma2(const float2& a, const float2& b, const float2& c) {
   float2 r;
@@ -132,6 +113,30 @@ __device__ __forceinline__ uint4 pack8(const float2* v, bool bf16) {
   return pack8(f, bf16);
 }
 
+// D-point Hadamard transform of a row held by D/16 neighbouring lanes, two
+// chunks of eight consecutive values a lane: chunks l and l + D/16.  Strides in
+// rising order (the sums round).
+template <int D>
+__device__ __forceinline__ void hadamard_lanes(float2 (&v)[8], int l) {
+#pragma unroll
+  for (int x = 0; x < 8; ++x) v[x] = make_float2(__fadd_rn(v[x].x, v[x].y), __fsub_rn(v[x].x, v[x].y));
+#pragma unroll
+  for (int s = 1; s < 4; s *= 2)
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+      if (!(x & s)) butterfly(v[x], v[x + s]);
+#pragma unroll
+  for (int s = 1; s < D / 16; s *= 2) {
+    const float2 sign = twice((l & s) != 0 ? -1.0f : 1.0f);
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      const float2 o = make_float2(__shfl_xor_sync(0xffffffffu, v[x].x, s), __shfl_xor_sync(0xffffffffu, v[x].y, s));
+      v[x] = fma2(v[x], sign, o);  // exact product: the sum or the difference, rounded once
+    }
+  }
+#pragma unroll
+  for (int x = 0; x < 4; ++x) butterfly(v[x], v[x + 4]);
+}
 // The same for a row held by four lanes, D/32 chunks of eight consecutive
 // values a lane, of integers whose sums are exact: every bit of the place in a
 // lane and of the lane is one stage, in any order.
@@ -166,17 +171,18 @@ __device__ __forceinline__ float max_mag(float a, float b) {
   return y;
 }
 
-// A row's eight values a lane (all lanes of the warp come here) quantised into
-// row `row` of a cache side; nothing is stored where `keep` is false.
+// A row's values as hadamard_lanes takes them (all lanes of the warp come here)
+// quantised into row `row` of a cache side; nothing is stored where `keep` is
+// false.
 template <int D>
-__device__ __forceinline__ void quantise_row(float (&v)[8], int l, bool int8, uint8_t* dst, uint16_t* scales, int64_t row,
+__device__ __forceinline__ void quantise_row(float2 (&v)[8], int l, bool int8, uint8_t* dst, uint16_t* scales, int64_t row,
                                              bool keep) {
-  hadamard_lanes<D>(v, threadIdx.x);
-  float top = fabsf(v[0]);
+  hadamard_lanes<D>(v, l);
+  float top = fabsf(v[0].x);
 #pragma unroll
-  for (int j = 1; j < 8; ++j) top = max_mag(top, v[j]);
+  for (int x = 0; x < 8; ++x) top = max_mag(max_mag(top, v[x].x), v[x].y);
 #pragma unroll
-  for (int s = 1; s < D / 8; s *= 2) top = max_mag(top, __shfl_xor_sync(0xffffffffu, top, s));
+  for (int s = 1; s < D / 16; s *= 2) top = max_mag(top, __shfl_xor_sync(0xffffffffu, top, s));
   const bool finite = top < __builtin_huge_valf();
   // y = v / 8: the eighth goes into the maximum and the reciprocal, exactly
   top *= 0.125f;
@@ -185,20 +191,32 @@ __device__ __forceinline__ void quantise_row(float (&v)[8], int l, bool int8, ui
   scale = fmaxf(scale, 7.888609052210118e-31f);                               // 2^-100: its reciprocal is finite
   if (top == 0.0f) scale = 1.0f;
   const float inv = __fdiv_rn(1.0f, scale) * 0.125f;
-  // the product, rounded, plus 1.5 * 2^23 (and the offset): rounded to an integer in the low bits
+  // the product, rounded, plus 1.5 * 2^23 (and the offset): rounded to an integer in the low bits.  (One by one: a
+  // product and a sum of pairs become one rounding, whatever they are told.)
   const float magic = int8 ? 12582912.0f + 128.0f : 12582912.0f + 8.0f;
-  uint32_t c[8];
+  uint32_t lo[2], hi[2];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) c[j] = __float_as_uint(__fadd_rn(__fmul_rn(v[j], inv), magic));
-  uint32_t lo = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
-  uint32_t hi = __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410);
-  if (!finite) lo = hi = int8 ? 0x80808080u : 0x08080808u;
+  for (int i = 0; i < 2; ++i) {
+    uint32_t c[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      c[2 * j] = __float_as_uint(__fadd_rn(__fmul_rn(v[4 * i + j].x, inv), magic));
+      c[2 * j + 1] = __float_as_uint(__fadd_rn(__fmul_rn(v[4 * i + j].y, inv), magic));
+    }
+    lo[i] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+    hi[i] = __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410);
+    if (!finite) lo[i] = hi[i] = int8 ? 0x80808080u : 0x08080808u;
+  }
   if (!keep) return;
-  if (int8) {
-    *reinterpret_cast<uint2*>(dst + row * D + 8 * l) = make_uint2(lo, hi);
-  } else {
-    lo &= 0x0F0F0F0Fu, hi &= 0x0F0F0F0Fu;
-    *reinterpret_cast<uint32_t*>(dst + row * (D / 2) + 4 * l) = __byte_perm(lo | lo >> 4, hi | hi >> 4, 0x6420);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (int8) {
+      *reinterpret_cast<uint2*>(dst + row * D + i * (D / 2) + 8 * l) = make_uint2(lo[i], hi[i]);
+    } else {
+      lo[i] &= 0x0F0F0F0Fu, hi[i] &= 0x0F0F0F0Fu;
+      *reinterpret_cast<uint32_t*>(dst + row * (D / 2) + i * (D / 4) + 4 * l) =
+          __byte_perm(lo[i] | lo[i] >> 4, hi[i] | hi[i] >> 4, 0x6420);
+    }
   }
   // a row with a value that is not finite reads back as NaN
   if (l == 0) scales[row] = finite ? (uint16_t)(__float_as_uint(scale) >> 16) : (uint16_t)0x7FC0u;
@@ -211,10 +229,13 @@ __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
   b = __fadd_rn(__fmul_rn(q, c), __fmul_rn(p, s));
 }
 
-template <int D>
-__global__ void __launch_bounds__(kRopeThreads) rope_write_kernel(const RopeWriteArgs a, int units_per_block) {
+// KV: there are keys and values
+template <int D, bool KV>
+__global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_write_kernel(const RopeWriteArgs a, int units_per_block) {
   constexpr int LANES = D / 8;
   constexpr int GROUPS = kRopeThreads / LANES;
+  constexpr int KLANES = D / 16;  // lanes of a key's or value's row, sixteen values each
+  constexpr int KGROUPS = kRopeThreads / KLANES;
   __shared__ __align__(16) float cs[D / 2], sn[D / 2];
   const int64_t t = blockIdx.x;
   const int l = threadIdx.x % LANES;
@@ -227,9 +248,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_write_kernel(const RopeWrit
   const int at0 = !pairs && turns ? 4 * l : 8 * l;
   const int at1 = !pairs && turns ? half + 4 * l : 8 * l + 4;
 
-  // this block's units of GROUPS rows: of x, then of keys, then of values (a unit is of one kind)
-  const int xu = (a.x_heads + GROUPS - 1) / GROUPS, ku = (a.kv_heads + GROUPS - 1) / GROUPS;
-  const int u0 = blockIdx.y * units_per_block, u1 = min(xu + 2 * ku, u0 + units_per_block);
+  // this block's units: of x, GROUPS rows each, then of keys and values, KGROUPS rows each
+  const int xu = (a.x_heads + GROUPS - 1) / GROUPS, ku = KV ? (2 * a.kv_heads + KGROUPS - 1) / KGROUPS : 0;
+  const int u0 = blockIdx.y * units_per_block, u1 = min(xu + ku, u0 + units_per_block);
 
   const uint16_t* x = static_cast<const uint16_t*>(a.x.data) + t * a.x.token_stride;
   uint2 raw[kRopeBatch][2];
@@ -249,7 +270,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_write_kernel(const RopeWrit
   // where the keys and values go; nowhere for a negative or too large slot
   int64_t page = -1;
   int off = 0;
-  if (a.kv_heads > 0) {
+  if (KV) {
     const int64_t slot = a.slots[t];
     if (slot >= 0 && slot < (a.cache.num_pages << a.cache.page_shift)) {
       page = slot >> a.cache.page_shift;
@@ -257,16 +278,23 @@ __global__ void __launch_bounds__(kRopeThreads) rope_write_kernel(const RopeWrit
     }
   }
   // the first keys and values are in flight too while the sines and cosines are computed
-  const int ku0 = max(u0, xu);
-  auto load_kv = [&](int u) {
-    const bool isk = u < xu + ku;
-    const int h = (isk ? u - xu : u - xu - ku) * GROUPS + group;
+  const int ku0 = max(u0, xu), kl = threadIdx.x % KLANES;
+  uint4 next[2];
+  auto kv_row = [&](int u) { return (u - xu) * KGROUPS + (int)threadIdx.x / KLANES; };  // a key head, or kv_heads + a value head
+  auto kv_src = [&](int r) {
+    const bool isk = r < a.kv_heads;
     const HeadsView& src = isk ? a.k : a.v;
-    if (u >= u1 || h >= a.kv_heads || page < 0) return make_uint4(0u, 0u, 0u, 0u);
-    return *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(src.data) + t * src.token_stride +
-                                           (int64_t)h * src.head_stride + 8 * l);
+    return static_cast<const uint16_t*>(src.data) + t * src.token_stride + (int64_t)(isk ? r : r - a.kv_heads) * src.head_stride;
   };
-  uint4 next = load_kv(ku0);
+  auto load_kv = [&](int u) {
+    const int r = kv_row(u);
+    next[0] = next[1] = make_uint4(0u, 0u, 0u, 0u);
+    if (u >= u1 || r >= 2 * a.kv_heads) return;  // (the slot is still on its way)
+    const uint16_t* src = kv_src(r);
+    next[0] = *reinterpret_cast<const uint4*>(src + 8 * kl);
+    next[1] = *reinterpret_cast<const uint4*>(src + D / 2 + 8 * kl);
+  };
+  if (KV) load_kv(ku0);
 
   if ((int)threadIdx.x < half) {
     const uint64_t turned = (uint64_t)(int64_t)a.rope.positions[t] * a.rope.phases[threadIdx.x];
@@ -305,50 +333,58 @@ __global__ void __launch_bounds__(kRopeThreads) rope_write_kernel(const RopeWrit
       }
     }
   }
-  if (page < 0) return;  // alike in the whole block
+  if constexpr (KV) {
+    if (page < 0) return;  // alike in the whole block
 
-  for (int u = ku0; u < u1; ++u) {
-    uint4 w = next;
-    next = load_kv(u + 1);
-    const bool isk = u < xu + ku;
-    const int h = (isk ? u - xu : u - xu - ku) * GROUPS + group;
-    const bool there = h < a.kv_heads;
-    if (isk && half > 0) {
-      const bool in = 8 * l < 2 * half;
-      float v[8];
-      unpack8(w, bf16, v);
-      if (pairs) {
+    for (int u = ku0; u < u1; ++u) {
+      uint4 w[2] = {next[0], next[1]};
+      load_kv(u + 1);
+      const int r = kv_row(u);
+      const bool there = r < 2 * a.kv_heads, isk = r < a.kv_heads;
+      if (isk && half > 0) {
+        const int hl = half >> 3;  // chunks of one half
+        const uint4 raw0 = w[0], raw1 = w[1];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (in) turn(v[2 * j], v[2 * j + 1], cs[4 * l + j], sn[4 * l + j]);
-      } else {
-        const int hl = half >> 3;  // lanes of one half
-        const bool upper = l >= hl;
-        const int lane = threadIdx.x & 31;
-        const int partner = in ? (upper ? lane - hl : lane + hl) : lane;
-        const int f = 8 * (upper ? l - hl : l);
-        float o[8];
-        unpack8(make_uint4(__shfl_sync(0xffffffffu, w.x, partner), __shfl_sync(0xffffffffu, w.y, partner),
-                           __shfl_sync(0xffffffffu, w.z, partner), __shfl_sync(0xffffffffu, w.w, partner)),
-                bf16, o);
-        if (in) {
+        for (int i = 0; i < 2; ++i) {
+          const int ch = kl + KLANES * i;
+          if (8 * ch >= 2 * half) continue;
+          float2 v[4];
+          unpack8(w[i], bf16, v);
+          if (pairs) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float c = cs[f + j], s = sn[f + j];
-            v[j] = upper ? __fadd_rn(__fmul_rn(v[j], c), __fmul_rn(o[j], s)) : __fsub_rn(__fmul_rn(v[j], c), __fmul_rn(o[j], s));
+            for (int j = 0; j < 4; ++j) turn(v[j].x, v[j].y, cs[4 * ch + j], sn[4 * ch + j]);
+          } else {
+            // the other values of the pairs: this lane's own where the whole row turns, else read once more
+            const bool upper = ch >= hl;
+            const int f = 8 * (upper ? ch - hl : ch);
+            float2 o[4];
+            unpack8(hl == KLANES ? (i == 0 ? raw1 : raw0) : *reinterpret_cast<const uint4*>(kv_src(r) + 8 * (upper ? ch - hl : ch + hl)),
+                    bf16, o);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 c = *reinterpret_cast<const float2*>(cs + f + 2 * j);
+              const float2 s = *reinterpret_cast<const float2*>(sn + f + 2 * j);
+              // less a product is plus the product of the negated sine, to the bit
+              v[j].x = __fadd_rn(__fmul_rn(v[j].x, c.x), __fmul_rn(o[j].x, upper ? s.x : -s.x));
+              v[j].y = __fadd_rn(__fmul_rn(v[j].y, c.y), __fmul_rn(o[j].y, upper ? s.y : -s.y));
+            }
           }
+          w[i] = pack8(v, bf16);
         }
       }
-      if (in) w = pack8(v, bf16);
-    }
-    const int64_t row = there ? ((page * a.kv_heads + h) << a.cache.page_shift) + off : 0;
-    uint8_t* dst = isk ? a.cache.k : a.cache.v;
-    if (!kv_quantised(a.cache.format)) {
-      if (there) *reinterpret_cast<uint4*>(dst + row * (2 * D) + 16 * l) = w;
-    } else {
-      float v[8];
-      unpack8(w, bf16, v);  // the row as its type holds it is what gets quantised
-      quantise_row<D>(v, l, a.cache.format == kKvInt8, dst, isk ? a.cache.k_scale : a.cache.v_scale, row, there);
+      const int64_t row = there ? ((page * a.kv_heads + (isk ? r : r - a.kv_heads)) << a.cache.page_shift) + off : 0;
+      uint8_t* dst = isk ? a.cache.k : a.cache.v;
+      if (!kv_quantised(a.cache.format)) {
+        if (there) {
+          *reinterpret_cast<uint4*>(dst + row * (2 * D) + 16 * kl) = w[0];
+          *reinterpret_cast<uint4*>(dst + row * (2 * D) + D + 16 * kl) = w[1];
+        }
+      } else {
+        float2 v[8];
+        unpack8(w[0], bf16, v);  // the row as its type holds it is what gets quantised
+        unpack8(w[1], bf16, v + 4);
+        quantise_row<D>(v, kl, a.cache.format == kKvInt8, dst, isk ? a.cache.k_scale : a.cache.v_scale, row, there);
+      }
     }
   }
 }
@@ -452,14 +488,13 @@ __global__ void __launch_bounds__(kRopeThreads) kv_read_kernel(const KvReadArgs 
 
 cudaError_t launch_rope_write(const RopeWriteArgs& a, int head_dim, cudaStream_t stream) {
   const int groups = kRopeThreads / (head_dim / 8);
-  const int units = (a.x_heads + groups - 1) / groups + 2 * ((a.kv_heads + groups - 1) / groups);
+  const int units = (a.x_heads + groups - 1) / groups + (2 * a.kv_heads + 2 * groups - 1) / (2 * groups);
   // one block a token, or, while that leaves SMs idle, a token's rows over several blocks
   const int per = a.tokens >= 152 * 4 ? units : a.tokens >= 152 ? (units < kRopeBatch ? units : kRopeBatch) : 1;
   const dim3 grid((unsigned)a.tokens, (unsigned)((units + per - 1) / per));
-  if (head_dim == 64)
-    rope_write_kernel<64><<<grid, kRopeThreads, 0, stream>>>(a, per);
-  else
-    rope_write_kernel<128><<<grid, kRopeThreads, 0, stream>>>(a, per);
+  auto kernel = head_dim == 64 ? (a.kv_heads > 0 ? rope_write_kernel<64, true> : rope_write_kernel<64, false>)
+                               : (a.kv_heads > 0 ? rope_write_kernel<128, true> : rope_write_kernel<128, false>);
+  kernel<<<grid, kRopeThreads, 0, stream>>>(a, per);
   return cudaGetLastError();
 }
 
