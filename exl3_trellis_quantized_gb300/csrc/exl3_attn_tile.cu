@@ -28,8 +28,8 @@
 //   one prompt of 16384 tokens, 32 and 8 heads, bf16           1411 us: 1560 TFLOP/s, 82% of a large matrix product's
 //   ten prompts of 1 to 2048 tokens, 40 and 8 heads            144 us: 920 TFLOP/s; an item has 8 to 32 blocks of
 //     about 0.95 us each, and its diagonal blocks, first scores and output (2 to 4.5 us) weigh more
-//   512 tokens over 32768 16-bit keys, 32 and 8 heads          222 us: 1230 TFLOP/s; 64 items in seven parts each, three
-//     a CTA of 73 blocks, and about 18 us for the parts' results and their join
+//   512 tokens over 32768 16-bit keys, 32 and 8 heads          218 us: 1250 TFLOP/s; 64 items in seven parts each, three
+//     a CTA of 73 blocks, and about 15 us for the parts' results and their join
 //   chunks of 129 to 700 tokens and single ones over up to 15000 8-bit keys, window 4096, 96 and 8 heads
 //     221 us: 920 TFLOP/s; four warps make fp16 rows of the codes, and an output costs 4 to 12 us
 // What holds the first below the peak is the products themselves: with the softmax reduced to passing the barriers on,
@@ -1131,7 +1131,10 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
   if (warp == 8) tmem_dealloc(tmem, 512);
 }
 
-// Joins the parts of split key ranges: a warp a row, parts in order.
+// Joins the parts of split key ranges (at most 16): a warp a row, parts in order,
+// the loads of four parts ahead of their sums (512 tokens of 32 heads in seven
+// parts: 3 us off the call, a load at a time took 20; eight or sixteen ahead gained less).
+constexpr int kJoinParts = 4;
 template <int D>
 __global__ void __launch_bounds__(256) attn_tile_join_kernel(const AttnArgs a) {
   constexpr int PER = D / 32;
@@ -1147,24 +1150,36 @@ __global__ void __launch_bounds__(256) attn_tile_join_kernel(const AttnArgs a) {
     mine = mine || (tok >= c0 && tok < c1);
   }
   if (!__any_sync(0xffffffffu, mine)) return;
-  float top = kNegInf;
-  for (int s = lane; s < a.splits; s += 32) top = fmaxf(top, a.part_ml[s * n + row].x);
+  // a lane a part: its maximum and sum, then its factor
+  const float2 ml = lane < a.splits ? a.part_ml[lane * n + row] : make_float2(kNegInf, 0.0f);
+  float top = ml.x;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  // a part without a maximum has a sum of 0, or NaN, and its output is not looked at
+  const float factor = ml.x == kNegInf ? 0.0f : ex2(ml.x - top);
+  const float part = ml.x == kNegInf ? ml.y : ml.y * factor;
   float l = 0.0f, o[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) o[i] = 0.0f;
-  for (int s = 0; s < a.splits; ++s) {
-    const float2 ml = a.part_ml[s * n + row];
-    if (ml.x == kNegInf) {
-      l += ml.y;  // 0, or NaN
-      continue;
-    }
-    const float f = ex2(ml.x - top);
-    l = fmaf(ml.y, f, l);
-    const float* src = a.part_o + (s * n + row) * D + PER * lane;
+  for (int s0 = 0; s0 < a.splits; s0 += kJoinParts) {
+    float v[kJoinParts][PER];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) o[i] = fmaf(src[i], f, o[i]);
+    for (int y = 0; y < kJoinParts; ++y) {
+      const bool in = s0 + y < a.splits && __shfl_sync(0xffffffffu, ml.x, s0 + y) != kNegInf;
+      const float* src = a.part_o + ((s0 + y) * n + row) * D + PER * lane;
+#pragma unroll
+      for (int i = 0; i < PER; i += 2) {
+        const float2 w = in ? *reinterpret_cast<const float2*>(src + i) : make_float2(0.0f, 0.0f);
+        v[y][i] = w.x, v[y][i + 1] = w.y;
+      }
+    }
+#pragma unroll
+    for (int y = 0; y < kJoinParts; ++y) {
+      const float f = __shfl_sync(0xffffffffu, factor, s0 + y);
+      l += __shfl_sync(0xffffffffu, part, s0 + y);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) o[i] = fmaf(v[y][i], f, o[i]);
+    }
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   uint16_t* dst = static_cast<uint16_t*>(a.out) + tok * a.out_token_stride +

@@ -221,3 +221,25 @@ def test_no_tokens_and_refusals():
         E.KVCache(cache.k, cache.v, None, None, "int8")
     with pytest.raises(ValueError):
         E.kv_read(cache, slots, dtype=torch.float32)
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("rot", [16, 32, 48, 64, 96, 128])
+@pytest.mark.parametrize("dim,kv,heads,tokens", [(128, 1, 3, 5), (128, 3, 6, 170), (128, 24, 24, 3), (64, 5, 5, 650), (64, 8, 16, 9)])
+def test_write_rotates_parts_of_heads(layout, rot, dim, kv, heads, tokens):
+    """Every rotated width, with the partners of a pair near and far: the fused call against rope and a plain write."""
+    if rot > dim:
+        pytest.skip("no such width")
+    x = fused(tokens, heads + 2 * kv, dim, "f16", 11, pad=0).view(tokens, heads + 2 * kv, dim)
+    q, k, v = x[:, :heads], x[:, heads:heads + kv], x[:, heads + kv:]
+    phases, amplitude = E.rope_phases(rot, scaling="linear", factor=3.0)
+    positions = torch.arange(77, 77 + tokens, dtype=torch.int32, device=DEV)
+    slots = torch.randperm((tokens // 16 + 2) * 16, generator=torch.Generator().manual_seed(3))[:tokens].to(DEV)
+    turned = E.rope(x[:, :heads + kv], positions, phases, layout, amplitude)
+    for fmt in ("f16", "int8", "int4"):
+        one, two = (E.KVCache.empty(tokens // 16 + 2, 16, kv, dim, fmt) for _ in range(2))
+        qr = E.kv_write(one, k, v, slots, q=q, positions=positions, phases=phases, layout=layout, amplitude=amplitude)
+        E.kv_write(two, turned[:, heads:], v, slots)
+        assert torch.equal(qr, turned[:, :heads])
+        for a, b in ((one.k, two.k), (one.v, two.v), (one.k_scale, two.k_scale), (one.v_scale, two.v_scale)):
+            assert a is None or torch.equal(a, b)
