@@ -97,6 +97,13 @@ constexpr int kTokenRows = 16;
 constexpr int token_ctas_per_sm(int rows) { return rows <= 8 ? 3 : 2; }
 // Keys per scheduling unit of the token kernel.
 constexpr int kTokenUnit = 64;
+// fp16 operands of the quantised formats are held in units of a power of two near their largest value.  Exponent field of
+// the power at or below x, well inside fp32's range; 1's for a 0 and for what is not finite.
+__device__ __forceinline__ uint32_t unit_exponent(float x) {
+  const uint32_t e = __float_as_uint(x) >> 23 & 255u;
+  return x == 0.0f || e == 255u ? 127u : e < 24u ? 24u : e > 230u ? 230u : e;
+}
+__device__ __forceinline__ float power(uint32_t e) { return __uint_as_float(e << 23); }  // 2^(e - 127)
 // Few query rows a sequence (max_q * group <= kTokenRows) over a paged cache.
 cudaError_t launch_attn_token(const AttnArgs& a, cudaStream_t stream);
 // Rows of a row tile of the tile kernel: it holds kTileTokenRows / group whole query tokens.

@@ -31,7 +31,7 @@
 //   512 tokens over 32768 16-bit keys, 32 and 8 heads          218 us: 1250 TFLOP/s; 64 items in seven parts each, three
 //     a CTA of 73 blocks, and about 15 us for the parts' results and their join
 //   chunks of 129 to 700 tokens and single ones over up to 15000 8-bit keys, window 4096, 96 and 8 heads
-//     221 us: 920 TFLOP/s; four warps make fp16 rows of the codes, and an output costs 4 to 12 us
+//     225 us: 900 TFLOP/s; four warps make fp16 rows of the codes, and an output costs 4 to 12 us
 // What holds the first below the peak is the products themselves: with the softmax reduced to passing the barriers on,
 // the same prompt takes 1331 us.  A score product of N = 64 reads its 128 rows of q from shared memory for half the
 // operations that N = 128 would have (48 cycles instead of 32 a k16 step), and a commit, a wait and the next issue leave
@@ -54,8 +54,9 @@
 // Quantised rows stay in the rotated basis (see exl3_rope_cache.cu): q is rotated
 // on its way into shared memory and the output on its way out, each a transform
 // within a thread.  Keys, values and q round to fp16 there, 2^-11 of each entry at the most, below the codes' own
-// steps.  (With bf16 rows the results are as exact as 64-bit sums rounded to bf16; with fp16 rows the error is 0.00055
-// of the result's norm, of which rounding the result is 0.0002.  A second fp16 term of q, as few rows have it, would
+// steps, in units of powers of two near a row's (q) and a first tile's (keys, values) largest, so that their size does
+// not matter.  (With bf16 rows the results are as exact as 64-bit sums rounded to bf16; with fp16 rows the error is
+// 0.0006 (4 bits) to 0.0009 (8 bits) of the result's norm, of which rounding the result is 0.0002.  A second fp16 term of q, as few rows have it, would
 // take 64 KB of shared memory that the rings need, and twice the score products.)
 //
 // Tensor memory: S of row tile i at columns 128 i and 128 i + 64, O at 256 + 128 i.
@@ -102,7 +103,7 @@ struct TileCfg {
   static constexpr int kRing = 2 * kTileRows * D * 2;
   static constexpr int kRawRing = kRing + kSlots * kSlot;
   static constexpr int kCtrl = kRawRing + kRaws * kRaw;  // barriers, items, a joint item's exponents
-  static constexpr int kSmem = 1024 + kCtrl + 1280;
+  static constexpr int kSmem = 1024 + kCtrl + 1312;
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(kSmem > 114 * 1024, "one CTA an SM: each allocates all of tensor memory");
   static_assert(kRing >= kTileRows * D * 4, "q's room holds a tile's output for the join");
@@ -410,6 +411,7 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
   uint8_t* answer = base + 480;                          // 16 bytes
   Item* items = reinterpret_cast<Item*>(base + 496);     // [2]
   float* jlse = reinterpret_cast<float*>(base + 768);    // [128] joint item: log2 of half 1's sums
+  float* unit = reinterpret_cast<float*>(base + 1280);   // [2][4] quantised: what an item's keys / values are in units of
   static_assert((2 * 8 + 2 * 4 + 35) * 8 + 4 <= 480 && 496 + 2 * sizeof(Item) <= 768, "control area");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -469,7 +471,8 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t s_col = tmem + lanes + 128 * i;  // buffer 0
     const uint32_t o_col = tmem + lanes + 256 + 128 * i;
-    const float c = a.scale_log2;
+    float c = a.scale_log2;  // times the units of q's row and of the keys
+    float q_unit = 1.0f;
     // Rotate the half's q where the copy has put it, a thread a row.
     auto rotate_q = [&](uint32_t parity) {
       if (!bar_wait(&qraw[i], parity)) return false;
@@ -495,13 +498,19 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
         }
       }
       hadamard_row<D>(v);
+      // in units of a power of two near its largest value, so that fp16 holds rows of any size alike
+      float top = 0.0f;
+#pragma unroll
+      for (int x = 0; x < D; ++x) top = fmaxf(top, fabsf(v[x]));
+      const uint32_t e = unit_exponent(top);
+      q_unit = power(e) * (8.0f / D);
+      const float f = power(254 - e);
 #pragma unroll
       for (int x = 0; x < D / 8; ++x) {
         uint32_t w[4];
 #pragma unroll
         for (int y = 0; y < 4; ++y)
-          w[y] = pack2<false>(v[column_value<SRC>(8 * x + 2 * y)] * (8.0f / D),
-                              v[column_value<SRC>(8 * x + 2 * y + 1)] * (8.0f / D));
+          w[y] = pack2<false>(v[column_value<SRC>(8 * x + 2 * y)] * f, v[column_value<SRC>(8 * x + 2 * y + 1)] * f);
         sts128(at + row_chunk(r, x), w[0], w[1], w[2], w[3]);
       }
       fence_proxy_async_smem();
@@ -540,6 +549,7 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
         ok = bar_wait(&sfull[2 * i + buf], blocks >> 1 & 1u);
         if (!ok) break;
         tc_fence_after();
+        if (C::kQuant && b == sp.b0) c = a.scale_log2 * q_unit * unit[n & 3u];
         float s[kBlock];
         const uint32_t col = s_col + kBlock * buf;
 #pragma unroll
@@ -634,6 +644,7 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // a row that saw no key gives zeros
         f0 *= inv, f1 *= inv;
       }
+      if (C::kQuant) f0 *= unit[4 + (n & 3u)];
       if (!any) f0 = 0.0f;
       float* jo = reinterpret_cast<float*>(data + C::kQ) + r;  // [D][128]: a thread a column
       if (ok && it.joint && i == 1) jlse[r] = m + log2f(l);
@@ -938,8 +949,8 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
                 const int key = t + lane * page_rows;
                 const int id = a.table[(int64_t)it.b * a.table_width + (key >> a.cache.page_shift)];
                 page_ok = id >= 0 && id < a.cache.num_pages;
-                // an id outside the cache: past the map's last row, which reads as zeros (16 bits); page 0 in its
-                // place (the codes count for something, but nothing outside the cache is read)
+                // an id outside the cache: past the map's last row, which reads as zeros (16 bits); page 0's codes
+                // with scales of zero
                 row = page_ok ? (((int64_t)id * a.kv_heads + it.kvh) << a.cache.page_shift) +
                                     (key & ((1 << a.cache.page_shift) - 1))
                               : C::kQuant ? 0 : (a.cache.num_pages * a.kv_heads) << a.cache.page_shift;
@@ -982,13 +993,24 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
                 }
               } else {
                 uint8_t* dst = data + C::kRawRing + s * C::kRaw;
-                if (lane == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)(copies * page_rows * (C::kRowBytes + 2)));
+                const int bad = __popc(__ballot_sync(0xffffffffu, !page_ok));
+                if (bad > 0) {
+                  if (!page_ok) {
+                    for (int x = 0; x < page_rows * 2; x += 16)
+                      sts128(smem_u32(dst + C::kCodes + lane * page_rows * 2 + x), 0u, 0u, 0u, 0u);
+                    fence_proxy_async_smem();
+                  }
+                  __syncwarp();
+                }
+                if (lane == 0)
+                  mbar_arrive_expect_tx(&full[s], (uint32_t)(copies * page_rows * (C::kRowBytes + 2) - bad * page_rows * 2));
                 __syncwarp();
                 if (lane < copies) {
                   tma_bulk_g2s(dst + lane * page_rows * C::kRowBytes, (value ? a.cache.v : a.cache.k) + row * C::kRowBytes,
                                (uint32_t)(page_rows * C::kRowBytes), &full[s]);
-                  tma_bulk_g2s(dst + C::kCodes + lane * page_rows * 2, (value ? a.cache.v_scale : a.cache.k_scale) + row,
-                               (uint32_t)(page_rows * 2), &full[s]);
+                  if (page_ok)
+                    tma_bulk_g2s(dst + C::kCodes + lane * page_rows * 2, (value ? a.cache.v_scale : a.cache.k_scale) + row,
+                                 (uint32_t)(page_rows * 2), &full[s]);
                 }
                 __syncwarp();
               }
@@ -1065,6 +1087,7 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
     Item it;
     uint32_t n = 0, raw = 0, filled = 0;
     while (ok && read_item(n, &it)) {
+      float f[2] = {1.0f, 1.0f};  // one over the units of the item's keys and values
       for (int x = 0; ok && x < 2 * (it.jhi - it.jlo); ++x, ++raw, ++filled) {
         const uint32_t rs = raw % C::kRaws, s = filled % NS;
         ok = bar_wait(&rawfull[rs], raw / C::kRaws & 1u) && bar_wait(&kvempty[s], (filled / NS & 1u) ^ 1u);
@@ -1072,6 +1095,20 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
         const int left = it.kv_len - it.base - (it.jlo + (x >> 1)) * kKeys;  // keys before the length
         const uint32_t src = smem_u32(data + C::kRawRing) + rs * C::kRaw;
         const uint32_t dst = smem_u32(data + C::kRing) + s * C::kSlot;
+        if (x < 2) {
+          // The item's keys (values) are in units of eight times the largest scale of its first tile, to a power of
+          // two: codes then reach 32 there, and scales 2000 times larger and smaller still find room in fp16.  Every
+          // warp comes to the same.  Rows of four items may be on their way.
+          uint32_t w[2];
+          asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(src + C::kCodes + 8 * lane) : "memory");
+          float top = 0.0f;  // a NaN does not count
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            if (4 * lane + y < left) top = fmaxf(top, fabsf(__uint_as_float(y & 1 ? w[y >> 1] & 0xFFFF0000u : w[y >> 1] << 16)));
+          const uint32_t e = unit_exponent(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)))) + 3;
+          (x ? f[1] : f[0]) = power(254 - e);
+          if (lw == 0 && lane == 0) unit[4 * x + (n & 3u)] = power(e);
+        }
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
           const int rr = 32 * lw + p * RPP + lane / LPR;
@@ -1086,7 +1123,7 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
             sb = (uint32_t)s16 << 16;
           }
           const bool none = rr >= left;  // past the length: zeros
-          const float sf = __uint_as_float(sb);
+          const float sf = __uint_as_float(sb) * ((x & 1) ? f[1] : f[0]);
           const uint32_t sh = pack2<false>(sf, sf);
           if constexpr (SRC == kPaged8) {
             uint32_t h[8];

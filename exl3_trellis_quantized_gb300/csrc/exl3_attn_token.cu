@@ -31,7 +31,8 @@
 // own ring of asynchronous copies and its own (m, l, o), joined at the item's end.
 //
 // Quantised rows stay in the rotated basis (see exl3_rope_cache.cu): q is
-// rotated by the D-point Hadamard transform times 8/D once, the output once.  The
+// rotated by the D-point Hadamard transform times 8/D once, the output once, and
+// held in units of a power of two near its largest value.  The
 // rotated q is not exact in fp16: for fp16 queries it goes in as two fp16 terms
 // (22 bits), since one alone moved the outputs by 1.7 times their own rounding
 // (bf16 outputs round eight times coarser: one term).
@@ -247,7 +248,8 @@ struct TokenCfg {
   static constexpr int kJoin = kRows * D * 4 + kRows * 8;  // a warp's (o, m, l) at an item's end
   static constexpr int kWarpBytes = ((kRing > kJoin ? kRing : kJoin) + 127) / 128 * 128;
   static constexpr int kQBytes = kQuant ? 2 * kRows * D * 2 : 0;  // the rotated q and the fragments of its second term
-  static constexpr int kSmem = kWarps * kWarpBytes + kQBytes;
+  static constexpr int kTops = kWarps * kWarpBytes + kQBytes;     // [kWarps] largest magnitudes of the rotated q
+  static constexpr int kSmem = kTops + (kQuant ? 4 * kWarps : 0);
   static constexpr int kChunks = kRow / 16;  // 16-byte chunks of a row
   static constexpr int kTpr = kThreads / kRows;  // threads of a row where the CTA works on whole rows
   static constexpr int kPer = D / kTpr;          // and values of each
@@ -424,10 +426,11 @@ __global__ void __launch_bounds__(kThreads, token_ctas_per_sm(8 * NR)) attn_toke
 #pragma unroll
     for (int i = 0; i < C::kStages - 1; ++i) issue(i);
 
+    float unit = 1.0f;  // of a score over a quantised cache: the rotated q's units, 8/D and the scale
     // the second term of the rotated q, only for fp16 queries: [n][k][lane] fragments
     const uint32_t qlo = smem_u32(smem) + kWarps * C::kWarpBytes + C::kRows * D * 2;
     if constexpr (C::kQuant) {
-      // rotate, times 8/D, to fp16 in shared memory, one term after the other
+      // rotate, to fp16 in shared memory, one term after the other
       uint16_t* qs = reinterpret_cast<uint16_t*>(smem + kWarps * C::kWarpBytes);
       float v[C::kPer];
 #pragma unroll
@@ -436,8 +439,18 @@ __global__ void __launch_bounds__(kThreads, token_ctas_per_sm(8 * NR)) attn_toke
         v[2 * i + 1] = to_f32((uint16_t)(qraw[i] >> 16), a.bf16 != 0);
       }
       hadamard_threads<C::kPer, C::kTpr>(v, part);
+      // in units of a power of two near the rows' largest value, so that fp16 holds any q
+      float top = 0.0f;
 #pragma unroll
-      for (int i = 0; i < C::kPer; ++i) v[i] *= 8.0f / D;
+      for (int i = 0; i < C::kPer; ++i) top = fmaxf(top, fabsf(v[i]));
+      uint32_t* tops = reinterpret_cast<uint32_t*>(smem + C::kTops);
+      const uint32_t mine_top = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+      if (lane == 0) tops[warp] = mine_top;
+      __syncthreads();
+      const uint32_t e = unit_exponent(__uint_as_float(max(max(tops[0], tops[1]), max(tops[2], tops[3]))));
+      unit = a.scale_log2 * (8.0f / D) * power(e);
+#pragma unroll
+      for (int i = 0; i < C::kPer; ++i) v[i] *= power(254u - e);
       // fragments in the order in which the codes come out of their words
       auto fragments = [&](uint32_t (&dst)[KS][2], int n) {
         const uint16_t* src = qs + (8 * n + g) * D;
@@ -580,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, token_ctas_per_sm(8 * NR)) attn_toke
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
             const uint32_t at = kb + 2 * C::kSide + 2 * (16 * x + 8 * y + g);
-            const float kc = lds_bf16(at) * a.scale_log2;
+            const float kc = lds_bf16(at) * unit;
             // a NaN scale (a row that reads back as NaN) stays one
             const float vc = max_nan(lds_bf16(at + 2 * C::kStep), 7.888609052210118e-31f);
             const float lv = lg2(vc);

@@ -332,3 +332,45 @@ def test_refusals():
     none = torch.empty((0, 4, 128), dtype=torch.bfloat16, device=DEV)
     assert E.attention_prompt(none, none[:, :2], none[:, :2], torch.zeros(1, dtype=torch.int32, device=DEV)).shape == (0, 4, 128)
     assert E.device_status() == 0
+
+
+@pytest.mark.parametrize("fmt", ["int8", "int4"])
+@pytest.mark.parametrize("q_len", [1, 4, 150])
+@pytest.mark.parametrize("q_by,k_by,v_by", [(1.0, 1.0, 1e-6), (1e5, 1e-5, 1e5), (1e-6, 1e6, 1e-12), (1.0, 1.0, 1e-24), (3e4, 1e-3, 3e4)])
+def test_paged_quantised_sizes(fmt, q_len, q_by, k_by, v_by):
+    """Queries, keys and values of any size, some tokens' 64 times those of others."""
+    lens, heads, kv, dim, page = 333, 8, 2, 128, 32
+    g = torch.Generator().manual_seed(4)
+    each = 2.0 ** torch.randint(-3, 4, (lens, 1, 1), generator=g)
+    k = (torch.randn((lens, kv, dim), generator=g) * k_by * each.clamp(max=1.0)).to(torch.bfloat16)
+    v = (torch.randn((lens, kv, dim), generator=g) * v_by * each.flip(0)).to(torch.bfloat16)
+    q = (torch.randn((q_len, heads, dim), generator=g) * q_by).to(torch.bfloat16)
+    pages = (lens + page - 1) // page
+    cache = E.KVCache.empty(pages, page, kv, dim, fmt)
+    E.kv_write(cache, k.to(DEV), v.to(DEV), torch.arange(lens, device=DEV))
+    table = torch.arange(pages, dtype=torch.int32, device=DEV)[None]
+    got = E.attention_paged(q.to(DEV), cache, table, cu([q_len]), torch.tensor([lens], dtype=torch.int32, device=DEV), q_len, lens)
+    torch.cuda.synchronize()
+    assert E.device_status() == 0
+    kk, vv = (A.read_back(*A.quantise(t.float().numpy(), fmt)) for t in (k, v))
+    want, tol = bound(q.double().numpy(), kk, vv, 0, None, "bf16", fmt)
+    assert_close(f64(got), want, tol, f"{q_len} tokens")
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int8", "int4"])
+@pytest.mark.parametrize("q_len", [1, 40])
+def test_page_outside_the_cache_counts_as_zeros(fmt, q_len):
+    kv_len, page = 300, 32
+    cache, table, rows = make_cache([kv_len], 2, 128, page, fmt, 15)
+    q = torch.randn((q_len, 8, 128), generator=torch.Generator().manual_seed(6)).to(torch.bfloat16)
+    k, v = (r.copy() for r in rows[0])
+    for at, entry in ((2, -1), (4, 10**6), (7, -2**31)):
+        table[0, at] = entry
+        k[at * page:(at + 1) * page] = 0.0
+        v[at * page:(at + 1) * page] = 0.0
+    lens = torch.tensor([kv_len], dtype=torch.int32, device=DEV)
+    got = E.attention_paged(q.to(DEV), cache, table, cu([q_len]), lens, q_len, kv_len)
+    torch.cuda.synchronize()
+    assert E.device_status() == 0
+    want, tol = bound(q.double().numpy(), k, v, 0, None, "bf16", fmt)
+    assert_close(f64(got), want, tol, f"{q_len} tokens")
