@@ -56,8 +56,8 @@
 // within a thread.  Keys, values and q round to fp16 there, 2^-11 of each entry at the most, below the codes' own
 // steps, in units of powers of two near a row's (q) and a first tile's (keys, values) largest, so that their size does
 // not matter.  (With bf16 rows the results are as exact as 64-bit sums rounded to bf16; with fp16 rows the error is
-// 0.0006 (4 bits) to 0.0009 (8 bits) of the result's norm, of which rounding the result is 0.0002.  A second fp16 term of q, as few rows have it, would
-// take 64 KB of shared memory that the rings need, and twice the score products.)
+// 0.0006 (4 bits) to 0.0009 (8 bits) of the result's norm, of which rounding the result is 0.0002.  A second fp16
+// term of q, as few rows have it, would take 64 KB of shared memory that the rings need, and twice the score products.)
 //
 // Tensor memory: S of row tile i at columns 128 i and 128 i + 64, O at 256 + 128 i.
 #include <cuda_bf16.h>
