@@ -407,12 +407,13 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
   uint64_t* qempty = qraw + 2;                           // [2] a half's scores of an item are done
   uint64_t* clc = qempty + 2;                              // answer to a cancel request
   uint64_t* mdrain = clc + 1;                            // [2] MMAs issued before a wait gave up
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mdrain + 2);
-  uint8_t* answer = base + 480;                          // 16 bytes
-  Item* items = reinterpret_cast<Item*>(base + 496);     // [2]
+  uint64_t* jopen = mdrain + 2;                          // joint item: half 0 is done with q's room
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(jopen + 1);
+  uint8_t* answer = base + 496;                          // 16 bytes
+  Item* items = reinterpret_cast<Item*>(base + 512);     // [2]
   float* jlse = reinterpret_cast<float*>(base + 768);    // [128] joint item: log2 of half 1's sums
   float* unit = reinterpret_cast<float*>(base + 1280);   // [2][4] quantised: what an item's keys / values are in units of
-  static_assert((2 * 8 + 2 * 4 + 35) * 8 + 4 <= 480 && 496 + 2 * sizeof(Item) <= 768, "control area");
+  static_assert(((2 * 8 + 2 * 4) + (8 + 28)) * 8 + 4 <= 496 && 512 + 2 * sizeof(Item) <= 768, "control area");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int group = a.heads / a.kv_heads;
@@ -440,6 +441,7 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
       mbar_init(&iempty[i], 11 + C::kConverters);
       mbar_init(&mdrain[i], 1);
     }
+    mbar_init(jopen, 4);
     mbar_init(jfull, 4);
     mbar_init(jfree, 4);
     mbar_init(clc, 1);
@@ -523,7 +525,7 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
     Item it;
     uint32_t n = 0, jphase = 0;
     uint32_t blocks = 0;  // of this half so far: the buffers and their phases
-    uint32_t oph = 0;     // phases of the halves' outputs (a bit a half; an item without blocks of a half has none)
+    uint32_t oph = 0;     // phase of this half's outputs (an item without blocks of it has none)
     bool have = read_item(n, &it);
     uint32_t qph = 0;
     // this thread's row: query token (from the half's first) and head (of the group); none past the tile's whole tokens
@@ -619,12 +621,20 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
       // ---- the rows' output.  Tensor memory is read sixteen rows at a time, a quad of lanes two of them: of rows
       // g and g + 8 a lane gets columns 8x + 2q, + 1.
       const int g = lane >> 2, q = lane & 3;
-      // a joint item's meeting place is q's room, of both halves
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (it.span[h].b0 >= it.span[h].b1) continue;
-        if (ok && (h == i || it.joint)) ok = bar_wait(&ofull[h], oph >> h & 1u);
-        oph ^= 1u << h;
+      if (used(it)) {
+        ok = ok && bar_wait(&ofull[i], oph);
+        oph ^= 1u;
+      }
+      // A joint item's meeting place is q's room, of both halves: half 1 may write there once half 0's products of this
+      // item and of those before it are done.  (A look at half 0's ofull cannot tell: half 0 may be an item behind,
+      // whose phase of that barrier has the other parity, or have no blocks here.)
+      if (it.joint) {
+        if (i == 0) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(jopen);
+        } else if (ok) {
+          ok = bar_wait(jopen, jphase);
+        }
       }
       tc_fence_after();
       // this thread's row: its own part times f0, a joint item's other half's (already divided by its sum) times f1
