@@ -31,7 +31,8 @@
 //   512 tokens over 32768 16-bit keys, 32 and 8 heads          218 us: 1250 TFLOP/s; 64 items in seven parts each, three
 //     a CTA of 73 blocks, and about 15 us for the parts' results and their join
 //   chunks of 129 to 700 tokens and single ones over up to 15000 8-bit keys, window 4096, 96 and 8 heads
-//     225 us: 900 TFLOP/s; four warps make fp16 rows of the codes, and an output costs 4 to 12 us
+//     226 us: 895 TFLOP/s; four warps make fp16 rows of the codes, four passes' codes loaded ahead (one after the other:
+//     246), and an output costs 4 to 12 us
 // What holds the first below the peak is the products themselves: with the softmax reduced to passing the barriers on,
 // the same prompt takes 1331 us.  A score product of N = 64 reads its 128 rows of q from shared memory for half the
 // operations that N = 128 would have (48 cycles instead of 32 a k16 step), and a commit, a wait and the next issue leave
@@ -54,8 +55,10 @@
 // Quantised rows stay in the rotated basis (see exl3_rope_cache.cu): q is rotated
 // on its way into shared memory and the output on its way out, each a transform
 // within a thread.  Keys, values and q round to fp16 there, 2^-11 of each entry at the most, below the codes' own
-// steps, in units of powers of two near a row's (q) and a first tile's (keys, values) largest, so that their size does
-// not matter.  (With bf16 rows the results are as exact as 64-bit sums rounded to bf16; with fp16 rows the error is
+// steps, in units of powers of two: a row's of q, and of every 16 keys and 16 values, by their largest scale, which
+// nothing can pass.  A group's key unit is a factor of its scores, its value unit an addend of its exponents, so groups
+// of any sizes meet (one unit an item, from its first tile's scales, made a later row of 2000 times the scale
+// infinite).  (With bf16 rows the results are as exact as 64-bit sums rounded to bf16; with fp16 rows the error is
 // 0.0006 (4 bits) to 0.0009 (8 bits) of the result's norm, of which rounding the result is 0.0002.  A second fp16
 // term of q, as few rows have it, would take 64 KB of shared memory that the rings need, and twice the score products.)
 //
@@ -78,6 +81,19 @@ constexpr int kBlock = 64;      // keys of a step
 constexpr int kTileRows = 128;  // rows of a tile; a CTA has two tiles
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kSlack = 8.0f;
+
+constexpr int kUnitKeys = 16;   // keys that share a unit (quantised formats)
+// What the fp16 operands of a tile of a quantised cache are in units of: powers of two for every 16 keys and values.
+struct Units {
+  int k[kKeys / kUnitKeys], v[kKeys / kUnitKeys];  // log2
+};
+// A group's largest scale lies in [2^kScaleTop, 2^(kScaleTop + 1)) of its unit: codes then reach 2^15, and scales 2^24
+// times smaller still have all their bits.  No unit is below 2^kLeastUnit, so that sums of weights, which the values'
+// units divide, stay within fp32.
+constexpr int kScaleTop = 7, kLeastUnit = -80;
+// Weights over a quantised cache may reach 2^15 (2^8 by the maximum's slack), so that those far below the largest are
+// still normal fp16 numbers.
+constexpr float kRoom = 7.0f;
 
 template <int D, int SRC>
 struct TileCfg {
@@ -102,8 +118,8 @@ struct TileCfg {
   static constexpr int kQ = 0;
   static constexpr int kRing = 2 * kTileRows * D * 2;
   static constexpr int kRawRing = kRing + kSlots * kSlot;
-  static constexpr int kCtrl = kRawRing + kRaws * kRaw;  // barriers, items, a joint item's exponents
-  static constexpr int kSmem = 1024 + kCtrl + 1312;
+  static constexpr int kCtrl = kRawRing + kRaws * kRaw;  // barriers, items, a joint item's exponents, tiles' units
+  static constexpr int kSmem = 1024 + kCtrl + 1280 + (kQuant ? kSlots / 2 * (int)sizeof(Units) : 0);
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(kSmem > 114 * 1024, "one CTA an SM: each allocates all of tensor memory");
   static_assert(kRing >= kTileRows * D * 4, "q's room holds a tile's output for the join");
@@ -412,7 +428,7 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
   uint8_t* answer = base + 496;                          // 16 bytes
   Item* items = reinterpret_cast<Item*>(base + 512);     // [2]
   float* jlse = reinterpret_cast<float*>(base + 768);    // [128] joint item: log2 of half 1's sums
-  float* unit = reinterpret_cast<float*>(base + 1280);   // [2][4] quantised: what an item's keys / values are in units of
+  Units* units = reinterpret_cast<Units*>(base + 1280);  // [NS / 2] quantised: of the tile whose values are in slot 2x + 1
   static_assert(((2 * 8 + 2 * 4) + (8 + 28)) * 8 + 4 <= 496 && 512 + 2 * sizeof(Item) <= 768, "control area");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -473,8 +489,8 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t s_col = tmem + lanes + 128 * i;  // buffer 0
     const uint32_t o_col = tmem + lanes + 256 + 128 * i;
-    float c = a.scale_log2;  // times the units of q's row and of the keys
-    float q_unit = 1.0f;
+    float c = a.scale_log2;  // quantised: times the unit of q's row, and a group's times the unit of its keys
+    uint32_t tiles = 0;      // quantised: key tiles of the items before
     // Rotate the half's q where the copy has put it, a thread a row.
     auto rotate_q = [&](uint32_t parity) {
       if (!bar_wait(&qraw[i], parity)) return false;
@@ -505,7 +521,7 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
 #pragma unroll
       for (int x = 0; x < D; ++x) top = fmaxf(top, fabsf(v[x]));
       const uint32_t e = unit_exponent(top);
-      q_unit = power(e) * (8.0f / D);
+      c = a.scale_log2 * (power(e) * (8.0f / D));
       const float f = power(254 - e);
 #pragma unroll
       for (int x = 0; x < D / 8; ++x) {
@@ -551,7 +567,16 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
         ok = bar_wait(&sfull[2 * i + buf], blocks >> 1 & 1u);
         if (!ok) break;
         tc_fence_after();
-        if (C::kQuant && b == sp.b0) c = a.scale_log2 * q_unit * unit[n & 3u];
+        int ek[4] = {}, ev[4] = {};  // quantised: this block's units
+        if constexpr (C::kQuant) {
+          const uint32_t t = tiles + (uint32_t)((b >> 1) - it.jlo), x = t % (NS / 2);
+          ok = bar_wait(&kvfull[2 * x + 1], t / (NS / 2) & 1u);  // they come with the tile's values
+          if (!ok) break;
+          const int4 k4 = *reinterpret_cast<const int4*>(units[x].k + 4 * (b & 1));
+          const int4 v4 = *reinterpret_cast<const int4*>(units[x].v + 4 * (b & 1));
+          ek[0] = k4.x, ek[1] = k4.y, ek[2] = k4.z, ek[3] = k4.w;
+          ev[0] = v4.x, ev[1] = v4.y, ev[2] = v4.z, ev[3] = v4.w;
+        }
         float s[kBlock];
         const uint32_t col = s_col + kBlock * buf;
 #pragma unroll
@@ -565,13 +590,30 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
             if (x > hi || x < lo) s[x] = kNegInf;
         }
         float t[4];
+        float top;
+        float cg[4];  // quantised: factor of a group's scores
+        if constexpr (C::kQuant) {
+          // The values' units go into the exponents: weight times unit is what the product with the values needs, and
+          // what the maximum is taken of.
 #pragma unroll
-        for (int x = 0; x < 4; ++x) t[x] = max3(s[x], s[x + 4], s[x + 8]);
+          for (int y = 0; y < 4; ++y) {
+            const float* x = s + kUnitKeys * y;
+            t[y] = max3(max3(x[0], x[1], x[2]), x[3], x[4]);
+            const float u = max3(max3(x[5], x[6], x[7]), x[8], x[9]), v = max3(max3(x[10], x[11], x[12]), x[13], x[14]);
+            t[y] = fmaxf(max3(t[y], u, v), x[15]);
+            cg[y] = c * power(127 + ek[y]);
+            t[y] = fmaf(t[y], cg[y], (float)ev[y]);
+          }
+          top = fmaxf(max3(t[0], t[1], t[2]), t[3]);
+        } else {
 #pragma unroll
-        for (int x = 12; x < 60; x += 8)
+          for (int x = 0; x < 4; ++x) t[x] = max3(s[x], s[x + 4], s[x + 8]);
 #pragma unroll
-          for (int y = 0; y < 4; ++y) t[y] = max3(t[y], s[x + y], s[x + y + 4]);
-        const float top = fmaxf(max3(t[0], t[1], t[2]), max3(max3(t[3], s[60], s[61]), s[62], s[63])) * c;
+          for (int x = 12; x < 60; x += 8)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) t[y] = max3(t[y], s[x + y], s[x + y + 4]);
+          top = fmaxf(max3(t[0], t[1], t[2]), max3(max3(t[3], s[60], s[61]), s[62], s[63])) * c;
+        }
         const bool up = top > m + kSlack;
         if (__any_sync(0xffffffffu, up)) {
           const float f = up ? ex2(m - top) : 1.0f;
@@ -594,18 +636,32 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
         }
         any = true;
         // nothing seen yet: all scores are -inf, any finite reference does
-        const float ref = m == kNegInf ? 0.0f : m;
-        const float2 cc = make_float2(c, c), mm = make_float2(-ref, -ref);
+        const float ref = m == kNegInf ? 0.0f : C::kQuant ? m - kRoom : m;
         uint32_t w[32];
+        constexpr int kGroup = C::kQuant ? kUnitKeys : kBlock;
 #pragma unroll
-        for (int y = 0; y < 32; y += 2) {
-          const float* x = s + 2 * y;
-          float2 p = fma2(make_float2(x[0], x[1]), cc, mm), q = fma2(make_float2(x[2], x[3]), cc, mm);
-          p.x = ex2(p.x), p.y = ex2(p.y), q.x = ex2(q.x), q.y = ex2(q.y);
-          l0 = add2(l0, p);
-          l1 = add2(l1, q);
-          w[y] = pack2<BF16>(p.x, p.y);
-          w[y + 1] = pack2<BF16>(q.x, q.y);
+        for (int y = 0; y < 32; y += kGroup / 2) {
+          const int gi = y / (kUnitKeys / 2);
+          const float cf = C::kQuant ? cg[gi] : c, mf = C::kQuant ? (float)ev[gi] - ref : -ref;
+          const float2 cc = make_float2(cf, cf), mm = make_float2(mf, mf);
+          float2 g0 = C::kQuant ? make_float2(0.0f, 0.0f) : l0, g1 = C::kQuant ? make_float2(0.0f, 0.0f) : l1;
+#pragma unroll
+          for (int z = y; z < y + kGroup / 2; z += 2) {
+            const float* x = s + 2 * z;
+            float2 p = fma2(make_float2(x[0], x[1]), cc, mm), q = fma2(make_float2(x[2], x[3]), cc, mm);
+            p.x = ex2(p.x), p.y = ex2(p.y), q.x = ex2(q.x), q.y = ex2(q.y);
+            g0 = add2(g0, p);
+            g1 = add2(g1, q);
+            w[z] = pack2<BF16>(p.x, p.y);
+            w[z + 1] = pack2<BF16>(q.x, q.y);
+          }
+          if constexpr (C::kQuant) {
+            const float inv = power(127 - ev[gi]);  // the sum is of the weights alone
+            l0 = fma2(g0, make_float2(inv, inv), l0);
+            l1 = fma2(g1, make_float2(inv, inv), l1);
+          } else {
+            l0 = g0, l1 = g1;
+          }
         }
         tmem_st_x32(col, w);
         tmem_st_wait();
@@ -615,6 +671,10 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
       }
 
       float l = (l0.x + l0.y) + (l1.x + l1.y);
+      if (C::kQuant) {
+        m -= kRoom;  // what l and O are held relative to
+        tiles += (uint32_t)(it.jhi - it.jlo);
+      }
       Item next;
       have = ok && read_item(n + 1, &next);
 
@@ -654,7 +714,6 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // a row that saw no key gives zeros
         f0 *= inv, f1 *= inv;
       }
-      if (C::kQuant) f0 *= unit[4 + (n & 3u)];
       if (!any) f0 = 0.0f;
       float* jo = reinterpret_cast<float*>(data + C::kQ) + r;  // [D][128]: a thread a column
       if (ok && it.joint && i == 1) jlse[r] = m + log2f(l);
@@ -1092,59 +1151,63 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
     constexpr int LPR = C::kRowBytes / 16;  // lanes of a row
     constexpr int RPP = 32 / LPR;           // rows a warp takes at a time
     constexpr int NP = 32 / RPP;            // passes over the warp's 32 rows
+    constexpr int AHEAD = NP < 4 ? NP : 4;  // passes whose codes are read at a time
     const int lw = warp - 12, sub = lane % LPR;
     bool ok = true;
     Item it;
     uint32_t n = 0, raw = 0, filled = 0;
+    static_assert(kUnitKeys == 16, "a warp's 32 rows are two groups");
     while (ok && read_item(n, &it)) {
-      float f[2] = {1.0f, 1.0f};  // one over the units of the item's keys and values
+      int ek[2] = {};  // units of this warp's two groups of the tile's keys
       for (int x = 0; ok && x < 2 * (it.jhi - it.jlo); ++x, ++raw, ++filled) {
         const uint32_t rs = raw % C::kRaws, s = filled % NS;
-        ok = bar_wait(&rawfull[rs], raw / C::kRaws & 1u) && bar_wait(&kvempty[s], (filled / NS & 1u) ^ 1u);
+        ok = bar_wait(&rawfull[rs], raw / C::kRaws & 1u);
         if (!ok) break;
         const int left = it.kv_len - it.base - (it.jlo + (x >> 1)) * kKeys;  // keys before the length
         const uint32_t src = smem_u32(data + C::kRawRing) + rs * C::kRaw;
         const uint32_t dst = smem_u32(data + C::kRing) + s * C::kSlot;
-        if (x < 2) {
-          // The item's keys (values) are in units of eight times the largest scale of its first tile, to a power of
-          // two: codes then reach 32 there, and scales 2000 times larger and smaller still find room in fp16.  Every
-          // warp comes to the same.  Rows of four items may be on their way.
-          uint32_t w[2];
-          asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(src + C::kCodes + 8 * lane) : "memory");
-          float top = 0.0f;  // a NaN does not count
+        uint32_t ww[AHEAD][4];
+        auto load = [&](int p) {
 #pragma unroll
-          for (int y = 0; y < 4; ++y)
-            if (4 * lane + y < left) top = fmaxf(top, fabsf(__uint_as_float(y & 1 ? w[y >> 1] & 0xFFFF0000u : w[y >> 1] << 16)));
-          const uint32_t e = unit_exponent(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)))) + 3;
-          (x ? f[1] : f[0]) = power(254 - e);
-          if (lw == 0 && lane == 0) unit[4 * x + (n & 3u)] = power(e);
+          for (int y = 0; y < AHEAD; ++y)
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(ww[y][0]), "=r"(ww[y][1]), "=r"(ww[y][2]), "=r"(ww[y][3])
+                         : "r"(src + (32 * lw + (p + y) * RPP + lane / LPR) * C::kRowBytes + 16 * sub)
+                         : "memory");
+        };
+        // row 32 lw + lane: its scale in units of its group's, from the group's largest scale; 0 past the length, which
+        // makes zeros of any codes
+        uint16_t s16;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(s16) : "r"(src + C::kCodes + 2 * (32 * lw + lane)) : "memory");
+        load(0);
+        const uint32_t scale = 32 * lw + lane < left ? (uint32_t)s16 << 16 : 0u;
+        const uint32_t mag = (scale & 0x7FFFFFFFu) < 0x7F800000u ? scale & 0x7FFFFFFFu : 0u;  // a NaN row does not count
+        int e[2];
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+          e[y] = max((int)(__reduce_max_sync(0xffffffffu, lane >> 4 == y ? mag : 0u) >> 23) - 127 - kScaleTop, kLeastUnit);
+        const float sf = __uint_as_float(scale) * power(127 - (lane >> 4 ? e[1] : e[0]));
+        const uint32_t mine = pack2<false>(sf, sf);
+        ok = bar_wait(&kvempty[s], (filled / NS & 1u) ^ 1u);
+        if (!ok) break;
+        if (!(x & 1)) {
+          ek[0] = e[0], ek[1] = e[1];
+        } else if (lane == 0) {
+          units[s >> 1].k[2 * lw] = ek[0], units[s >> 1].k[2 * lw + 1] = ek[1];
+          units[s >> 1].v[2 * lw] = e[0], units[s >> 1].v[2 * lw + 1] = e[1];
         }
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
           const int rr = 32 * lw + p * RPP + lane / LPR;
-          uint32_t ww[4], sb;
-          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(ww[0]), "=r"(ww[1]), "=r"(ww[2]), "=r"(ww[3])
-                       : "r"(src + rr * C::kRowBytes + 16 * sub)
-                       : "memory");
-          {
-            uint16_t s16;
-            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(s16) : "r"(src + C::kCodes + 2 * rr) : "memory");
-            sb = (uint32_t)s16 << 16;
-          }
-          const bool none = rr >= left;  // past the length: zeros
-          const float sf = __uint_as_float(sb) * ((x & 1) ? f[1] : f[0]);
-          const uint32_t sh = pack2<false>(sf, sf);
+          if (p > 0 && p % AHEAD == 0) load(p);
+          const uint32_t(&w4)[4] = ww[p % AHEAD];
+          const uint32_t sh = __shfl_sync(0xffffffffu, mine, rr & 31);
           if constexpr (SRC == kPaged8) {
             uint32_t h[8];
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
-              h[2 * y] = hmul2(hsub2(__byte_perm(ww[y], 0x64646464u, 0x4140), 0x64806480u), sh);
-              h[2 * y + 1] = hmul2(hsub2(__byte_perm(ww[y], 0x64646464u, 0x4342), 0x64806480u), sh);
-            }
-            if (none) {
-#pragma unroll
-              for (int y = 0; y < 8; ++y) h[y] = 0u;
+              h[2 * y] = hmul2(hsub2(__byte_perm(w4[y], 0x64646464u, 0x4140), 0x64806480u), sh);
+              h[2 * y + 1] = hmul2(hsub2(__byte_perm(w4[y], 0x64646464u, 0x4342), 0x64806480u), sh);
             }
             sts128(dst + row_chunk(rr, 2 * sub), h[0], h[1], h[2], h[3]);
             sts128(dst + row_chunk(rr, 2 * sub + 1), h[4], h[5], h[6], h[7]);
@@ -1154,11 +1217,10 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
               uint32_t h[4];
 #pragma unroll
               for (int z = 0; z < 2; ++z) {
-                const uint32_t w = ww[y] >> (8 * z);
+                const uint32_t w = w4[y] >> (8 * z);
                 h[2 * z] = hmul2(hsub2((w & 0x000F000Fu) | 0x64006400u, 0x64086408u), sh);
                 h[2 * z + 1] = hmul2(hfma2((w & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u), sh);
               }
-              if (none) h[0] = h[1] = h[2] = h[3] = 0u;
               sts128(dst + row_chunk(rr, 4 * sub + y), h[0], h[1], h[2], h[3]);
             }
           }

@@ -338,7 +338,10 @@ exl3_status_t exl3_rope(const exl3_heads_t* x, exl3_dtype_t dtype, int64_t token
  * A row with a NaN or an infinity gets zero codes and a NaN scale and reads back as NaN.  The values read back are
  * H(codes) * scale * 8 / head_dim.  Attention works on the rotated rows: it
  * rotates q and its output instead.  Over a quantised cache its operands are fp16
- * in that basis, so rotated keys, values and queries must stay below 65504 (entries below 8000 always do).
+ * in that basis, in units of powers of two taken from the rows themselves, so rows of any size
+ * do.  Two limits: where max_q * (q_heads / kv_heads) is above 16, a row whose scale is 2^24 times below the largest
+ * of the 16 keys (counted from a multiple of 16) that it lies among loses bits; and value scales that one query sees
+ * may differ by a factor of 2^100.
  */
 typedef enum { EXL3_KV_F16 = 0, EXL3_KV_BF16 = 1, EXL3_KV_INT8 = 2, EXL3_KV_INT4 = 3 } exl3_kv_format_t;
 typedef struct {
