@@ -1180,7 +1180,22 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
         uint16_t s16;
         asm volatile("ld.shared.u16 %0, [%1];" : "=h"(s16) : "r"(src + C::kCodes + 2 * (32 * lw + lane)) : "memory");
         load(0);
-        const uint32_t scale = 32 * lw + lane < left ? (uint32_t)s16 << 16 : 0u;
+        uint32_t scale = 32 * lw + lane < left ? (uint32_t)s16 << 16 : 0u;
+        // A row of zeros has the scale 1, which would set the unit although nothing is in it: taken as 0.
+        if (__any_sync(0xffffffffu, scale == 0x3F800000u)) {
+          constexpr uint32_t kZero = SRC == kPaged8 ? 0x80808080u : 0x88888888u;
+          uint32_t codes = scale == 0x3F800000u ? 0u : 1u;
+#pragma unroll 1
+          for (int y = 0; y < LPR; ++y) {
+            uint32_t w[4];
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                         : "r"(src + (32 * lw + lane) * C::kRowBytes + 16 * y)
+                         : "memory");
+            codes |= (w[0] ^ kZero) | (w[1] ^ kZero) | (w[2] ^ kZero) | (w[3] ^ kZero);
+          }
+          if (codes == 0u) scale = 0u;
+        }
         const uint32_t mag = (scale & 0x7FFFFFFFu) < 0x7F800000u ? scale & 0x7FFFFFFFu : 0u;  // a NaN row does not count
         int e[2];
 #pragma unroll

@@ -587,6 +587,7 @@ __global__ void __launch_bounds__(kThreads, token_ctas_per_sm(8 * NR)) attn_toke
 
       // ---- scale, mask, running maximum
       float rv[NK][2];  // quantised: 1 / value scale of this lane's keys
+      bool ones = false;  // a value scale of exactly 1 among them
 #pragma unroll
       for (int x = 0; x < NK; ++x) {
         if constexpr (C::kQuant) {
@@ -596,6 +597,7 @@ __global__ void __launch_bounds__(kThreads, token_ctas_per_sm(8 * NR)) attn_toke
             const float kc = lds_bf16(at) * unit;
             // a NaN scale (a row that reads back as NaN) stays one
             const float vc = max_nan(lds_bf16(at + 2 * C::kStep), 7.888609052210118e-31f);
+            ones = ones || vc == 1.0f;
             const float lv = lg2(vc);
             rv[x][y] = rcp(vc);
 #pragma unroll
@@ -609,6 +611,33 @@ __global__ void __launch_bounds__(kThreads, token_ctas_per_sm(8 * NR)) attn_toke
           for (int n = 0; n < NR; ++n)
 #pragma unroll
             for (int c = 0; c < 4; ++c) sc[x][n][c] *= a.scale_log2;
+        }
+      }
+      if constexpr (C::kQuant) {
+        // A row of zeros has the scale 1, which would lift the maximum over smaller rows' weights although nothing is in
+        // it: its weight goes into the sum alone, by a scale of 2^-80.
+        if (__any_sync(0xffffffffu, ones)) {
+          constexpr uint32_t kZero = FMT == kKvInt8 ? 0x80808080u : 0x88888888u;
+#pragma unroll
+          for (int x = 0; x < NK; ++x)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const int row = 16 * x + 8 * y + g;
+              uint32_t codes = lds_bf16(kb + 2 * C::kSide + 2 * C::kStep + 2 * row) == 1.0f ? 0u : 1u;
+#pragma unroll
+              for (int ch = 0; ch < C::kChunks; ch += 4) {
+                if (ch + q >= C::kChunks) continue;
+                const uint4 w = lds128(vb + ring_offset<C::kRow>(row, ch + q));
+                codes |= (w.x ^ kZero) | (w.y ^ kZero) | (w.z ^ kZero) | (w.w ^ kZero);
+              }
+              codes |= __shfl_xor_sync(0xffffffffu, codes, 1);
+              codes |= __shfl_xor_sync(0xffffffffu, codes, 2);
+              if (codes == 0u) {
+                rv[x][y] = power(127 + 80);
+#pragma unroll
+                for (int n = 0; n < NR; ++n) sc[x][n][2 * y] -= 80.0f, sc[x][n][2 * y + 1] -= 80.0f;
+              }
+            }
         }
       }
       if (t + C::kStep - 1 > lim_all || t < low_all) {

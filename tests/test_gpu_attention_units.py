@@ -91,3 +91,36 @@ def test_results_do_not_depend_on_the_split(fmt, q_len):
     sizes[128:3000] = 2000.0
     sizes[3000:] = 0.01
     run(queries(q_len, heads, 128, "bf16"), rows(n, kv, 128, torch.ones(n), 1), rows(n, kv, 128, sizes, 2), fmt, 128)
+
+
+@pytest.mark.parametrize("fmt,dtype", [("int8", "bf16"), ("int4", "f16")])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("size", [1e-3, 1e-6, 1e-12, 1e4])
+@pytest.mark.parametrize("zeros", ["one", "first tile", "every third", "from the middle"])
+def test_rows_of_zeros(fmt, dtype, dim, shape, size, zeros):
+    """A row of zeros (stored with the scale 1) counts in the sum of the weights and in nothing else."""
+    q_len, n, heads, kv = shape
+    sizes = torch.full((n,), size)
+    at = {"one": slice(5, 6), "first tile": slice(0, 128), "every third": slice(1, n, 3), "from the middle": slice(n // 2, n)}
+    sizes[at[zeros]] = 0.0
+    # queries that give keys of any size scores of about one
+    q = queries(q_len, heads, dim, dtype, min(1e4, 1.0 / size))
+    run(q, rows(n, kv, dim, sizes, 1), rows(n, kv, dim, torch.ones(n) * size, 2), fmt)
+    run(queries(q_len, heads, dim, dtype), rows(n, kv, dim, torch.ones(n), 1), rows(n, kv, dim, sizes, 2), fmt)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "int4"])
+@pytest.mark.parametrize("q_len", [1, 4, 40, 150])
+def test_scales_of_one_that_are_not_zeros(fmt, q_len):
+    """Rows whose scale is exactly 1 are rows like others."""
+    n, kv, dim = 500, 2, 128
+    k, v = rows(n, kv, dim, torch.ones(n), 1), rows(n, kv, dim, torch.ones(n), 2)
+    # x = H e_i 8 / dim * top has one entry of top in the rotated basis: scale 1 (from rounding 1 - 2^-24 up), one code that is not zero
+    top = A.TOP[fmt]
+    h = torch.tensor(A.hadamard(dim)) * (8.0 / dim) * top
+    for i in range(0, n, 3):
+        v[i, :] = h[(i * 7) % dim].to(torch.bfloat16)
+    _, scales = A.quantise(v.float().numpy(), fmt)
+    assert (scales[::3] == 1.0).all()
+    run(queries(q_len, 8, dim, "bf16"), k, v, fmt)
