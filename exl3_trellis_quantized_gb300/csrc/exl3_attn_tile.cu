@@ -601,7 +601,7 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
             t[y] = max3(max3(x[0], x[1], x[2]), x[3], x[4]);
             const float u = max3(max3(x[5], x[6], x[7]), x[8], x[9]), v = max3(max3(x[10], x[11], x[12]), x[13], x[14]);
             t[y] = fmaxf(max3(t[y], u, v), x[15]);
-            cg[y] = c * power(127 + ek[y]);
+            cg[y] = fmaxf(c * power(127 + ek[y]), 1.1754944e-38f);  // not 0: a masked score stays -inf
             t[y] = fmaf(t[y], cg[y], (float)ev[y]);
           }
           top = fmaxf(max3(t[0], t[1], t[2]), t[3]);

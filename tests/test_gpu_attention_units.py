@@ -124,3 +124,14 @@ def test_scales_of_one_that_are_not_zeros(fmt, q_len):
     _, scales = A.quantise(v.float().numpy(), fmt)
     assert (scales[::3] == 1.0).all()
     run(queries(q_len, 8, dim, "bf16"), k, v, fmt)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "int4"])
+@pytest.mark.parametrize("q_len", [1, 40, 150])
+@pytest.mark.parametrize("q_by,k_by", [(1e-22, 1e-22), (1e-30, 1e-12), (1e-12, 1e-28)])
+def test_scores_below_the_range(fmt, q_len, q_by, k_by):
+    """Products too small for fp32 are scores of zero, and what a mask hides stays hidden."""
+    n = 300
+    run(queries(q_len, 8, 128, "bf16", q_by), rows(n, 2, 128, torch.ones(n) * k_by, 1), rows(n, 2, 128, torch.ones(n), 2), fmt)
+    run(queries(q_len, 8, 128, "bf16", q_by), rows(n, 2, 128, torch.ones(n) * k_by, 1), rows(n, 2, 128, torch.ones(n), 2), fmt,
+        window=70)
