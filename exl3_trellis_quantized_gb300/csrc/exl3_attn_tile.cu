@@ -307,8 +307,12 @@ struct Item {
   Span span[2];
   int jlo, jhi;      // key tiles (two blocks each) that a half uses
   int tail;          // the key tile that the length ends in, where its value rows past the end must be made zeros; or -1
+  int lead;          // rows of key tile 0 before the first that the item's queries see: value rows to be made zeros too
   int done;          // no item
 };
+
+// Whether value rows of key tile j must be made zeros: a weight of zero does not hide what is not finite.
+__device__ __forceinline__ bool mend_values(int j, int tail, int lead) { return j == tail || (j == 0 && lead > 0); }
 
 // Blocks of n0 .. n1 that half i of the item uses.
 __device__ Span half_span(const AttnArgs& a, const Item& it, int n0, int n1, int i) {
@@ -369,15 +373,18 @@ __device__ bool find_item(const AttnArgs& a, int lane, int64_t idx, Item* it) {
       // positions of the item's first and last token
       const int p0 = it->first + it->tok0, p1 = p0 + it->toks - 1;
       int lo = a.window > 0 && p0 - a.window + 1 > 0 ? p0 - a.window + 1 : 0;
+      const int seen = lo;
       if constexpr (SRC != kPacked) {
         // whole pages (or 128 keys of a larger one), so that a page is never cut by a tile's first key
         const int align = a.cache.page_shift < 7 ? 1 << a.cache.page_shift : kKeys;
         lo &= ~(align - 1);
       }
       it->base = lo;
+      it->lead = seen - lo;
       const int blocks = p1 >= lo ? (p1 - lo) / kBlock + 1 : 0;
-      const int n0 = (int)((int64_t)blocks * it->split / a.splits);
-      const int n1 = (int)((int64_t)blocks * (it->split + 1) / a.splits);
+      const int from = min(it->lead / kBlock, blocks);  // blocks before the first key are nobody's
+      const int n0 = from + (int)((int64_t)(blocks - from) * it->split / a.splits);
+      const int n1 = from + (int)((int64_t)(blocks - from) * (it->split + 1) / a.splits);
       it->span[0] = half_span(a, *it, n0, n1, 0);
       it->span[1] = half_span(a, *it, n0, n1, 1);
       // the spans of two non-empty halves overlap or touch
@@ -418,7 +425,7 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
   uint64_t* iempty = ifull + 2;                          // [2] and read by every warp
   uint64_t* jfull = iempty + 2;                          // joint item: half 1's output in shared memory
   uint64_t* jfree = jfull + 1;                           // and read by half 0
-  uint64_t* vfix = jfree + 1;                            // [NS] a tail's value rows past the length are zeros
+  uint64_t* vfix = jfree + 1;                            // [NS] value rows that no query sees are zeros
   uint64_t* qraw = vfix + 8;                             // [2] a half's q as it is (quantised formats: still to be rotated)
   uint64_t* qempty = qraw + 2;                           // [2] a half's scores of an item are done
   uint64_t* clc = qempty + 2;                              // answer to a cancel request
@@ -865,7 +872,7 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
       const uint32_t one = elect_one();
       bool ok = true;
       uint32_t n = 0, qph = 0, blocks = 0;
-      uint32_t fph = 0;  // phases of the slots' tails (a bit a slot)
+      uint32_t fph = 0;  // phases of the slots' vfix (a bit a slot)
       // The ring holds K(jlo), V(jlo), K(jlo + 1), ... of each item: where the next tile's keys and values lie.
       uint32_t slot[2] = {0u, 1u}, sph[2] = {0u, 0u};
       auto next_slot = [&](int value) {
@@ -880,7 +887,7 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
         if (!__all_sync(0xffffffffu, read_item(n, &it))) break;
         ++n;
         const int b0 = uni(i ? it.span[1].b0 : it.span[0].b0), b1 = uni(i ? it.span[1].b1 : it.span[0].b1), step = uni(it.joint) + 1;
-        const int jlo = uni(it.jlo), jhi = uni(it.jhi), tail = uni(it.tail), keys = uni(it.kv_len - it.base);
+        const int jlo = uni(it.jlo), jhi = uni(it.jhi), tail = uni(it.tail), lead = uni(it.lead), keys = uni(it.kv_len - it.base);
         int kt = jlo, vt = jlo;  // tiles whose keys / values come next
         // Tiles that this half does not use, before its first and after its last: released once they are filled, so that
         // releases stay in step with fills, and in the ring's order.
@@ -891,7 +898,7 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
             for (int value = 0; value < 2; ++value) {
               ok = bar_wait<true>(&kvfull[slot[value]], sph[value]) && ok;
               if (one) mbar_arrive(&kvempty[slot[value]]);
-              if (value && vt == tail) fph ^= 1u << slot[1];
+              if (value && mend_values(vt, tail, lead)) fph ^= 1u << slot[1];
               next_slot(value);
             }
             ok = __all_sync(0xffffffffu, ok);
@@ -931,7 +938,7 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
             const int pb = b - step;
             const uint32_t s = slot[1], g = blocks - 1, buf = g & 1u;
             ok = bar_wait<true>(&kvfull[s], sph[1]) && ok;
-            if (!C::kQuant && vt == tail) ok = bar_wait<true>(&vfix[s], fph >> s & 1u) && ok;
+            if (!C::kQuant && mend_values(vt, tail, lead)) ok = bar_wait<true>(&vfix[s], fph >> s & 1u) && ok;
             // keys past the length take no part: whole steps of 16 are left out
             const int steps = (min(kBlock, keys - pb * kBlock) + 15) >> 4;
             const uint64_t vd = vd0 + (uint64_t)(s * (C::kSlot >> 4) + (pb & 1) * (kBlock * 128 >> 4));
@@ -955,7 +962,7 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
             if (one) tc_commit(&pvdone[i]);
             if (b >= b1 || b >> 1 != pb >> 1) {  // the tile's last values
               if (one) tc_commit(&kvempty[s]);
-              if (vt == tail) fph ^= 1u << s;
+              if (mend_values(vt, tail, lead)) fph ^= 1u << s;
               next_slot(1);
               ++vt;
             }
@@ -1048,14 +1055,18 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
                   }
                 }
                 __syncwarp();
-                if (value && j == it.tail) {
-                  // zeros from the length to the next multiple of 16 keys of the tile
+                if (value && mend_values(j, it.tail, it.lead)) {
                   ok = bar_wait(&full[s], ph);
                   if (!ok) break;
-                  const int keys = it.kv_len - t, upto = (keys + 15) & ~15;
-                  const uint32_t d32 = smem_u32(dst);
-                  for (int x = lane; x < (upto - keys) * (D / 8); x += 32)
-                    sts128(d32 + row_chunk(keys + x / (D / 8), x % (D / 8)), 0u, 0u, 0u, 0u);
+                  auto zeros = [&](int from, int to) {
+                    for (int x = lane; x < (to - from) * (D / 8); x += 32)
+                      sts128(smem_u32(dst) + row_chunk(from + x / (D / 8), x % (D / 8)), 0u, 0u, 0u, 0u);
+                  };
+                  // from the length to the next multiple of 16 keys of the tile (the products' step); and from the block
+                  // that the first key lies in to it
+                  const int keys = it.kv_len - t;
+                  if (j == it.tail) zeros(keys, (keys + 15) & ~15);
+                  if (j == 0) zeros(it.lead & ~(kBlock - 1), it.lead);
                   fence_proxy_async_smem();
                   __syncwarp();
                   if (lane == 0) mbar_arrive(&vfix[s]);
@@ -1163,7 +1174,7 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
         const uint32_t rs = raw % C::kRaws, s = filled % NS;
         ok = bar_wait(&rawfull[rs], raw / C::kRaws & 1u);
         if (!ok) break;
-        const int left = it.kv_len - it.base - (it.jlo + (x >> 1)) * kKeys;  // keys before the length
+        const int at = (it.jlo + (x >> 1)) * kKeys + 32 * lw + lane;  // row 32 lw + lane of the tile, from the item's first key
         const uint32_t src = smem_u32(data + C::kRawRing) + rs * C::kRaw;
         const uint32_t dst = smem_u32(data + C::kRing) + s * C::kSlot;
         uint32_t ww[AHEAD][4];
@@ -1175,12 +1186,12 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
                          : "r"(src + (32 * lw + (p + y) * RPP + lane / LPR) * C::kRowBytes + 16 * sub)
                          : "memory");
         };
-        // row 32 lw + lane: its scale in units of its group's, from the group's largest scale; 0 past the length, which
-        // makes zeros of any codes
+        // that row's scale in units of its group's, from the group's largest scale; 0 past the length and before the first
+        // key that the item sees, which makes zeros of any codes
         uint16_t s16;
         asm volatile("ld.shared.u16 %0, [%1];" : "=h"(s16) : "r"(src + C::kCodes + 2 * (32 * lw + lane)) : "memory");
         load(0);
-        uint32_t scale = 32 * lw + lane < left ? (uint32_t)s16 << 16 : 0u;
+        uint32_t scale = at < it.kv_len - it.base && at >= it.lead ? (uint32_t)s16 << 16 : 0u;
         // A row of zeros has the scale 1, which would set the unit although nothing is in it: taken as 0.
         if (__any_sync(0xffffffffu, scale == 0x3F800000u)) {
           constexpr uint32_t kZero = SRC == kPaged8 ? 0x80808080u : 0x88888888u;

@@ -385,6 +385,8 @@ exl3_status_t exl3_kv_read(const exl3_kv_cache_t* cache, const int64_t* slots, i
  * Scores, softmax statistics and sums are fp32; the weights round to the type
  * before they meet v.
  *   q, k, v    [total] tokens of `dtype`;  scale  positive and finite
+ *   v          a value that is not finite may also reach those queries of its sequence that do not see it (a weight
+ *              of zero still multiplies it), never another sequence
  *   cu_seqlens device, int32 [batch + 1]: sequence b is tokens [cu[b], cu[b + 1]); tokens of no
  *              sequence keep their output
  *   out        device, [total] tokens of q_heads heads; may be q itself (same strides), else it overlaps
@@ -414,7 +416,8 @@ exl3_status_t exl3_attention_prompt(const exl3_heads_t* q, const exl3_heads_t* k
  *   workspace   device, 16-byte aligned, at least exl3_attention_paged_workspace_bytes of the same sizes
  *               (0 bytes: may be NULL), any contents.  Calls that share it must be ordered on one stream.
  * Values (and value scales) of keys that one query of a call may not see but another of the same sequence
- * does must be finite: a weight of zero still multiplies them.  Rows past a length may hold anything.
+ * does must be finite: a weight of zero still multiplies them.  Rows past a length, and rows before the first that a
+ * query of the call sees, may hold anything.
  * If a kernel gives up on a bounded wait (exl3_device_status reports it), out is undefined.
  */
 size_t exl3_attention_paged_workspace_bytes(int64_t total_q, int32_t batch, int32_t q_heads, int32_t kv_heads,
