@@ -22,6 +22,9 @@ bool valid_heads(const exl3_heads_t* h) {
 bool valid_out(const exl3_heads_t* x, const void* out, int64_t token, int64_t head) {
   return aligned16(out) && (out != x->data || (token == x->token_stride && head == x->head_stride));
 }
+// No sequence is longer than 2^30 keys, so a window of that size is none; the kernels subtract smaller ones from positions,
+// which may be negative, in 32 bits.
+int kernel_window(int32_t window) { return window >= (1 << 30) ? 0 : window; }
 // A group's query heads are rows of one tile.
 bool valid_head_counts(int32_t q_heads, int32_t kv_heads) {
   return kv_heads >= 1 && q_heads >= 1 && q_heads % kv_heads == 0 && q_heads / kv_heads <= 128 && q_heads <= 65536;
@@ -240,7 +243,7 @@ exl3_status_t exl3_attention_prompt(const exl3_heads_t* q, const exl3_heads_t* k
   a.heads = q_heads;
   a.kv_heads = kv_heads;
   a.head_dim = head_dim;
-  a.window = window;
+  a.window = kernel_window(window);
   a.scale_log2 = scale * 1.4426950408889634f;
   a.bf16 = dtype == EXL3_BF16;
   a.splits = 1;
@@ -291,7 +294,7 @@ exl3_status_t exl3_attention_paged(const exl3_heads_t* q, exl3_dtype_t dtype, in
   a.kv_heads = a.cache.kv_heads;
   a.head_dim = a.cache.head_dim;
   a.max_q = max_q;
-  a.window = window;
+  a.window = kernel_window(window);
   a.scale_log2 = scale * 1.4426950408889634f;
   a.bf16 = dtype == EXL3_BF16;
   a.splits = plan.splits;

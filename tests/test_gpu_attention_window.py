@@ -37,3 +37,21 @@ def test_rows_before_every_window(fmt, dtype, dim, page, q_len, kv_len, window):
     torch.cuda.synchronize()
     assert E.device_status() == 0
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int8"])
+@pytest.mark.parametrize("q_lens,kv_lens", [([1, 2], [70, 1]), ([40, 200], [3, 500]), ([300], [290])])
+def test_a_window_of_any_size(fmt, q_lens, kv_lens):
+    """Windows beyond every length, up to the largest int32, with queries before the first key among them, are none."""
+    cache, table, _ = make_cache(kv_lens, 2, 128, 32, fmt, 5)
+    q = torch.randn((sum(q_lens), 8, 128), generator=torch.Generator().manual_seed(6)).to(torch.bfloat16).to(DEV)
+    lens = torch.tensor(kv_lens, dtype=torch.int32, device=DEV)
+    args = (q, cache, table, cu(q_lens), lens, max(q_lens), max(kv_lens))
+    want = E.attention_paged(*args)
+    for window in (2**20, 2**30 - 1, 2**30, 2**31 - 300, 2**31 - 1):
+        assert torch.equal(E.attention_paged(*args, window=window), want)
+    k = torch.randn((sum(q_lens), 2, 128), generator=torch.Generator().manual_seed(7)).to(torch.bfloat16).to(DEV)
+    want = E.attention_prompt(q, k, k, cu(q_lens))
+    for window in (2**20, 2**30, 2**31 - 1):
+        assert torch.equal(E.attention_prompt(q, k, k, cu(q_lens), window=window), want)
+    assert E.device_status() == 0
