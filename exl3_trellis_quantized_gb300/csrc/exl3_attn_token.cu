@@ -32,7 +32,7 @@
 //
 // Quantised rows stay in the rotated basis (see exl3_rope_cache.cu): q is
 // rotated by the D-point Hadamard transform times 8/D once, the output once, and
-// held in units of a power of two near its largest value.  The
+// each row held in units of a power of two near its largest value.  The
 // rotated q is not exact in fp16: for fp16 queries it goes in as two fp16 terms
 // (22 bits), since one alone moved the outputs by 1.7 times their own rounding
 // (bf16 outputs round eight times coarser: one term).
@@ -162,6 +162,13 @@ __device__ __forceinline__ float lds_bf16(uint32_t addr) {
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
   return __uint_as_float((uint32_t)v << 16);
 }
+// Two scores times a factor and two units, plus an addend, two numbers an instruction.
+__device__ __forceinline__ void scale2(float& x, float& y, float factor, const float (&unit)[2], float add) {
+  asm("{\n .reg .b64 s, f, u, a;\n mov.b64 s, {%0, %1};\n mov.b64 f, {%2, %2};\n mov.b64 u, {%3, %4};\n mov.b64 a, {%5, %5};\n"
+      " mul.rn.f32x2 f, f, u;\n fma.rn.f32x2 s, s, f, a;\n mov.b64 {%0, %1}, s;\n}\n"
+      : "+f"(x), "+f"(y)
+      : "f"(factor), "f"(unit[0]), "f"(unit[1]), "f"(add));
+}
 // Two bytes (offset codes) widened by the pattern of 1024: {1024 + c0, 1024 + c1} - 1152.
 __device__ __forceinline__ uint32_t bytes_to_h2(uint32_t w, uint32_t sel) {
   return hsub2(__byte_perm(w, 0x64646464u, sel), 0x64806480u);
@@ -248,8 +255,8 @@ struct TokenCfg {
   static constexpr int kJoin = kRows * D * 4 + kRows * 8;  // a warp's (o, m, l) at an item's end
   static constexpr int kWarpBytes = ((kRing > kJoin ? kRing : kJoin) + 127) / 128 * 128;
   static constexpr int kQBytes = kQuant ? 2 * kRows * D * 2 : 0;  // the rotated q and the fragments of its second term
-  static constexpr int kTops = kWarps * kWarpBytes + kQBytes;     // [kWarps] largest magnitudes of the rotated q
-  static constexpr int kSmem = kTops + (kQuant ? 4 * kWarps : 0);
+  static constexpr int kUnits = kWarps * kWarpBytes + kQBytes;    // [kRows] of the rotated q's rows: unit times 8/D and the scale
+  static constexpr int kSmem = kUnits + (kQuant ? 4 * kRows : 0);
   static constexpr int kChunks = kRow / 16;  // 16-byte chunks of a row
   static constexpr int kTpr = kThreads / kRows;  // threads of a row where the CTA works on whole rows
   static constexpr int kPer = D / kTpr;          // and values of each
@@ -426,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, token_ctas_per_sm(8 * NR)) attn_toke
 #pragma unroll
     for (int i = 0; i < C::kStages - 1; ++i) issue(i);
 
-    float unit = 1.0f;  // of a score over a quantised cache: the rotated q's units, 8/D and the scale
+    float unit[NR][2];  // of the scores of rows 8n + 2q, + 1 over a quantised cache: the rotated q's units, 8/D and the scale
     // the second term of the rotated q, only for fp16 queries: [n][k][lane] fragments
     const uint32_t qlo = smem_u32(smem) + kWarps * C::kWarpBytes + C::kRows * D * 2;
     if constexpr (C::kQuant) {
@@ -439,16 +446,15 @@ __global__ void __launch_bounds__(kThreads, token_ctas_per_sm(8 * NR)) attn_toke
         v[2 * i + 1] = to_f32((uint16_t)(qraw[i] >> 16), a.bf16 != 0);
       }
       hadamard_threads<C::kPer, C::kTpr>(v, part);
-      // in units of a power of two near the rows' largest value, so that fp16 holds any q
+      // in units of a power of two near the row's largest value, so that fp16 holds any q
       float top = 0.0f;
 #pragma unroll
       for (int i = 0; i < C::kPer; ++i) top = fmaxf(top, fabsf(v[i]));
-      uint32_t* tops = reinterpret_cast<uint32_t*>(smem + C::kTops);
-      const uint32_t mine_top = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
-      if (lane == 0) tops[warp] = mine_top;
-      __syncthreads();
-      const uint32_t e = unit_exponent(__uint_as_float(max(max(tops[0], tops[1]), max(tops[2], tops[3]))));
-      unit = a.scale_log2 * (8.0f / D) * power(e);
+#pragma unroll
+      for (int st = 1; st < C::kTpr; st *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, st));
+      const uint32_t e = unit_exponent(top);
+      float* units = reinterpret_cast<float*>(smem + C::kUnits);
+      if (part == 0) units[jr] = a.scale_log2 * (8.0f / D) * power(e);
 #pragma unroll
       for (int i = 0; i < C::kPer; ++i) v[i] *= power(254u - e);
       // fragments in the order in which the codes come out of their words
@@ -492,7 +498,11 @@ __global__ void __launch_bounds__(kThreads, token_ctas_per_sm(8 * NR)) attn_toke
       for (int i = 0; i < C::kPer; i += 2) *reinterpret_cast<uint32_t*>(qs + jr * D + part * C::kPer + i) = pack2<false>(v[i], v[i + 1]);
       __syncthreads();
 #pragma unroll
-      for (int n = 0; n < NR; ++n) fragments(qb[n], n);
+      for (int n = 0; n < NR; ++n) {
+        fragments(qb[n], n);
+        const float2 u = *reinterpret_cast<const float2*>(units + 8 * n + 2 * q);
+        unit[n][0] = u.x, unit[n][1] = u.y;
+      }
     }
 
     // ---- this lane's rows 8n + 2q, + 1: what they see, and their running softmax
@@ -594,17 +604,14 @@ __global__ void __launch_bounds__(kThreads, token_ctas_per_sm(8 * NR)) attn_toke
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
             const uint32_t at = kb + 2 * C::kSide + 2 * (16 * x + 8 * y + g);
-            const float kc = lds_bf16(at) * unit;
+            const float kc = lds_bf16(at);
             // a NaN scale (a row that reads back as NaN) stays one
             const float vc = max_nan(lds_bf16(at + 2 * C::kStep), 7.888609052210118e-31f);
             ones = ones || vc == 1.0f;
             const float lv = lg2(vc);
             rv[x][y] = rcp(vc);
 #pragma unroll
-            for (int n = 0; n < NR; ++n) {
-              sc[x][n][2 * y] = fmaf(sc[x][n][2 * y], kc, lv);
-              sc[x][n][2 * y + 1] = fmaf(sc[x][n][2 * y + 1], kc, lv);
-            }
+            for (int n = 0; n < NR; ++n) scale2(sc[x][n][2 * y], sc[x][n][2 * y + 1], kc, unit[n], lv);
           }
         } else {
 #pragma unroll

@@ -135,3 +135,30 @@ def test_scores_below_the_range(fmt, q_len, q_by, k_by):
     run(queries(q_len, 8, 128, "bf16", q_by), rows(n, 2, 128, torch.ones(n) * k_by, 1), rows(n, 2, 128, torch.ones(n), 2), fmt)
     run(queries(q_len, 8, 128, "bf16", q_by), rows(n, 2, 128, torch.ones(n) * k_by, 1), rows(n, 2, 128, torch.ones(n), 2), fmt,
         window=70)
+
+
+@pytest.mark.parametrize("fmt,dtype", [("int8", "bf16"), ("int8", "f16"), ("int4", "bf16"), ("int4", "f16")])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("q_len,heads,kv", [(1, 8, 2), (1, 16, 1), (3, 8, 2), (2, 6, 2), (30, 8, 2)])
+def test_query_rows_do_not_depend_on_each_other(fmt, dtype, dim, q_len, heads, kv):
+    """Heads and tokens of very different sizes in one call, one of them not finite: every row as if it were alone."""
+    n = 700
+    k, v = rows(n, kv, dim, torch.ones(n), 1), rows(n, kv, dim, torch.ones(n), 2)
+    q = queries(q_len, heads, dim, dtype)
+    # sizes a factor of 2^9 apart (of fp16 down to its smallest normal numbers), large ones beside small ones
+    by = 2.0 ** torch.tensor([0.0, 9.0, -9.0, 4.0])[torch.arange(q_len * heads) % 4].view(q_len, heads, 1)
+    q = (q.float() * by).to(q.dtype)
+    run(q, k, v, fmt)
+    pages = (n + 31) // 32
+    cache = E.KVCache.empty(pages, 32, kv, dim, fmt)
+    E.kv_write(cache, k.to(DEV), v.to(DEV), torch.arange(n, device=DEV))
+    args = (cache, torch.arange(pages, dtype=torch.int32, device=DEV)[None], cu([q_len]),
+            torch.tensor([n], dtype=torch.int32, device=DEV), q_len, n)
+    want = E.attention_paged(q.to(DEV), *args)
+    other = q.clone()
+    other[:, 1] = float("inf")
+    other[:, 2] *= 8.0
+    got = E.attention_paged(other.to(DEV), *args)
+    keep = [h for h in range(heads) if h not in (1, 2)]
+    assert torch.equal(got[:, keep], want[:, keep])
+    assert torch.isnan(got[:, 1]).all() and torch.isfinite(got[:, 2]).all()
