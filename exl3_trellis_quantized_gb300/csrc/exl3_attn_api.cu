@@ -278,6 +278,7 @@ exl3_status_t exl3_attention_paged(const exl3_heads_t* q, exl3_dtype_t dtype, in
   for (const void* p : ints)
     if (p == nullptr || (reinterpret_cast<uintptr_t>(p) & 3u) != 0) return EXL3_EINVAL;
   const PagedPlan plan = paged_plan(total_q, batch, q_heads, a.cache.kv_heads, a.cache.head_dim, max_q, max_kv, window);
+  if (plan.token && (int64_t)batch * a.cache.kv_heads > INT32_MAX) return EXL3_EUNSUPPORTED;  // blocks of the join
   if (plan.o_bytes > 0 && !aligned16(workspace)) return EXL3_EINVAL;
   if (workspace_bytes < plan.o_bytes + plan.ml_bytes) return EXL3_EWORKSPACE;
   a.q = view(q);

@@ -411,6 +411,7 @@ exl3_status_t exl3_attention_prompt(const exl3_heads_t* q, const exl3_heads_t* k
  *   cu_q        device, int32 [batch + 1]: query tokens of sequence b, as cu_seqlens above
  *   kv_lens     device, int32 [batch]: cached tokens, the new ones among them; at most table_width * page_size
  *   out         as for exl3_attention_prompt
+ *   batch       times kv_heads below 2^31
  *   max_q       HOST: no sequence has more query tokens (the outputs of one that has are undefined)
  *   max_kv      HOST: about the longest length; it only steers how the work is split
  *   workspace   device, 16-byte aligned, at least exl3_attention_paged_workspace_bytes of the same sizes

@@ -265,3 +265,12 @@ def test_oracle_attention_closed_forms():
     out, _, _ = A.attention(zero[:2], zero[:1, :1], v[:1])  # more query tokens than keys: the first sees nothing
     assert not out[0].any()
     np.testing.assert_allclose(out[1, 0], v[0, 0])
+
+
+def test_paged_refuses_more_items_than_a_grid(L):
+    """Sequences times key heads index one axis of a grid, also where most sequences are empty."""
+    kv, batch = 1024, 1 << 22
+    need = L.exl3_attention_paged_workspace_bytes(4, batch, kv, kv, 128, 1, 64, 0)
+    st = L.exl3_attention_paged(heads(token=kv * 128), BF16, 4, kv, cache(kv=kv), FAKE, 4, FAKE, FAKE, batch, 1, 64, 0, 1.0,
+                                FAKE * 2, kv * 128, 128, FAKE * 4, need, None)
+    assert st == EUNSUPPORTED
