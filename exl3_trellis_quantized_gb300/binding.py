@@ -436,7 +436,9 @@ KV_FORMATS = {"f16": 0, "bf16": 1, "int8": 2, "int4": 3}
 _KV_DTYPES = {"f16": torch.float16, "bf16": torch.bfloat16, "int8": torch.uint8, "int4": torch.uint8}
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's handle, without a Stream object
+# The current stream's handle, without a Stream object where torch has a call for that (not a public one).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _type(t: torch.Tensor, name: str) -> int:
