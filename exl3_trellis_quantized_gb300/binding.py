@@ -536,7 +536,10 @@ def rope(x: torch.Tensor, positions: torch.Tensor, phases: torch.Tensor, layout:
 
 class KVCache:
     """A paged cache: k and v [pages, kv_heads, page_size, row] (row: head_dim values in 16 bits, head_dim bytes for
-    "int8", head_dim / 2 for "int4"), and for the quantised formats bf16 scales [pages, kv_heads, page_size]."""
+    "int8", head_dim / 2 for "int4"), and for the quantised formats bf16 scales [pages, kv_heads, page_size].
+
+    The calls take the addresses of these tensors as they were at construction, so the attributes cannot be assigned:
+    other tensors are another KVCache (which costs a few checks and no copy)."""
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: Optional[torch.Tensor],
                  v_scale: Optional[torch.Tensor], fmt: str):
@@ -553,12 +556,15 @@ class KVCache:
                 raise ValueError(f"an {fmt} cache needs scales")
             _alike(k_scale, torch.bfloat16, (pages, heads, page), "k_scale")
             _alike(v_scale, torch.bfloat16, (pages, heads, page), "v_scale")
-        self.k, self.v, self.k_scale, self.v_scale, self.fmt = k, v, k_scale, v_scale, fmt
-        self.num_pages, self.kv_heads, self.page_size = pages, heads, page
-        self.head_dim = 2 * row if fmt == "int4" else row
-        self.args = _Cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if k_scale is not None else None,
-                           v_scale.data_ptr() if v_scale is not None else None, pages, page, heads, self.head_dim,
-                           KV_FORMATS[fmt])
+        head_dim = 2 * row if fmt == "int4" else row
+        args = _Cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if k_scale is not None else None,
+                      v_scale.data_ptr() if v_scale is not None else None, pages, page, heads, head_dim,
+                      KV_FORMATS[fmt])
+        self.__dict__.update(k=k, v=v, k_scale=k_scale, v_scale=v_scale, fmt=fmt, num_pages=pages, kv_heads=heads,
+                             page_size=page, head_dim=head_dim, args=args)
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"KVCache.{name} cannot be assigned: make a KVCache of the new tensors")
 
     @classmethod
     def empty(cls, num_pages: int, page_size: int, kv_heads: int, head_dim: int, fmt: str, device="cuda") -> "KVCache":
