@@ -465,16 +465,40 @@ def _heads(t: torch.Tensor, dtype, name: str) -> _Heads:
     return _Heads(t.data_ptr(), ts if tokens > 1 else heads * d or 8, hs if heads > 1 else d)
 
 
-def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
-    """Whether the memory that two views span overlaps."""
-    def span(t):
-        last = sum((n - 1) * st for n, st in zip(t.shape, t.stride()))
-        return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
+def _comb(t: torch.Tensor):
+    """(first byte, pieces, bytes from one to the next, bytes of one) that cover a view: its tokens, or with heads
+    outermost its heads."""
+    at, es = t.data_ptr(), t.element_size()
+    if t.dim() == 3 and not t.is_contiguous():
+        (n, h, d), (ts, hs, ds) = t.shape, t.stride()
+        for pieces, step, others, stride in ((n, ts, h, hs), (h, hs, n, ts)):
+            width = (others - 1) * stride + (d - 1) * ds + 1
+            if width <= step:
+                return at, pieces, step * es, width * es
+    span = (1 + sum((n - 1) * st for n, st in zip(t.shape, t.stride()))) * es
+    return at, 1, span, span
 
+
+def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
+    """Whether two views share memory.  Views of different strides in one buffer may be taken to."""
     if a.numel() == 0 or b.numel() == 0:
         return False
-    (a0, a1), (b0, b1) = span(a), span(b)
-    return a0 < b1 and b0 < a1
+    (a0, na, sa, wa), (b0, nb, sb, wb) = _comb(a), _comb(b)
+    if a0 + (na - 1) * sa + wa <= b0 or b0 + (nb - 1) * sb + wb <= a0:
+        return False
+    if na > 1 and nb > 1 and sa != sb:
+        return True
+    # pieces i of a and i + k of b meet if -wb < b0 + k s - a0 < wa: the smallest k that passes the first
+    s = sa if na > 1 else sb
+    k = max(-(na - 1), (a0 - b0 - wb) // s + 1)
+    return k < nb and b0 + k * s - a0 < wa
+
+
+def _apart(out: torch.Tensor, name: str, **others) -> None:
+    """Refuses an output that the caller gave if it shares memory with one of the call's other tensors."""
+    for other, t in others.items():
+        if t is not None and _overlap(out, t):
+            raise ValueError(f"{name} overlaps {other}")
 
 
 def _out_like(x: torch.Tensor, out: Optional[torch.Tensor], name: str):
@@ -606,6 +630,8 @@ def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tens
         if q.dim() != 3 or q.shape[0] != tokens or q.shape[2] != cache.head_dim:
             raise ValueError("q must be [tokens, heads, head_dim]")
         qh, heads = _heads(q, k.dtype, "q"), q.shape[1]
+        if q_out is not None:
+            _apart(q_out, "q_out", k=k, v=v, cache_k=cache.k, cache_v=cache.v, k_scale=cache.k_scale, v_scale=cache.v_scale)
         q_out, oh = _out_like(q, q_out, "q_out")
         qo = (oh.data, oh.token_stride, oh.head_stride)
     elif q_out is not None:
@@ -622,6 +648,10 @@ def kv_read(cache: KVCache, slots: torch.Tensor, dtype=torch.bfloat16, k: Option
     if slots.dim() != 1:
         raise ValueError("slots must be [tokens]")
     shape = (slots.numel(), cache.kv_heads, cache.head_dim)
+    if k is not None:
+        _apart(k, "k", cache_k=cache.k, cache_v=cache.v, k_scale=cache.k_scale, v_scale=cache.v_scale, v=v)
+    if v is not None:
+        _apart(v, "v", cache_k=cache.k, cache_v=cache.v, k_scale=cache.k_scale, v_scale=cache.v_scale)
     k = torch.empty(shape, dtype=dtype, device=slots.device) if k is None else k
     v = torch.empty(shape, dtype=dtype, device=slots.device) if v is None else v
     _alike(k, dtype, shape, "k")
@@ -648,6 +678,8 @@ def attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     _need(cu_seqlens, torch.int32, "cu_seqlens")
     if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
         raise ValueError("cu_seqlens must be [batch + 1]")
+    if out is not None:
+        _apart(out, "out", k=k, v=v)
     out, oh = _out_like(q, out, "out")
     st = lib().exl3_attention_prompt(qh, kh, vh, dt, total, heads, k.shape[1], d, cu_seqlens.data_ptr(),
                                      cu_seqlens.numel() - 1, int(window), d ** -0.5 if scale is None else float(scale),
@@ -688,6 +720,8 @@ def attention_paged(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, 
     _need(block_table, torch.int32, "block_table")
     if block_table.dim() != 2 or block_table.shape[0] != batch:
         raise ValueError("block_table must be [batch, width]")
+    if out is not None:
+        _apart(out, "out", cache_k=cache.k, cache_v=cache.v, k_scale=cache.k_scale, v_scale=cache.v_scale)
     out, oh = _out_like(q, out, "out")
     if workspace is None:
         need = _workspace_bytes(total, batch, heads, cache.kv_heads, d, int(max_q), int(max_kv), int(window))

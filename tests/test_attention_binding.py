@@ -4,6 +4,7 @@ import subprocess
 import sys
 
 import pytest
+import torch
 
 from exl3_trellis_quantized_gb300 import binding as B
 
@@ -38,3 +39,28 @@ def test_cache_addresses_stay_those_of_its_tensors(on_cpu, fmt):
         t = getattr(cache, name)
         assert getattr(cache.args, name) == (None if t is None else t.data_ptr())
     assert (cache.num_pages, cache.kv_heads, cache.page_size, cache.head_dim, cache.fmt) == (3, 2, 16, 64, fmt)
+
+
+def touched(t):
+    """Addresses of a view's elements."""
+    at = torch.zeros((), dtype=torch.int64)
+    for n, st in zip(t.shape, t.stride()):
+        at = at.unsqueeze(-1) + torch.arange(n) * st
+    return set((t.data_ptr() + t.element_size() * at.flatten()).tolist())
+
+
+def test_overlap_of_views():
+    """No overlap is missed, and views side by side in a fused projection's rows are not taken for one."""
+    x = torch.zeros(10, 6, 8, dtype=torch.bfloat16)
+    h = torch.zeros(6, 10, 8, dtype=torch.bfloat16).transpose(0, 1)  # heads outermost
+    flat = x.view(-1)
+    views = [x[:, :2], x[:, 2:4], x[:, 4:], x[:, 1:3], x[3:, :2], x[:3, 2:], x[9:, :], x[:1, 5:], x[2:2], x, flat[:96], flat[96:112],
+             flat[24:48], flat[8:40].view(2, 2, 8), x[::2, :3], x[1::2, 3:], h, h[:, :3], h[:, 3:], h[:4, 2:], h[4:, 2:], h[:4]]
+    for a in views:
+        for b in views:
+            assert B._overlap(a, b) == B._overlap(b, a)
+            if touched(a) & touched(b):
+                assert B._overlap(a, b)
+    for a, b in ((0, 1), (0, 2), (1, 2), (4, 1), (6, 4 - 4), (16, 0), (17, 18), (12, 7)):
+        if not touched(views[a]) & touched(views[b]):
+            assert not B._overlap(views[a], views[b]), (a, b)
