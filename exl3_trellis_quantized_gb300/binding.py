@@ -539,6 +539,8 @@ def rope_phases(rot_dim: int, base: float = 10000.0, scaling: str = "plain", fac
 def _rope_args(positions: torch.Tensor, phases: torch.Tensor, layout: str, amplitude: float, tokens: int) -> _Rope:
     _alike(positions, torch.int32, (tokens,), "positions")
     _need(phases, torch.int64, "phases")
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}")
     return _Rope(phases.data_ptr(), positions.data_ptr(), 2 * phases.numel(), ROPE_LAYOUTS[layout], float(amplitude))
 
 

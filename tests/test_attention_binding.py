@@ -64,3 +64,10 @@ def test_overlap_of_views():
     for a, b in ((0, 1), (0, 2), (1, 2), (4, 1), (6, 4 - 4), (16, 0), (17, 18), (12, 7)):
         if not touched(views[a]) & touched(views[b]):
             assert not B._overlap(views[a], views[b]), (a, b)
+
+
+def test_unknown_layout_is_a_value_error(on_cpu):
+    positions, phases = torch.zeros(2, dtype=torch.int32), torch.zeros(8, dtype=torch.int64)
+    with pytest.raises(ValueError):
+        B._rope_args(positions, phases, "neox", 1.0, 2)
+    assert B._rope_args(positions, phases, "half", 1.0, 2).rot_dim == 16
