@@ -465,6 +465,13 @@ def _heads(t: torch.Tensor, dtype, name: str) -> _Heads:
     return _Heads(t.data_ptr(), ts if tokens > 1 else heads * d or 8, hs if heads > 1 else d)
 
 
+def _one_device(first: torch.Tensor, *others: Optional[torch.Tensor]) -> None:
+    device = first.device
+    for t in others:
+        if t is not None and t.device != device:
+            raise ValueError(f"tensors of one call must lie on one device: {device} and {t.device}")
+
+
 def _comb(t: torch.Tensor):
     """(first byte, pieces, bytes from one to the next, bytes of one) that cover a view: its tokens, or with heads
     outermost its heads."""
@@ -554,6 +561,7 @@ def rope(x: torch.Tensor, positions: torch.Tensor, phases: torch.Tensor, layout:
     xh = _heads(x, x.dtype, "x")
     tokens, heads, d = x.shape
     r = _rope_args(positions, phases, layout, amplitude, tokens)
+    _one_device(x, positions, phases, out)
     out, oh = _out_like(x, out, "out")
     st = lib().exl3_rope(xh, dt, tokens, heads, d, r, oh.data, oh.token_stride, oh.head_stride, _raw_stream(x.device.index))
     _check(st, "exl3_rope")
@@ -582,6 +590,7 @@ class KVCache:
                 raise ValueError(f"an {fmt} cache needs scales")
             _alike(k_scale, torch.bfloat16, (pages, heads, page), "k_scale")
             _alike(v_scale, torch.bfloat16, (pages, heads, page), "v_scale")
+        _one_device(k, v, k_scale, v_scale)
         head_dim = 2 * row if fmt == "int4" else row
         args = _Cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if k_scale is not None else None,
                       v_scale.data_ptr() if v_scale is not None else None, pages, page, heads, head_dim,
@@ -620,6 +629,7 @@ def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tens
     if tuple(k.shape) != (tokens, cache.kv_heads, cache.head_dim) or v.shape != k.shape:
         raise ValueError("k and v must be [tokens, kv_heads, head_dim] of the cache")
     _alike(slots, torch.int64, (tokens,), "slots")
+    _one_device(k, v, cache.k, slots, q, positions, phases, q_out)
     r = qh = None
     heads, qo = 0, (None, 0, 0)
     if phases is not None:
@@ -649,6 +659,7 @@ def kv_read(cache: KVCache, slots: torch.Tensor, dtype=torch.bfloat16, k: Option
     _need(slots, torch.int64, "slots")
     if slots.dim() != 1:
         raise ValueError("slots must be [tokens]")
+    _one_device(slots, cache.k, k, v)
     shape = (slots.numel(), cache.kv_heads, cache.head_dim)
     if k is not None:
         _apart(k, "k", cache_k=cache.k, cache_v=cache.v, k_scale=cache.k_scale, v_scale=cache.v_scale, v=v)
@@ -680,6 +691,7 @@ def attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     _need(cu_seqlens, torch.int32, "cu_seqlens")
     if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
         raise ValueError("cu_seqlens must be [batch + 1]")
+    _one_device(q, k, v, cu_seqlens, out)
     if out is not None:
         _apart(out, "out", k=k, v=v)
     out, oh = _out_like(q, out, "out")
@@ -722,6 +734,7 @@ def attention_paged(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, 
     _need(block_table, torch.int32, "block_table")
     if block_table.dim() != 2 or block_table.shape[0] != batch:
         raise ValueError("block_table must be [batch, width]")
+    _one_device(q, cache.k, block_table, cu_q, kv_lens, out, workspace)
     if out is not None:
         _apart(out, "out", cache_k=cache.k, cache_v=cache.v, k_scale=cache.k_scale, v_scale=cache.v_scale)
     out, oh = _out_like(q, out, "out")

@@ -8,6 +8,7 @@ import torch
 
 from exl3_trellis_quantized_gb300 import binding as B
 
+FAKE = 1 << 20  # an aligned address that is never followed
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
@@ -71,3 +72,50 @@ def test_unknown_layout_is_a_value_error(on_cpu):
     with pytest.raises(ValueError):
         B._rope_args(positions, phases, "neox", 1.0, 2)
     assert B._rope_args(positions, phases, "half", 1.0, 2).rot_dim == 16
+
+
+def test_tensors_of_one_call_lie_on_one_device(monkeypatch):
+    """Told apart before any address reaches a kernel (the meta device stands in for a second GPU)."""
+    reached = []
+    monkeypatch.setattr(B, "_need", lambda t, dtype, name: None)
+    monkeypatch.setattr(B, "_heads", lambda t, dtype, name: B._Heads(FAKE, 128, 64))
+    monkeypatch.setattr(B, "_out_like", lambda x, out, name: (x, B._Heads(FAKE, 128, 64)))
+    monkeypatch.setattr(B, "_raw_stream", lambda index: None)
+    monkeypatch.setattr(B, "_workspace_bytes", lambda *sizes: 16)
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *args: reached.append(name) or 0
+
+    monkeypatch.setattr(B, "lib", lambda: Library())
+
+    def ints(*shape, dtype=torch.int32, device="cpu"):
+        return torch.zeros(shape, dtype=dtype, device=device)
+
+    def rows(device="cpu"):
+        return torch.zeros((2, 2, 64), dtype=torch.bfloat16, device=device)
+
+    cache = B.KVCache.empty(3, 16, 2, 64, "int8", device="cpu")
+    far = B.KVCache.empty(3, 16, 2, 64, "int8", device="meta")
+    calls = {
+        "rope": (lambda x, p, f: B.rope(x, p, f), [rows(), ints(2), ints(32, dtype=torch.int64)]),
+        "kv_write": (lambda c, k, v, s, q, p, f: B.kv_write(c, k, v, s, q=q, positions=p, phases=f),
+                     [cache, rows(), rows(), ints(2, dtype=torch.int64), rows(), ints(2), ints(32, dtype=torch.int64)]),
+        "kv_read": (lambda c, s, k, v: B.kv_read(c, s, k=k, v=v), [cache, ints(2, dtype=torch.int64), rows(), rows()]),
+        "attention_prompt": (lambda q, k, v, cu: B.attention_prompt(q, k, v, cu), [rows(), rows(), rows(), ints(2)]),
+        "attention_paged": (lambda q, c, t, cu, n, w: B.attention_paged(q, c, t, cu, n, 1, 1, workspace=w),
+                            [rows(), cache, ints(1, 3), ints(2), ints(1), ints(64, dtype=torch.uint8)]),
+    }
+    for name, (call, args) in calls.items():
+        reached.clear()
+        call(*args)
+        assert reached == ["exl3_" + name]
+        for i, t in enumerate(args):
+            other = list(args)
+            other[i] = far if t is cache else t.to("meta")
+            reached.clear()
+            with pytest.raises(ValueError, match="device"):
+                call(*other)
+            assert not reached
+    with pytest.raises(ValueError, match="device"):
+        B.KVCache(cache.k, far.v, cache.k_scale, cache.v_scale, "int8")
