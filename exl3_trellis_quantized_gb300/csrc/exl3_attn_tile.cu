@@ -89,8 +89,8 @@ struct Units {
 };
 // A group's largest scale lies in [2^kScaleTop, 2^(kScaleTop + 1)) of its unit: codes then reach 2^15, and scales 2^24
 // times smaller still have all their bits.  No unit is below 2^kLeastUnit, so that sums of weights, which the values'
-// units divide, stay within fp32.
-constexpr int kScaleTop = 7, kLeastUnit = -80;
+// units divide, stay within fp32; the format's least scale, 2^-100, has its bits in that unit too.
+constexpr int kScaleTop = 7, kLeastUnit = -90;
 // Weights over a quantised cache may reach 2^15 (2^8 by the maximum's slack), so that those far below the largest are
 // still normal fp16 numbers.
 constexpr float kRoom = 7.0f;

@@ -341,7 +341,7 @@ exl3_status_t exl3_rope(const exl3_heads_t* x, exl3_dtype_t dtype, int64_t token
  * in that basis, in units of powers of two taken from the rows themselves, so rows of any size
  * do.  Two limits: where max_q * (q_heads / kv_heads) is above 16, a row whose scale is 2^24 times below the largest
  * of the 16 keys (counted from a multiple of 16) that it lies among loses bits; and value scales that one query sees
- * may differ by a factor of 2^100 (there a row of zeros counts as 2^-73, whatever its stored scale).
+ * may differ by a factor of 2^100 (a row of zeros, whatever its stored scale, may lie beside scales up to 2^40).
  */
 typedef enum { EXL3_KV_F16 = 0, EXL3_KV_BF16 = 1, EXL3_KV_INT8 = 2, EXL3_KV_INT4 = 3 } exl3_kv_format_t;
 typedef struct {

@@ -162,3 +162,14 @@ def test_query_rows_do_not_depend_on_each_other(fmt, dtype, dim, q_len, heads, k
     keep = [h for h in range(heads) if h not in (1, 2)]
     assert torch.equal(got[:, keep], want[:, keep])
     assert torch.isnan(got[:, 1]).all() and torch.isfinite(got[:, 2]).all()
+
+
+@pytest.mark.parametrize("fmt", ["int8", "int4"])
+@pytest.mark.parametrize("q_len", [1, 40, 150])
+@pytest.mark.parametrize("size", [1e-27, 1e-28, 4e-29])
+def test_smallest_scales(fmt, q_len, size):
+    """Rows down to the format's least scale, 2^-100, keep every bit of it."""
+    n = 300
+    small = rows(n, 2, 128, torch.full((n,), size), 2)
+    run(queries(q_len, 8, 128, "bf16"), rows(n, 2, 128, torch.ones(n), 1), small, fmt)
+    run(queries(q_len, 8, 128, "bf16", 0.3 / size), small, rows(n, 2, 128, torch.ones(n), 1), fmt)
