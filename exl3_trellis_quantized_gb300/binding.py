@@ -533,7 +533,8 @@ def rope_phases(rot_dim: int, base: float = 10000.0, scaling: str = "plain", fac
     """(phases, amplitude) for rope and kv_write: int64 [rot_dim / 2] on ``device``, turns per position in 2^-64.
 
     scaling: "plain", "linear" (positions / factor), "ntk" (larger base) or "yarn" (slow frequencies / factor,
-    fast ones kept, a ramp between ``slow`` and ``fast`` turns over ``original_len`` positions).
+    fast ones kept, a ramp between ``slow`` and ``fast`` turns over ``original_len`` positions, as in the paper; code
+    that ramps over the pairs' index gives other frequencies there: make such phases yourself).
     """
     out = torch.empty(max(0, int(rot_dim)) // 2, dtype=torch.int64)
     amplitude = ctypes.c_float(0.0)

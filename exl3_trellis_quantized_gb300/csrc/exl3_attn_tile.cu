@@ -25,14 +25,16 @@
 // for one another, and 16384 tokens of 32 heads took 1529 us.)
 //
 // Measured (query heads, key heads of 128; rates by the multiply-adds that the mask leaves):
-//   one prompt of 16384 tokens, 32 and 8 heads, bf16           1411 us: 1560 TFLOP/s, 82% of a large matrix product's
+//   one prompt of 16384 tokens, 32 and 8 heads, bf16           1400 us: 1570 TFLOP/s, 82% of a large matrix product's;
+//     in a loop that runs into the power limit 1510 to 1540 us, 76%
 //   ten prompts of 1 to 2048 tokens, 40 and 8 heads            144 us: 920 TFLOP/s; an item has 8 to 32 blocks of
 //     about 0.95 us each, and its diagonal blocks, first scores and output (2 to 4.5 us) weigh more
-//   512 tokens over 32768 16-bit keys, 32 and 8 heads          218 us: 1250 TFLOP/s; 64 items in seven parts each, three
+//   512 tokens over 32768 16-bit keys, 32 and 8 heads          220 us: 1240 TFLOP/s; 64 items in seven parts each, three
 //     a CTA of 73 blocks, and about 15 us for the parts' results and their join
 //   chunks of 129 to 700 tokens and single ones over up to 15000 8-bit keys, window 4096, 96 and 8 heads
-//     226 us: 895 TFLOP/s; four warps make fp16 rows of the codes, four passes' codes loaded ahead (one after the other:
+//     229 us: 885 TFLOP/s; four warps make fp16 rows of the codes, four passes' codes loaded ahead (one after the other:
 //     246), and an output costs 4 to 12 us
+// The kernels over 16-bit rows spill 12 bytes a thread beside their 168 registers; those over codes spill none.
 // What holds the first below the peak is the products themselves: with the softmax reduced to passing the barriers on,
 // the same prompt takes 1331 us.  A score product of N = 64 reads its 128 rows of q from shared memory for half the
 // operations that N = 128 would have (48 cycles instead of 32 a k16 step), and a commit, a wait and the next issue leave

@@ -14,9 +14,9 @@
 // from shared memory to operands in registers without a 16-bit copy in between.
 //
 // Measured, 32 query and 8 key heads of 128:
-//   48 sequences of 0 to 16384 keys, one token each, 8 bits   125 us, 713 MB: 5700 GB/s, 84% of a copy's
+//   48 sequences of 0 to 16384 keys, one token each, 8 bits   126 us, 713 MB: 5650 GB/s, 83% of a copy's
 //   8 sequences of 9000 to 32768 keys, 1 to 4 tokens, 4 bits, fp16 queries
-//     92 us, 216 MB: 2350 GB/s; two CTAs an SM (245 registers) issue what the widening of four-bit codes and
+//     94 us, 216 MB: 2300 GB/s; two CTAs an SM (246 registers) issue what the widening of four-bit codes and
 //     the second term take.  Three CTAs of fewer registers 118 us, pairs of warps on one ring 123 us.
 //   one sequence of 4097 keys, one token, 16 bits             12.4 us, 16.8 MB: the chain lengths, page ids,
 //     copies, join of the two launches

@@ -305,7 +305,10 @@ typedef struct {
  *                     context; g_i = clamp((r_i - slow) / (fast - slow), 0, 1);
  *                     f_i * (g_i + (1 - g_i) / factor), amplitude 0.1 ln(factor) + 1
  *                     (Peng et al., "YaRN: Efficient Context Window Extension of
- *                     Large Language Models")
+ *                     Large Language Models").  The ramp is the paper's, over turns;
+ *                     a checkpoint whose code ramps over the index i between two
+ *                     rounded bounds has other frequencies there, and takes phases
+ *                     of its own: any uint64 [rot_dim / 2] will do
  * factor >= 1, base > 1; fast > slow > 0 and original_len > 0 are read for YARN only.
  *   phases  HOST, uint64 [rot_dim / 2] (output);  amplitude  HOST (output)
  */
