@@ -5,15 +5,18 @@ The compute lives in ``libexl3.so`` (hand-written CUDA behind a C ABI, see
 tensors into pointers and sizes and calls the library.  There is no CPU or
 PyTorch fallback; if the library is missing every call raises.
 
-Beside the layer: rotary positions (``rope``), a paged cache of 16, 8 or 4 bits
-(``KVCache``, ``kv_write``, ``kv_read``) and attention over prompts
-(``attention_prompt``) and over the cache (``attention_paged``).
+Beside the layer: rotary positions of one or several axes and the norms of
+query and key heads (``rope``), a paged cache of 16, 8 or 4 bits (``KVCache``,
+``kv_write``, ``kv_read``), its page tables and a step's slots (``KVTables``,
+``kv_plan``, ``kv_release``), and attention over prompts (``attention_prompt``)
+and over the cache (``attention_paged``).
 """
 from .binding import (  # noqa: F401
     CODEBOOKS,
     KV_FORMATS,
     Exl3Error,
     KVCache,
+    KVTables,
     attention_paged,
     attention_paged_workspace_bytes,
     attention_prompt,
@@ -24,7 +27,9 @@ from .binding import (  # noqa: F401
     gemm_splitk,
     input_transform,
     input_transform_swiglu,
+    kv_plan,
     kv_read,
+    kv_release,
     kv_write,
     lib,
     linear,

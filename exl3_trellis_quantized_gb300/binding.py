@@ -37,6 +37,20 @@ class _Cache(ctypes.Structure):  # exl3_kv_cache_t
                 ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("format", ctypes.c_int)]
 
 
+class _Norm(ctypes.Structure):  # exl3_head_norm_t
+    _fields_ = [("weight", ctypes.c_void_p), ("head_stride", ctypes.c_int64), ("eps", ctypes.c_float)]
+
+
+class _Axes(ctypes.Structure):  # exl3_rope_axes_t
+    _fields_ = [("axes", ctypes.c_void_p), ("num_axes", ctypes.c_int32)]
+
+
+class _Tables(ctypes.Structure):  # exl3_kv_tables_t
+    _fields_ = [("block_table", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p), ("held", ctypes.c_void_p),
+                ("free_pages", ctypes.c_void_p), ("free_count", ctypes.c_void_p), ("batch", ctypes.c_int32),
+                ("table_width", ctypes.c_int32), ("page_size", ctypes.c_int32), ("capacity", ctypes.c_int32)]
+
+
 class Exl3Error(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -109,6 +123,14 @@ def lib() -> ctypes.CDLL:
     L.exl3_attention_paged_workspace_bytes.restype = sz
     L.exl3_attention_paged.argtypes = [heads, ctypes.c_int, i64, i32, cache, vp, i32, vp, vp, i32, i32, i32, i32, f32,
                                        vp, i64, i64, vp, sz, vp]
+    norm, axes, tables = ctypes.POINTER(_Norm), ctypes.POINTER(_Axes), ctypes.POINTER(_Tables)
+    L.exl3_norm_rope.argtypes = [heads, ctypes.c_int, i64, i32, i32, norm, rope_p, axes, vp, i64, i64, vp]
+    L.exl3_norm_kv_write.argtypes = [cache, heads, heads, ctypes.c_int, i64, vp, norm, norm, rope_p, axes, heads, i32, vp,
+                                     i64, i64, vp]
+    L.exl3_kv_plan.argtypes = [tables, vp, i64] + [vp] * 8
+    L.exl3_kv_release.argtypes = [tables] + [vp] * 6
+    for name in ("exl3_norm_rope", "exl3_norm_kv_write", "exl3_kv_plan", "exl3_kv_release"):
+        getattr(L, name).restype = ctypes.c_int
     for name in ("exl3_rope_phases", "exl3_rope", "exl3_kv_write", "exl3_kv_read", "exl3_attention_prompt",
                  "exl3_attention_paged"):
         getattr(L, name).restype = ctypes.c_int
@@ -544,28 +566,63 @@ def rope_phases(rot_dim: int, base: float = 10000.0, scaling: str = "plain", fac
     return out.to(device), float(amplitude.value)
 
 
-def _rope_args(positions: torch.Tensor, phases: torch.Tensor, layout: str, amplitude: float, tokens: int) -> _Rope:
-    _alike(positions, torch.int32, (tokens,), "positions")
+def _rope_args(positions: torch.Tensor, phases: torch.Tensor, layout: str, amplitude: float, tokens: int,
+               axes: Optional[torch.Tensor] = None) -> _Rope:
     _need(phases, torch.int64, "phases")
+    if axes is None:
+        _alike(positions, torch.int32, (tokens,), "positions")
+    elif positions.dim() != 2 or not 1 <= positions.shape[0] <= 255:
+        raise ValueError("positions must be [axes, tokens] where axes are given")
+    else:
+        _alike(positions, torch.int32, (positions.shape[0], tokens), "positions")
+        _alike(axes, torch.uint8, (phases.numel(),), "axes")
     if layout not in ROPE_LAYOUTS:
         raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}")
     return _Rope(phases.data_ptr(), positions.data_ptr(), 2 * phases.numel(), ROPE_LAYOUTS[layout], float(amplitude))
 
 
+def _axes_args(positions: torch.Tensor, axes: Optional[torch.Tensor]) -> Optional[_Axes]:
+    return None if axes is None else _Axes(axes.data_ptr(), positions.shape[0])
+
+
+def _norm_args(weight: Optional[torch.Tensor], eps: float, dtype, heads: int, d: int, name: str) -> Optional[_Norm]:
+    """exl3_head_norm_t of weights [head_dim], the same for all heads, or [heads, head_dim]."""
+    if weight is None:
+        return None
+    one = weight.dim() == 1
+    _alike(weight, dtype, (d,) if one else (heads, d), name)
+    return _Norm(weight.data_ptr(), 0 if one else d, float(eps))
+
+
 def rope(x: torch.Tensor, positions: torch.Tensor, phases: torch.Tensor, layout: str = "half", amplitude: float = 1.0,
-         out: Optional[torch.Tensor] = None) -> torch.Tensor:
+         out: Optional[torch.Tensor] = None, axes: Optional[torch.Tensor] = None, weight: Optional[torch.Tensor] = None,
+         eps: float = 1e-6) -> torch.Tensor:
     """Rotary positions on the heads of x [tokens, heads, head_dim] (a view of a fused projection will do).
 
     The first 2 * phases.numel() values of every head turn.  ``out`` may be x itself.
+
+    axes (uint8 [phases.numel()]): positions are int32 [number of axes, tokens], and pair i turns by the row axes[i] of
+    them (time, height and width of images and video).  weight ([head_dim], or [heads, head_dim], of x's type): every
+    head is first divided by sqrt(mean of its squares + eps) and multiplied by the weight, in the same pass and without
+    a rounding in between.
     """
     dt = _type(x, "x")
     xh = _heads(x, x.dtype, "x")
     tokens, heads, d = x.shape
-    r = _rope_args(positions, phases, layout, amplitude, tokens)
-    _one_device(x, positions, phases, out)
+    r = _rope_args(positions, phases, layout, amplitude, tokens, axes)
+    norm = _norm_args(weight, eps, x.dtype, heads, d, "weight")
+    _one_device(x, positions, phases, out, axes, weight)
+    if out is not None and weight is not None:
+        _apart(out, "out", weight=weight)
     out, oh = _out_like(x, out, "out")
-    st = lib().exl3_rope(xh, dt, tokens, heads, d, r, oh.data, oh.token_stride, oh.head_stride, _raw_stream(x.device.index))
-    _check(st, "exl3_rope")
+    stream = _raw_stream(x.device.index)
+    if norm is None and axes is None:
+        st = lib().exl3_rope(xh, dt, tokens, heads, d, r, oh.data, oh.token_stride, oh.head_stride, stream)
+        _check(st, "exl3_rope")
+    else:
+        st = lib().exl3_norm_rope(xh, dt, tokens, heads, d, norm, r, _axes_args(positions, axes), oh.data,
+                                  oh.token_stride, oh.head_stride, stream)
+        _check(st, "exl3_norm_rope")
     return out
 
 
@@ -617,12 +674,18 @@ class KVCache:
 
 def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, q: Optional[torch.Tensor] = None,
              positions: Optional[torch.Tensor] = None, phases: Optional[torch.Tensor] = None, layout: str = "half",
-             amplitude: float = 1.0, q_out: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
+             amplitude: float = 1.0, q_out: Optional[torch.Tensor] = None, axes: Optional[torch.Tensor] = None,
+             q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+             eps: float = 1e-6) -> Optional[torch.Tensor]:
     """Write k and v [tokens, kv_heads, head_dim] into the cache rows ``slots`` (int64; page * page_size + row,
     anything outside the cache writes nothing).
 
     With positions and phases the keys are rotated first, and so is q [tokens, heads, head_dim] when given: the
     rotated q (q_out, a new tensor unless given) is returned, else None.
+
+    axes: positions are [number of axes, tokens], as for rope.  q_weight, k_weight ([head_dim], or [heads, head_dim]):
+    the heads of q and k are first divided by their root mean square and multiplied by these, as for rope; with
+    q_weight q needs no positions.
     """
     dt = _type(k, "k")
     tokens = k.shape[0]
@@ -630,27 +693,39 @@ def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tens
     if tuple(k.shape) != (tokens, cache.kv_heads, cache.head_dim) or v.shape != k.shape:
         raise ValueError("k and v must be [tokens, kv_heads, head_dim] of the cache")
     _alike(slots, torch.int64, (tokens,), "slots")
-    _one_device(k, v, cache.k, slots, q, positions, phases, q_out)
+    _one_device(k, v, cache.k, slots, q, positions, phases, q_out, axes, q_weight, k_weight)
     r = qh = None
     heads, qo = 0, (None, 0, 0)
     if phases is not None:
         if positions is None:
             raise ValueError("phases need positions")
-        r = _rope_args(positions, phases, layout, amplitude, tokens)
+        r = _rope_args(positions, phases, layout, amplitude, tokens, axes)
+    elif axes is not None:
+        raise ValueError("axes need positions and phases")
+    kn = _norm_args(k_weight, eps, k.dtype, cache.kv_heads, cache.head_dim, "k_weight")
+    qn = None
     if q is not None:
-        if r is None:
-            raise ValueError("q is only taken to be rotated: it needs positions and phases")
+        if r is None and q_weight is None:
+            raise ValueError("q is only taken to be rotated or normed: it needs positions and phases, or q_weight")
         if q.dim() != 3 or q.shape[0] != tokens or q.shape[2] != cache.head_dim:
             raise ValueError("q must be [tokens, heads, head_dim]")
         qh, heads = _heads(q, k.dtype, "q"), q.shape[1]
+        qn = _norm_args(q_weight, eps, k.dtype, heads, cache.head_dim, "q_weight")
         if q_out is not None:
-            _apart(q_out, "q_out", k=k, v=v, cache_k=cache.k, cache_v=cache.v, k_scale=cache.k_scale, v_scale=cache.v_scale)
+            _apart(q_out, "q_out", k=k, v=v, cache_k=cache.k, cache_v=cache.v, k_scale=cache.k_scale, v_scale=cache.v_scale,
+                   q_weight=q_weight, k_weight=k_weight)
         q_out, oh = _out_like(q, q_out, "q_out")
         qo = (oh.data, oh.token_stride, oh.head_stride)
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    st = lib().exl3_kv_write(cache.args, kh, vh, dt, tokens, slots.data_ptr(), r, qh, heads, *qo, _raw_stream(k.device.index))
-    _check(st, "exl3_kv_write")
+    elif q_out is not None or q_weight is not None:
+        raise ValueError(("q_out" if q_out is not None else "q_weight") + " without q")
+    stream = _raw_stream(k.device.index)
+    if qn is None and kn is None and axes is None:
+        st = lib().exl3_kv_write(cache.args, kh, vh, dt, tokens, slots.data_ptr(), r, qh, heads, *qo, stream)
+        _check(st, "exl3_kv_write")
+    else:
+        st = lib().exl3_norm_kv_write(cache.args, kh, vh, dt, tokens, slots.data_ptr(), qn, kn, r,
+                                      _axes_args(positions, axes), qh, heads, *qo, stream)
+        _check(st, "exl3_norm_kv_write")
     return q_out
 
 
@@ -673,6 +748,125 @@ def kv_read(cache: KVCache, slots: torch.Tensor, dtype=torch.bfloat16, k: Option
     st = lib().exl3_kv_read(cache.args, slots.data_ptr(), shape[0], _type(k, "k"), k.data_ptr(), v.data_ptr(), _raw_stream(slots.device.index))
     _check(st, "exl3_kv_read")
     return k, v
+
+
+class KVTables:
+    """Page tables of a batch of requests on the GPU, and the free pages of a cache as a stack.
+
+    block_table int32 [batch, width], kv_lens int32 [batch] (cached tokens), held int32 [batch] (pages in the table's row),
+    free_pages int32 [capacity], of which the first free_count (int32 [1]) are free.  kv_lens may be set back (refused
+    drafts) without touching held.  As with KVCache, the calls take the addresses that the tensors have now."""
+
+    def __init__(self, block_table: torch.Tensor, kv_lens: torch.Tensor, held: torch.Tensor, free_pages: torch.Tensor,
+                 free_count: torch.Tensor, page_size: int):
+        _need(block_table, torch.int32, "block_table")
+        if block_table.dim() != 2 or block_table.shape[1] < 1:
+            raise ValueError("block_table must be [batch, width]")
+        batch, width = block_table.shape
+        _alike(kv_lens, torch.int32, (batch,), "kv_lens")
+        _alike(held, torch.int32, (batch,), "held")
+        _need(free_pages, torch.int32, "free_pages")
+        if free_pages.dim() != 1 or free_pages.numel() < 1:
+            raise ValueError("free_pages must be [capacity]")
+        _alike(free_count, torch.int32, (1,), "free_count")
+        _one_device(block_table, kv_lens, held, free_pages, free_count)
+        if page_size not in (16, 32, 64, 128, 256) or width * page_size > 1 << 30:
+            raise ValueError("page_size must be 16, 32, 64, 128 or 256, and a row of the table at most 2^30 tokens")
+        parts = {"block_table": block_table, "kv_lens": kv_lens, "held": held, "free_pages": free_pages, "free_count": free_count}
+        names = list(parts)
+        for i, name in enumerate(names):
+            _apart(parts[name], name, **{n: parts[n] for n in names[i + 1:]})
+        args = _Tables(block_table.data_ptr(), kv_lens.data_ptr(), held.data_ptr(), free_pages.data_ptr(),
+                       free_count.data_ptr(), batch, width, page_size, free_pages.numel())
+        spans = tuple((t.data_ptr(), t.data_ptr() + 4 * t.numel()) for t in (kv_lens, held, free_count))
+        same = (block_table.data_ptr(), free_pages.data_ptr(), batch, width, page_size, free_pages.numel())
+        self.__dict__.update(parts, batch=batch, table_width=width, page_size=page_size, args=args, _spans=spans, _same=same)
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"KVTables.{name} cannot be assigned: make a KVTables of the new tensors")
+
+    @classmethod
+    def empty(cls, batch: int, max_len: int, num_pages: int, page_size: int, device="cuda") -> "KVTables":
+        """Tables of requests without tokens, each with room for max_len, over a cache of num_pages free pages."""
+        width = max(1, (max_len + page_size - 1) // page_size)
+
+        def ints(*shape):
+            return torch.zeros(shape, dtype=torch.int32, device=device)
+
+        free = torch.arange(num_pages - 1, -1, -1, dtype=torch.int32, device=device)  # page 0 is taken first
+        return cls(ints(batch, width) - 1, ints(batch), ints(batch), free, ints(1) + num_pages, page_size)
+
+
+def _new_state(tables: KVTables, into: Optional[KVTables]) -> KVTables:
+    """Where a call writes the new lengths, held pages and count: the tables' own, or those of another KVTables over the
+    same table and stack."""
+    if into is None or into is tables:
+        return tables
+    if into._same != tables._same:
+        raise ValueError("into must share block_table and free_pages with the tables")
+    for i, (a0, a1) in enumerate(into._spans):
+        for j, (b0, b1) in enumerate(tables._spans):
+            if a0 < b1 and b0 < a1 and (i != j or a0 != b0):
+                raise ValueError("into overlaps the tables without being in their place")
+    return into
+
+
+def kv_plan(tables: KVTables, new_lens: torch.Tensor, total: int, into: Optional[KVTables] = None,
+            cu_q: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+            slots: Optional[torch.Tensor] = None, granted: Optional[torch.Tensor] = None):
+    """(cu_q, positions, slots, granted): a step's packing of new_lens[b] (int32 [batch]) new tokens of each request, and
+    pages for them, all on the GPU.
+
+    cu_q int32 [batch + 1]; positions int32 [total] and slots int64 [total] of the packed tokens (rows past the last
+    token: position 0 and slot -1, so ``total`` may be the fixed size of a captured step); granted bool [batch].  The
+    tables' lengths, rows and stack move on, or with ``into`` (a KVTables over the same block_table and free_pages) the
+    new lengths, held pages and count go there.  A request whose pages are not to be had (or whose tokens do not fit
+    into total, or pages into the table) is not granted: its state stays and its slots are -1; none after it gets
+    pages that it waits for.  The four outputs are new tensors unless given.
+    """
+    total, batch, device = int(total), tables.batch, tables.kv_lens.device
+    _alike(new_lens, torch.int32, (batch,), "new_lens")
+    state = _new_state(tables, into)
+    outs = {}
+    for name, t, dtype, n in (("cu_q", cu_q, torch.int32, batch + 1), ("positions", positions, torch.int32, total),
+                              ("slots", slots, torch.int64, total), ("granted", granted, torch.bool, batch)):
+        if t is None:
+            t = torch.empty(max(0, n), dtype=dtype, device=device)
+        else:
+            _alike(t, dtype, (n,), name)
+            _apart(t, name, new_lens=new_lens, **_state_parts(tables, state), **outs)
+        outs[name] = t
+    _one_device(tables.kv_lens, new_lens, state.kv_lens, *outs.values())
+    st = lib().exl3_kv_plan(tables.args, new_lens.data_ptr(), total, state.kv_lens.data_ptr(), state.held.data_ptr(),
+                            state.free_count.data_ptr(), *(t.data_ptr() for t in outs.values()),
+                            _raw_stream(device.index))
+    _check(st, "exl3_kv_plan")
+    return tuple(outs.values())
+
+
+def _state_parts(tables: KVTables, state: KVTables) -> dict:
+    parts = {n: getattr(tables, n) for n in ("block_table", "kv_lens", "held", "free_pages", "free_count")}
+    if state is not tables:
+        parts.update({"into_" + n: getattr(state, n) for n in ("kv_lens", "held", "free_count")})
+    return parts
+
+
+def kv_release(tables: KVTables, ended: torch.Tensor, shared: Optional[torch.Tensor] = None,
+               into: Optional[KVTables] = None) -> None:
+    """Requests end (bool [batch]): their pages go back onto the stack, their lengths and held pages become 0.
+
+    shared (int32 [batch]): leading pages of an ended request's row that belong to others too and stay off the stack.
+    ``into`` as for kv_plan.
+    """
+    _alike(ended, torch.bool, (tables.batch,), "ended")
+    if shared is not None:
+        _alike(shared, torch.int32, (tables.batch,), "shared")
+    state = _new_state(tables, into)
+    _one_device(tables.kv_lens, ended, shared, state.kv_lens)
+    st = lib().exl3_kv_release(tables.args, ended.data_ptr(), None if shared is None else shared.data_ptr(),
+                               state.kv_lens.data_ptr(), state.held.data_ptr(), state.free_count.data_ptr(),
+                               _raw_stream(tables.kv_lens.device.index))
+    _check(st, "exl3_kv_release")
 
 
 def attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, max_len: int = 0,

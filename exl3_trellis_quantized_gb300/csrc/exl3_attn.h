@@ -35,12 +35,21 @@ struct KvCache {
   int kv_heads, head_dim, format;
 };
 
-// Rotary positions; rot_dim 0: none.
+// Rotary positions; rot_dim 0: none.  axes: the row of positions [num_axes][tokens] that each pair turns by, null: one row.
 struct RopeArgs {
   const uint64_t* phases;
   const int32_t* positions;
   int rot_dim, interleaved;
   float amplitude;
+  const uint8_t* axes;
+  int num_axes;
+};
+
+// Root mean square norm of heads: weight [heads] rows of head_dim, head_stride apart (0: one row for all); null: none.
+struct HeadNorm {
+  const uint16_t* weight;
+  int64_t head_stride;
+  float eps;
 };
 
 // Rotary rows to `out` (heads [0, rope_heads) of the call), then the key and
@@ -56,6 +65,7 @@ struct RopeWriteArgs {
   int kv_heads;
   int64_t tokens;
   RopeArgs rope;
+  HeadNorm x_norm, k_norm;
   int bf16;
 };
 cudaError_t launch_rope_write(const RopeWriteArgs& a, int head_dim, cudaStream_t stream);
@@ -69,6 +79,32 @@ struct KvReadArgs {
   int bf16;  // type of k and v
 };
 cudaError_t launch_kv_read(const KvReadArgs& a, cudaStream_t stream);
+
+// Page tables of a batch of requests and the stack of free pages.
+struct KvTables {
+  int32_t* table;       // [batch][table_width]
+  const int32_t* kv_lens;
+  const int32_t* held;  // pages of each request's row
+  int32_t* free_pages;  // [capacity]
+  const int32_t* free_count;
+  int batch, table_width, page_shift, capacity;
+};
+struct KvPlanArgs {
+  KvTables t;
+  const int32_t* new_lens;
+  int64_t total;
+  int32_t *kv_lens_out, *held_out, *free_count_out, *cu_q, *positions;
+  int64_t* slots;
+  uint8_t* granted;
+};
+struct KvReleaseArgs {
+  KvTables t;
+  const uint8_t* ended;
+  const int32_t* shared;  // may be null
+  int32_t *kv_lens_out, *held_out, *free_count_out;
+};
+cudaError_t launch_kv_plan(const KvPlanArgs& a, cudaStream_t stream);
+cudaError_t launch_kv_release(const KvReleaseArgs& a, cudaStream_t stream);
 
 struct AttnArgs {
   HeadsView q, k, v;  // k, v: prompt attention only

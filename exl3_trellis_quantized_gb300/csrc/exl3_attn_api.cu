@@ -41,16 +41,46 @@ exl3_status_t check_rope(const exl3_rope_t* r, int32_t head_dim, int64_t tokens,
   if (!isfinite(r->amplitude)) return EXL3_EINVAL;
   if (r->phases == nullptr || (reinterpret_cast<uintptr_t>(r->phases) & 7u) != 0) return EXL3_EINVAL;
   if (tokens > 0 && (r->positions == nullptr || (reinterpret_cast<uintptr_t>(r->positions) & 3u) != 0)) return EXL3_EINVAL;
-  *out = {r->phases, r->positions, r->rot_dim, r->layout == EXL3_ROPE_INTERLEAVED ? 1 : 0, r->amplitude};
+  *out = {r->phases, r->positions, r->rot_dim, r->layout == EXL3_ROPE_INTERLEAVED ? 1 : 0, r->amplitude, nullptr, 1};
+  return EXL3_OK;
+}
+// Adds the axes of a checked rotation's pairs; null: the positions have one row.
+exl3_status_t check_axes(const exl3_rope_axes_t* axes, exl3::RopeArgs* out) {
+  if (axes == nullptr) return EXL3_OK;
+  if (axes->axes == nullptr || axes->num_axes < 1 || axes->num_axes > 255) return EXL3_EINVAL;
+  out->axes = axes->axes;
+  out->num_axes = axes->num_axes;
+  return EXL3_OK;
+}
+exl3_status_t check_norm(const exl3_head_norm_t* n, exl3::HeadNorm* out) {
+  if (n == nullptr) return EXL3_OK;
+  if (!aligned16(n->weight) || n->head_stride < 0 || n->head_stride % 8 != 0 || n->head_stride > (int64_t(1) << 32)) return EXL3_EINVAL;
+  if (!(n->eps >= 1.1754944e-38f) || !isfinite(n->eps)) return EXL3_EINVAL;  // a row of zeros stays one
+  *out = {static_cast<const uint16_t*>(n->weight), n->head_stride, n->eps};
+  return EXL3_OK;
+}
+bool aligned4(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+// log2 of a page size that the cache has, or -1.
+int page_shift(int32_t page_size) {
+  for (int shift = 4; shift <= 8; ++shift)
+    if ((1 << shift) == page_size) return shift;
+  return -1;
+}
+exl3_status_t check_tables(const exl3_kv_tables_t* t, exl3::KvTables* out) {
+  if (t == nullptr || !valid_rows(t->batch) || t->table_width < 1 || t->capacity < 1) return EXL3_EINVAL;
+  const int shift = page_shift(t->page_size);
+  if (shift < 0 || ((int64_t)t->table_width << shift) > (int64_t(1) << 30) || t->capacity > (1 << 30)) return EXL3_EINVAL;
+  if (!aligned4(t->free_pages) || !aligned4(t->free_count)) return EXL3_EINVAL;
+  if (t->batch > 0 && (!aligned4(t->block_table) || !aligned4(t->kv_lens) || !aligned4(t->held))) return EXL3_EINVAL;
+  *out = {t->block_table, t->kv_lens, t->held, t->free_pages, t->free_count, t->batch, t->table_width, shift, t->capacity};
   return EXL3_OK;
 }
 
 exl3_status_t check_cache(const exl3_kv_cache_t* c, exl3::KvCache* out) {
   if (c == nullptr || c->format < EXL3_KV_F16 || c->format > EXL3_KV_INT4) return EXL3_EINVAL;
   if (c->kv_heads < 1 || c->kv_heads > 65536 || c->num_pages < 1 || c->num_pages >= (int64_t(1) << 31)) return EXL3_EINVAL;
-  int shift = 4;
-  while (shift < 8 && (1 << shift) != c->page_size) ++shift;
-  if ((1 << shift) != c->page_size) return EXL3_EINVAL;
+  const int shift = page_shift(c->page_size);
+  if (shift < 0) return EXL3_EINVAL;
   const exl3_status_t st = check_head_dim(c->head_dim);
   if (st != EXL3_OK) return st;
   // cache rows (and one past the last) are coordinates of a tensor map
@@ -147,12 +177,25 @@ exl3_status_t exl3_rope_phases(int32_t rot_dim, double base, exl3_rope_scaling_t
 exl3_status_t exl3_rope(const exl3_heads_t* x, exl3_dtype_t dtype, int64_t tokens, int32_t heads, int32_t head_dim,
                         const exl3_rope_t* rope, void* out, int64_t out_token_stride, int64_t out_head_stride,
                         void* stream) {
+  return exl3_norm_rope(x, dtype, tokens, heads, head_dim, nullptr, rope, nullptr, out, out_token_stride, out_head_stride, stream);
+}
+
+exl3_status_t exl3_norm_rope(const exl3_heads_t* x, exl3_dtype_t dtype, int64_t tokens, int32_t heads, int32_t head_dim,
+                             const exl3_head_norm_t* norm, const exl3_rope_t* rope, const exl3_rope_axes_t* axes, void* out,
+                             int64_t out_token_stride, int64_t out_head_stride, void* stream) {
   if (!valid_rows(tokens) || heads < 1 || heads > 65536 || !valid_dtype(dtype)) return EXL3_EINVAL;
   exl3_status_t st = check_head_dim(head_dim);
   if (st != EXL3_OK) return st;
   exl3::RopeWriteArgs a = {};
-  st = check_rope(rope, head_dim, tokens, &a.rope);
+  st = check_norm(norm, &a.x_norm);
   if (st != EXL3_OK) return st;
+  if (rope != nullptr || norm == nullptr) {
+    st = check_rope(rope, head_dim, tokens, &a.rope);
+    if (st == EXL3_OK) st = check_axes(axes, &a.rope);
+    if (st != EXL3_OK) return st;
+  } else if (axes != nullptr) {
+    return EXL3_EINVAL;
+  }
   if (!valid_strides(out_token_stride, out_head_stride)) return EXL3_EINVAL;
   if (tokens == 0) return EXL3_OK;
   if (!valid_heads(x) || !valid_out(x, out, out_token_stride, out_head_stride)) return EXL3_EINVAL;
@@ -163,24 +206,39 @@ exl3_status_t exl3_rope(const exl3_heads_t* x, exl3_dtype_t dtype, int64_t token
   a.out_head_stride = out_head_stride;
   a.tokens = tokens;
   a.bf16 = dtype == EXL3_BF16;
-  return exl3::api_status(exl3::launch_rope_write(a, head_dim, static_cast<cudaStream_t>(stream)), "exl3_rope");
+  return exl3::api_status(exl3::launch_rope_write(a, head_dim, static_cast<cudaStream_t>(stream)), norm != nullptr ? "exl3_norm_rope" : "exl3_rope");
 }
 
 exl3_status_t exl3_kv_write(const exl3_kv_cache_t* cache, const exl3_heads_t* k, const exl3_heads_t* v,
                             exl3_dtype_t dtype, int64_t tokens, const int64_t* slots, const exl3_rope_t* rope,
                             const exl3_heads_t* q, int32_t q_heads, void* q_out, int64_t q_out_token_stride,
                             int64_t q_out_head_stride, void* stream) {
+  return exl3_norm_kv_write(cache, k, v, dtype, tokens, slots, nullptr, nullptr, rope, nullptr, q, q_heads, q_out,
+                            q_out_token_stride, q_out_head_stride, stream);
+}
+
+exl3_status_t exl3_norm_kv_write(const exl3_kv_cache_t* cache, const exl3_heads_t* k, const exl3_heads_t* v,
+                                 exl3_dtype_t dtype, int64_t tokens, const int64_t* slots,
+                                 const exl3_head_norm_t* q_norm, const exl3_head_norm_t* k_norm,
+                                 const exl3_rope_t* rope, const exl3_rope_axes_t* axes, const exl3_heads_t* q,
+                                 int32_t q_heads, void* q_out, int64_t q_out_token_stride, int64_t q_out_head_stride,
+                                 void* stream) {
   if (!valid_rows(tokens) || !valid_dtype(dtype) || q_heads < 0 || q_heads > 65536) return EXL3_EINVAL;
   exl3::RopeWriteArgs a = {};
   exl3_status_t st = check_cache(cache, &a.cache);
   if (st != EXL3_OK) return st;
   if (!format_fits(a.cache.format, dtype)) return EXL3_EINVAL;
+  st = check_norm(k_norm, &a.k_norm);
+  if (st == EXL3_OK) st = check_norm(q_norm, &a.x_norm);
+  if (st != EXL3_OK) return st;
   if (rope != nullptr) {
     st = check_rope(rope, a.cache.head_dim, tokens, &a.rope);
+    if (st == EXL3_OK) st = check_axes(axes, &a.rope);
     if (st != EXL3_OK) return st;
-  } else if (q_heads != 0) {
+  } else if ((q_heads != 0 && q_norm == nullptr) || axes != nullptr) {
     return EXL3_EINVAL;
   }
+  if (q_norm != nullptr && q_heads == 0) return EXL3_EINVAL;
   if (q_heads > 0 && !valid_strides(q_out_token_stride, q_out_head_stride)) return EXL3_EINVAL;
   if (tokens == 0) return EXL3_OK;
   if (!valid_heads(k) || !valid_heads(v)) return EXL3_EINVAL;
@@ -200,6 +258,42 @@ exl3_status_t exl3_kv_write(const exl3_kv_cache_t* cache, const exl3_heads_t* k,
   a.tokens = tokens;
   a.bf16 = dtype == EXL3_BF16;
   return exl3::api_status(exl3::launch_rope_write(a, a.cache.head_dim, static_cast<cudaStream_t>(stream)), "exl3_kv_write");
+}
+
+exl3_status_t exl3_kv_plan(const exl3_kv_tables_t* tables, const int32_t* new_lens, int64_t total, int32_t* kv_lens_out,
+                           int32_t* held_out, int32_t* free_count_out, int32_t* cu_q, int32_t* positions, int64_t* slots,
+                           uint8_t* granted, void* stream) {
+  exl3::KvPlanArgs a = {};
+  const exl3_status_t st = check_tables(tables, &a.t);
+  if (st != EXL3_OK) return st;
+  if (!valid_rows(total) || !aligned4(cu_q) || !aligned4(free_count_out)) return EXL3_EINVAL;
+  if (a.t.batch > 0 && (!aligned4(new_lens) || !aligned4(kv_lens_out) || !aligned4(held_out) || granted == nullptr)) return EXL3_EINVAL;
+  if (total > 0 && (!aligned4(positions) || slots == nullptr || (reinterpret_cast<uintptr_t>(slots) & 7u) != 0)) return EXL3_EINVAL;
+  a.new_lens = new_lens;
+  a.total = total;
+  a.kv_lens_out = kv_lens_out;
+  a.held_out = held_out;
+  a.free_count_out = free_count_out;
+  a.cu_q = cu_q;
+  a.positions = positions;
+  a.slots = slots;
+  a.granted = granted;
+  return exl3::api_status(exl3::launch_kv_plan(a, static_cast<cudaStream_t>(stream)), "exl3_kv_plan");
+}
+
+exl3_status_t exl3_kv_release(const exl3_kv_tables_t* tables, const uint8_t* ended, const int32_t* shared,
+                              int32_t* kv_lens_out, int32_t* held_out, int32_t* free_count_out, void* stream) {
+  exl3::KvReleaseArgs a = {};
+  const exl3_status_t st = check_tables(tables, &a.t);
+  if (st != EXL3_OK) return st;
+  if (!aligned4(free_count_out) || (reinterpret_cast<uintptr_t>(shared) & 3u) != 0) return EXL3_EINVAL;
+  if (a.t.batch > 0 && (ended == nullptr || !aligned4(kv_lens_out) || !aligned4(held_out))) return EXL3_EINVAL;
+  a.ended = ended;
+  a.shared = shared;
+  a.kv_lens_out = kv_lens_out;
+  a.held_out = held_out;
+  a.free_count_out = free_count_out;
+  return exl3::api_status(exl3::launch_kv_release(a, static_cast<cudaStream_t>(stream)), "exl3_kv_release");
 }
 
 exl3_status_t exl3_kv_read(const exl3_kv_cache_t* cache, const int64_t* slots, int64_t tokens, exl3_dtype_t dtype,

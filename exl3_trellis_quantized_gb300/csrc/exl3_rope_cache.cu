@@ -229,8 +229,32 @@ __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
   b = __fadd_rn(__fmul_rn(q, c), __fmul_rn(p, s));
 }
 
-// KV: there are keys and values
-template <int D, bool KV>
+// Sum over the LANES neighbouring lanes of a row (aligned; other rows of the warp need not come here).
+template <int LANES>
+__device__ __forceinline__ float row_sum(float x) {
+  const uint32_t mask = ((1u << LANES) - 1u) << ((threadIdx.x & 31) & ~(LANES - 1));
+#pragma unroll
+  for (int s = 1; s < LANES; s *= 2) x += __shfl_xor_sync(mask, x, s);
+  return x;
+}
+template <int N>
+__device__ __forceinline__ float square_sum(const float2 (&v)[N]) {
+  float2 s = mul2(v[0], v[0]);
+#pragma unroll
+  for (int j = 1; j < N; ++j) s = fma2(v[j], v[j], s);
+  return s.x + s.y;
+}
+// v times the row's 1 / rms, times the weights of the same places.
+__device__ __forceinline__ void scale_row(float2* v, float inv, const uint4& weight, bool bf16) {
+  float2 w[4];
+  unpack8(weight, bf16, w);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = mul2(mul2(v[j], twice(inv)), w[j]);
+}
+
+// KV: there are keys and values.  NORM: x's rows or the keys' (or both) are divided by their root mean square and
+// multiplied by weights first, in fp32 and without a rounding before the rotation.
+template <int D, bool KV, bool NORM>
 __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_write_kernel(const RopeWriteArgs a, int units_per_block) {
   constexpr int LANES = D / 8;
   constexpr int GROUPS = kRopeThreads / LANES;
@@ -297,7 +321,9 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_write_kernel(c
   if (KV) load_kv(ku0);
 
   if ((int)threadIdx.x < half) {
-    const uint64_t turned = (uint64_t)(int64_t)a.rope.positions[t] * a.rope.phases[threadIdx.x];
+    int64_t at = t;
+    if (a.rope.axes != nullptr) at += min((int)a.rope.axes[threadIdx.x], a.rope.num_axes - 1) * a.tokens;
+    const uint64_t turned = (uint64_t)(int64_t)a.rope.positions[at] * a.rope.phases[threadIdx.x];
     const float angle = __fmul_rn((float)(int32_t)(turned >> 32), 1.46291807926715968e-9f);  // pi / 2^31
     cs[threadIdx.x] = __fmul_rn(cosf(angle), a.rope.amplitude);
     sn[threadIdx.x] = __fmul_rn(sinf(angle), a.rope.amplitude);
@@ -309,6 +335,15 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_write_kernel(c
 #pragma unroll
     for (int j = 0; j < 4; ++j) c[j] = turns ? cs[4 * l + j] : 1.0f, s[j] = turns ? sn[4 * l + j] : 0.0f;
     uint16_t* out = static_cast<uint16_t*>(a.out) + t * a.out_token_stride;
+    // weights of this lane's places
+    auto weight_of = [&](int r) {
+      const uint16_t* src = a.x_norm.weight + r * a.x_norm.head_stride;
+      const uint2 lo = *reinterpret_cast<const uint2*>(src + at0), hi = *reinterpret_cast<const uint2*>(src + at1);
+      return make_uint4(lo.x, lo.y, hi.x, hi.y);
+    };
+    const bool normed = NORM && a.x_norm.weight != nullptr;
+    uint4 weight = make_uint4(0u, 0u, 0u, 0u);
+    if (normed) weight = weight_of(0);
     for (int u = u0; u < min(xu, u1); u += kRopeBatch) {
       if (u > u0) load_x(u);
 #pragma unroll
@@ -316,7 +351,24 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_write_kernel(c
         const int r = (u + i) * GROUPS + group;
         if (u + i >= min(xu, u1) || r >= a.x_heads) break;
         uint4 w = make_uint4(raw[i][0].x, raw[i][0].y, raw[i][1].x, raw[i][1].y);
-        if (turns) {
+        if (NORM && normed) {
+          float2 v[4];
+          unpack8(w, bf16, v);
+          if (a.x_norm.head_stride != 0) weight = weight_of(r);
+          const float inv = rsqrtf(fmaf(row_sum<LANES>(square_sum(v)), 1.0f / D, a.x_norm.eps));
+          scale_row(v, inv, weight, bf16);
+          if (turns) {
+            float f[8] = {v[0].x, v[0].y, v[1].x, v[1].y, v[2].x, v[2].y, v[3].x, v[3].y};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if (pairs) turn(f[2 * j], f[2 * j + 1], c[j], s[j]);
+              else turn(f[j], f[4 + j], c[j], s[j]);
+            }
+            w = pack8(f, bf16);
+          } else {
+            w = pack8(v, bf16);
+          }
+        } else if (turns) {
           float v[8];
           unpack8(w, bf16, v);
           if (pairs) {
@@ -341,7 +393,51 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_write_kernel(c
       load_kv(u + 1);
       const int r = kv_row(u);
       const bool there = r < 2 * a.kv_heads, isk = r < a.kv_heads;
-      if (isk && half > 0) {
+      if (NORM && isk && a.k_norm.weight != nullptr) {
+        const int hl = half >> 3;  // chunks of one half
+        const uint16_t* weights = a.k_norm.weight + r * a.k_norm.head_stride;
+        float2 v[8];
+        unpack8(w[0], bf16, v);
+        unpack8(w[1], bf16, v + 4);
+        const float inv = rsqrtf(fmaf(row_sum<KLANES>(square_sum(v)), 1.0f / D, a.k_norm.eps));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) scale_row(v + 4 * i, inv, *reinterpret_cast<const uint4*>(weights + 8 * (kl + KLANES * i)), bf16);
+        if (pairs) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int ch = kl + KLANES * i;
+            if (8 * ch >= 2 * half) continue;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) turn(v[4 * i + j].x, v[4 * i + j].y, cs[4 * ch + j], sn[4 * ch + j]);
+          }
+        } else if (hl == KLANES) {  // the whole row turns: both values of each pair are this lane's
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            turn(v[j].x, v[4 + j].x, cs[8 * kl + 2 * j], sn[8 * kl + 2 * j]);
+            turn(v[j].y, v[4 + j].y, cs[8 * kl + 2 * j + 1], sn[8 * kl + 2 * j + 1]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int ch = kl + KLANES * i;
+            if (8 * ch >= 2 * half) continue;
+            // the other values of the pairs, read once more
+            const bool upper = ch >= hl;
+            const int other = upper ? ch - hl : ch + hl, f = 8 * (upper ? ch - hl : ch);
+            float2 o[4];
+            unpack8(*reinterpret_cast<const uint4*>(kv_src(r) + 8 * other), bf16, o);
+            scale_row(o, inv, *reinterpret_cast<const uint4*>(weights + 8 * other), bf16);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              float2& x = v[4 * i + j];
+              x.x = __fadd_rn(__fmul_rn(x.x, cs[f + 2 * j]), __fmul_rn(o[j].x, upper ? sn[f + 2 * j] : -sn[f + 2 * j]));
+              x.y = __fadd_rn(__fmul_rn(x.y, cs[f + 2 * j + 1]), __fmul_rn(o[j].y, upper ? sn[f + 2 * j + 1] : -sn[f + 2 * j + 1]));
+            }
+          }
+        }
+        w[0] = pack8(v, bf16);
+        w[1] = pack8(v + 4, bf16);
+      } else if (isk && half > 0) {
         const int hl = half >> 3;  // chunks of one half
         const uint4 raw0 = w[0], raw1 = w[1];
 #pragma unroll
@@ -492,8 +588,14 @@ cudaError_t launch_rope_write(const RopeWriteArgs& a, int head_dim, cudaStream_t
   // one block a token, or, while that leaves SMs idle, a token's rows over several blocks
   const int per = a.tokens >= 152 * 4 ? units : a.tokens >= 152 ? (units < kRopeBatch ? units : kRopeBatch) : 1;
   const dim3 grid((unsigned)a.tokens, (unsigned)((units + per - 1) / per));
-  auto kernel = head_dim == 64 ? (a.kv_heads > 0 ? rope_write_kernel<64, true> : rope_write_kernel<64, false>)
-                               : (a.kv_heads > 0 ? rope_write_kernel<128, true> : rope_write_kernel<128, false>);
+  const bool norm = a.x_norm.weight != nullptr || a.k_norm.weight != nullptr, kv = a.kv_heads > 0;
+  using Kernel = void (*)(const RopeWriteArgs, int);
+  static constexpr Kernel kernels[2][2][2] = {
+      {{rope_write_kernel<64, false, false>, rope_write_kernel<64, false, true>},
+       {rope_write_kernel<64, true, false>, rope_write_kernel<64, true, true>}},
+      {{rope_write_kernel<128, false, false>, rope_write_kernel<128, false, true>},
+       {rope_write_kernel<128, true, false>, rope_write_kernel<128, true, true>}}};
+  const Kernel kernel = kernels[head_dim == 128][kv][norm];
   kernel<<<grid, kRopeThreads, 0, stream>>>(a, per);
   return cudaGetLastError();
 }

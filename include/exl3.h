@@ -327,6 +327,34 @@ exl3_status_t exl3_rope(const exl3_heads_t* x, exl3_dtype_t dtype, int64_t token
                         int64_t out_head_stride, void* stream);
 
 /*
+ * exl3_norm_rope -- the same with each head first divided by its root mean
+ * square and multiplied by weights, and with positions of several axes:
+ *     y[d] = x[d] * 1 / sqrt(sum_j x[j]^2 / head_dim + eps) * weight[d],  then rotated,
+ * all in fp32, rounded to the type once, at the end.  (Squares are fp32: a head with values above 2^60 or so
+ * comes out as zeros, one with a value that is not finite as NaN or zeros.)
+ *   norm  NULL: none.  weight: device, 16-byte aligned, of `dtype`: row h, head_stride elements (a multiple of 8)
+ *         from the one before, belongs to head h; head_stride 0: one row for all.  eps: a normal positive number
+ *   rope  NULL (with a norm): nothing is rotated
+ *   axes  NULL: positions [tokens] as for exl3_rope.  Else positions is [num_axes][tokens] and pair i turns by
+ *         row axes[i] of it (time, height, width: any assignment of pairs to axes); axes: device, uint8
+ *         [rot_dim / 2], an entry past the last axis is taken as the last
+ * Other arguments as for exl3_rope; out may be x itself.
+ */
+typedef struct {
+  const void* weight;
+  int64_t head_stride;
+  float eps;
+} exl3_head_norm_t;
+typedef struct {
+  const uint8_t* axes;
+  int32_t num_axes; /* 1 to 255 */
+} exl3_rope_axes_t;
+exl3_status_t exl3_norm_rope(const exl3_heads_t* x, exl3_dtype_t dtype, int64_t tokens, int32_t heads,
+                             int32_t head_dim, const exl3_head_norm_t* norm, const exl3_rope_t* rope,
+                             const exl3_rope_axes_t* axes, void* out, int64_t out_token_stride,
+                             int64_t out_head_stride, void* stream);
+
+/*
  * The paged cache.  Slot s is row s % page_size of page s / page_size.
  *   k, v              device, [num_pages][kv_heads][page_size][row bytes]
  *   k_scale, v_scale  device, bf16 [num_pages][kv_heads][page_size]; NULL for the 16-bit formats
@@ -373,12 +401,78 @@ exl3_status_t exl3_kv_write(const exl3_kv_cache_t* cache, const exl3_heads_t* k,
                             int64_t q_out_head_stride, void* stream);
 
 /*
+ * exl3_norm_kv_write -- the same with the norms of exl3_norm_rope on the heads of
+ * q and k (either may be NULL: none) and the axes of its positions.  A key's row
+ * is normed, rotated, rounded to the type, then quantised.  q is taken if there
+ * is something to do with it: q_heads > 0 needs rope or q_norm.
+ */
+exl3_status_t exl3_norm_kv_write(const exl3_kv_cache_t* cache, const exl3_heads_t* k, const exl3_heads_t* v,
+                                 exl3_dtype_t dtype, int64_t tokens, const int64_t* slots,
+                                 const exl3_head_norm_t* q_norm, const exl3_head_norm_t* k_norm,
+                                 const exl3_rope_t* rope, const exl3_rope_axes_t* axes, const exl3_heads_t* q,
+                                 int32_t q_heads, void* q_out, int64_t q_out_token_stride, int64_t q_out_head_stride,
+                                 void* stream);
+
+/*
  * exl3_kv_read -- the rows of `tokens` slots, as `dtype` (each one rounding of
  * the value read back).  A slot outside the cache reads as zeros.
  *   k, v  device, [tokens][kv_heads][head_dim] (outputs)
  */
 exl3_status_t exl3_kv_read(const exl3_kv_cache_t* cache, const int64_t* slots, int64_t tokens,
                            exl3_dtype_t dtype, void* k, void* v, void* stream);
+
+/*
+ * Page tables of a batch of requests, kept on the GPU, with the free pages as a
+ * stack.  Request b's row of block_table holds its first held[b] pages (which may be more than its kv_lens[b]
+ * cached tokens fill: a length may be set back, when drafted tokens are refused, without giving pages back).
+ *   block_table  device, int32 [batch][table_width];  table_width * page_size at most 2^30
+ *   kv_lens, held  device, int32 [batch]
+ *   free_pages   device, int32 [capacity]: the free pages are its first free_count[0] entries;  capacity at most 2^30
+ *   page_size    as for the cache
+ * What lies outside its range (a length above table_width * page_size, a count above capacity) is taken as the
+ * nearest that does not.
+ */
+typedef struct {
+  int32_t* block_table;
+  const int32_t* kv_lens;
+  const int32_t* held;
+  int32_t* free_pages;
+  const int32_t* free_count;
+  int32_t batch, table_width, page_size, capacity;
+} exl3_kv_tables_t;
+
+/*
+ * exl3_kv_plan -- a step's packing, positions and slots from the number of new
+ * tokens of each request, and pages for them: one launch, no host copy.
+ *   n_b = max(0, new_lens[b]);  cu_q[b] = min(total, sum of n before b), cu_q[batch] likewise of all
+ *   need_b = max(0, ceil((kv_lens[b] + n_b) / page_size) - held[b]), 0 where n_b = 0
+ *   a request can be served if its rows lie below total and its pages fit into table_width.  One that can and
+ *   needs no page is granted; one that needs some is granted if its need and those of all requests before it that
+ *   can be served are at most free_count (so none overtakes one that waits for pages)
+ * Granted: its new pages come from the top of the stack, in order, into its row of the table; kv_lens_out =
+ * kv_lens + n, held_out = held + need.  Row cu_q[b] + i has position kv_lens[b] + i and the slot of that position.
+ * Not granted: length, pages and table stay; its rows have positions as above and the slot -1, which exl3_kv_write
+ * skips.  Rows from cu_q[batch] to total (padding of a captured step): position 0, slot -1.
+ *   new_lens  device, int32 [batch]
+ *   kv_lens_out, held_out, free_count_out  device (outputs): the new state; may be the tables' own (updated in place)
+ *   cu_q      device, int32 [batch + 1];  positions  int32 [total];  slots  int64 [total];  granted  uint8 [batch], 0 or 1
+ * Entries of block_table from held on, and free_pages above the stack, are never read.
+ */
+exl3_status_t exl3_kv_plan(const exl3_kv_tables_t* tables, const int32_t* new_lens, int64_t total,
+                           int32_t* kv_lens_out, int32_t* held_out, int32_t* free_count_out, int32_t* cu_q,
+                           int32_t* positions, int64_t* slots, uint8_t* granted, void* stream);
+
+/*
+ * exl3_kv_release -- requests end: their pages go onto the stack (in order of the
+ * requests, a row's pages in order; those past capacity are dropped), their
+ * lengths and held pages become 0; others keep theirs.  The table's entries stay.
+ *   ended   device, uint8 [batch]: not 0 where the request ends
+ *   shared  device, int32 [batch], may be NULL: leading pages of an ended request that are not its own and stay out
+ *           of the stack
+ *   other arguments as for exl3_kv_plan
+ */
+exl3_status_t exl3_kv_release(const exl3_kv_tables_t* tables, const uint8_t* ended, const int32_t* shared,
+                              int32_t* kv_lens_out, int32_t* held_out, int32_t* free_count_out, void* stream);
 
 /*
  * exl3_attention_prompt -- causal attention over whole prompts, packed one

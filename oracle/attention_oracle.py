@@ -39,6 +39,23 @@ def rope(x, positions, phase_words, layout, amplitude):
     return y
 
 
+def norm_rope(x, weight, eps, positions, axes, phase_words, layout, amplitude):
+    """(result, the normed row before the rotation) of x [T, H, D]: divided by the root mean square (weight [D] or [H, D];
+    None: as it is), pair i turned by positions[axes[i]] (positions [A, T]; phase_words None: not at all)."""
+    x = np.asarray(x, dtype=np.float64)
+    y = x if weight is None else x / np.sqrt((x * x).mean(-1, keepdims=True) + eps) * weight
+    if phase_words is None:
+        return y, y
+    out = np.array(y)
+    n = len(phase_words)
+    for i, word in enumerate(phase_words):
+        a, b = (i, i + n) if layout == "half" else (2 * i, 2 * i + 1)
+        t = np.array([(int(p) * int(word)) % 2**64 / 2.0**64 for p in positions[axes[i]]])[:, None] * 2 * math.pi
+        out[..., a] = amplitude * (y[..., a] * np.cos(t) - y[..., b] * np.sin(t))
+        out[..., b] = amplitude * (y[..., b] * np.cos(t) + y[..., a] * np.sin(t))
+    return out, y
+
+
 def hadamard(d):
     return np.array([[-1.0 if bin(i & j).count("1") % 2 else 1.0 for j in range(d)] for i in range(d)])
 
