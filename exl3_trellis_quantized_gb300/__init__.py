@@ -9,7 +9,8 @@ Beside the layer: rotary positions of one or several axes and the norms of
 query and key heads (``rope``), a paged cache of 16, 8 or 4 bits (``KVCache``,
 ``kv_write``, ``kv_read``), its page tables and a step's slots (``KVTables``,
 ``kv_plan``, ``kv_release``), and attention over prompts (``attention_prompt``)
-and over the cache (``attention_paged``).
+and over the cache (``attention_paged``; ``attention_shared`` where sequences
+begin with the same tokens).
 """
 from .binding import (  # noqa: F401
     CODEBOOKS,
@@ -20,6 +21,8 @@ from .binding import (  # noqa: F401
     attention_paged,
     attention_paged_workspace_bytes,
     attention_prompt,
+    attention_shared,
+    attention_shared_workspace_bytes,
     autotune_entries,
     clear_autotune,
     device_status,

@@ -129,7 +129,11 @@ def lib() -> ctypes.CDLL:
                                      i64, i64, vp]
     L.exl3_kv_plan.argtypes = [tables, vp, i64] + [vp] * 8
     L.exl3_kv_release.argtypes = [tables] + [vp] * 6
-    for name in ("exl3_norm_rope", "exl3_norm_kv_write", "exl3_kv_plan", "exl3_kv_release"):
+    L.exl3_attention_shared_workspace_bytes.argtypes = [i64] + [i32] * 8
+    L.exl3_attention_shared_workspace_bytes.restype = sz
+    L.exl3_attention_shared.argtypes = [heads, ctypes.c_int, i64, i32, cache, vp, i32, vp, vp, i32, vp, vp, i32, i32, i32,
+                                        i32, f32, vp, i64, i64, vp, sz, vp]
+    for name in ("exl3_norm_rope", "exl3_norm_kv_write", "exl3_kv_plan", "exl3_kv_release", "exl3_attention_shared"):
         getattr(L, name).restype = ctypes.c_int
     for name in ("exl3_rope_phases", "exl3_rope", "exl3_kv_write", "exl3_kv_read", "exl3_attention_prompt",
                  "exl3_attention_paged"):
@@ -943,4 +947,62 @@ def attention_paged(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, 
                                 d ** -0.5 if scale is None else float(scale), oh.data, oh.token_stride,
                                 oh.head_stride, workspace.data_ptr(), workspace.numel(), _raw_stream(q.device.index))
     _check(st, "exl3_attention_paged")
+    return out
+
+
+@functools.lru_cache(maxsize=1024)
+def _shared_workspace_bytes(*sizes) -> int:
+    return int(lib().exl3_attention_shared_workspace_bytes(*sizes))
+
+
+def attention_shared_workspace_bytes(total_q: int, batch: int, groups: int, heads: int, kv_heads: int, head_dim: int,
+                                     max_q: int, max_kv: int, max_prefix: int) -> int:
+    return _shared_workspace_bytes(total_q, batch, groups, heads, kv_heads, head_dim, max_q, max_kv, max_prefix)
+
+
+def attention_shared(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, cu_q: torch.Tensor,
+                     kv_lens: torch.Tensor, cu_groups: torch.Tensor, prefix_lens: torch.Tensor, max_q: int, max_kv: int,
+                     max_prefix: int, scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """attention_paged for sequences that begin with the same cached tokens, which are read once for all of them.
+
+    Group g is the sequences cu_groups[g] .. cu_groups[g + 1] - 1 (int32 [groups + 1]; sequences outside are of no
+    group), whose first prefix_lens[g] (int32 [groups]) keys and values are the same and are read through the table of
+    the first of them that has queries.  max_prefix: about the longest of the prefixes; below 256 nothing is shared.
+    ``workspace``: uint8, at least attention_shared_workspace_bytes (allocated when not given).
+    Other arguments as for attention_paged.
+    """
+    dt = _type(q, "q")
+    qh = _heads(q, q.dtype, "q")
+    total, heads, d = q.shape
+    if d != cache.head_dim:
+        raise ValueError("q and the cache differ in head_dim")
+    _need(cu_q, torch.int32, "cu_q")
+    if cu_q.dim() != 1 or cu_q.numel() < 1:
+        raise ValueError("cu_q must be [batch + 1]")
+    batch = cu_q.numel() - 1
+    _alike(kv_lens, torch.int32, (batch,), "kv_lens")
+    _need(block_table, torch.int32, "block_table")
+    if block_table.dim() != 2 or block_table.shape[0] != batch:
+        raise ValueError("block_table must be [batch, width]")
+    _need(cu_groups, torch.int32, "cu_groups")
+    if cu_groups.dim() != 1 or cu_groups.numel() < 1:
+        raise ValueError("cu_groups must be [groups + 1]")
+    groups = cu_groups.numel() - 1
+    _alike(prefix_lens, torch.int32, (groups,), "prefix_lens")
+    _one_device(q, cache.k, block_table, cu_q, kv_lens, cu_groups, prefix_lens, out, workspace)
+    if out is not None:
+        _apart(out, "out", cache_k=cache.k, cache_v=cache.v, k_scale=cache.k_scale, v_scale=cache.v_scale)
+    out, oh = _out_like(q, out, "out")
+    if workspace is None:
+        need = _shared_workspace_bytes(total, batch, groups, heads, cache.kv_heads, d, int(max_q), int(max_kv), int(max_prefix))
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    else:
+        _need(workspace, torch.uint8, "workspace")
+    st = lib().exl3_attention_shared(qh, dt, total, heads, cache.args, block_table.data_ptr(), block_table.shape[1],
+                                     cu_q.data_ptr(), kv_lens.data_ptr(), batch, cu_groups.data_ptr(),
+                                     prefix_lens.data_ptr(), groups, int(max_q), int(max_kv), int(max_prefix),
+                                     d ** -0.5 if scale is None else float(scale), oh.data, oh.token_stride,
+                                     oh.head_stride, workspace.data_ptr(), workspace.numel(), _raw_stream(q.device.index))
+    _check(st, "exl3_attention_shared")
     return out

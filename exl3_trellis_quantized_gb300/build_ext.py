@@ -30,8 +30,10 @@ def units():
     """(source, object, extra flags) for every translation unit."""
     out = []
     for name in ("exl3_api.cu", "exl3_transform.cu", "exl3_kernels_misc.cu", "exl3_tc_host.cu", "exl3_noalloc.cu",
-                 "exl3_attn_api.cu", "exl3_rope_cache.cu", "exl3_pages.cu", "exl3_attn_token.cu", "exl3_attn_tile.cu"):
+                 "exl3_attn_api.cu", "exl3_rope_cache.cu", "exl3_pages.cu", "exl3_attn_token.cu", "exl3_attn_tile.cu", "exl3_attn_shared.cu"):
         out.append((name, name.replace(".cu", ".o"), []))
+    for name in ("exl3_attn_token.cu", "exl3_attn_tile.cu"):
+        out.append((name, name.replace(".cu", "_shared.o"), ["-DEXL3_ATTN_SHARED"]))
     for b in range(1, 9):
         out.append(("exl3_gemm_tc_inst.cu", f"exl3_gemm_tc_b{b}.o", [f"-DEXL3_INST_BITS={b}"]))
     return out

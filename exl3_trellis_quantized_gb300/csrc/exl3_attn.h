@@ -126,6 +126,13 @@ struct AttnArgs {
   int ctas;               // grid of the token kernel
   float* part_o;
   float2* part_ml;
+  // Attention behind shared prefixes (else zeros): parts [prefix_splits + splits][total_q][heads], first those of the
+  // prefixes, then those of the sequences' own keys; cut_*: the token kernel's parts of items that its ranges cut.
+  int groups, prefix_splits, prefix_tiles;
+  const int4* group;      // [groups] what shared_prep_kernel makes of each: first query token, tokens, prefix, first sequence
+  const int32_t* start;   // [batch] first key that is a sequence's own
+  float* cut_o;
+  float2* cut_ml;
 };
 // Rows (query tokens x heads of a group) one item of the token kernel holds.
 constexpr int kTokenRows = 16;
@@ -146,6 +153,21 @@ cudaError_t launch_attn_token(const AttnArgs& a, cudaStream_t stream);
 constexpr int kTileTokenRows = 128;
 // Query rows in row tiles, prompt (k, v) or paged.
 cudaError_t launch_attn_tile(const AttnArgs& a, bool paged, cudaStream_t stream);
+// The same kernels for sequences that begin with keys of their group: prefixes (and with `own` the sequences' own keys)
+// in row tiles, own keys of few rows a sequence; both leave parts only.
+cudaError_t launch_attn_tile_shared(const AttnArgs& a, bool own, cudaStream_t stream);
+cudaError_t launch_attn_token_shared(const AttnArgs& a, cudaStream_t stream);
+// What comes first and last: groups and starts from the lengths (into a.group and a.start), and the join of all parts.
+cudaError_t launch_shared_prep(const AttnArgs& a, const int32_t* cu_groups, const int32_t* prefix_lens, cudaStream_t stream);
+cudaError_t launch_shared_join(const AttnArgs& a, bool token, cudaStream_t stream);
+// Prefixes are used in whole tiles of this many keys.
+constexpr int kPrefixKeys = 128;
+// Row tiles of `per` tokens that the tokens of at most `lists` lists can fill.
+constexpr int64_t shared_tiles(int64_t tokens, int64_t lists, int64_t per) {
+  return tokens < lists ? tokens : (tokens + lists * (per - 1)) / per;
+}
+// A shorter one is read by every sequence for itself.
+constexpr int kLeastPrefix = 2 * kPrefixKeys;
 // Lets KERNEL use `bytes` of dynamic shared memory and, with regs > 0, checks that it was built for `regs` registers a
 // thread: asked of the runtime once a kernel and device.
 template <auto* KERNEL>
@@ -167,7 +189,8 @@ cudaError_t allow_smem(int bytes, int regs = 0) {
 }
 // A CUDA result as a status; keeps an error's text for exl3_last_error.
 exl3_status_t api_status(cudaError_t e, const char* where);
-// Wait-timeout flag of the tile kernel's translation unit.
+// Wait-timeout flags of the tile kernel's translation units.
 cudaError_t take_device_error_attn(uint32_t* flags);
+cudaError_t take_device_error_attn_shared(uint32_t* flags);
 
 }  // namespace exl3

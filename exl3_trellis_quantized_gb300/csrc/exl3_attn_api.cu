@@ -96,6 +96,26 @@ bool format_fits(int format, exl3_dtype_t dtype) {
   return exl3::kv_quantised(format) || (format == EXL3_KV_BF16) == (dtype == EXL3_BF16);
 }
 
+// The keys of each item of row tiles may go to several CTAs: the number of parts is the one that a simple model of the
+// time likes best, waves of items, each as long as its blocks of 64 keys (about 0.85 us each) and the beginning and end
+// of an item (about 4 us), and what the parts cost to write and join.  512 tokens of 32 heads over 32768 keys of 8: 232,
+// 234, 218 and 230 us in 2, 4, 7 and 9 parts, 230, 238, 217 and 232 by the model.
+int64_t item_parts(int64_t items, int64_t keys, int64_t values) {
+  const double blocks = (double)(keys > 64 ? keys : 64) / 64.0;
+  double best = 0.0;
+  int64_t parts = 1;
+  for (int64_t s = 1; s <= 16 && blocks / s >= 8.0 && (s == 1 || items <= kSms); ++s) {
+    const double waves = (double)((items * s + kSms - 1) / kSms);
+    const double join = s > 1 ? 4.0 + (double)s * values * 8.0 / 8.0e6 : 0.0;
+    const double us = waves * (blocks / s * 0.85 + 4.0) + join;
+    if (s == 1 || us < 0.97 * best) {
+      best = us;
+      parts = s;
+    }
+  }
+  return parts;
+}
+
 // How a paged call is split: by the token kernel (few rows a sequence) over
 // equal ranges of all keys, else by row tiles and parts of their keys.
 struct PagedPlan {
@@ -118,32 +138,89 @@ PagedPlan paged_plan(int64_t total_q, int64_t batch, int64_t q_heads, int64_t kv
     p.ml_bytes = (size_t)2 * p.ctas * exl3::kTokenRows * 2 * sizeof(float);
     return p;
   }
-  // Row tiles, two an item.  The keys of each item may go to several CTAs: the number of parts is the one that a simple
-  // model of the time likes best, waves of items, each as long as its blocks of 64 keys (about 0.85 us each) and the
-  // beginning and end of an item (about 4 us), and what the parts cost to write and join.  512 tokens of 32 heads over
-  // 32768 keys of 8: 232, 234, 218 and 230 us in 2, 4, 7 and 9 parts, 230, 238, 217 and 232 by the model.
+  // row tiles, two an item
   const int64_t per = 2 * (exl3::kTileTokenRows / group);
   const int64_t tiles = batch == 1 ? (total_q + per - 1) / per : total_q / per + (total_q < batch ? total_q : batch);
   const int64_t items = tiles * kv_heads;
   const int64_t seen = window > 0 && window + per < max_kv ? window + per : max_kv;  // keys of an item
-  const double blocks = (double)(seen > 64 ? seen : 64) / 64.0;
-  double best = 0.0;
-  int64_t splits = 1;
-  for (int64_t s = 1; s <= 16 && blocks / s >= 8.0 && (s == 1 || items <= kSms); ++s) {
-    const double waves = (double)((items * s + kSms - 1) / kSms);
-    const double join = s > 1 ? 4.0 + (double)s * total_q * q_heads * head_dim * 8.0 / 8.0e6 : 0.0;
-    const double us = waves * (blocks / s * 0.85 + 4.0) + join;
-    if (s == 1 || us < 0.97 * best) {
-      best = us;
-      splits = s;
-    }
-  }
+  const int64_t splits = item_parts(items, seen, total_q * q_heads * head_dim);
   if (splits > 1) {
     p.splits = (int)splits;
     p.o_bytes = (size_t)splits * total_q * q_heads * head_dim * sizeof(float);
     p.ml_bytes = (size_t)splits * total_q * q_heads * 2 * sizeof(float);
   }
   return p;
+}
+
+// How a call behind shared prefixes is split: parts of the prefixes' row tiles, then the sequences' own keys as in a
+// paged call.  `bytes`: part_o, part_ml, cut_o, cut_ml, groups, starts, each a multiple of 16.
+struct SharedPlan {
+  bool token;
+  int ctas, prefix_splits, prefix_tiles, splits;
+  size_t bytes[6];
+  size_t all() const { return bytes[0] + bytes[1] + bytes[2] + bytes[3] + bytes[4] + bytes[5]; }
+};
+SharedPlan shared_plan(int64_t total_q, int64_t batch, int64_t groups, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                       int64_t max_q, int64_t max_kv, int64_t max_prefix) {
+  SharedPlan p = {};
+  const int64_t group = q_heads / kv_heads, per = 2 * (exl3::kTileTokenRows / group), values = total_q * q_heads * head_dim;
+  p.prefix_tiles = (int)exl3::shared_tiles(total_q, groups, per);
+  p.prefix_splits = (int)item_parts(p.prefix_tiles * kv_heads, max_prefix, values);
+  p.splits = 1;
+  p.token = max_q * group <= exl3::kTokenRows;
+  if (p.token) {
+    const PagedPlan own = paged_plan(total_q, batch, q_heads, kv_heads, head_dim, max_q, max_kv, 0);
+    p.ctas = own.ctas;
+    p.bytes[2] = own.o_bytes;
+    p.bytes[3] = own.ml_bytes;
+  } else {
+    const int64_t own = max_kv - max_prefix > max_q ? max_kv - max_prefix : max_q;
+    p.splits = (int)item_parts(exl3::shared_tiles(total_q, batch, per) * kv_heads, own, values);
+  }
+  const int64_t parts = p.prefix_splits + p.splits;
+  auto whole = [](int64_t bytes) { return (size_t)((bytes + 15) / 16 * 16); };
+  p.bytes[0] = whole(parts * values * 4);
+  p.bytes[1] = whole(parts * total_q * q_heads * 8);
+  p.bytes[4] = whole(groups * 16);
+  p.bytes[5] = whole(batch * 4);
+  return p;
+}
+
+// Checks of a paged call and what the kernels take of it, but for the split; an empty call is not filled in.
+exl3_status_t paged_args(const exl3_heads_t* q, exl3_dtype_t dtype, int64_t total_q, int32_t q_heads, const exl3_kv_cache_t* cache,
+                         const int32_t* block_table, int32_t table_width, const int32_t* cu_q, const int32_t* kv_lens, int32_t batch,
+                         int32_t max_q, int32_t max_kv, int32_t window, float scale, void* out, int64_t out_token_stride,
+                         int64_t out_head_stride, exl3::AttnArgs* args) {
+  exl3::AttnArgs& a = *args;
+  if (!valid_rows(total_q) || !valid_rows(batch) || !valid_dtype(dtype)) return EXL3_EINVAL;
+  const exl3_status_t st = check_cache(cache, &a.cache);
+  if (st != EXL3_OK) return st;
+  if (!valid_head_counts(q_heads, a.cache.kv_heads) || !format_fits(a.cache.format, dtype)) return EXL3_EINVAL;
+  if (table_width < 1 || ((int64_t)table_width << a.cache.page_shift) > (int64_t(1) << 30)) return EXL3_EINVAL;
+  if (max_q < 1 || max_kv < 0 || window < 0 || !(scale > 0.0f) || !isfinite(scale)) return EXL3_EINVAL;
+  if (!valid_strides(out_token_stride, out_head_stride)) return EXL3_EINVAL;
+  if (total_q == 0 || batch == 0) return EXL3_OK;
+  if (!valid_heads(q) || !valid_out(q, out, out_token_stride, out_head_stride)) return EXL3_EINVAL;
+  if (!aligned4(block_table) || !aligned4(cu_q) || !aligned4(kv_lens)) return EXL3_EINVAL;
+  a.q = view(q);
+  a.out = out;
+  a.out_token_stride = out_token_stride;
+  a.out_head_stride = out_head_stride;
+  a.table = block_table;
+  a.table_width = table_width;
+  a.cu_q = cu_q;
+  a.kv_lens = kv_lens;
+  a.total_q = total_q;
+  a.batch = batch;
+  a.heads = q_heads;
+  a.kv_heads = a.cache.kv_heads;
+  a.head_dim = a.cache.head_dim;
+  a.max_q = max_q;
+  a.window = kernel_window(window);
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.bf16 = dtype == EXL3_BF16;
+  a.tile_tokens = exl3::kTileTokenRows / (q_heads / a.kv_heads);
+  return EXL3_OK;
 }
 
 }  // namespace
@@ -358,47 +435,71 @@ exl3_status_t exl3_attention_paged(const exl3_heads_t* q, exl3_dtype_t dtype, in
                                    const int32_t* cu_q, const int32_t* kv_lens, int32_t batch, int32_t max_q,
                                    int32_t max_kv, int32_t window, float scale, void* out, int64_t out_token_stride,
                                    int64_t out_head_stride, void* workspace, size_t workspace_bytes, void* stream) {
-  if (!valid_rows(total_q) || !valid_rows(batch) || !valid_dtype(dtype)) return EXL3_EINVAL;
   exl3::AttnArgs a = {};
-  const exl3_status_t st = check_cache(cache, &a.cache);
-  if (st != EXL3_OK) return st;
-  if (!valid_head_counts(q_heads, a.cache.kv_heads) || !format_fits(a.cache.format, dtype)) return EXL3_EINVAL;
-  if (table_width < 1 || ((int64_t)table_width << a.cache.page_shift) > (int64_t(1) << 30)) return EXL3_EINVAL;
-  if (max_q < 1 || max_kv < 0 || window < 0 || !(scale > 0.0f) || !isfinite(scale)) return EXL3_EINVAL;
-  if (!valid_strides(out_token_stride, out_head_stride)) return EXL3_EINVAL;
-  if (total_q == 0 || batch == 0) return EXL3_OK;
-  if (!valid_heads(q) || !valid_out(q, out, out_token_stride, out_head_stride)) return EXL3_EINVAL;
-  const void* ints[3] = {block_table, cu_q, kv_lens};
-  for (const void* p : ints)
-    if (p == nullptr || (reinterpret_cast<uintptr_t>(p) & 3u) != 0) return EXL3_EINVAL;
-  const PagedPlan plan = paged_plan(total_q, batch, q_heads, a.cache.kv_heads, a.cache.head_dim, max_q, max_kv, window);
-  if (plan.token && (int64_t)batch * a.cache.kv_heads > INT32_MAX) return EXL3_EUNSUPPORTED;  // blocks of the join
+  const exl3_status_t st = paged_args(q, dtype, total_q, q_heads, cache, block_table, table_width, cu_q, kv_lens, batch, max_q, max_kv,
+                                      window, scale, out, out_token_stride, out_head_stride, &a);
+  if (st != EXL3_OK || total_q == 0 || batch == 0) return st;
+  const PagedPlan plan = paged_plan(total_q, batch, q_heads, a.kv_heads, a.head_dim, max_q, max_kv, window);
+  if (plan.token && (int64_t)batch * a.kv_heads > INT32_MAX) return EXL3_EUNSUPPORTED;  // blocks of the join
   if (plan.o_bytes > 0 && !aligned16(workspace)) return EXL3_EINVAL;
   if (workspace_bytes < plan.o_bytes + plan.ml_bytes) return EXL3_EWORKSPACE;
-  a.q = view(q);
-  a.out = out;
-  a.out_token_stride = out_token_stride;
-  a.out_head_stride = out_head_stride;
-  a.table = block_table;
-  a.table_width = table_width;
-  a.cu_q = cu_q;
-  a.kv_lens = kv_lens;
-  a.total_q = total_q;
-  a.batch = batch;
-  a.heads = q_heads;
-  a.kv_heads = a.cache.kv_heads;
-  a.head_dim = a.cache.head_dim;
-  a.max_q = max_q;
-  a.window = kernel_window(window);
-  a.scale_log2 = scale * 1.4426950408889634f;
-  a.bf16 = dtype == EXL3_BF16;
   a.splits = plan.splits;
-  a.tile_tokens = exl3::kTileTokenRows / (q_heads / a.kv_heads);
   a.ctas = plan.ctas;
   a.part_o = static_cast<float*>(workspace);
   a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + plan.o_bytes);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return exl3::api_status(plan.token ? exl3::launch_attn_token(a, s) : exl3::launch_attn_tile(a, true, s), "exl3_attention_paged");
+}
+
+size_t exl3_attention_shared_workspace_bytes(int64_t total_q, int32_t batch, int32_t groups, int32_t q_heads,
+                                             int32_t kv_heads, int32_t head_dim, int32_t max_q, int32_t max_kv,
+                                             int32_t max_prefix) {
+  if (!valid_rows(total_q) || !valid_rows(batch) || !valid_rows(groups) || !valid_head_counts(q_heads, kv_heads)) return 0;
+  if (check_head_dim(head_dim) != EXL3_OK || max_q < 1 || max_kv < 0 || max_prefix < 0 || total_q == 0 || batch == 0) return 0;
+  if (groups == 0 || max_prefix < exl3::kLeastPrefix)
+    return exl3_attention_paged_workspace_bytes(total_q, batch, q_heads, kv_heads, head_dim, max_q, max_kv, 0);
+  return shared_plan(total_q, batch, groups, q_heads, kv_heads, head_dim, max_q, max_kv, max_prefix).all();
+}
+
+exl3_status_t exl3_attention_shared(const exl3_heads_t* q, exl3_dtype_t dtype, int64_t total_q, int32_t q_heads,
+                                    const exl3_kv_cache_t* cache, const int32_t* block_table, int32_t table_width,
+                                    const int32_t* cu_q, const int32_t* kv_lens, int32_t batch, const int32_t* cu_groups,
+                                    const int32_t* prefix_lens, int32_t groups, int32_t max_q, int32_t max_kv,
+                                    int32_t max_prefix, float scale, void* out, int64_t out_token_stride,
+                                    int64_t out_head_stride, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!valid_rows(groups) || max_prefix < 0) return EXL3_EINVAL;
+  if (groups > 0 && total_q != 0 && batch != 0 && (!aligned4(cu_groups) || !aligned4(prefix_lens))) return EXL3_EINVAL;
+  if (groups == 0 || max_prefix < exl3::kLeastPrefix)
+    return exl3_attention_paged(q, dtype, total_q, q_heads, cache, block_table, table_width, cu_q, kv_lens, batch, max_q, max_kv, 0,
+                                scale, out, out_token_stride, out_head_stride, workspace, workspace_bytes, stream);
+  exl3::AttnArgs a = {};
+  const exl3_status_t st = paged_args(q, dtype, total_q, q_heads, cache, block_table, table_width, cu_q, kv_lens, batch, max_q, max_kv, 0,
+                                      scale, out, out_token_stride, out_head_stride, &a);
+  if (st != EXL3_OK || total_q == 0 || batch == 0) return st;
+  const SharedPlan plan = shared_plan(total_q, batch, groups, q_heads, a.kv_heads, a.head_dim, max_q, max_kv, max_prefix);
+  if (plan.token && (int64_t)batch * a.kv_heads > INT32_MAX) return EXL3_EUNSUPPORTED;  // blocks of the join
+  if (!aligned16(workspace)) return EXL3_EINVAL;
+  if (workspace_bytes < plan.all()) return EXL3_EWORKSPACE;
+  uint8_t* at = static_cast<uint8_t*>(workspace);
+  void* parts[6];
+  for (int i = 0; i < 6; at += plan.bytes[i], ++i) parts[i] = at;
+  a.groups = groups;
+  a.prefix_splits = plan.prefix_splits;
+  a.prefix_tiles = plan.prefix_tiles;
+  a.splits = plan.splits;
+  a.ctas = plan.ctas;
+  a.part_o = static_cast<float*>(parts[0]);
+  a.part_ml = static_cast<float2*>(parts[1]);
+  a.cut_o = static_cast<float*>(parts[2]);
+  a.cut_ml = static_cast<float2*>(parts[3]);
+  a.group = static_cast<const int4*>(parts[4]);
+  a.start = static_cast<const int32_t*>(parts[5]);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = exl3::launch_shared_prep(a, cu_groups, prefix_lens, s);
+  if (e == cudaSuccess) e = exl3::launch_attn_tile_shared(a, !plan.token, s);
+  if (e == cudaSuccess && plan.token) e = exl3::launch_attn_token_shared(a, s);
+  if (e == cudaSuccess) e = exl3::launch_shared_join(a, plan.token, s);
+  return exl3::api_status(e, "exl3_attention_shared");
 }
 
 }  // extern "C"

@@ -77,6 +77,15 @@
 namespace exl3 {
 namespace {
 
+// Compiled once for whole sequences and once for sequences that begin with their group's keys.  Then an item is a row
+// tile of a group's query tokens over the group's prefix, or of a sequence's own tokens over its own keys, and its
+// result stays a part (over a quantised cache in the rotated basis) for a join of all parts of a row.
+#ifdef EXL3_ATTN_SHARED
+constexpr bool kShared = true;
+#else
+constexpr bool kShared = false;
+#endif
+
 enum Source { kPacked = 0, kPaged16 = 1, kPaged8 = 2, kPaged4 = 3 };
 constexpr int kKeys = 128;      // keys of a copy (a tile)
 constexpr int kBlock = 64;      // keys of a step
@@ -327,6 +336,82 @@ __device__ Span half_span(const AttnArgs& a, const Item& it, int n0, int n1, int
   return s0 < s1 ? Span{s0, s1, 1} : Span{n0, n0, 1};
 }
 
+// The same behind shared prefixes: CTAs for the prefixes' row tiles first, then those of the sequences' own keys.
+template <int SRC>
+__device__ bool find_item_shared(const AttnArgs& a, int lane, int64_t idx, Item* it) {
+  const int64_t prefix_ctas = (int64_t)a.prefix_tiles * a.kv_heads * a.prefix_splits;
+  const bool prefix = idx < prefix_ctas;
+  if (!prefix) idx -= prefix_ctas;
+  const int splits = prefix ? a.prefix_splits : a.splits, lists = prefix ? a.groups : a.batch;
+  const int per = 2 * a.tile_tokens;
+  const int split = (int)(idx % splits);
+  idx /= splits;
+  it->split = prefix ? split : a.prefix_splits + split;  // the part's place
+  it->kvh = (int)(idx % a.kv_heads);
+  const int64_t tile = idx / a.kv_heads;
+  int64_t base = 0;
+  for (int b0 = 0; b0 < lists; b0 += 32) {
+    const int b = b0 + lane;
+    int64_t c0 = 0, n = 0;
+    int keys = 0, seq = b;
+    if (b < lists) {
+      if (prefix) {
+        const int4 m = __ldcg(a.group + b);
+        c0 = m.x, n = m.z > 0 ? m.y : 0, keys = m.z, seq = m.w;
+      } else {
+        c0 = a.cu_q[b];
+        c0 = c0 < 0 ? 0 : c0 > a.total_q ? a.total_q : c0;
+        const int64_t c1 = a.cu_q[b + 1] > a.total_q ? a.total_q : a.cu_q[b + 1];
+        n = c1 > c0 ? c1 - c0 : 0;
+        const int64_t room = (int64_t)a.table_width << a.cache.page_shift;
+        const int64_t kl = a.kv_lens[b];
+        keys = (int)(kl < 0 ? 0 : kl > room ? room : kl);
+      }
+    }
+    const int tiles = ((int)n + per - 1) / per;
+    int64_t inc = tiles;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t p = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += p;
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, base + inc > tile);
+    if (hit) {
+      const int at = __ffs(hit) - 1;
+      const int64_t before = base + __shfl_sync(0xffffffffu, inc - tiles, at);
+      const int count = __shfl_sync(0xffffffffu, tiles, at);
+      const int q_len = (int)__shfl_sync(0xffffffffu, n, at);
+      it->q0 = __shfl_sync(0xffffffffu, c0, at);
+      it->b = __shfl_sync(0xffffffffu, seq, at);
+      it->kv_len = __shfl_sync(0xffffffffu, keys, at);
+      it->tok0 = (count - 1 - (int)(tile - before)) * per;
+      it->toks = min(per, q_len - it->tok0);
+      // every query of a group sees all of the prefix: as if it stood behind it
+      it->first = prefix ? it->kv_len - 1 : it->kv_len - q_len;
+      it->joint = it->toks <= a.tile_tokens;
+      // whole tiles of keys, so that no page is cut by a tile's first key
+      const int lo = prefix ? 0 : __ldcg(a.start + it->b);
+      const int p1 = min(it->first + it->tok0 + it->toks, it->kv_len) - 1;
+      it->base = lo;
+      it->lead = 0;
+      const int blocks = p1 >= lo ? (p1 - lo) / kBlock + 1 : 0;
+      const int n0 = (int)((int64_t)blocks * split / splits), n1 = (int)((int64_t)blocks * (split + 1) / splits);
+      it->span[0] = half_span(a, *it, n0, n1, 0);
+      it->span[1] = half_span(a, *it, n0, n1, 1);
+      const Span s0 = it->span[0], s1 = it->span[1];
+      const bool use0 = s0.b0 < s0.b1, use1 = s1.b0 < s1.b1;
+      it->jlo = (use0 && use1 ? min(s0.b0, s1.b0) : use0 ? s0.b0 : use1 ? s1.b0 : 0) >> 1;
+      it->jhi = ((use0 && use1 ? max(s0.b1, s1.b1) : use0 ? s0.b1 : use1 ? s1.b1 : 0) + 1) >> 1;
+      const int over = it->kv_len - lo;
+      it->tail = (over & 15) != 0 && over / kKeys >= it->jlo && over / kKeys < it->jhi ? over / kKeys : -1;
+      it->done = 0;
+      return true;
+    }
+    base += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  return false;
+}
+
 // The item of CTA index idx (a whole warp); false past the last row tile.
 template <int SRC>
 __device__ bool find_item(const AttnArgs& a, int lane, int64_t idx, Item* it) {
@@ -480,6 +565,10 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if constexpr (kShared) {
+    pdl_wait();  // groups and starts
+    pdl_launch_dependents();
+  }
 
   // The n-th item, as every warp but the loader reads it; false when there is none (or a wait gave up).
   auto read_item = [&](uint32_t n, Item* it) {
@@ -718,7 +807,7 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
         l = l * f0 + f1;
         m = both;
       }
-      const bool partial = a.splits > 1 && !(it.joint && i == 1);
+      const bool partial = (kShared || a.splits > 1) && !(it.joint && i == 1);
       if (!partial) {
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // a row that saw no key gives zeros
         f0 *= inv, f1 *= inv;
@@ -740,7 +829,7 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
 #pragma unroll
           for (int x = 0; x < D / 2; ++x) o[x] = 0.0f;
         }
-        if constexpr (C::kQuant) {
+        if constexpr (C::kQuant && !kShared) {
           // Back out of the rotated basis.  Column 8x + 2q + y of the operands holds value 8x + 2q + y, or for the 4-bit
           // codes' order 8x + 4y + q: its bits are this lane's q, y and x.
 #pragma unroll
@@ -1006,7 +1095,7 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
       }
       while (ok && more) {
         Item it;
-        const bool valid = find_item<SRC>(a, lane, idx, &it);
+        const bool valid = kShared ? find_item_shared<SRC>(a, lane, idx, &it) : find_item<SRC>(a, lane, idx, &it);
         if (valid) {
           ok = bar_wait(&iempty[n & 1], ((n >> 1) & 1u) ^ 1u);
           if (!ok) break;
@@ -1356,7 +1445,7 @@ cudaError_t make_map(CUtensorMap* map, const void* data, int d, int64_t heads, i
 }
 
 template <int D, int SRC, bool BF16>
-cudaError_t launch_tile(const AttnArgs& a, cudaStream_t stream) {
+cudaError_t launch_tile(const AttnArgs& a, cudaStream_t stream, bool own = true) {
   using C = TileCfg<D, SRC>;
   TileMaps maps = {};
   const int group = a.heads / a.kv_heads;
@@ -1375,34 +1464,61 @@ cudaError_t launch_tile(const AttnArgs& a, cudaStream_t stream) {
   // the register split waits for registers that a launch with fewer would never have
   e = allow_smem<attn_tile_kernel<D, SRC, BF16>>(C::kSmem, C::kLaunchRegs);
   if (e != cudaSuccess) return e;
-  // items: no more than all tokens' and one partly filled for each sequence
-  const int64_t tiles = a.total_q / (2 * a.tile_tokens) + (a.total_q < a.batch ? a.total_q : a.batch);
-  const int64_t blocks = tiles * a.kv_heads * a.splits;
-  if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-  attn_tile_kernel<D, SRC, BF16><<<(unsigned)blocks, C::kThreads, C::kSmem, stream>>>(maps, a);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || a.splits == 1) return e;
-  attn_tile_join_kernel<D><<<(unsigned)((a.total_q * a.heads + 7) / 8), 256, 0, stream>>>(a);
-  return cudaGetLastError();
+  if constexpr (kShared) {
+    const int64_t tiles = shared_tiles(a.total_q, a.batch, 2 * a.tile_tokens);
+    const int64_t blocks = ((int64_t)a.prefix_tiles * a.prefix_splits + (own ? tiles * a.splits : 0)) * a.kv_heads;
+    if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks, 1u, 1u);
+    cfg.blockDim = dim3(C::kThreads, 1u, 1u);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_tile_kernel<D, SRC, BF16>, maps, a);
+  } else {
+    // items: no more than all tokens' and one partly filled for each sequence
+    const int64_t tiles = a.total_q / (2 * a.tile_tokens) + (a.total_q < a.batch ? a.total_q : a.batch);
+    const int64_t blocks = tiles * a.kv_heads * a.splits;
+    if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    attn_tile_kernel<D, SRC, BF16><<<(unsigned)blocks, C::kThreads, C::kSmem, stream>>>(maps, a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || a.splits == 1) return e;
+    attn_tile_join_kernel<D><<<(unsigned)((a.total_q * a.heads + 7) / 8), 256, 0, stream>>>(a);
+    return cudaGetLastError();
+  }
 }
 
 template <int D>
-cudaError_t launch_tile_d(const AttnArgs& a, bool paged, cudaStream_t stream) {
-  if (!paged) return a.bf16 ? launch_tile<D, kPacked, true>(a, stream) : launch_tile<D, kPacked, false>(a, stream);
+cudaError_t launch_tile_d(const AttnArgs& a, bool paged, cudaStream_t stream, bool own = true) {
+  if constexpr (!kShared) {
+    if (!paged) return a.bf16 ? launch_tile<D, kPacked, true>(a, stream) : launch_tile<D, kPacked, false>(a, stream);
+  }
   switch (a.cache.format) {
-    case kKvF16: return launch_tile<D, kPaged16, false>(a, stream);
-    case kKvBf16: return launch_tile<D, kPaged16, true>(a, stream);
-    case kKvInt8: return launch_tile<D, kPaged8, false>(a, stream);
-    default: return launch_tile<D, kPaged4, false>(a, stream);
+    case kKvF16: return launch_tile<D, kPaged16, false>(a, stream, own);
+    case kKvBf16: return launch_tile<D, kPaged16, true>(a, stream, own);
+    case kKvInt8: return launch_tile<D, kPaged8, false>(a, stream, own);
+    default: return launch_tile<D, kPaged4, false>(a, stream, own);
   }
 }
 
 }  // namespace
 
+#ifdef EXL3_ATTN_SHARED
+cudaError_t launch_attn_tile_shared(const AttnArgs& a, bool own, cudaStream_t stream) {
+  return a.head_dim == 64 ? launch_tile_d<64>(a, true, stream, own) : launch_tile_d<128>(a, true, stream, own);
+}
+
+cudaError_t take_device_error_attn_shared(uint32_t* flags) { return take_tu_device_error(flags); }
+#else
 cudaError_t launch_attn_tile(const AttnArgs& a, bool paged, cudaStream_t stream) {
   return a.head_dim == 64 ? launch_tile_d<64>(a, paged, stream) : launch_tile_d<128>(a, paged, stream);
 }
 
 cudaError_t take_device_error_attn(uint32_t* flags) { return take_tu_device_error(flags); }
+#endif
 
 }  // namespace exl3

@@ -44,11 +44,19 @@
 #include <cuda_fp16.h>
 
 #include "exl3_attn.h"
+#include "exl3_attn_seq.cuh"
 #include "exl3_ptx.cuh"
 #include "exl3_sm100.cuh"
 
 namespace exl3 {
 namespace {
+
+// Compiled once for whole sequences and once for those that begin with their group's keys, whose results stay parts.
+#ifdef EXL3_ATTN_SHARED
+constexpr bool kShared = true;
+#else
+constexpr bool kShared = false;
+#endif
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
@@ -56,8 +64,6 @@ constexpr float kNegInf = -__builtin_huge_valf();
 // The reference of the exponents moves only when the maximum has grown by more
 // than this (log2), so most steps rescale nothing; weights stay below 2^8.
 constexpr float kSlack = 8.0f;
-// What an item's beginning and end cost, in units of keys (for the cuts).
-constexpr int kItemUnits = 4;
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -179,38 +185,10 @@ __device__ __forceinline__ uint32_t nib_hi(uint32_t w) {
   return hfma2((w & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u);  // / 16 - 72
 }
 
-// What a sequence asks for: its packed query tokens, its cached length, and its units of 64 keys.
-struct Seq {
-  int64_t q0;
-  int q_len, kv_len;
-  int first;  // first key that any row sees
-  int lo;     // first key of the first unit
-  int units;  // 0: no query tokens
-  // units that the cuts count for one of its items: kItemUnits, then the units
-  __device__ __forceinline__ int weight() const { return units == 0 ? 0 : units + kItemUnits; }
-};
-__device__ __forceinline__ Seq load_seq(const AttnArgs& a, int b) {
-  Seq s;
-  const int64_t c0 = a.cu_q[b], c1 = a.cu_q[b + 1];
-  s.q0 = c0 < 0 ? 0 : c0 > a.total_q ? a.total_q : c0;
-  const int64_t n = (c1 > a.total_q ? a.total_q : c1) - s.q0;
-  s.q_len = n < 0 ? 0 : n > a.max_q ? a.max_q : (int)n;
-  const int64_t room = (int64_t)a.table_width << a.cache.page_shift;
-  const int64_t kl = a.kv_lens[b];
-  s.kv_len = (int)(kl < 0 ? 0 : kl > room ? room : kl);
-  const int64_t first = a.window > 0 ? (int64_t)s.kv_len - s.q_len - a.window + 1 : 0;
-  s.first = first > 0 ? (int)first : 0;
-  s.lo = s.first / kTokenUnit * kTokenUnit;
-  // a sequence without keys still has a unit: its rows are zeros
-  const int u = (s.kv_len - s.lo + kTokenUnit - 1) / kTokenUnit;
-  s.units = s.q_len == 0 ? 0 : u < 1 ? 1 : u;
-  return s;
-}
-
 // All units of the call (one warp; every lane gets the sum).
 __device__ int64_t total_units(const AttnArgs& a, int lane) {
   int64_t sum = 0;
-  for (int b = lane; b < a.batch; b += 32) sum += load_seq(a, b).weight();
+  for (int b = lane; b < a.batch; b += 32) sum += load_seq<kShared>(a, b).weight();
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   return sum * a.kv_heads;
@@ -219,7 +197,7 @@ __device__ int64_t total_units(const AttnArgs& a, int lane) {
 __device__ int find_seq(const AttnArgs& a, int lane, int64_t u, int64_t* before) {
   int64_t base = 0;
   for (int b0 = 0; b0 < a.batch; b0 += 32) {
-    int64_t n = b0 + lane < a.batch ? (int64_t)load_seq(a, b0 + lane).weight() * a.kv_heads : 0;
+    int64_t n = b0 + lane < a.batch ? (int64_t)load_seq<kShared>(a, b0 + lane).weight() * a.kv_heads : 0;
     int64_t inc = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -314,13 +292,16 @@ __global__ void __launch_bounds__(kThreads, token_ctas_per_sm(8 * NR)) attn_toke
   const int64_t grid = gridDim.x;
   int64_t u = total * blockIdx.x / grid;
   const int64_t u_end = total * (blockIdx.x + 1) / grid;
-  if (u >= u_end) return;
+  if (u >= u_end) {
+    if constexpr (kShared) pdl_wait();
+    return;
+  }
   int64_t before;
   int b = find_seq(a, lane, u, &before);
 
   while (u < u_end) {
-    Seq s = load_seq(a, b);
-    while (s.units == 0) s = load_seq(a, ++b);  // there is a unit left, so a sequence that has it
+    Seq s = load_seq<kShared>(a, b);
+    while (s.units == 0) s = load_seq<kShared>(a, ++b);  // there is a unit left, so a sequence that has it
     const int weight = s.weight();
     const int64_t in_seq = u - before;
     const int h = (int)(in_seq / weight);
@@ -838,7 +819,8 @@ __global__ void __launch_bounds__(kThreads, token_ctas_per_sm(8 * NR)) attn_toke
           v[4 * i + 3] = fmaf(x.w, f, v[4 * i + 3]);
         }
       }
-      if (unit0 == 0 && unit1 == s.units) {
+      const bool whole = unit0 == 0 && unit1 == s.units;
+      if (!kShared && whole) {
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
         if constexpr (C::kQuant) {
           hadamard_threads<PER, C::kTpr>(v, part);
@@ -863,14 +845,25 @@ __global__ void __launch_bounds__(kThreads, token_ctas_per_sm(8 * NR)) attn_toke
       } else if (jr < rows) {
         // a range begins inside at most one item and ends inside at most one
         const int64_t slot = 2 * (int64_t)blockIdx.x + (unit0 == 0 ? 1 : 0);
-        float4* dst = reinterpret_cast<float4*>(a.part_o + (slot * kTokenRows + jr) * D + part * PER);
+        int64_t at = slot * kTokenRows + jr;
+        float* part_o = kShared ? a.cut_o : a.part_o;
+        float2* part_ml = kShared ? a.cut_ml : a.part_ml;
+        if (kShared && whole) {
+          // the part behind those of the prefix
+          const int tok = jr / group;
+          at = (a.prefix_splits * a.total_q + s.q0 + tok) * a.heads + h * group + jr - tok * group;
+          part_o = a.part_o, part_ml = a.part_ml;
+        }
+        float4* dst = reinterpret_cast<float4*>(part_o + at * D + part * PER);
 #pragma unroll
         for (int i = 0; i < PER / 4; ++i) dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-        if (part == 0) a.part_ml[slot * kTokenRows + jr] = make_float2(top, sum);
+        if (part == 0) part_ml[at] = make_float2(top, sum);
       }
     }
     __syncthreads();  // the next item's copies refill what was read here
   }
+  // the prefixes' kernel is waited for, so that the end of this grid stands for the end of both
+  if constexpr (kShared) pdl_wait();
 }
 
 // Joins the parts of the items that were cut: one block an item and row; its
@@ -887,12 +880,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_token_join_kernel(const 
   const int group = a.heads / a.kv_heads;
   const int r = blockIdx.y;
   const int b = blockIdx.x / a.kv_heads, h = blockIdx.x % a.kv_heads;
-  const Seq s = load_seq(a, b);
+  const Seq s = load_seq<kShared>(a, b);
   const int rows = s.q_len * group;
   // units before this sequence, and of the call
   int64_t total = 0, before = 0;
   for (int i = lane; i < a.batch; i += 32) {
-    const int n = load_seq(a, i).weight();
+    const int n = load_seq<kShared>(a, i).weight();
     total += n;
     before += i < b ? n : 0;
   }
@@ -984,20 +977,28 @@ cudaError_t launch_token(const AttnArgs& a, cudaStream_t stream) {
   using C = TokenCfg<FMT, D, NR, TWO>;
   cudaError_t e = allow_smem<attn_token_kernel<FMT, D, NR, TWO>>(C::kSmem);
   if (e != cudaSuccess) return e;
-  attn_token_kernel<FMT, D, NR, TWO><<<(unsigned)a.ctas, kThreads, C::kSmem, stream>>>(a);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  const int rows = a.max_q * (a.heads / a.kv_heads);
-  cfg.gridDim = dim3((unsigned)(a.batch * a.kv_heads), (unsigned)rows, 1u);
-  cfg.blockDim = dim3(32u * kJoinWarps, 1u, 1u);
-  cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_token_join_kernel<D, C::kQuant>, a);
+  if constexpr (kShared) {
+    // beside the prefixes' kernel, which comes before; the join comes later
+    cfg.gridDim = dim3((unsigned)a.ctas, 1u, 1u);
+    cfg.blockDim = dim3(kThreads, 1u, 1u);
+    cfg.dynamicSmemBytes = C::kSmem;
+    return cudaLaunchKernelEx(&cfg, attn_token_kernel<FMT, D, NR, TWO>, a);
+  } else {
+    attn_token_kernel<FMT, D, NR, TWO><<<(unsigned)a.ctas, kThreads, C::kSmem, stream>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const int rows = a.max_q * (a.heads / a.kv_heads);
+    cfg.gridDim = dim3((unsigned)(a.batch * a.kv_heads), (unsigned)rows, 1u);
+    cfg.blockDim = dim3(32u * kJoinWarps, 1u, 1u);
+    return cudaLaunchKernelEx(&cfg, attn_token_join_kernel<D, C::kQuant>, a);
+  }
 }
 template <int FMT, bool TWO>
 cudaError_t launch_token_fmt(const AttnArgs& a, cudaStream_t stream) {
@@ -1008,7 +1009,11 @@ cudaError_t launch_token_fmt(const AttnArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
+#ifdef EXL3_ATTN_SHARED
+cudaError_t launch_attn_token_shared(const AttnArgs& a, cudaStream_t stream) {
+#else
 cudaError_t launch_attn_token(const AttnArgs& a, cudaStream_t stream) {
+#endif
   switch (a.cache.format) {
     case kKvF16: return launch_token_fmt<kKvF16, false>(a, stream);
     case kKvBf16: return launch_token_fmt<kKvBf16, false>(a, stream);

@@ -670,9 +670,10 @@ cudaError_t launch_moe_gemm_tc(const GemmArgs& a, int bits, int cb, int block, c
 cudaError_t take_device_errors(uint32_t* flags) {
   *flags = 0;
   cudaError_t e = cudaSuccess;
-  cudaError_t (*fns[9])(uint32_t*) = {take_device_error_tc<1>, take_device_error_tc<2>, take_device_error_tc<3>,
+  cudaError_t (*fns[10])(uint32_t*) = {take_device_error_tc<1>, take_device_error_tc<2>, take_device_error_tc<3>,
                                       take_device_error_tc<4>, take_device_error_tc<5>, take_device_error_tc<6>,
-                                      take_device_error_tc<7>, take_device_error_tc<8>, take_device_error_attn};
+                                      take_device_error_tc<7>, take_device_error_tc<8>, take_device_error_attn,
+                                      take_device_error_attn_shared};
   for (auto f : fns) {
     cudaError_t r = f(flags);
     if (r != cudaSuccess) e = r;
