@@ -106,6 +106,12 @@ struct KvReleaseArgs {
 cudaError_t launch_kv_plan(const KvPlanArgs& a, cudaStream_t stream);
 cudaError_t launch_kv_release(const KvReleaseArgs& a, cudaStream_t stream);
 
+// A group of sequences that share their first keys: its packed query tokens, the keys, the sequence whose table names
+// them, and the items of its row tiles: first one, and parts of each.
+struct SharedGroup {
+  int q0, tokens, keys, lead, item, parts;
+};
+
 struct AttnArgs {
   HeadsView q, k, v;  // k, v: prompt attention only
   void* out;
@@ -126,13 +132,16 @@ struct AttnArgs {
   int ctas;               // grid of the token kernel
   float* part_o;
   float2* part_ml;
-  // Attention behind shared prefixes (else zeros): parts [prefix_splits + splits][total_q][heads], first those of the
-  // prefixes, then those of the sequences' own keys; cut_*: the token kernel's parts of items that its ranges cut.
-  int groups, prefix_splits, prefix_tiles;
-  const int4* group;      // [groups] what shared_prep_kernel makes of each: first query token, tokens, prefix, first sequence
-  const int32_t* start;   // [batch] first key that is a sequence's own
-  float* cut_o;
-  float2* cut_ml;
+  // Attention behind shared prefixes (else zeros).  prefix_o and prefix_ml: the parts of the prefixes' items, in order of
+  // the CTAs that make them, kPrefixRows rows each; own_*: the parts of the sequences' own keys, [splits][total_q][heads]
+  // (token kernel: one, of whole items; cut_*: of items that its ranges cut).
+  int groups, prefix_ctas;
+  const SharedGroup* group;  // [groups] made by shared_prep_kernel, as what follows
+  const int2* seq;           // [batch] first key that is a sequence's own, and its group
+  const int64_t* units;      // [batch + 1] units of the sequences before each (token kernel)
+  const int32_t* items;      // [1] items of all prefixes
+  float *prefix_o, *own_o, *cut_o;
+  float2 *prefix_ml, *own_ml, *cut_ml;
 };
 // Rows (query tokens x heads of a group) one item of the token kernel holds.
 constexpr int kTokenRows = 16;
@@ -157,11 +166,14 @@ cudaError_t launch_attn_tile(const AttnArgs& a, bool paged, cudaStream_t stream)
 // in row tiles, own keys of few rows a sequence; both leave parts only.
 cudaError_t launch_attn_tile_shared(const AttnArgs& a, bool own, cudaStream_t stream);
 cudaError_t launch_attn_token_shared(const AttnArgs& a, cudaStream_t stream);
-// What comes first and last: groups and starts from the lengths (into a.group and a.start), and the join of all parts.
-cudaError_t launch_shared_prep(const AttnArgs& a, const int32_t* cu_groups, const int32_t* prefix_lens, cudaStream_t stream);
+// What comes first and last: groups and starts from the lengths (into a.group, a.seq, a.units and a.items), and the join of all parts.
+cudaError_t launch_shared_prep(const AttnArgs& a, const int32_t* cu_groups, const int32_t* prefix_lens, bool token,
+                               cudaStream_t stream);
 cudaError_t launch_shared_join(const AttnArgs& a, bool token, cudaStream_t stream);
 // Prefixes are used in whole tiles of this many keys.
 constexpr int kPrefixKeys = 128;
+// Rows of an item of row tiles at the most.
+constexpr int kPrefixRows = 256;
 // Row tiles of `per` tokens that the tokens of at most `lists` lists can fill.
 constexpr int64_t shared_tiles(int64_t tokens, int64_t lists, int64_t per) {
   return tokens < lists ? tokens : (tokens + lists * (per - 1)) / per;

@@ -152,37 +152,35 @@ PagedPlan paged_plan(int64_t total_q, int64_t batch, int64_t q_heads, int64_t kv
   return p;
 }
 
-// How a call behind shared prefixes is split: parts of the prefixes' row tiles, then the sequences' own keys as in a
-// paged call.  `bytes`: part_o, part_ml, cut_o, cut_ml, groups, starts, each a multiple of 16.
+// How a call behind shared prefixes is split: the prefixes' row tiles into CTAs (how many each gets is for the GPU to say,
+// which knows the lengths), then the sequences' own keys as in a paged call.
 struct SharedPlan {
   bool token;
-  int ctas, prefix_splits, prefix_tiles, splits;
-  size_t bytes[6];
-  size_t all() const { return bytes[0] + bytes[1] + bytes[2] + bytes[3] + bytes[4] + bytes[5]; }
+  int ctas, prefix_ctas, splits;
+  size_t at[11];  // where in the workspace each array begins, and the end
 };
 SharedPlan shared_plan(int64_t total_q, int64_t batch, int64_t groups, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
                        int64_t max_q, int64_t max_kv, int64_t max_prefix) {
   SharedPlan p = {};
-  const int64_t group = q_heads / kv_heads, per = 2 * (exl3::kTileTokenRows / group), values = total_q * q_heads * head_dim;
-  p.prefix_tiles = (int)exl3::shared_tiles(total_q, groups, per);
-  p.prefix_splits = (int)item_parts(p.prefix_tiles * kv_heads, max_prefix, values);
-  p.splits = 1;
+  const int64_t group = q_heads / kv_heads, per = 2 * (exl3::kTileTokenRows / group), rows = total_q * q_heads;
   p.token = max_q * group <= exl3::kTokenRows;
+  // an item for each row tile, and room for parts: one wave of CTAs, or where the row tiles alone are more than that
+  // two more, which even out the last
+  const int64_t tiles = exl3::shared_tiles(total_q, groups, per) * kv_heads;
+  p.prefix_ctas = (int)(tiles + (tiles < kSms ? kSms : 2 * kSms));
+  int64_t cut = 0;
   if (p.token) {
     const PagedPlan own = paged_plan(total_q, batch, q_heads, kv_heads, head_dim, max_q, max_kv, 0);
     p.ctas = own.ctas;
-    p.bytes[2] = own.o_bytes;
-    p.bytes[3] = own.ml_bytes;
+    cut = 2 * (int64_t)own.ctas * exl3::kTokenRows;
   } else {
     const int64_t own = max_kv - max_prefix > max_q ? max_kv - max_prefix : max_q;
-    p.splits = (int)item_parts(exl3::shared_tiles(total_q, batch, per) * kv_heads, own, values);
+    p.splits = (int)item_parts(exl3::shared_tiles(total_q, batch, per) * kv_heads, own, rows * head_dim);
   }
-  const int64_t parts = p.prefix_splits + p.splits;
-  auto whole = [](int64_t bytes) { return (size_t)((bytes + 15) / 16 * 16); };
-  p.bytes[0] = whole(parts * values * 4);
-  p.bytes[1] = whole(parts * total_q * q_heads * 8);
-  p.bytes[4] = whole(groups * 16);
-  p.bytes[5] = whole(batch * 4);
+  const int64_t own = p.token ? rows : p.splits * rows, prefix = (int64_t)p.prefix_ctas * exl3::kPrefixRows;
+  const int64_t bytes[10] = {prefix * head_dim * 4, prefix * 8, own * head_dim * 4, own * 8, cut * head_dim * 4, cut * 8,
+                             groups * (int64_t)sizeof(exl3::SharedGroup), batch * 8, p.token ? (batch + 1) * 8 : 0, 4};
+  for (int i = 0; i < 10; ++i) p.at[i + 1] = p.at[i] + (size_t)((bytes[i] + 15) / 16 * 16);
   return p;
 }
 
@@ -458,7 +456,7 @@ size_t exl3_attention_shared_workspace_bytes(int64_t total_q, int32_t batch, int
   if (check_head_dim(head_dim) != EXL3_OK || max_q < 1 || max_kv < 0 || max_prefix < 0 || total_q == 0 || batch == 0) return 0;
   if (groups == 0 || max_prefix < exl3::kLeastPrefix)
     return exl3_attention_paged_workspace_bytes(total_q, batch, q_heads, kv_heads, head_dim, max_q, max_kv, 0);
-  return shared_plan(total_q, batch, groups, q_heads, kv_heads, head_dim, max_q, max_kv, max_prefix).all();
+  return shared_plan(total_q, batch, groups, q_heads, kv_heads, head_dim, max_q, max_kv, max_prefix).at[10];
 }
 
 exl3_status_t exl3_attention_shared(const exl3_heads_t* q, exl3_dtype_t dtype, int64_t total_q, int32_t q_heads,
@@ -477,25 +475,26 @@ exl3_status_t exl3_attention_shared(const exl3_heads_t* q, exl3_dtype_t dtype, i
                                       scale, out, out_token_stride, out_head_stride, &a);
   if (st != EXL3_OK || total_q == 0 || batch == 0) return st;
   const SharedPlan plan = shared_plan(total_q, batch, groups, q_heads, a.kv_heads, a.head_dim, max_q, max_kv, max_prefix);
-  if (plan.token && (int64_t)batch * a.kv_heads > INT32_MAX) return EXL3_EUNSUPPORTED;  // blocks of the join
+  if (total_q * q_heads > INT32_MAX) return EXL3_EUNSUPPORTED;  // blocks of the join
   if (!aligned16(workspace)) return EXL3_EINVAL;
-  if (workspace_bytes < plan.all()) return EXL3_EWORKSPACE;
-  uint8_t* at = static_cast<uint8_t*>(workspace);
-  void* parts[6];
-  for (int i = 0; i < 6; at += plan.bytes[i], ++i) parts[i] = at;
+  if (workspace_bytes < plan.at[10]) return EXL3_EWORKSPACE;
+  uint8_t* w = static_cast<uint8_t*>(workspace);
   a.groups = groups;
-  a.prefix_splits = plan.prefix_splits;
-  a.prefix_tiles = plan.prefix_tiles;
+  a.prefix_ctas = plan.prefix_ctas;
   a.splits = plan.splits;
   a.ctas = plan.ctas;
-  a.part_o = static_cast<float*>(parts[0]);
-  a.part_ml = static_cast<float2*>(parts[1]);
-  a.cut_o = static_cast<float*>(parts[2]);
-  a.cut_ml = static_cast<float2*>(parts[3]);
-  a.group = static_cast<const int4*>(parts[4]);
-  a.start = static_cast<const int32_t*>(parts[5]);
+  a.prefix_o = reinterpret_cast<float*>(w + plan.at[0]);
+  a.prefix_ml = reinterpret_cast<float2*>(w + plan.at[1]);
+  a.own_o = reinterpret_cast<float*>(w + plan.at[2]);
+  a.own_ml = reinterpret_cast<float2*>(w + plan.at[3]);
+  a.cut_o = reinterpret_cast<float*>(w + plan.at[4]);
+  a.cut_ml = reinterpret_cast<float2*>(w + plan.at[5]);
+  a.group = reinterpret_cast<const exl3::SharedGroup*>(w + plan.at[6]);
+  a.seq = reinterpret_cast<const int2*>(w + plan.at[7]);
+  a.units = reinterpret_cast<const int64_t*>(w + plan.at[8]);
+  a.items = reinterpret_cast<const int32_t*>(w + plan.at[9]);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = exl3::launch_shared_prep(a, cu_groups, prefix_lens, s);
+  cudaError_t e = exl3::launch_shared_prep(a, cu_groups, prefix_lens, plan.token, s);
   if (e == cudaSuccess) e = exl3::launch_attn_tile_shared(a, !plan.token, s);
   if (e == cudaSuccess && plan.token) e = exl3::launch_attn_token_shared(a, s);
   if (e == cudaSuccess) e = exl3::launch_shared_join(a, plan.token, s);

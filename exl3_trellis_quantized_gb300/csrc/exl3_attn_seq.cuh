@@ -20,7 +20,7 @@ struct Seq {
   // units that the cuts count for one of its items: kItemUnits, then the units
   __device__ __forceinline__ int weight() const { return units == 0 ? 0 : units + kItemUnits; }
 };
-// SHARED: the keys before a.start[b] are not its own.
+// SHARED: the keys before a.seq[b].x are not its own.
 template <bool SHARED>
 __device__ __forceinline__ Seq load_seq(const AttnArgs& a, int b) {
   Seq s;
@@ -31,7 +31,7 @@ __device__ __forceinline__ Seq load_seq(const AttnArgs& a, int b) {
   const int64_t room = (int64_t)a.table_width << a.cache.page_shift;
   const int64_t kl = a.kv_lens[b];
   s.kv_len = (int)(kl < 0 ? 0 : kl > room ? room : kl);
-  const int64_t first = SHARED ? __ldcg(a.start + b) : a.window > 0 ? (int64_t)s.kv_len - s.q_len - a.window + 1 : 0;
+  const int64_t first = SHARED ? __ldcg(&a.seq[b].x) : a.window > 0 ? (int64_t)s.kv_len - s.q_len - a.window + 1 : 0;
   s.first = first > 0 ? (int)first : 0;
   s.lo = s.first / kTokenUnit * kTokenUnit;
   // a sequence without keys still has a unit: its rows are zeros

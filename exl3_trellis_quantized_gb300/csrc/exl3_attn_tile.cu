@@ -320,6 +320,13 @@ struct Item {
   int tail;          // the key tile that the length ends in, where its value rows past the end must be made zeros; or -1
   int lead;          // rows of key tile 0 before the first that the item's queries see: value rows to be made zeros too
   int done;          // no item
+#ifdef EXL3_ATTN_SHARED
+  // where the rows' parts go: row part_row + token (in the sequence or group) * part_stride + head (in the group)
+  float* part_o;
+  float2* part_ml;
+  int64_t part_row;
+  int part_stride;
+#endif
 };
 
 // Whether value rows of key tile j must be made zeros: a weight of zero does not hide what is not finite.
@@ -336,28 +343,35 @@ __device__ Span half_span(const AttnArgs& a, const Item& it, int n0, int n1, int
   return s0 < s1 ? Span{s0, s1, 1} : Span{n0, n0, 1};
 }
 
-// The same behind shared prefixes: CTAs for the prefixes' row tiles first, then those of the sequences' own keys.
+#ifdef EXL3_ATTN_SHARED
+// The item of CTA index idx (a whole warp); false past the last.  The prefixes' row tiles come first, then those of the
+// sequences' own keys.
 template <int SRC>
-__device__ bool find_item_shared(const AttnArgs& a, int lane, int64_t idx, Item* it) {
-  const int64_t prefix_ctas = (int64_t)a.prefix_tiles * a.kv_heads * a.prefix_splits;
-  const bool prefix = idx < prefix_ctas;
-  if (!prefix) idx -= prefix_ctas;
-  const int splits = prefix ? a.prefix_splits : a.splits, lists = prefix ? a.groups : a.batch;
-  const int per = 2 * a.tile_tokens;
-  const int split = (int)(idx % splits);
-  idx /= splits;
-  it->split = prefix ? split : a.prefix_splits + split;  // the part's place
-  it->kvh = (int)(idx % a.kv_heads);
-  const int64_t tile = idx / a.kv_heads;
+__device__ bool find_item(const AttnArgs& a, int lane, int64_t idx, Item* it) {
+  const int per = 2 * a.tile_tokens, group = a.heads / a.kv_heads;
+  const int prefix_items = __ldcg(a.items);
+  const bool prefix = idx < prefix_items;
+  if (!prefix && a.splits == 0) return false;  // own keys go through the token kernel
+  const int64_t item = idx;
+  const int lists = prefix ? a.groups : a.batch;
+  if (!prefix) idx -= prefix_items;
+  // in items of a prefix's group; of own keys, whose parts are the same for all: in tiles
+  int split = 0;
+  if (!prefix) {
+    split = (int)(idx % a.splits);
+    idx /= a.splits;
+    it->kvh = (int)(idx % a.kv_heads);
+    idx /= a.kv_heads;
+  }
   int64_t base = 0;
   for (int b0 = 0; b0 < lists; b0 += 32) {
     const int b = b0 + lane;
     int64_t c0 = 0, n = 0;
-    int keys = 0, seq = b;
+    int keys = 0, seq = b, parts = 1;
     if (b < lists) {
       if (prefix) {
-        const int4 m = __ldcg(a.group + b);
-        c0 = m.x, n = m.z > 0 ? m.y : 0, keys = m.z, seq = m.w;
+        const SharedGroup* g = a.group + b;
+        c0 = __ldcg(&g->q0), n = __ldcg(&g->tokens), keys = __ldcg(&g->keys), seq = __ldcg(&g->lead), parts = __ldcg(&g->parts);
       } else {
         c0 = a.cu_q[b];
         c0 = c0 < 0 ? 0 : c0 > a.total_q ? a.total_q : c0;
@@ -368,34 +382,49 @@ __device__ bool find_item_shared(const AttnArgs& a, int lane, int64_t idx, Item*
         keys = (int)(kl < 0 ? 0 : kl > room ? room : kl);
       }
     }
-    const int tiles = ((int)n + per - 1) / per;
-    int64_t inc = tiles;
+    const int tiles = prefix && keys == 0 ? 0 : ((int)n + per - 1) / per;
+    const int64_t here = prefix ? (int64_t)tiles * a.kv_heads * parts : tiles;
+    int64_t inc = here;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t p = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += p;
     }
-    const uint32_t hit = __ballot_sync(0xffffffffu, base + inc > tile);
+    const uint32_t hit = __ballot_sync(0xffffffffu, base + inc > idx);
     if (hit) {
       const int at = __ffs(hit) - 1;
-      const int64_t before = base + __shfl_sync(0xffffffffu, inc - tiles, at);
+      int64_t place = idx - base - __shfl_sync(0xffffffffu, inc - here, at);
       const int count = __shfl_sync(0xffffffffu, tiles, at);
+      const int splits = prefix ? __shfl_sync(0xffffffffu, parts, at) : a.splits;
+      if (prefix) {
+        split = (int)(place % splits);
+        place /= splits;
+        it->kvh = (int)(place % a.kv_heads);
+        place /= a.kv_heads;
+      }
       const int q_len = (int)__shfl_sync(0xffffffffu, n, at);
       it->q0 = __shfl_sync(0xffffffffu, c0, at);
       it->b = __shfl_sync(0xffffffffu, seq, at);
       it->kv_len = __shfl_sync(0xffffffffu, keys, at);
-      it->tok0 = (count - 1 - (int)(tile - before)) * per;
+      it->tok0 = (count - 1 - (int)place) * per;
       it->toks = min(per, q_len - it->tok0);
+      it->split = split;
+      it->part_o = prefix ? a.prefix_o : a.own_o;
+      it->part_ml = prefix ? a.prefix_ml : a.own_ml;
+      it->part_stride = prefix ? group : a.heads;
+      it->part_row = prefix ? item * kPrefixRows - (int64_t)it->tok0 * group : (split * a.total_q + it->q0) * a.heads + it->kvh * group;
       // every query of a group sees all of the prefix: as if it stood behind it
       it->first = prefix ? it->kv_len - 1 : it->kv_len - q_len;
       it->joint = it->toks <= a.tile_tokens;
       // whole tiles of keys, so that no page is cut by a tile's first key
-      const int lo = prefix ? 0 : __ldcg(a.start + it->b);
+      const int lo = prefix ? 0 : __ldcg(&a.seq[it->b].x);
       const int p1 = min(it->first + it->tok0 + it->toks, it->kv_len) - 1;
       it->base = lo;
       it->lead = 0;
       const int blocks = p1 >= lo ? (p1 - lo) / kBlock + 1 : 0;
-      const int n0 = (int)((int64_t)blocks * split / splits), n1 = (int)((int64_t)blocks * (split + 1) / splits);
+      // in whole tiles of two blocks, so that none is copied twice
+      const int64_t pairs = (blocks + 1) >> 1;
+      const int n0 = 2 * (int)(pairs * split / splits), n1 = min(blocks, 2 * (int)(pairs * (split + 1) / splits));
       it->span[0] = half_span(a, *it, n0, n1, 0);
       it->span[1] = half_span(a, *it, n0, n1, 1);
       const Span s0 = it->span[0], s1 = it->span[1];
@@ -412,6 +441,7 @@ __device__ bool find_item_shared(const AttnArgs& a, int lane, int64_t idx, Item*
   return false;
 }
 
+#else
 // The item of CTA index idx (a whole warp); false past the last row tile.
 template <int SRC>
 __device__ bool find_item(const AttnArgs& a, int lane, int64_t idx, Item* it) {
@@ -489,6 +519,8 @@ __device__ bool find_item(const AttnArgs& a, int lane, int64_t idx, Item* it) {
   }
   return false;
 }
+
+#endif
 
 // D: head size.  BF16: operand type (fp16 for the quantised formats).
 template <int D, int SRC, bool BF16>
@@ -815,8 +847,12 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
       if (!any) f0 = 0.0f;
       float* jo = reinterpret_cast<float*>(data + C::kQ) + r;  // [D][128]: a thread a column
       if (ok && it.joint && i == 1) jlse[r] = m + log2f(l);
+#ifdef EXL3_ATTN_SHARED
+      if (ok && partial && there) it.part_ml[it.part_row + (int64_t)tok * it.part_stride + row_head] = make_float2(m, l);
+#else
       const int64_t row = (it.q0 + tok) * a.heads + it.kvh * group + row_head;
       if (ok && partial && there) a.part_ml[(int64_t)it.split * a.total_q * a.heads + row] = make_float2(m, l);
+#endif
 #pragma unroll 1
       for (int h = 0; ok && h < 2; ++h) {
         float o[D / 2];  // o[4x + 2e + y]: row 16h + 8e + g of the warp, column 8x + 2q + y
@@ -877,7 +913,11 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
             }
           }
           if (partial) {
+#ifdef EXL3_ATTN_SHARED
+            float* dst = it.part_o + (it.part_row + (int64_t)rtok * it.part_stride + rhead) * D;
+#else
             float* dst = a.part_o + (((int64_t)it.split * a.total_q + it.q0 + rtok) * a.heads + it.kvh * group + rhead) * D;
+#endif
 #pragma unroll
             for (int x = 0; x < D / 8; ++x) {
               if (!rthere) continue;
@@ -1095,7 +1135,7 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
       }
       while (ok && more) {
         Item it;
-        const bool valid = kShared ? find_item_shared<SRC>(a, lane, idx, &it) : find_item<SRC>(a, lane, idx, &it);
+        const bool valid = find_item<SRC>(a, lane, idx, &it);
         if (valid) {
           ok = bar_wait(&iempty[n & 1], ((n >> 1) & 1u) ^ 1u);
           if (!ok) break;
@@ -1466,7 +1506,7 @@ cudaError_t launch_tile(const AttnArgs& a, cudaStream_t stream, bool own = true)
   if (e != cudaSuccess) return e;
   if constexpr (kShared) {
     const int64_t tiles = shared_tiles(a.total_q, a.batch, 2 * a.tile_tokens);
-    const int64_t blocks = ((int64_t)a.prefix_tiles * a.prefix_splits + (own ? tiles * a.splits : 0)) * a.kv_heads;
+    const int64_t blocks = a.prefix_ctas + (own ? tiles * a.splits * a.kv_heads : 0);
     if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)blocks, 1u, 1u);

@@ -187,6 +187,7 @@ __device__ __forceinline__ uint32_t nib_hi(uint32_t w) {
 
 // All units of the call (one warp; every lane gets the sum).
 __device__ int64_t total_units(const AttnArgs& a, int lane) {
+  if constexpr (kShared) return __ldcg(a.units + a.batch) * a.kv_heads;
   int64_t sum = 0;
   for (int b = lane; b < a.batch; b += 32) sum += load_seq<kShared>(a, b).weight();
 #pragma unroll
@@ -195,6 +196,20 @@ __device__ int64_t total_units(const AttnArgs& a, int lane) {
 }
 // The sequence that holds unit u, and the units of the sequences before it.
 __device__ int find_seq(const AttnArgs& a, int lane, int64_t u, int64_t* before) {
+  if constexpr (kShared) {
+    for (int b0 = 0; b0 < a.batch; b0 += 32) {
+      const int b = min(b0 + lane, a.batch - 1);
+      const int64_t first = __ldcg(a.units + b) * a.kv_heads, end = __ldcg(a.units + b + 1) * a.kv_heads;
+      const uint32_t hit = __ballot_sync(0xffffffffu, end > u);
+      if (hit) {
+        const int at = __ffs(hit) - 1;
+        *before = __shfl_sync(0xffffffffu, first, at);
+        return b0 + at;
+      }
+    }
+    *before = u;
+    return a.batch;
+  }
   int64_t base = 0;
   for (int b0 = 0; b0 < a.batch; b0 += 32) {
     int64_t n = b0 + lane < a.batch ? (int64_t)load_seq<kShared>(a, b0 + lane).weight() * a.kv_heads : 0;
@@ -849,10 +864,9 @@ __global__ void __launch_bounds__(kThreads, token_ctas_per_sm(8 * NR)) attn_toke
         float* part_o = kShared ? a.cut_o : a.part_o;
         float2* part_ml = kShared ? a.cut_ml : a.part_ml;
         if (kShared && whole) {
-          // the part behind those of the prefix
           const int tok = jr / group;
-          at = (a.prefix_splits * a.total_q + s.q0 + tok) * a.heads + h * group + jr - tok * group;
-          part_o = a.part_o, part_ml = a.part_ml;
+          at = (s.q0 + tok) * a.heads + h * group + jr - tok * group;
+          part_o = a.own_o, part_ml = a.own_ml;
         }
         float4* dst = reinterpret_cast<float4*>(part_o + at * D + part * PER);
 #pragma unroll
