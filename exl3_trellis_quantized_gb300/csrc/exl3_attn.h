@@ -139,7 +139,7 @@ struct AttnArgs {
   const SharedGroup* group;  // [groups] made by shared_prep_kernel, as what follows
   const int2* seq;           // [batch] first key that is a sequence's own, and its group
   const int64_t* units;      // [batch + 1] units of the sequences before each (token kernel)
-  const int32_t* items;      // [1] items of all prefixes
+  const int2* counts;        // [1] items of all prefixes, CTAs of the token kernel that take part
   float *prefix_o, *own_o, *cut_o;
   float2 *prefix_ml, *own_ml, *cut_ml;
 };
@@ -166,7 +166,7 @@ cudaError_t launch_attn_tile(const AttnArgs& a, bool paged, cudaStream_t stream)
 // in row tiles, own keys of few rows a sequence; both leave parts only.
 cudaError_t launch_attn_tile_shared(const AttnArgs& a, bool own, cudaStream_t stream);
 cudaError_t launch_attn_token_shared(const AttnArgs& a, cudaStream_t stream);
-// What comes first and last: groups and starts from the lengths (into a.group, a.seq, a.units and a.items), and the join of all parts.
+// What comes first and last: groups and starts from the lengths (into a.group, a.seq, a.units and a.counts), and the join of all parts.
 cudaError_t launch_shared_prep(const AttnArgs& a, const int32_t* cu_groups, const int32_t* prefix_lens, bool token,
                                cudaStream_t stream);
 cudaError_t launch_shared_join(const AttnArgs& a, bool token, cudaStream_t stream);

@@ -179,7 +179,7 @@ SharedPlan shared_plan(int64_t total_q, int64_t batch, int64_t groups, int64_t q
   }
   const int64_t own = p.token ? rows : p.splits * rows, prefix = (int64_t)p.prefix_ctas * exl3::kPrefixRows;
   const int64_t bytes[10] = {prefix * head_dim * 4, prefix * 8, own * head_dim * 4, own * 8, cut * head_dim * 4, cut * 8,
-                             groups * (int64_t)sizeof(exl3::SharedGroup), batch * 8, p.token ? (batch + 1) * 8 : 0, 4};
+                             groups * (int64_t)sizeof(exl3::SharedGroup), batch * 8, p.token ? (batch + 1) * 8 : 0, 8};
   for (int i = 0; i < 10; ++i) p.at[i + 1] = p.at[i] + (size_t)((bytes[i] + 15) / 16 * 16);
   return p;
 }
@@ -492,7 +492,7 @@ exl3_status_t exl3_attention_shared(const exl3_heads_t* q, exl3_dtype_t dtype, i
   a.group = reinterpret_cast<const exl3::SharedGroup*>(w + plan.at[6]);
   a.seq = reinterpret_cast<const int2*>(w + plan.at[7]);
   a.units = reinterpret_cast<const int64_t*>(w + plan.at[8]);
-  a.items = reinterpret_cast<const int32_t*>(w + plan.at[9]);
+  a.counts = reinterpret_cast<const int2*>(w + plan.at[9]);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = exl3::launch_shared_prep(a, cu_groups, prefix_lens, plan.token, s);
   if (e == cudaSuccess) e = exl3::launch_attn_tile_shared(a, !plan.token, s);

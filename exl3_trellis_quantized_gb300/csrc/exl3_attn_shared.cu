@@ -34,7 +34,7 @@ struct SharedState {
   SharedGroup* group;
   int2* seq;
   int64_t* units;
-  int32_t* items;
+  int2* counts;
 };
 
 // Sums before each thread's value, in thread order, after those that came before (`carry`, which moves on).
@@ -60,20 +60,31 @@ __device__ __forceinline__ int64_t block_sums(int64_t v, int64_t* part, int64_t*
   return before;
 }
 
-// Groups, starts, items and units from the lengths, in one block.
+// Groups, starts, units and items from the lengths, in one block.
 //
 // The prefix that is used: whole tiles of keys that every query of the group sees, none for a group with queries of
 // fewer than two sequences.
 //
 // Parts.  Each row tile's keys go to ceil(blocks / u) CTAs, u blocks of 64 keys at the most; u is the same for all, so
 // that long and short prefixes make items of about one length.  Of 32 sizes u (the longest prefix in 1 to 32) the one
-// that a model of the time likes best: an item takes 0.85 us a block and 4 us; up to 152 items the longest counts, more
-// are taken up in turn, so all of them by 152 and 0.7 of the last; and what the parts cost to write and join.
+// that a model of the time likes best.  An item takes `block` us a block (half of it where its rows fill one tile: its
+// halves take blocks in turn) and 5 us.
+//   With the token kernel, own keys take `unit` us a unit and SM.  Up to 120 items leave SMs for it, so both run at the
+// same time and the longer counts; else one follows the other.
+//   Without, up to 152 items the longest counts; more are taken up in turn: all of them by 152, and 0.7 of the last.
+// And every item's rows are written and joined, at 4 TB/s.
 constexpr int kPrepThreads = 256;
-constexpr float kSms = 152.0f;
+constexpr int kSms = 152, kMostBeside = 120;
+struct SharedCosts {
+  float block, unit;  // us
+  int token, per_sm;  // the token kernel takes the own keys, so many CTAs an SM
+};
 __global__ void __launch_bounds__(kPrepThreads) shared_prep_kernel(const AttnArgs a, const int32_t* cu_groups,
-                                                                   const int32_t* prefix_lens, const SharedState s, int token) {
+                                                                   const int32_t* prefix_lens, const SharedState s,
+                                                                   const SharedCosts cost) {
+  constexpr int kHeld = 256;  // groups whose sizes shared memory holds
   __shared__ int64_t part[kPrepThreads / 32];
+  __shared__ int2 held[kHeld];  // blocks and tokens
   __shared__ int longest;
   __shared__ int unit;
   pdl_launch_dependents();
@@ -86,10 +97,10 @@ __global__ void __launch_bounds__(kPrepThreads) shared_prep_kernel(const AttnArg
   for (int g = tid >> 5; g < a.groups; g += kPrepThreads / 32) {  // one warp a group
     const int s0 = max(0, min(cu_groups[g], a.batch)), s1 = max(s0, min(cu_groups[g + 1], a.batch));
     int keys = max(0, min(prefix_lens[g], room)), first = INT32_MAX, queries = 0;
+    const int q0 = max(0, min(a.cu_q[s0], total)), q1 = max(q0, min(a.cu_q[s1], total));
     for (int b = s0 + lane; b < s1; b += 32) {
-      const int c0 = max(0, a.cu_q[b]), c1 = min(a.cu_q[b + 1], total);
+      const int c0 = max(0, a.cu_q[b]), c1 = min(a.cu_q[b + 1], total), kl = max(0, min(a.kv_lens[b], room));
       if (c1 <= c0) continue;
-      const int kl = max(0, min(a.kv_lens[b], room));
       keys = min(keys, max(0, kl - (c1 - c0) + 1));  // what its first query sees
       first = min(first, b);
       ++queries;
@@ -101,24 +112,38 @@ __global__ void __launch_bounds__(kPrepThreads) shared_prep_kernel(const AttnArg
     if (keys > 0)
       for (int b = s0 + lane; b < s1; b += 32) s.seq[b] = make_int2(keys, g);
     if (lane == 0) {
-      const int c0 = max(0, min(a.cu_q[s0], total)), c1 = max(c0, min(a.cu_q[s1], total));
-      s.group[g] = {c0, c1 - c0, keys, keys > 0 ? first : 0, 0, 0};
-      atomicMax(&longest, keys);
+      s.group[g] = {q0, q1 - q0, keys, keys > 0 ? first : 0, 0, 0};
+      if (g < kHeld) held[g] = make_int2(keys / 64, q1 - q0);
+      atomicMax(&longest, keys / 64);
     }
   }
   __syncthreads();
+  auto sizes = [&](int g) { return g < kHeld ? held[g] : make_int2(s.group[g].keys / 64, s.group[g].tokens); };
+  int64_t units = 0;
+  if (cost.token) {
+    for (int b0 = 0; b0 < a.batch; b0 += kPrepThreads) {
+      const int b = b0 + tid;
+      const int64_t before = block_sums(b < a.batch ? load_seq<true>(a, b).weight() : 0, part, &units);
+      if (b < a.batch) s.units[b] = before;
+    }
+    if (tid == 0) s.units[a.batch] = units;
+  }
   if (tid < 32) {
     // a lane a size
-    const int most = longest / 64, u = max(4, (most + lane) / (lane + 1) + 1 & ~1);
-    float items = 0.0f, blocks = 0.0f;
+    const int u = max(4, ((longest + lane) / (lane + 1) + 1) & ~1);
+    float items = 0.0f, us = 0.0f, one = 0.0f;
     for (int g = 0; g < a.groups; ++g) {
-      const int keys = s.group[g].keys / 64, tiles = keys > 0 ? (s.group[g].tokens + per - 1) / per : 0;
-      items += (float)(tiles * a.kv_heads) * (float)((keys + u - 1) / u);
-      blocks += (float)(tiles * a.kv_heads) * (float)keys;
+      const int2 n = sizes(g);
+      if (n.x == 0) continue;
+      const float tiles = (float)((n.y + per - 1) / per * a.kv_heads), block = n.y <= a.tile_tokens ? 0.5f * cost.block : cost.block;
+      items += tiles * (float)((n.x + u - 1) / u);
+      us += tiles * ((float)n.x * block + (float)((n.x + u - 1) / u) * 5.0f);
+      one = fmaxf(one, (float)min(n.x, u) * block + 5.0f);
     }
-    const float one = 0.85f * (float)u + 4.0f;
-    float us = items <= kSms ? one : (0.85f * blocks + 4.0f * items) / kSms + 0.7f * one;
-    us += items * (float)(kPrefixRows * a.head_dim) * 8.0f / 8.0e6f;
+    const float sms = (float)kSms, all = items <= sms ? one : us / sms + 0.7f * one;
+    const float own = (float)units * a.kv_heads * cost.unit;
+    us = cost.token && items <= (float)kMostBeside ? fmaxf(one, own / (sms - items) + 4.0f) : all + own / sms;
+    us += items * (float)(kPrefixRows * a.head_dim) * 8.0f / 4.0e6f;
     if (items > (float)a.prefix_ctas) us = __builtin_huge_valf();  // (the first size has an item a row tile: always room)
     float best = us;
 #pragma unroll
@@ -127,37 +152,32 @@ __global__ void __launch_bounds__(kPrepThreads) shared_prep_kernel(const AttnArg
     if (lane == __ffs(hit) - 1) unit = u;
   }
   __syncthreads();
-  int64_t carry = 0;
+  int64_t items = 0;
   for (int g0 = 0; g0 < a.groups; g0 += kPrepThreads) {
     const int g = g0 + tid;
     int tiles = 0, parts = 0;
     if (g < a.groups) {
-      const int keys = s.group[g].keys / 64;
-      tiles = keys > 0 ? (s.group[g].tokens + per - 1) / per : 0;
-      parts = (keys + unit - 1) / unit;
+      const int2 n = sizes(g);
+      tiles = n.x > 0 ? (n.y + per - 1) / per : 0;
+      parts = (n.x + unit - 1) / unit;
     }
-    const int64_t before = block_sums((int64_t)tiles * a.kv_heads * parts, part, &carry);
+    const int64_t before = block_sums((int64_t)tiles * a.kv_heads * parts, part, &items);
     if (g < a.groups) {
       s.group[g].item = (int)before;
       s.group[g].parts = parts;
     }
   }
-  if (tid == 0) s.items[0] = (int)min(carry, (int64_t)a.prefix_ctas);
-  if (!token) return;
-  carry = 0;
-  for (int b0 = 0; b0 < a.batch; b0 += kPrepThreads) {
-    const int b = b0 + tid;
-    const int64_t before = block_sums(b < a.batch ? load_seq<true>(a, b).weight() : 0, part, &carry);
-    if (b < a.batch) s.units[b] = before;
+  if (tid == 0) {
+    const int n = (int)min(items, (int64_t)a.prefix_ctas);
+    const int beside = n <= kMostBeside ? (kSms - n) * cost.per_sm : kSms * cost.per_sm;
+    s.counts[0] = make_int2(n, min(a.ctas, beside));
   }
-  if (tid == 0) s.units[a.batch] = carry;
 }
 
-// A row's running sum of parts.
-template <int PER>
+// A row's running sum of parts: eight values a lane.
 struct Sum {
-  float m = kNegInf, l = 0.0f, o[PER] = {};
-  __device__ __forceinline__ void add(const float2& ml, const float (&v)[PER]) {
+  float m = kNegInf, l = 0.0f, o[8] = {};
+  __device__ __forceinline__ void add(const float2& ml, const float (&v)[8]) {
     if (ml.x == kNegInf) {
       l += ml.y;  // 0, or NaN
       return;
@@ -166,53 +186,55 @@ struct Sum {
     const float f = m == kNegInf ? 0.0f : ex2(m - top), f1 = ex2(ml.x - top);
     l = (m == kNegInf ? l : l * f) + ml.y * f1;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) o[i] = o[i] * f + v[i] * f1;
+    for (int i = 0; i < 8; ++i) o[i] = o[i] * f + v[i] * f1;
     m = top;
   }
 };
 
-template <int PER>
-__device__ __forceinline__ void load_row(float (&v)[PER], const float* src) {
+__device__ __forceinline__ void load_row(float (&v)[8], const float* src) {
 #pragma unroll
-  for (int i = 0; i < PER; i += 2) {
-    const float2 w = *reinterpret_cast<const float2*>(src + i);
-    v[i] = w.x, v[i + 1] = w.y;
+  for (int i = 0; i < 8; i += 4) {
+    const float4 w = *reinterpret_cast<const float4*>(src + i);
+    v[i] = w.x, v[i + 1] = w.y, v[i + 2] = w.z, v[i + 3] = w.w;
   }
 }
 
-// One warp has a row's sum: out of the rotated basis, divided, stored.
+// A row's sum, held by D/8 lanes: out of the rotated basis, divided, stored (a whole warp; nothing where not `there`).
 template <int D, bool QUANT>
-__device__ __forceinline__ void finish_row(const AttnArgs& a, const Sum<D / 32>& s, int64_t tok, int head, int lane) {
-  constexpr int PER = D / 32;
+__device__ __forceinline__ void finish_row(const AttnArgs& a, const Sum& s, int64_t tok, int head, int l, bool there) {
   const float inv = s.l == 0.0f ? 0.0f : 1.0f / s.l;
-  float o[PER];
+  float o[8];
 #pragma unroll
-  for (int i = 0; i < PER; ++i) o[i] = s.o[i] * inv;
+  for (int i = 0; i < 8; ++i) o[i] = s.o[i] * inv;
   if constexpr (QUANT) {
 #pragma unroll
-    for (int st = 1; st < PER; st *= 2)
+    for (int st = 1; st < 8; st *= 2)
 #pragma unroll
-      for (int i = 0; i < PER; ++i)
+      for (int i = 0; i < 8; ++i)
         if (!(i & st)) {
           const float x = o[i], y = o[i + st];
           o[i] = x + y, o[i + st] = x - y;
         }
 #pragma unroll
-    for (int st = 1; st < 32; st *= 2)
+    for (int st = 1; st < D / 8; st *= 2)
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
+      for (int i = 0; i < 8; ++i) {
         const float x = __shfl_xor_sync(0xffffffffu, o[i], st);
-        o[i] = (lane & st) ? x - o[i] : o[i] + x;
+        o[i] = (l & st) ? x - o[i] : o[i] + x;
       }
 #pragma unroll
-    for (int i = 0; i < PER; ++i) o[i] *= 8.0f / D;
+    for (int i = 0; i < 8; ++i) o[i] *= 8.0f / D;
   }
-  uint16_t* dst = static_cast<uint16_t*>(a.out) + tok * a.out_token_stride + head * a.out_head_stride + PER * lane;
+  if (!there) return;
+  uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < PER; i += 2) {
-    if (a.bf16) *reinterpret_cast<__nv_bfloat162*>(dst + i) = __floats2bfloat162_rn(o[i], o[i + 1]);
-    else *reinterpret_cast<__half2*>(dst + i) = __floats2half2_rn(o[i], o[i + 1]);
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(o[2 * i], o[2 * i + 1]);
+    const __half2 y = __floats2half2_rn(o[2 * i], o[2 * i + 1]);
+    w[i] = a.bf16 ? *reinterpret_cast<const uint32_t*>(&x) : *reinterpret_cast<const uint32_t*>(&y);
   }
+  uint16_t* dst = static_cast<uint16_t*>(a.out) + tok * a.out_token_stride + head * a.out_head_stride + 8 * l;
+  *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // The part of row (tok, head) in the first of its prefix items; the next parts lie kPrefixRows rows on.
@@ -225,94 +247,140 @@ __device__ __forceinline__ SharedGroup load_group(const SharedGroup* g) {
   return {__ldcg(&g->q0), __ldcg(&g->tokens), __ldcg(&g->keys), __ldcg(&g->lead), __ldcg(&g->item), __ldcg(&g->parts)};
 }
 
-// The join: WARPS warps a row take its parts in turn (those of the prefix, then its own), kAhead loads at a time; with
-// more than one, the first joins them.  Every query token of a sequence has its rows here; the sequence is found from
-// cu_q.  TOKEN: own parts of the token kernel, one, or those of the ranges that cut the item.
-constexpr int kAhead = 6;
-template <int D, bool QUANT, bool TOKEN, int WARPS>
-__global__ void __launch_bounds__(256) shared_join_kernel(const AttnArgs a) {
-  constexpr int PER = D / 32, ROWS = 8 / WARPS;  // rows of a block
-  __shared__ float so[WARPS > 1 ? WARPS : 1][D];
-  __shared__ float2 sml[WARPS > 1 ? WARPS : 1];
-  const int warp = (threadIdx.x >> 5) % WARPS, lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * ROWS + (threadIdx.x >> 5) / WARPS, rows = a.total_q * a.heads;
-  const int group = a.heads / a.kv_heads;
-  const int tok = (int)(row / a.heads), head = (int)(row - (int64_t)tok * a.heads), h = head / group;
-  int b = -1;
-  if (row < rows) {
-    for (int b0 = 0; b0 < a.batch; b0 += 32) {
-      const int i = b0 + lane;
-      const uint32_t hit = __ballot_sync(0xffffffffu, i < a.batch && tok >= a.cu_q[i] && tok < a.cu_q[i + 1]);
-      if (hit) {
-        b = b0 + __ffs(hit) - 1;
-        break;
-      }
+// Where a row's parts lie.
+template <bool TOKEN>
+struct Parts {
+  int64_t row, prefix0;  // the row of [total_q][heads]; its place in the first of its prefix items
+  int shared, own;       // parts of the prefix, parts of its own keys
+  int64_t c0, total, first;
+  int ctas, r;
+  // Of row (tok, head); false where there are none.
+  __device__ __forceinline__ bool find(const AttnArgs& a, int b, int tok, int head) {
+    const int group = a.heads / a.kv_heads, h = head / group;
+    row = (int64_t)tok * a.heads + head;
+    const int g = __ldcg(&a.seq[b].y);
+    shared = 0;
+    prefix0 = 0;
+    if (g >= 0) {
+      const SharedGroup sg = load_group(a.group + g);
+      shared = sg.parts;
+      prefix0 = prefix_row(a, sg, tok, h, head - h * group, group);
     }
+    own = a.splits;
+    if constexpr (TOKEN) {
+      const Seq s = load_seq<true>(a, b);
+      r = (tok - (int)s.q0) * group + head - h * group;
+      if (r >= s.q_len * group) return false;  // more tokens than max_q
+      ctas = __ldcg(&a.counts->y);
+      total = __ldcg(a.units + a.batch) * a.kv_heads;
+      first = __ldcg(a.units + b) * a.kv_heads + (int64_t)h * s.weight() + kItemUnits;
+      // the CTA of a unit is the last whose range begins at or before it
+      c0 = ((first + 1) * ctas - 1) / total;
+      own = (int)(((first + s.units) * ctas - 1) / total - c0) + 1;
+    }
+    return true;
   }
+  // Part i's output (null: it has none) and statistics.
+  __device__ __forceinline__ const float* at(const AttnArgs& a, int i, int d, const float2** ml) const {
+    const float* o = a.own_o;
+    const float2* l = a.own_ml;
+    int64_t n = (i - shared) * a.total_q * a.heads + row;
+    if (i < shared) {
+      o = a.prefix_o, l = a.prefix_ml, n = prefix0 + (int64_t)i * kPrefixRows;
+    } else if (TOKEN && own > 1) {
+      const int64_t c = c0 + i - shared, begin = total * c / ctas;
+      if (begin >= total * (c + 1) / ctas) return nullptr;
+      o = a.cut_o, l = a.cut_ml, n = (2 * c + (begin <= first ? 1 : 0)) * kTokenRows + r;
+    }
+    *ml = l + n;
+    return o + n * d;
+  }
+};
+// The sequence of a token, -1 for none (a whole warp).
+__device__ __forceinline__ int find_sequence(const AttnArgs& a, int tok, int lane) {
+  for (int b0 = 0; b0 < a.batch; b0 += 32) {
+    const int i = b0 + lane;
+    const uint32_t hit = __ballot_sync(0xffffffffu, i < a.batch && tok >= a.cu_q[i] && tok < a.cu_q[i + 1]);
+    if (hit) return b0 + __ffs(hit) - 1;
+  }
+  return -1;
+}
+
+// The joins.  A row is held by D/8 lanes, eight values each, its parts kAhead loads at a time: those of the prefix, then
+// its own.  Many rows: a block takes one token, finds its parts once, and its lane groups take the heads in turn.
+// Few rows: a block takes one row, and its lane groups the parts in turn.
+constexpr int kAhead = 4;
+constexpr int kJoinThreads = 256;
+template <int D, bool QUANT, bool TOKEN>
+__global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const AttnArgs a) {
+  constexpr int LANES = D / 8;
+  const int lane = threadIdx.x & 31, l = threadIdx.x % LANES;
+  const int tok = (int)blockIdx.x;
+  const int b = find_sequence(a, tok, lane);
   pdl_wait();
-  if (b < 0) return;  // a token of no sequence (the whole block, where warps share a row)
-  const int g = __ldcg(&a.seq[b].y);
-  int shared = 0;
-  int64_t at0 = 0;
-  if (g >= 0) {
-    const SharedGroup sg = load_group(a.group + g);
-    shared = sg.parts;
-    at0 = prefix_row(a, sg, tok, h, head - h * group, group);
-  }
-  int64_t own = a.splits, c0 = 0, total = 0, first = 0;
-  int r = 0;
-  if constexpr (TOKEN) {
-    const Seq s = load_seq<true>(a, b);
-    r = (tok - (int)s.q0) * group + head - h * group;
-    if (r >= s.q_len * group) return;  // more tokens than max_q
-    total = __ldcg(a.units + a.batch) * a.kv_heads;
-    first = __ldcg(a.units + b) * a.kv_heads + (int64_t)h * s.weight() + kItemUnits;
-    const int64_t last = first + s.units - 1;
-    // the CTA of a unit is the last whose range begins at or before it
-    c0 = ((first + 1) * a.ctas - 1) / total;
-    own = ((last + 1) * a.ctas - 1) / total - c0 + 1;
-  }
-  const int64_t parts = shared + own;
-  Sum<PER> sum;
-  for (int64_t p = warp; p < parts; p += WARPS * kAhead) {
-    float2 ml[kAhead];
-    float v[kAhead][PER];
+  if (b < 0) return;
+  // whole warps go round, for the shuffles of the last step
+  const int step = gridDim.y * (kJoinThreads / LANES);
+  for (int head0 = blockIdx.y * (kJoinThreads / LANES) + threadIdx.x / 32 * (32 / LANES); head0 < a.heads; head0 += step) {
+    const int head = head0 + lane / LANES;
+    Parts<TOKEN> parts;
+    const bool there = head < a.heads && parts.find(a, b, tok, head);
+    Sum sum;
+    const int n = there ? parts.shared + parts.own : 0;
+    for (int i = 0; i < n; i += kAhead) {
+      float2 ml[kAhead];
+      float v[kAhead][8];
 #pragma unroll
-    for (int x = 0; x < kAhead; ++x) {
-      const int64_t i = p + x * WARPS, j = i - shared;
-      ml[x] = make_float2(kNegInf, 0.0f);
-      if (i >= parts) continue;
-      const float* o = a.own_o;
-      const float2* l = a.own_ml;
-      int64_t at = j * rows + row;
-      if (j < 0) {
-        o = a.prefix_o, l = a.prefix_ml, at = at0 + i * kPrefixRows;
-      } else if (TOKEN && own > 1) {
-        const int64_t cc = c0 + j, begin = total * cc / a.ctas;
-        if (begin >= total * (cc + 1) / a.ctas) continue;
-        o = a.cut_o, l = a.cut_ml, at = (2 * cc + (begin <= first ? 1 : 0)) * kTokenRows + r;
+      for (int x = 0; x < kAhead; ++x) {
+        const float2* pml;
+        ml[x] = make_float2(kNegInf, 0.0f);
+        const float* po = i + x < n ? parts.at(a, i + x, D, &pml) : nullptr;
+        if (po == nullptr) continue;
+        ml[x] = *pml;
+        load_row(v[x], po + 8 * l);
       }
-      ml[x] = l[at];
-      load_row(v[x], o + at * D + PER * lane);
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x) sum.add(ml[x], v[x]);
     }
-#pragma unroll
-    for (int x = 0; x < kAhead; ++x) sum.add(ml[x], v[x]);
+    finish_row<D, QUANT>(a, sum, tok, head, l, there);
   }
-  if constexpr (WARPS > 1) {
-#pragma unroll
-    for (int i = 0; i < PER; ++i) so[warp][PER * lane + i] = sum.o[i];
-    if (lane == 0) sml[warp] = make_float2(sum.m, sum.l);
-    __syncthreads();
-    if (warp != 0) return;
-    sum = Sum<PER>();
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-      float v[PER];
-      load_row(v, &so[w][PER * lane]);
-      sum.add(sml[w], v);
-    }
+}
+template <int D, bool QUANT, bool TOKEN>
+__global__ void __launch_bounds__(kJoinThreads) shared_join_row_kernel(const AttnArgs a) {
+  constexpr int LANES = D / 8, TEAMS = kJoinThreads / LANES;
+  __shared__ __align__(16) float so[TEAMS][D];
+  __shared__ float2 sml[TEAMS];
+  const int lane = threadIdx.x & 31, l = threadIdx.x % LANES, team = threadIdx.x / LANES;
+  const int tok = (int)blockIdx.x, head = (int)blockIdx.y;
+  const int b = find_sequence(a, tok, lane);
+  pdl_wait();
+  if (b < 0) return;
+  Parts<TOKEN> parts;
+  if (!parts.find(a, b, tok, head)) return;
+  const int n = parts.shared + parts.own;
+  Sum sum;
+  for (int i = team; i < n; i += TEAMS) {
+    const float2* pml;
+    const float* po = parts.at(a, i, D, &pml);
+    if (po == nullptr) continue;
+    float v[8];
+    load_row(v, po + 8 * l);
+    sum.add(*pml, v);
   }
-  finish_row<D, QUANT>(a, sum, tok, head, lane);
+#pragma unroll
+  for (int i = 0; i < 8; i += 4) *reinterpret_cast<float4*>(&so[team][8 * l + i]) = make_float4(sum.o[i], sum.o[i + 1], sum.o[i + 2], sum.o[i + 3]);
+  if (l == 0) sml[team] = make_float2(sum.m, sum.l);
+  __syncthreads();
+  if (threadIdx.x >= 32) return;
+  // one warp, whose lane groups do the same
+  Sum all;
+#pragma unroll 4
+  for (int t = 0; t < TEAMS; ++t) {
+    float v[8];
+    load_row(v, &so[t][8 * l]);
+    all.add(sml[t], v);
+  }
+  finish_row<D, QUANT>(a, all, tok, head, l, threadIdx.x < LANES);
 }
 
 }  // namespace
@@ -320,38 +388,43 @@ __global__ void __launch_bounds__(256) shared_join_kernel(const AttnArgs a) {
 cudaError_t launch_shared_prep(const AttnArgs& a, const int32_t* cu_groups, const int32_t* prefix_lens, bool token,
                                cudaStream_t stream) {
   const SharedState s = {const_cast<SharedGroup*>(a.group), const_cast<int2*>(a.seq), const_cast<int64_t*>(a.units),
-                         const_cast<int32_t*>(a.items)};
-  shared_prep_kernel<<<1, kPrepThreads, 0, stream>>>(a, cu_groups, prefix_lens, s, token ? 1 : 0);
+                         const_cast<int2*>(a.counts)};
+  // a unit's rows of keys and values at 37 GB/s an SM (4 bits: 15)
+  const bool int4 = a.cache.format == kKvInt4;
+  const float unit = (float)(128 * kv_row_bytes(a.cache.format, a.head_dim)) * (int4 ? 1e-3f / 15.0f : 1e-3f / 37.0f);
+  const float block = (kv_quantised(a.cache.format) ? 1.2f : 0.85f) * (float)a.head_dim / 128.0f;
+  const SharedCosts cost = {block, unit, token ? 1 : 0, token_ctas_per_sm(a.max_q * (a.heads / a.kv_heads))};
+  shared_prep_kernel<<<1, kPrepThreads, 0, stream>>>(a, cu_groups, prefix_lens, s, cost);
   return cudaGetLastError();
 }
 
-namespace {
-template <int D, bool QUANT>
-cudaError_t launch_join(const AttnArgs& a, bool token, cudaStream_t stream) {
+cudaError_t launch_shared_join(const AttnArgs& a, bool token, cudaStream_t stream) {
+  const int quant = kv_quantised(a.cache.format), wide = a.head_dim == 128, teams = kJoinThreads / (a.head_dim / 8);
   const int64_t rows = a.total_q * a.heads;
-  // few rows: eight warps each
-  const bool wide = rows <= 152 * 8;
+  const bool few = rows <= kSms * 4 && a.heads <= 65535;
+  // a block a token, or while that leaves SMs idle a token's heads over several
+  const int heads = (a.heads + teams - 1) / teams;
+  const unsigned y = few ? (unsigned)a.heads : (unsigned)(a.total_q >= 4 * kSms ? 1 : heads);
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(256u, 1u, 1u);
-  cfg.gridDim = dim3((unsigned)(wide ? rows : (rows + 7) / 8), 1u, 1u);
+  cfg.blockDim = dim3(kJoinThreads, 1u, 1u);
+  cfg.gridDim = dim3((unsigned)a.total_q, y, 1u);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (token)
-    return wide ? cudaLaunchKernelEx(&cfg, shared_join_kernel<D, QUANT, true, 8>, a)
-                : cudaLaunchKernelEx(&cfg, shared_join_kernel<D, QUANT, true, 1>, a);
-  return wide ? cudaLaunchKernelEx(&cfg, shared_join_kernel<D, QUANT, false, 8>, a)
-              : cudaLaunchKernelEx(&cfg, shared_join_kernel<D, QUANT, false, 1>, a);
-}
-}  // namespace
-
-cudaError_t launch_shared_join(const AttnArgs& a, bool token, cudaStream_t stream) {
-  const bool quant = kv_quantised(a.cache.format);
-  if (a.head_dim == 64) return quant ? launch_join<64, true>(a, token, stream) : launch_join<64, false>(a, token, stream);
-  return quant ? launch_join<128, true>(a, token, stream) : launch_join<128, false>(a, token, stream);
+  using Kernel = void (*)(const AttnArgs);
+  static constexpr Kernel kernels[2][2][2][2] = {
+      {{{shared_join_kernel<64, false, false>, shared_join_kernel<64, false, true>},
+        {shared_join_kernel<64, true, false>, shared_join_kernel<64, true, true>}},
+       {{shared_join_kernel<128, false, false>, shared_join_kernel<128, false, true>},
+        {shared_join_kernel<128, true, false>, shared_join_kernel<128, true, true>}}},
+      {{{shared_join_row_kernel<64, false, false>, shared_join_row_kernel<64, false, true>},
+        {shared_join_row_kernel<64, true, false>, shared_join_row_kernel<64, true, true>}},
+       {{shared_join_row_kernel<128, false, false>, shared_join_row_kernel<128, false, true>},
+        {shared_join_row_kernel<128, true, false>, shared_join_row_kernel<128, true, true>}}}};
+  return cudaLaunchKernelEx(&cfg, kernels[few][wide][quant][token], a);
 }
 
 }  // namespace exl3

@@ -218,6 +218,10 @@ __device__ __forceinline__ int cancelled_cta(uint32_t answer) {
       : "memory");
   return x;
 }
+// Bytes on their way into L2; address and size as for a bulk copy.
+__device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   uint32_t r;
@@ -349,7 +353,7 @@ __device__ Span half_span(const AttnArgs& a, const Item& it, int n0, int n1, int
 template <int SRC>
 __device__ bool find_item(const AttnArgs& a, int lane, int64_t idx, Item* it) {
   const int per = 2 * a.tile_tokens, group = a.heads / a.kv_heads;
-  const int prefix_items = __ldcg(a.items);
+  const int prefix_items = __ldcg(&a.counts->x);
   const bool prefix = idx < prefix_items;
   if (!prefix && a.splits == 0) return false;  // own keys go through the token kernel
   const int64_t item = idx;
@@ -1145,11 +1149,42 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
           }
           __syncwarp();
           ++n;
+#ifdef EXL3_ATTN_SHARED
+          // Cache rows of the next two tiles' copies: their page ids come, and for codes their bytes are on the way into L2,
+          // while the tile before them is copied.  (The ring of codes holds two tiles' sides; without this the copies'
+          // latency was 2.8 us a tile of 128 keys.)
+          int64_t rows_ahead[2];
+          auto look = [&](int j) -> int64_t {  // -1: no page of the cache
+            const int key = it.base + j * kKeys + lane * page_rows;
+            if (j >= it.jhi || lane * page_rows >= kKeys || key >= it.kv_len) return -1;
+            const int id = a.table[(int64_t)it.b * a.table_width + (key >> a.cache.page_shift)];
+            if (id < 0 || id >= a.cache.num_pages) return -1;
+            const int64_t row = (((int64_t)id * a.kv_heads + it.kvh) << a.cache.page_shift) + (key & ((1 << a.cache.page_shift) - 1));
+            if constexpr (C::kQuant) {
+              prefetch_l2(a.cache.k + row * C::kRowBytes, (uint32_t)(page_rows * C::kRowBytes));
+              prefetch_l2(a.cache.v + row * C::kRowBytes, (uint32_t)(page_rows * C::kRowBytes));
+              prefetch_l2(a.cache.k_scale + row, (uint32_t)(page_rows * 2));
+              prefetch_l2(a.cache.v_scale + row, (uint32_t)(page_rows * 2));
+            }
+            return row;
+          };
+          rows_ahead[0] = look(it.jlo), rows_ahead[1] = look(it.jlo + 1);
+#endif
           for (int j = it.jlo; ok && j < it.jhi; ++j) {
             const int t = it.base + j * kKeys;
             int64_t row = 0;  // cache row of this lane's copy (paged)
             int copies = 1;
             bool page_ok = true;
+#ifdef EXL3_ATTN_SHARED
+            copies = (min(kKeys, it.kv_len - t) + page_rows - 1) / page_rows;
+            row = rows_ahead[0];
+            rows_ahead[0] = rows_ahead[1];
+            rows_ahead[1] = look(j + 2);
+            if (lane < copies) {
+              page_ok = row >= 0;
+              if (!page_ok) row = C::kQuant ? 0 : (a.cache.num_pages * a.kv_heads) << a.cache.page_shift;
+            }
+#else
             if constexpr (SRC != kPacked) {
               copies = (min(kKeys, it.kv_len - t) + page_rows - 1) / page_rows;
               if (lane < copies) {
@@ -1163,6 +1198,7 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
                               : C::kQuant ? 0 : (a.cache.num_pages * a.kv_heads) << a.cache.page_shift;
               }
             }
+#endif
 #pragma unroll
             for (int value = 0; value < 2; ++value) {
               if (!ok) break;

@@ -304,7 +304,8 @@ __global__ void __launch_bounds__(kThreads, token_ctas_per_sm(8 * NR)) attn_toke
   pdl_launch_dependents();  // the join may be scheduled; it waits for this grid
 
   const int64_t total = total_units(a, lane);
-  const int64_t grid = gridDim.x;
+  const int64_t grid = kShared ? __ldcg(&a.counts->y) : gridDim.x;
+  if (kShared && blockIdx.x >= grid) return;  // the prefixes' kernel has its SM
   int64_t u = total * blockIdx.x / grid;
   const int64_t u_end = total * (blockIdx.x + 1) / grid;
   if (u >= u_end) {
