@@ -42,6 +42,8 @@ namespace {
 constexpr int kRopeThreads = 128;
 constexpr int kRopeBlocks = 9;  // blocks an SM: 56 registers a thread (seven blocks of 72: 83 us for 79 below)
 constexpr int kRopeBatch = 4;  // rows a lane group loads before it works on the first
+constexpr int kNormBlocks = 9;  // blocks an SM with norms
+constexpr int kNormBatch = 2;   // rows at a time with norms, the next ones on their way
 
 __device__ __forceinline__ void unpack8(const uint4& w, bool bf16, float (&v)[8]) {
   const uint32_t r[4] = {w.x, w.y, w.z, w.w};
@@ -229,32 +231,8 @@ __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
   b = __fadd_rn(__fmul_rn(q, c), __fmul_rn(p, s));
 }
 
-// Sum over the LANES neighbouring lanes of a row (aligned; other rows of the warp need not come here).
-template <int LANES>
-__device__ __forceinline__ float row_sum(float x) {
-  const uint32_t mask = ((1u << LANES) - 1u) << ((threadIdx.x & 31) & ~(LANES - 1));
-#pragma unroll
-  for (int s = 1; s < LANES; s *= 2) x += __shfl_xor_sync(mask, x, s);
-  return x;
-}
-template <int N>
-__device__ __forceinline__ float square_sum(const float2 (&v)[N]) {
-  float2 s = mul2(v[0], v[0]);
-#pragma unroll
-  for (int j = 1; j < N; ++j) s = fma2(v[j], v[j], s);
-  return s.x + s.y;
-}
-// v times the row's 1 / rms, times the weights of the same places.
-__device__ __forceinline__ void scale_row(float2* v, float inv, const uint4& weight, bool bf16) {
-  float2 w[4];
-  unpack8(weight, bf16, w);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) v[j] = mul2(mul2(v[j], twice(inv)), w[j]);
-}
-
-// KV: there are keys and values.  NORM: x's rows or the keys' (or both) are divided by their root mean square and
-// multiplied by weights first, in fp32 and without a rounding before the rotation.
-template <int D, bool KV, bool NORM>
+// KV: there are keys and values
+template <int D, bool KV>
 __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_write_kernel(const RopeWriteArgs a, int units_per_block) {
   constexpr int LANES = D / 8;
   constexpr int GROUPS = kRopeThreads / LANES;
@@ -335,15 +313,6 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_write_kernel(c
 #pragma unroll
     for (int j = 0; j < 4; ++j) c[j] = turns ? cs[4 * l + j] : 1.0f, s[j] = turns ? sn[4 * l + j] : 0.0f;
     uint16_t* out = static_cast<uint16_t*>(a.out) + t * a.out_token_stride;
-    // weights of this lane's places
-    auto weight_of = [&](int r) {
-      const uint16_t* src = a.x_norm.weight + r * a.x_norm.head_stride;
-      const uint2 lo = *reinterpret_cast<const uint2*>(src + at0), hi = *reinterpret_cast<const uint2*>(src + at1);
-      return make_uint4(lo.x, lo.y, hi.x, hi.y);
-    };
-    const bool normed = NORM && a.x_norm.weight != nullptr;
-    uint4 weight = make_uint4(0u, 0u, 0u, 0u);
-    if (normed) weight = weight_of(0);
     for (int u = u0; u < min(xu, u1); u += kRopeBatch) {
       if (u > u0) load_x(u);
 #pragma unroll
@@ -351,24 +320,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_write_kernel(c
         const int r = (u + i) * GROUPS + group;
         if (u + i >= min(xu, u1) || r >= a.x_heads) break;
         uint4 w = make_uint4(raw[i][0].x, raw[i][0].y, raw[i][1].x, raw[i][1].y);
-        if (NORM && normed) {
-          float2 v[4];
-          unpack8(w, bf16, v);
-          if (a.x_norm.head_stride != 0) weight = weight_of(r);
-          const float inv = rsqrtf(fmaf(row_sum<LANES>(square_sum(v)), 1.0f / D, a.x_norm.eps));
-          scale_row(v, inv, weight, bf16);
-          if (turns) {
-            float f[8] = {v[0].x, v[0].y, v[1].x, v[1].y, v[2].x, v[2].y, v[3].x, v[3].y};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              if (pairs) turn(f[2 * j], f[2 * j + 1], c[j], s[j]);
-              else turn(f[j], f[4 + j], c[j], s[j]);
-            }
-            w = pack8(f, bf16);
-          } else {
-            w = pack8(v, bf16);
-          }
-        } else if (turns) {
+        if (turns) {
           float v[8];
           unpack8(w, bf16, v);
           if (pairs) {
@@ -393,51 +345,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_write_kernel(c
       load_kv(u + 1);
       const int r = kv_row(u);
       const bool there = r < 2 * a.kv_heads, isk = r < a.kv_heads;
-      if (NORM && isk && a.k_norm.weight != nullptr) {
-        const int hl = half >> 3;  // chunks of one half
-        const uint16_t* weights = a.k_norm.weight + r * a.k_norm.head_stride;
-        float2 v[8];
-        unpack8(w[0], bf16, v);
-        unpack8(w[1], bf16, v + 4);
-        const float inv = rsqrtf(fmaf(row_sum<KLANES>(square_sum(v)), 1.0f / D, a.k_norm.eps));
-#pragma unroll
-        for (int i = 0; i < 2; ++i) scale_row(v + 4 * i, inv, *reinterpret_cast<const uint4*>(weights + 8 * (kl + KLANES * i)), bf16);
-        if (pairs) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int ch = kl + KLANES * i;
-            if (8 * ch >= 2 * half) continue;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) turn(v[4 * i + j].x, v[4 * i + j].y, cs[4 * ch + j], sn[4 * ch + j]);
-          }
-        } else if (hl == KLANES) {  // the whole row turns: both values of each pair are this lane's
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            turn(v[j].x, v[4 + j].x, cs[8 * kl + 2 * j], sn[8 * kl + 2 * j]);
-            turn(v[j].y, v[4 + j].y, cs[8 * kl + 2 * j + 1], sn[8 * kl + 2 * j + 1]);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int ch = kl + KLANES * i;
-            if (8 * ch >= 2 * half) continue;
-            // the other values of the pairs, read once more
-            const bool upper = ch >= hl;
-            const int other = upper ? ch - hl : ch + hl, f = 8 * (upper ? ch - hl : ch);
-            float2 o[4];
-            unpack8(*reinterpret_cast<const uint4*>(kv_src(r) + 8 * other), bf16, o);
-            scale_row(o, inv, *reinterpret_cast<const uint4*>(weights + 8 * other), bf16);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              float2& x = v[4 * i + j];
-              x.x = __fadd_rn(__fmul_rn(x.x, cs[f + 2 * j]), __fmul_rn(o[j].x, upper ? sn[f + 2 * j] : -sn[f + 2 * j]));
-              x.y = __fadd_rn(__fmul_rn(x.y, cs[f + 2 * j + 1]), __fmul_rn(o[j].y, upper ? sn[f + 2 * j + 1] : -sn[f + 2 * j + 1]));
-            }
-          }
-        }
-        w[0] = pack8(v, bf16);
-        w[1] = pack8(v + 4, bf16);
-      } else if (isk && half > 0) {
+      if (isk && half > 0) {
         const int hl = half >> 3;  // chunks of one half
         const uint4 raw0 = w[0], raw1 = w[1];
 #pragma unroll
@@ -479,6 +387,240 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_write_kernel(c
         float2 v[8];
         unpack8(w[0], bf16, v);  // the row as its type holds it is what gets quantised
         unpack8(w[1], bf16, v + 4);
+        quantise_row<D>(v, kl, a.cache.format == kKvInt8, dst, isk ? a.cache.k_scale : a.cache.v_scale, row, there);
+      }
+    }
+  }
+}
+
+// Sum over the LANES neighbouring lanes of a row (aligned; other rows of the warp need not come here).
+template <int LANES>
+__device__ __forceinline__ float row_sum(float x) {
+  const uint32_t mask = ((1u << LANES) - 1u) << ((threadIdx.x & 31) & ~(LANES - 1));
+#pragma unroll
+  for (int s = 1; s < LANES; s *= 2) x += __shfl_xor_sync(mask, x, s);
+  return x;
+}
+template <int N>
+__device__ __forceinline__ float square_sum(const float2 (&v)[N]) {
+  float2 s = mul2(v[0], v[0]);
+#pragma unroll
+  for (int j = 1; j < N; ++j) s = fma2(v[j], v[j], s);
+  return s.x + s.y;
+}
+// The same with norms: a head's values are divided by their root mean square and multiplied by weights before they
+// turn, in fp32 and without a rounding in between:
+//     y[d] = inv * (x[d] P[d] + x[pair of d] R[d]),  inv = 1 / sqrt(mean x^2 + eps),
+// where P = w cos and R = -+ w' sin (w' the pair's weight; P = w, R = 0 for values that do not turn) are the same for
+// all heads of a token: computed once a block, then a row costs a sum of squares and two multiply-adds a value, two
+// values an instruction.  Where heads have weights of their own, P and R are without them.
+//
+// Bound by DRAM as the rotation alone.
+// BF16: type of the rows (a choice at run time makes three instructions of every conversion).  PAIRS: interleaved.
+template <int D, bool KV, bool BF16, bool PAIRS>
+__global__ void __launch_bounds__(kRopeThreads, KV ? kNormBlocks - 1 : kNormBlocks) norm_write_kernel(const RopeWriteArgs a, int units_per_block) {
+  constexpr int LANES = D / 8;
+  constexpr int GROUPS = kRopeThreads / LANES;
+  constexpr int KLANES = D / 16;  // lanes of a key's or value's row, sixteen values each
+  constexpr int KGROUPS = kRopeThreads / KLANES;
+  __shared__ __align__(16) float xp[D], xr[D], kp[KV ? D : 4], kr[KV ? D : 4];  // P and R of x's rows and of the keys
+  const int64_t t = blockIdx.x;
+  const int l = threadIdx.x % LANES;
+  const int group = threadIdx.x / LANES;
+  const int half = a.rope.rot_dim >> 1;
+  // where the row's values lie that this lane turns: both of each pair
+  const bool apart = !PAIRS && 4 * l < half;
+  const int at0 = apart ? 4 * l : 8 * l, at1 = apart ? half + 4 * l : 8 * l + 4;
+  const bool xnorm = a.x_norm.weight != nullptr, knorm = a.k_norm.weight != nullptr;
+  const bool xeach = xnorm && a.x_norm.head_stride != 0, keach = knorm && a.k_norm.head_stride != 0;
+
+  // this block's units: of x, GROUPS rows each, then of keys and values, KGROUPS rows each
+  const int xu = (a.x_heads + GROUPS - 1) / GROUPS, ku = KV ? (2 * a.kv_heads + KGROUPS - 1) / KGROUPS : 0;
+  const int u0 = blockIdx.y * units_per_block, u1 = min(xu + ku, u0 + units_per_block);
+
+  const uint16_t* x = static_cast<const uint16_t*>(a.x.data) + t * a.x.token_stride;
+  auto load8 = [&](const uint16_t* row) {
+    const uint2 lo = *reinterpret_cast<const uint2*>(row + at0), hi = *reinterpret_cast<const uint2*>(row + at1);
+    return make_uint4(lo.x, lo.y, hi.x, hi.y);
+  };
+  uint4 raw[kNormBatch];
+  auto load_x = [&](int u) {
+#pragma unroll
+    for (int i = 0; i < kNormBatch; ++i) {
+      const int r = (u + i) * GROUPS + group;
+      raw[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (u + i < min(xu, u1) && r < a.x_heads) raw[i] = load8(x + (int64_t)r * a.x.head_stride);
+    }
+  };
+  load_x(u0);
+
+  // where the keys and values go; nowhere for a negative or too large slot
+  int64_t page = -1;
+  int off = 0;
+  if (KV) {
+    const int64_t slot = a.slots[t];
+    if (slot >= 0 && slot < (a.cache.num_pages << a.cache.page_shift)) {
+      page = slot >> a.cache.page_shift;
+      off = (int)(slot & ((1 << a.cache.page_shift) - 1));
+    }
+  }
+  const int ku0 = max(u0, xu), kl = threadIdx.x % KLANES;
+  uint4 next[2];
+  auto kv_row = [&](int u) { return (u - xu) * KGROUPS + (int)threadIdx.x / KLANES; };  // a key head, or kv_heads + a value head
+  auto kv_src = [&](int r) {
+    const bool isk = r < a.kv_heads;
+    const HeadsView& src = isk ? a.k : a.v;
+    return static_cast<const uint16_t*>(src.data) + t * src.token_stride + (int64_t)(isk ? r : r - a.kv_heads) * src.head_stride;
+  };
+  auto load_kv = [&](int u) {
+    const int r = kv_row(u);
+    next[0] = next[1] = make_uint4(0u, 0u, 0u, 0u);
+    if (u >= u1 || r >= 2 * a.kv_heads) return;
+    const uint16_t* src = kv_src(r);
+    next[0] = *reinterpret_cast<const uint4*>(src + 8 * kl);
+    next[1] = *reinterpret_cast<const uint4*>(src + D / 2 + 8 * kl);
+  };
+  if (KV) load_kv(ku0);
+
+  auto weight = [&](const HeadNorm& n, int d) {
+    if (n.weight == nullptr || n.head_stride != 0) return 1.0f;
+    const uint32_t w = n.weight[d];
+    return BF16 ? __uint_as_float(w << 16) : __half2float(__ushort_as_half((unsigned short)w));
+  };
+  if ((int)threadIdx.x < D / 2) {
+    const int i = threadIdx.x;
+    float c = 1.0f, s = 0.0f;
+    int d0 = i, d1 = i + D / 2;  // without a rotation: any two places
+    if (i < half) {
+      int64_t at = t;
+      if (a.rope.axes != nullptr) at += min((int)a.rope.axes[i], a.rope.num_axes - 1) * a.tokens;
+      const uint64_t turned = (uint64_t)(int64_t)a.rope.positions[at] * a.rope.phases[i];
+      sincospif((float)(int32_t)(turned >> 32) * 4.656612873077393e-10f, &s, &c);  // in half turns: times 2^-31
+      c *= a.rope.amplitude, s *= a.rope.amplitude;
+      d0 = PAIRS ? 2 * i : i, d1 = PAIRS ? 2 * i + 1 : i + half;
+    } else if (half > 0) {
+      d0 = 2 * i, d1 = 2 * i + 1;  // places from 2 half on, two a thread
+    }
+    const float w0 = weight(a.x_norm, d0), w1 = weight(a.x_norm, d1);
+    xp[d0] = c * w0, xp[d1] = c * w1, xr[d0] = -s * w1, xr[d1] = s * w0;
+    if (KV) {
+      const float v0 = weight(a.k_norm, d0), v1 = weight(a.k_norm, d1);
+      kp[d0] = c * v0, kp[d1] = c * v1, kr[d0] = -s * v1, kr[d1] = s * v0;
+    }
+  }
+  __syncthreads();
+
+  if (u0 < xu) {
+    float2 p[4], r4[4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      p[j] = *reinterpret_cast<const float2*>(xp + at0 + 2 * j), p[2 + j] = *reinterpret_cast<const float2*>(xp + at1 + 2 * j);
+      r4[j] = *reinterpret_cast<const float2*>(xr + at0 + 2 * j), r4[2 + j] = *reinterpret_cast<const float2*>(xr + at1 + 2 * j);
+    }
+    uint16_t* out = static_cast<uint16_t*>(a.out) + t * a.out_token_stride;
+    for (int u = u0; u < min(xu, u1); u += kNormBatch) {
+      float2 v[kNormBatch][4];
+      float inv[kNormBatch];
+#pragma unroll
+      for (int i = 0; i < kNormBatch; ++i) unpack8(raw[i], BF16, v[i]);
+      if (u + kNormBatch < min(xu, u1)) load_x(u + kNormBatch);
+      if (xnorm) {
+        // the rows' sums side by side: each is a chain of shuffles
+#pragma unroll
+        for (int i = 0; i < kNormBatch; ++i) inv[i] = square_sum(v[i]);
+#pragma unroll
+        for (int st = 1; st < LANES; st *= 2)
+#pragma unroll
+          for (int i = 0; i < kNormBatch; ++i) inv[i] += __shfl_xor_sync(0xffffffffu, inv[i], st);
+#pragma unroll
+        for (int i = 0; i < kNormBatch; ++i) inv[i] = rsqrtf(fmaf(inv[i], 1.0f / D, a.x_norm.eps));
+      }
+#pragma unroll
+      for (int i = 0; i < kNormBatch; ++i) {
+        const int r = (u + i) * GROUPS + group;
+        if (u + i >= min(xu, u1) || r >= a.x_heads) continue;
+        if (xeach) {
+          float2 w[4];
+          unpack8(load8(a.x_norm.weight + r * a.x_norm.head_stride), BF16, w);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[i][j] = mul2(v[i][j], w[j]);
+        }
+        float2 y[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          // the pair's value: the neighbour, or in the other half of the lane's values
+          const float2 o = PAIRS ? make_float2(v[i][j].y, v[i][j].x) : v[i][j ^ 2];
+          y[j] = fma2(v[i][j], p[j], mul2(o, r4[j]));
+          if (xnorm) y[j] = mul2(y[j], twice(inv[i]));
+        }
+        const uint4 w = pack8(y, BF16);
+        uint16_t* dst = out + (int64_t)r * a.out_head_stride;
+        *reinterpret_cast<uint2*>(dst + at0) = make_uint2(w.x, w.y);
+        *reinterpret_cast<uint2*>(dst + at1) = make_uint2(w.z, w.w);
+      }
+    }
+  }
+  if constexpr (KV) {
+    if (page < 0) return;  // alike in the whole block
+
+    for (int u = ku0; u < u1; ++u) {
+      uint4 w[2] = {next[0], next[1]};
+      load_kv(u + 1);
+      const int r = kv_row(u);
+      const bool there = r < 2 * a.kv_heads, isk = r < a.kv_heads;
+      if (isk && (knorm || half > 0)) {
+        float2 v[8];
+        unpack8(w[0], BF16, v);
+        unpack8(w[1], BF16, v + 4);
+        float inv = 1.0f;
+        if (knorm) inv = rsqrtf(fmaf(row_sum<KLANES>(square_sum(v)), 1.0f / D, a.k_norm.eps));
+        const uint16_t* weights = a.k_norm.weight + r * a.k_norm.head_stride;
+        auto times = [&](float2* x, int ch) {
+          if (!keach) return;
+          float2 f[4];
+          unpack8(*reinterpret_cast<const uint4*>(weights + 8 * ch), BF16, f);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[j] = mul2(x[j], f[j]);
+        };
+        times(v, kl);
+        times(v + 4, kl + KLANES);
+        const int hl = half >> 3;  // chunks of one half
+        float2 y[8];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int ch = kl + KLANES * i;
+          float2 o[4];
+          if (PAIRS || ch >= 2 * hl) {  // (there R is 0)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[j] = make_float2(v[4 * i + j].y, v[4 * i + j].x);
+          } else if (hl == KLANES) {  // the whole row turns: both values of each pair are this lane's
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[j] = v[(4 * i + j) ^ 4];
+          } else {  // read once more
+            const int other = ch >= hl ? ch - hl : ch + hl;
+            unpack8(*reinterpret_cast<const uint4*>(kv_src(r) + 8 * other), BF16, o);
+            times(o, other);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 p = *reinterpret_cast<const float2*>(kp + 8 * ch + 2 * j), q = *reinterpret_cast<const float2*>(kr + 8 * ch + 2 * j);
+            y[4 * i + j] = mul2(fma2(v[4 * i + j], p, mul2(o[j], q)), twice(inv));
+          }
+        }
+        w[0] = pack8(y, BF16);
+        w[1] = pack8(y + 4, BF16);
+      }
+      const int64_t row = there ? ((page * a.kv_heads + (isk ? r : r - a.kv_heads)) << a.cache.page_shift) + off : 0;
+      uint8_t* dst = isk ? a.cache.k : a.cache.v;
+      if (!kv_quantised(a.cache.format)) {
+        if (there) {
+          *reinterpret_cast<uint4*>(dst + row * (2 * D) + 16 * kl) = w[0];
+          *reinterpret_cast<uint4*>(dst + row * (2 * D) + D + 16 * kl) = w[1];
+        }
+      } else {
+        float2 v[8];
+        unpack8(w[0], BF16, v);  // the row as its type holds it is what gets quantised
+        unpack8(w[1], BF16, v + 4);
         quantise_row<D>(v, kl, a.cache.format == kKvInt8, dst, isk ? a.cache.k_scale : a.cache.v_scale, row, there);
       }
     }
@@ -590,12 +732,19 @@ cudaError_t launch_rope_write(const RopeWriteArgs& a, int head_dim, cudaStream_t
   const dim3 grid((unsigned)a.tokens, (unsigned)((units + per - 1) / per));
   const bool norm = a.x_norm.weight != nullptr || a.k_norm.weight != nullptr, kv = a.kv_heads > 0;
   using Kernel = void (*)(const RopeWriteArgs, int);
-  static constexpr Kernel kernels[2][2][2] = {
-      {{rope_write_kernel<64, false, false>, rope_write_kernel<64, false, true>},
-       {rope_write_kernel<64, true, false>, rope_write_kernel<64, true, true>}},
-      {{rope_write_kernel<128, false, false>, rope_write_kernel<128, false, true>},
-       {rope_write_kernel<128, true, false>, rope_write_kernel<128, true, true>}}};
-  const Kernel kernel = kernels[head_dim == 128][kv][norm];
+  static constexpr Kernel plain[2][2] = {{rope_write_kernel<64, false>, rope_write_kernel<64, true>},
+                                         {rope_write_kernel<128, false>, rope_write_kernel<128, true>}};
+  static constexpr Kernel normed[2][2][2][2] = {
+      {{{norm_write_kernel<64, false, false, false>, norm_write_kernel<64, false, false, true>},
+        {norm_write_kernel<64, false, true, false>, norm_write_kernel<64, false, true, true>}},
+       {{norm_write_kernel<64, true, false, false>, norm_write_kernel<64, true, false, true>},
+        {norm_write_kernel<64, true, true, false>, norm_write_kernel<64, true, true, true>}}},
+      {{{norm_write_kernel<128, false, false, false>, norm_write_kernel<128, false, false, true>},
+        {norm_write_kernel<128, false, true, false>, norm_write_kernel<128, false, true, true>}},
+       {{norm_write_kernel<128, true, false, false>, norm_write_kernel<128, true, false, true>},
+        {norm_write_kernel<128, true, true, false>, norm_write_kernel<128, true, true, true>}}}};
+  const int wide = head_dim == 128;
+  const Kernel kernel = norm ? normed[wide][kv][a.bf16 != 0][a.rope.interleaved != 0] : plain[wide][kv];
   kernel<<<grid, kRopeThreads, 0, stream>>>(a, per);
   return cudaGetLastError();
 }
