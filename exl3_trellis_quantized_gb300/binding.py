@@ -784,7 +784,8 @@ class KVTables:
                        free_count.data_ptr(), batch, width, page_size, free_pages.numel())
         spans = tuple((t.data_ptr(), t.data_ptr() + 4 * t.numel()) for t in (kv_lens, held, free_count))
         same = (block_table.data_ptr(), free_pages.data_ptr(), batch, width, page_size, free_pages.numel())
-        self.__dict__.update(parts, batch=batch, table_width=width, page_size=page_size, args=args, _spans=spans, _same=same)
+        self.__dict__.update(parts, batch=batch, table_width=width, page_size=page_size, args=args, _spans=spans, _same=same,
+                             _outs=tuple(at for at, _ in spans))
 
     def __setattr__(self, name, value):
         raise AttributeError(f"KVTables.{name} cannot be assigned: make a KVTables of the new tensors")
@@ -828,24 +829,30 @@ def kv_plan(tables: KVTables, new_lens: torch.Tensor, total: int, into: Optional
     into total, or pages into the table) is not granted: its state stays and its slots are -1; none after it gets
     pages that it waits for.  The four outputs are new tensors unless given.
     """
-    total, batch, device = int(total), tables.batch, tables.kv_lens.device
+    total, batch = int(total), tables.batch
+    device = tables.kv_lens.device
     _alike(new_lens, torch.int32, (batch,), "new_lens")
-    state = _new_state(tables, into)
-    outs = {}
-    for name, t, dtype, n in (("cu_q", cu_q, torch.int32, batch + 1), ("positions", positions, torch.int32, total),
-                              ("slots", slots, torch.int64, total), ("granted", granted, torch.bool, batch)):
-        if t is None:
-            t = torch.empty(max(0, n), dtype=dtype, device=device)
-        else:
-            _alike(t, dtype, (n,), name)
-            _apart(t, name, new_lens=new_lens, **_state_parts(tables, state), **outs)
-        outs[name] = t
-    _one_device(tables.kv_lens, new_lens, state.kv_lens, *outs.values())
-    st = lib().exl3_kv_plan(tables.args, new_lens.data_ptr(), total, state.kv_lens.data_ptr(), state.held.data_ptr(),
-                            state.free_count.data_ptr(), *(t.data_ptr() for t in outs.values()),
-                            _raw_stream(device.index))
+    state = tables if into is None else _new_state(tables, into)
+    given = {"cu_q": cu_q, "positions": positions, "slots": slots, "granted": granted}
+    if any(t is not None for t in given.values()):
+        shapes = {"cu_q": (torch.int32, batch + 1), "positions": (torch.int32, total), "slots": (torch.int64, total),
+                  "granted": (torch.bool, batch)}
+        seen = dict(_state_parts(tables, state), new_lens=new_lens)
+        for name, t in given.items():
+            if t is not None:
+                _alike(t, shapes[name][0], (shapes[name][1],), name)
+                _apart(t, name, **seen)
+                seen[name] = t
+    rows = max(0, total)
+    cu_q = torch.empty(batch + 1, dtype=torch.int32, device=device) if cu_q is None else cu_q
+    positions = torch.empty(rows, dtype=torch.int32, device=device) if positions is None else positions
+    slots = torch.empty(rows, dtype=torch.int64, device=device) if slots is None else slots
+    granted = torch.empty(batch, dtype=torch.bool, device=device) if granted is None else granted
+    _one_device(tables.kv_lens, new_lens, state.kv_lens, cu_q, positions, slots, granted)
+    st = lib().exl3_kv_plan(tables.args, new_lens.data_ptr(), total, *state._outs, cu_q.data_ptr(), positions.data_ptr(),
+                            slots.data_ptr(), granted.data_ptr(), _raw_stream(device.index))
     _check(st, "exl3_kv_plan")
-    return tuple(outs.values())
+    return cu_q, positions, slots, granted
 
 
 def _state_parts(tables: KVTables, state: KVTables) -> dict:
@@ -867,8 +874,7 @@ def kv_release(tables: KVTables, ended: torch.Tensor, shared: Optional[torch.Ten
         _alike(shared, torch.int32, (tables.batch,), "shared")
     state = _new_state(tables, into)
     _one_device(tables.kv_lens, ended, shared, state.kv_lens)
-    st = lib().exl3_kv_release(tables.args, ended.data_ptr(), None if shared is None else shared.data_ptr(),
-                               state.kv_lens.data_ptr(), state.held.data_ptr(), state.free_count.data_ptr(),
+    st = lib().exl3_kv_release(tables.args, ended.data_ptr(), None if shared is None else shared.data_ptr(), *state._outs,
                                _raw_stream(tables.kv_lens.device.index))
     _check(st, "exl3_kv_release")
 
