@@ -67,16 +67,18 @@ __device__ __forceinline__ int64_t block_sums(int64_t v, int64_t* part, int64_t*
 //
 // Parts.  Each row tile's keys go to ceil(blocks / u) CTAs, u blocks of 64 keys at the most; u is the same for all, so
 // that long and short prefixes make items of about one length.  Of 32 sizes u (the longest prefix in 1 to 32) the one
-// that a model of the time likes best.  An item takes `block` us a block (half of it where its rows fill one tile: its
-// halves take blocks in turn) and 5 us.
-//   With the token kernel, own keys take `unit` us a unit and SM.  Up to 120 items leave SMs for it, so both run at the
-// same time and the longer counts; else one follows the other.
+// that a model of the time likes best.  An item takes `block` us a block (`joint` where its rows fill one tile, whose
+// halves take blocks in turn) and `fixed` us.
+//   With the token kernel, own keys take `unit` us a unit and SM, and all of them at least their bytes at what DRAM
+// gives.  Up to 128 items leave SMs for it, so both run at the same time and the longer counts; else one follows the
+// other.  64 sequences of 1 to 2000 own keys behind 8192 shared ones, 32 and 8 heads of 128, 16 bits: 85, 70, 70, 71, 76,
+// 81 and (one after the other) 80 us with the prefix in 2, 3, 5, 6, 8, 12 and 16 parts.
 //   Without, up to 152 items the longest counts; more are taken up in turn: all of them by 152, and 0.7 of the last.
 // And every item's rows are written and joined, at 4 TB/s.
 constexpr int kPrepThreads = 256;
-constexpr int kSms = 152, kMostBeside = 120;
+constexpr int kSms = 152, kMostBeside = 128;
 struct SharedCosts {
-  float block, unit;  // us
+  float block, joint, fixed, unit, unit_dram;  // us
   int token, per_sm;  // the token kernel takes the own keys, so many CTAs an SM
 };
 __global__ void __launch_bounds__(kPrepThreads) shared_prep_kernel(const AttnArgs a, const int32_t* cu_groups,
@@ -135,14 +137,15 @@ __global__ void __launch_bounds__(kPrepThreads) shared_prep_kernel(const AttnArg
     for (int g = 0; g < a.groups; ++g) {
       const int2 n = sizes(g);
       if (n.x == 0) continue;
-      const float tiles = (float)((n.y + per - 1) / per * a.kv_heads), block = n.y <= a.tile_tokens ? 0.5f * cost.block : cost.block;
+      const float tiles = (float)((n.y + per - 1) / per * a.kv_heads), block = n.y <= a.tile_tokens ? cost.joint : cost.block;
       items += tiles * (float)((n.x + u - 1) / u);
-      us += tiles * ((float)n.x * block + (float)((n.x + u - 1) / u) * 5.0f);
-      one = fmaxf(one, (float)min(n.x, u) * block + 5.0f);
+      us += tiles * ((float)n.x * block + (float)((n.x + u - 1) / u) * cost.fixed);
+      one = fmaxf(one, (float)min(n.x, u) * block + cost.fixed);
     }
     const float sms = (float)kSms, all = items <= sms ? one : us / sms + 0.7f * one;
-    const float own = (float)units * a.kv_heads * cost.unit;
-    us = cost.token && items <= (float)kMostBeside ? fmaxf(one, own / (sms - items) + 4.0f) : all + own / sms;
+    const float n = (float)units * a.kv_heads, beside = items <= (float)kMostBeside ? sms - items : sms;
+    const float own = cost.token ? fmaxf(n * cost.unit / beside, n * cost.unit_dram) : 0.0f;
+    us = cost.token && items <= (float)kMostBeside ? fmaxf(one, own) : all + own;
     us += items * (float)(kPrefixRows * a.head_dim) * 8.0f / 4.0e6f;
     if (items > (float)a.prefix_ctas) us = __builtin_huge_valf();  // (the first size has an item a row tile: always room)
     float best = us;
@@ -237,10 +240,12 @@ __device__ __forceinline__ void finish_row(const AttnArgs& a, const Sum& s, int6
   *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The part of row (tok, head) in the first of its prefix items; the next parts lie kPrefixRows rows on.
-__device__ __forceinline__ int64_t prefix_row(const AttnArgs& a, const SharedGroup& g, int tok, int h, int head, int group) {
+// The part of row (tok, head) in the first of its prefix items.  The next item's lies kPrefixRows rows on; where the
+// item's rows fill one tile (twice: it has halves with a part each) half of that.
+__device__ __forceinline__ int64_t prefix_row(const AttnArgs& a, const SharedGroup& g, int tok, int h, int head, int group, bool* twice) {
   const int per = 2 * a.tile_tokens, t = tok - g.q0, tiles = (g.tokens + per - 1) / per, tile = t / per;
   const int64_t item = g.item + ((int64_t)(tiles - 1 - tile) * a.kv_heads + h) * g.parts;  // last tiles come first
+  *twice = g.tokens - tile * per <= a.tile_tokens;
   return item * kPrefixRows + (t - tile * per) * group + head;
 }
 __device__ __forceinline__ SharedGroup load_group(const SharedGroup* g) {
@@ -252,6 +257,7 @@ template <bool TOKEN>
 struct Parts {
   int64_t row, prefix0;  // the row of [total_q][heads]; its place in the first of its prefix items
   int shared, own;       // parts of the prefix, parts of its own keys
+  int step;              // rows from one part of the prefix to the next
   int64_t c0, total, first;
   int ctas, r;
   // Of row (tok, head); false where there are none.
@@ -259,12 +265,14 @@ struct Parts {
     const int group = a.heads / a.kv_heads, h = head / group;
     row = (int64_t)tok * a.heads + head;
     const int g = __ldcg(&a.seq[b].y);
-    shared = 0;
+    shared = step = 0;
     prefix0 = 0;
     if (g >= 0) {
       const SharedGroup sg = load_group(a.group + g);
-      shared = sg.parts;
-      prefix0 = prefix_row(a, sg, tok, h, head - h * group, group);
+      bool twice;
+      prefix0 = prefix_row(a, sg, tok, h, head - h * group, group, &twice);
+      shared = twice ? 2 * sg.parts : sg.parts;
+      step = twice ? kPrefixRows / 2 : kPrefixRows;
     }
     own = a.splits;
     if constexpr (TOKEN) {
@@ -286,7 +294,7 @@ struct Parts {
     const float2* l = a.own_ml;
     int64_t n = (i - shared) * a.total_q * a.heads + row;
     if (i < shared) {
-      o = a.prefix_o, l = a.prefix_ml, n = prefix0 + (int64_t)i * kPrefixRows;
+      o = a.prefix_o, l = a.prefix_ml, n = prefix0 + (int64_t)i * step;
     } else if (TOKEN && own > 1) {
       const int64_t c = c0 + i - shared, begin = total * c / ctas;
       if (begin >= total * (c + 1) / ctas) return nullptr;
@@ -389,11 +397,16 @@ cudaError_t launch_shared_prep(const AttnArgs& a, const int32_t* cu_groups, cons
                                cudaStream_t stream) {
   const SharedState s = {const_cast<SharedGroup*>(a.group), const_cast<int2*>(a.seq), const_cast<int64_t*>(a.units),
                          const_cast<int2*>(a.counts)};
-  // a unit's rows of keys and values at 37 GB/s an SM (4 bits: 15)
-  const bool int4 = a.cache.format == kKvInt4;
-  const float unit = (float)(128 * kv_row_bytes(a.cache.format, a.head_dim)) * (int4 ? 1e-3f / 15.0f : 1e-3f / 37.0f);
-  const float block = (kv_quantised(a.cache.format) ? 1.2f : 0.85f) * (float)a.head_dim / 128.0f;
-  const SharedCosts cost = {block, unit, token ? 1 : 0, token_ctas_per_sm(a.max_q * (a.heads / a.kv_heads))};
+  const bool quant = kv_quantised(a.cache.format), few = a.max_q * (a.heads / a.kv_heads) <= 8;
+  const float wide = (float)a.head_dim / 128.0f;
+  SharedCosts cost = {};
+  cost.block = (quant ? 1.3f : 1.05f) * wide;
+  cost.joint = 0.72f * wide;
+  cost.fixed = quant ? 18.0f : 11.0f;
+  cost.unit = (few ? 0.6f : 0.7f) * wide;
+  cost.unit_dram = (float)(128 * kv_row_bytes(a.cache.format, a.head_dim)) / 5.3e6f;
+  cost.token = token ? 1 : 0;
+  cost.per_sm = token_ctas_per_sm(a.max_q * (a.heads / a.kv_heads));
   shared_prep_kernel<<<1, kPrepThreads, 0, stream>>>(a, cu_groups, prefix_lens, s, cost);
   return cudaGetLastError();
 }

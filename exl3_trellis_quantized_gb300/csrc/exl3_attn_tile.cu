@@ -330,8 +330,16 @@ struct Item {
   float2* part_ml;
   int64_t part_row;
   int part_stride;
+  int merge;  // the halves of a joint item meet in shared memory; else each leaves a part of its own
 #endif
 };
+__device__ __forceinline__ bool merges(const Item& it) {
+#ifdef EXL3_ATTN_SHARED
+  return it.merge != 0;
+#else
+  return it.joint != 0;
+#endif
+}
 
 // Whether value rows of key tile j must be made zeros: a weight of zero does not hide what is not finite.
 __device__ __forceinline__ bool mend_values(int j, int tail, int lead) { return j == tail || (j == 0 && lead > 0); }
@@ -356,70 +364,56 @@ __device__ bool find_item(const AttnArgs& a, int lane, int64_t idx, Item* it) {
   const int prefix_items = __ldcg(&a.counts->x);
   const bool prefix = idx < prefix_items;
   if (!prefix && a.splits == 0) return false;  // own keys go through the token kernel
-  const int64_t item = idx;
-  const int lists = prefix ? a.groups : a.batch;
-  if (!prefix) idx -= prefix_items;
-  // in items of a prefix's group; of own keys, whose parts are the same for all: in tiles
-  int split = 0;
-  if (!prefix) {
-    split = (int)(idx % a.splits);
-    idx /= a.splits;
-    it->kvh = (int)(idx % a.kv_heads);
-    idx /= a.kv_heads;
-  }
-  int64_t base = 0;
+  // Items come in lists, one a group or (own keys) a sequence: of each its row tiles, of each its key heads, of each its
+  // parts.  In 32 bits: a grid has no more.
+  int place = prefix ? (int)idx : (int)idx - prefix_items, base = 0;
+  const int lists = prefix ? a.groups : a.batch, total = (int)a.total_q;
+#pragma unroll 1
   for (int b0 = 0; b0 < lists; b0 += 32) {
     const int b = b0 + lane;
-    int64_t c0 = 0, n = 0;
-    int keys = 0, seq = b, parts = 1;
+    int c0 = 0, n = 0, keys = 0, seq = b, parts = a.splits;
     if (b < lists) {
       if (prefix) {
         const SharedGroup* g = a.group + b;
         c0 = __ldcg(&g->q0), n = __ldcg(&g->tokens), keys = __ldcg(&g->keys), seq = __ldcg(&g->lead), parts = __ldcg(&g->parts);
+        if (keys == 0) n = 0;
       } else {
-        c0 = a.cu_q[b];
-        c0 = c0 < 0 ? 0 : c0 > a.total_q ? a.total_q : c0;
-        const int64_t c1 = a.cu_q[b + 1] > a.total_q ? a.total_q : a.cu_q[b + 1];
-        n = c1 > c0 ? c1 - c0 : 0;
-        const int64_t room = (int64_t)a.table_width << a.cache.page_shift;
-        const int64_t kl = a.kv_lens[b];
-        keys = (int)(kl < 0 ? 0 : kl > room ? room : kl);
+        c0 = max(0, min(a.cu_q[b], total));
+        n = max(0, min(a.cu_q[b + 1], total) - c0);
+        keys = max(0, min(a.kv_lens[b], a.table_width << a.cache.page_shift));
       }
     }
-    const int tiles = prefix && keys == 0 ? 0 : ((int)n + per - 1) / per;
-    const int64_t here = prefix ? (int64_t)tiles * a.kv_heads * parts : tiles;
-    int64_t inc = here;
+    const int tiles = (n + per - 1) / per, here = tiles * a.kv_heads * parts;
+    int inc = here;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t p = __shfl_up_sync(0xffffffffu, inc, o);
+      const int p = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += p;
     }
-    const uint32_t hit = __ballot_sync(0xffffffffu, base + inc > idx);
+    const uint32_t hit = __ballot_sync(0xffffffffu, base + inc > place);
     if (hit) {
       const int at = __ffs(hit) - 1;
-      int64_t place = idx - base - __shfl_sync(0xffffffffu, inc - here, at);
-      const int count = __shfl_sync(0xffffffffu, tiles, at);
-      const int splits = prefix ? __shfl_sync(0xffffffffu, parts, at) : a.splits;
-      if (prefix) {
-        split = (int)(place % splits);
-        place /= splits;
-        it->kvh = (int)(place % a.kv_heads);
-        place /= a.kv_heads;
-      }
-      const int q_len = (int)__shfl_sync(0xffffffffu, n, at);
-      it->q0 = __shfl_sync(0xffffffffu, c0, at);
+      place -= base + __shfl_sync(0xffffffffu, inc - here, at);
+      const int count = __shfl_sync(0xffffffffu, tiles, at), splits = __shfl_sync(0xffffffffu, parts, at);
+      const int q_len = __shfl_sync(0xffffffffu, n, at);
+      const int q0 = __shfl_sync(0xffffffffu, c0, at);
+      it->q0 = q0;
       it->b = __shfl_sync(0xffffffffu, seq, at);
       it->kv_len = __shfl_sync(0xffffffffu, keys, at);
-      it->tok0 = (count - 1 - (int)place) * per;
+      const int split = place % splits;
+      place /= splits;
+      it->kvh = place % a.kv_heads;
+      it->tok0 = (count - 1 - place / a.kv_heads) * per;
       it->toks = min(per, q_len - it->tok0);
       it->split = split;
       it->part_o = prefix ? a.prefix_o : a.own_o;
       it->part_ml = prefix ? a.prefix_ml : a.own_ml;
       it->part_stride = prefix ? group : a.heads;
-      it->part_row = prefix ? item * kPrefixRows - (int64_t)it->tok0 * group : (split * a.total_q + it->q0) * a.heads + it->kvh * group;
+      it->part_row = prefix ? idx * kPrefixRows - it->tok0 * group : (split * a.total_q + q0) * a.heads + it->kvh * group;
       // every query of a group sees all of the prefix: as if it stood behind it
       it->first = prefix ? it->kv_len - 1 : it->kv_len - q_len;
       it->joint = it->toks <= a.tile_tokens;
+      it->merge = it->joint && !prefix;
       // whole tiles of keys, so that no page is cut by a tile's first key
       const int lo = prefix ? 0 : __ldcg(&a.seq[it->b].x);
       const int p1 = min(it->first + it->tok0 + it->toks, it->kv_len) - 1;
@@ -427,8 +421,9 @@ __device__ bool find_item(const AttnArgs& a, int lane, int64_t idx, Item* it) {
       it->lead = 0;
       const int blocks = p1 >= lo ? (p1 - lo) / kBlock + 1 : 0;
       // in whole tiles of two blocks, so that none is copied twice
-      const int64_t pairs = (blocks + 1) >> 1;
-      const int n0 = 2 * (int)(pairs * split / splits), n1 = min(blocks, 2 * (int)(pairs * (split + 1) / splits));
+      // (2^24 pairs at the most, and 32 parts: below 2^31)
+      const int pairs = (blocks + 1) >> 1;
+      const int n0 = 2 * (pairs * split / splits), n1 = min(blocks, 2 * (pairs * (split + 1) / splits));
       it->span[0] = half_span(a, *it, n0, n1, 0);
       it->span[1] = half_span(a, *it, n0, n1, 1);
       const Span s0 = it->span[0], s1 = it->span[1];
@@ -625,8 +620,73 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
     const uint32_t o_col = tmem + lanes + 256 + 128 * i;
     float c = a.scale_log2;  // quantised: times the unit of q's row, and a group's times the unit of its keys
     uint32_t tiles = 0;      // quantised: key tiles of the items before
+#ifdef EXL3_ATTN_SHARED
+    // Rotate the half's q where the copy has put it: four lanes a row, chunk 4 x + l of eight values the x-th of lane l, and
+    // only rows that there are.  (A thread a row is 1400 instructions in a line, which an item that runs once has to fetch
+    // first; sixteen lanes a row have more than twice the shuffles.)
+    auto rotate_q = [&](const Item& x, uint32_t parity) {
+      if (!bar_wait(&qraw[i], parity)) return false;
+      constexpr int N = D / 4, RP = 8;  // values a lane; rows a warp takes at a time
+      const uint32_t at = smem_u32(data + C::kQ) + (uint32_t)i * (kTileRows * D * 2);
+      const int l = lane & 3, rows = min(a.tile_tokens, x.toks - (x.joint ? 0 : i * a.tile_tokens)) * group;
+#pragma unroll 1
+      for (int p = 0; p < 32 / RP; ++p) {
+        const int first = 32 * (warp & 3) + p * RP;
+        if (first >= rows) break;
+        float v[N];
+#pragma unroll
+        for (int y = 0; y < N / 8; ++y) {
+          uint32_t w[4];
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                       : "r"(at + row_chunk(first + (lane >> 2), 4 * y + l))
+                       : "memory");
+          if (a.bf16) {
+#pragma unroll
+            for (int z = 0; z < 4; ++z) v[8 * y + 2 * z] = __uint_as_float(w[z] << 16), v[8 * y + 2 * z + 1] = __uint_as_float(w[z] & 0xFFFF0000u);
+          } else {
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[z]));
+              v[8 * y + 2 * z] = f.x, v[8 * y + 2 * z + 1] = f.y;
+            }
+          }
+        }
+        hadamard_row<N>(v);  // every bit of the place in a chunk and of the lane's chunk
+#pragma unroll
+        for (int st = 1; st < 4; st *= 2)
+#pragma unroll
+          for (int y = 0; y < N; ++y) {
+            const float o = __shfl_xor_sync(0xffffffffu, v[y], st);
+            v[y] = (l & st) ? o - v[y] : v[y] + o;
+          }
+        float top = 0.0f;
+#pragma unroll
+        for (int y = 0; y < N; ++y) top = fmaxf(top, fabsf(v[y]));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // in units of a power of two near its largest value, so that fp16 holds rows of any size alike
+        const uint32_t e = unit_exponent(top);
+        const float unit = __shfl_sync(0xffffffffu, power(e), 4 * (lane % RP));
+        if (lane / RP == p) c = a.scale_log2 * (unit * (8.0f / D));  // this thread's row
+        const float f = power(254 - e);
+#pragma unroll
+        for (int y = 0; y < N / 8; ++y) {
+          uint32_t w[4];
+#pragma unroll
+          for (int z = 0; z < 4; ++z)
+            w[z] = pack2<false>(v[8 * y + column_value<SRC>(2 * z)] * f, v[8 * y + column_value<SRC>(2 * z + 1)] * f);
+          sts128(at + row_chunk(first + (lane >> 2), 4 * y + l), w[0], w[1], w[2], w[3]);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&qfull[i]);
+      return true;
+    };
+#else
     // Rotate the half's q where the copy has put it, a thread a row.
-    auto rotate_q = [&](uint32_t parity) {
+    auto rotate_q = [&](const Item&, uint32_t parity) {
       if (!bar_wait(&qraw[i], parity)) return false;
       const uint32_t at = smem_u32(data + C::kQ) + (uint32_t)i * (kTileRows * D * 2);
       float v[D];
@@ -670,6 +730,7 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
       if (lane == 0) mbar_arrive(&qfull[i]);
       return true;
     };
+#endif
     auto used = [&](const Item& x) { return i ? x.span[1].b0 < x.span[1].b1 : x.span[0].b0 < x.span[0].b1; };
 
     Item it;
@@ -681,7 +742,7 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
     // this thread's row: query token (from the half's first) and head (of the group); none past the tile's whole tokens
     const int row_tok = r / group, row_head = r - row_tok * group;
     if (C::kQuant && have && used(it)) {
-      have = rotate_q(qph);
+      have = rotate_q(it, qph);
       qph ^= 1u;
     }
     while (have) {
@@ -822,7 +883,8 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
       // A joint item's meeting place is q's room, of both halves: half 1 may write there once half 0's products of this
       // item and of those before it are done.  (A look at half 0's ofull cannot tell: half 0 may be an item behind,
       // whose phase of that barrier has the other parity, or have no blocks here.)
-      if (it.joint) {
+      const bool merge = merges(it);
+      if (merge) {
         if (i == 0) {
           __syncwarp();
           if (lane == 0) mbar_arrive(jopen);
@@ -833,7 +895,7 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
       tc_fence_after();
       // this thread's row: its own part times f0, a joint item's other half's (already divided by its sum) times f1
       float f0 = 1.0f, f1 = 0.0f;
-      if (ok && it.joint && i == 0) {
+      if (ok && merge && i == 0) {
         ok = bar_wait(jfull, jphase);
         const float other = jlse[r];
         const float both = fmaxf(m, other);
@@ -843,16 +905,18 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
         l = l * f0 + f1;
         m = both;
       }
-      const bool partial = (kShared || a.splits > 1) && !(it.joint && i == 1);
+      const bool partial = (kShared || a.splits > 1) && !(merge && i == 1);
       if (!partial) {
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // a row that saw no key gives zeros
         f0 *= inv, f1 *= inv;
       }
       if (!any) f0 = 0.0f;
       float* jo = reinterpret_cast<float*>(data + C::kQ) + r;  // [D][128]: a thread a column
-      if (ok && it.joint && i == 1) jlse[r] = m + log2f(l);
+      if (ok && merge && i == 1) jlse[r] = m + log2f(l);
 #ifdef EXL3_ATTN_SHARED
-      if (ok && partial && there) it.part_ml[it.part_row + (int64_t)tok * it.part_stride + row_head] = make_float2(m, l);
+      // half 1 of a joint item that does not meet half 0: its part lies a tile's rows on
+      const int64_t part_row = it.part_row + (i == 1 && it.joint && !merge ? kTileRows : 0);
+      if (ok && partial && there) it.part_ml[part_row + (int64_t)tok * it.part_stride + row_head] = make_float2(m, l);
 #else
       const int64_t row = (it.q0 + tok) * a.heads + it.kvh * group + row_head;
       if (ok && partial && there) a.part_ml[(int64_t)it.split * a.total_q * a.heads + row] = make_float2(m, l);
@@ -903,7 +967,7 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
           const bool rthere = __shfl_sync(0xffffffffu, (int)there, src) != 0;
 #pragma unroll
           for (int x = 2 * e; x < D / 2; x += 4) o[x] *= s0, o[x + 1] *= s0;
-          if (it.joint) {
+          if (merge) {
             float* at = jo + h * (D / 2) * kTileRows;
             if (i == 1) {
 #pragma unroll
@@ -918,7 +982,7 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
           }
           if (partial) {
 #ifdef EXL3_ATTN_SHARED
-            float* dst = it.part_o + (it.part_row + (int64_t)rtok * it.part_stride + rhead) * D;
+            float* dst = it.part_o + (part_row + (int64_t)rtok * it.part_stride + rhead) * D;
 #else
             float* dst = a.part_o + (((int64_t)it.split * a.total_q + it.q0 + rtok) * a.heads + it.kvh * group + rhead) * D;
 #endif
@@ -974,7 +1038,7 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
           }
         }
       }
-      if (it.joint) {
+      if (merge) {
         fence_proxy_async_smem();  // the next q is copied over what was written and read here
         __syncwarp();
         if (lane == 0) mbar_arrive(i ? jfull : jfree);
@@ -983,7 +1047,7 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
       }
       tc_fence_before();
       if (C::kQuant && ok && have && used(next)) {
-        ok = rotate_q(qph);
+        ok = rotate_q(next, qph);
         qph ^= 1u;
       }
       have = have && ok;
@@ -1150,41 +1214,43 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
           __syncwarp();
           ++n;
 #ifdef EXL3_ATTN_SHARED
-          // Cache rows of the next two tiles' copies: their page ids come, and for codes their bytes are on the way into L2,
-          // while the tile before them is copied.  (The ring of codes holds two tiles' sides; without this the copies'
-          // latency was 2.8 us a tile of 128 keys.)
-          int64_t rows_ahead[2];
-          auto look = [&](int j) -> int64_t {  // -1: no page of the cache
-            const int key = it.base + j * kKeys + lane * page_rows;
-            if (j >= it.jhi || lane * page_rows >= kKeys || key >= it.kv_len) return -1;
-            const int id = a.table[(int64_t)it.b * a.table_width + (key >> a.cache.page_shift)];
-            if (id < 0 || id >= a.cache.num_pages) return -1;
-            const int64_t row = (((int64_t)id * a.kv_heads + it.kvh) << a.cache.page_shift) + (key & ((1 << a.cache.page_shift) - 1));
-            if constexpr (C::kQuant) {
-              prefetch_l2(a.cache.k + row * C::kRowBytes, (uint32_t)(page_rows * C::kRowBytes));
-              prefetch_l2(a.cache.v + row * C::kRowBytes, (uint32_t)(page_rows * C::kRowBytes));
-              prefetch_l2(a.cache.k_scale + row, (uint32_t)(page_rows * 2));
-              prefetch_l2(a.cache.v_scale + row, (uint32_t)(page_rows * 2));
+          // Cache rows of the next two tiles' copies: their page ids come, and for codes their bytes are on the way into L2
+          // (the ring of codes holds two tiles' sides), while the tile before them is copied.
+          int64_t ahead[2] = {-1, -1};
+#pragma unroll 1
+          for (int j = it.jlo - 2; ok && j < it.jhi; ++j) {
+            const int64_t here = ahead[0];
+            ahead[0] = ahead[1];
+            ahead[1] = -1;  // no page of the cache
+            const int key = it.base + (j + 2) * kKeys + lane * page_rows;
+            if (j + 2 < it.jhi && lane * page_rows < kKeys && key < it.kv_len) {
+              const int id = a.table[(int64_t)it.b * a.table_width + (key >> a.cache.page_shift)];
+              if (id >= 0 && id < a.cache.num_pages) {
+                const int64_t row = (((int64_t)id * a.kv_heads + it.kvh) << a.cache.page_shift) + (key & ((1 << a.cache.page_shift) - 1));
+                ahead[1] = row;
+                if constexpr (C::kQuant) {
+                  prefetch_l2(a.cache.k + row * C::kRowBytes, (uint32_t)(page_rows * C::kRowBytes));
+                  prefetch_l2(a.cache.v + row * C::kRowBytes, (uint32_t)(page_rows * C::kRowBytes));
+                  prefetch_l2(a.cache.k_scale + row, (uint32_t)(page_rows * 2));
+                  prefetch_l2(a.cache.v_scale + row, (uint32_t)(page_rows * 2));
+                }
+              }
             }
-            return row;
-          };
-          rows_ahead[0] = look(it.jlo), rows_ahead[1] = look(it.jlo + 1);
-#endif
+            if (j < it.jlo) continue;
+            const int t = it.base + j * kKeys;
+            const int copies = (min(kKeys, it.kv_len - t) + page_rows - 1) / page_rows;
+            bool page_ok = true;
+            int64_t row = here;  // cache row of this lane's copy
+            if (lane < copies) {
+              page_ok = here >= 0;
+              if (!page_ok) row = C::kQuant ? 0 : (a.cache.num_pages * a.kv_heads) << a.cache.page_shift;
+            }
+#else
           for (int j = it.jlo; ok && j < it.jhi; ++j) {
             const int t = it.base + j * kKeys;
             int64_t row = 0;  // cache row of this lane's copy (paged)
             int copies = 1;
             bool page_ok = true;
-#ifdef EXL3_ATTN_SHARED
-            copies = (min(kKeys, it.kv_len - t) + page_rows - 1) / page_rows;
-            row = rows_ahead[0];
-            rows_ahead[0] = rows_ahead[1];
-            rows_ahead[1] = look(j + 2);
-            if (lane < copies) {
-              page_ok = row >= 0;
-              if (!page_ok) row = C::kQuant ? 0 : (a.cache.num_pages * a.kv_heads) << a.cache.page_shift;
-            }
-#else
             if constexpr (SRC != kPacked) {
               copies = (min(kKeys, it.kv_len - t) + page_rows - 1) / page_rows;
               if (lane < copies) {
@@ -1296,14 +1362,14 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
       bool ok = true;
       Item it;
       uint32_t n = 0, eph = 3u, jph = 0, filled[2] = {0u, 0u};  // eph: phases of qempty (a bit a half); nothing to wait for at first
-      bool joint = false;                                       // the item before
+      bool joint = false;                                       // the item before: its halves met in q's room
       while (ok && read_item(n, &it)) {
         ++n;
         if (joint) {
           ok = bar_wait(jfree, jph);
           jph ^= 1u;
         }
-        joint = it.joint != 0;
+        joint = merges(it);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           if (!ok || it.span[i].b0 >= it.span[i].b1) continue;
