@@ -18,6 +18,7 @@ from .binding import (  # noqa: F401
     Exl3Error,
     KVCache,
     KVTables,
+    SHARE_ALWAYS,
     attention_paged,
     attention_paged_workspace_bytes,
     attention_prompt,

@@ -129,7 +129,7 @@ def lib() -> ctypes.CDLL:
                                      i64, i64, vp]
     L.exl3_kv_plan.argtypes = [tables, vp, i64] + [vp] * 8
     L.exl3_kv_release.argtypes = [tables] + [vp] * 6
-    L.exl3_attention_shared_workspace_bytes.argtypes = [i64] + [i32] * 8
+    L.exl3_attention_shared_workspace_bytes.argtypes = [i64] + [i32] * 5 + [ctypes.c_int] + [i32] * 3
     L.exl3_attention_shared_workspace_bytes.restype = sz
     L.exl3_attention_shared.argtypes = [heads, ctypes.c_int, i64, i32, cache, vp, i32, vp, vp, i32, vp, vp, i32, i32, i32,
                                         i32, f32, vp, i64, i64, vp, sz, vp]
@@ -833,8 +833,8 @@ def kv_plan(tables: KVTables, new_lens: torch.Tensor, total: int, into: Optional
     device = tables.kv_lens.device
     _alike(new_lens, torch.int32, (batch,), "new_lens")
     state = tables if into is None else _new_state(tables, into)
-    given = {"cu_q": cu_q, "positions": positions, "slots": slots, "granted": granted}
-    if any(t is not None for t in given.values()):
+    if not (cu_q is None and positions is None and slots is None and granted is None):
+        given = {"cu_q": cu_q, "positions": positions, "slots": slots, "granted": granted}
         shapes = {"cu_q": (torch.int32, batch + 1), "positions": (torch.int32, total), "slots": (torch.int64, total),
                   "granted": (torch.bool, batch)}
         seen = dict(_state_parts(tables, state), new_lens=new_lens)
@@ -956,14 +956,18 @@ def attention_paged(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, 
     return out
 
 
+SHARE_ALWAYS = 2**31 - 1  # EXL3_SHARE_ALWAYS in include/exl3.h
+
+
 @functools.lru_cache(maxsize=1024)
 def _shared_workspace_bytes(*sizes) -> int:
     return int(lib().exl3_attention_shared_workspace_bytes(*sizes))
 
 
-def attention_shared_workspace_bytes(total_q: int, batch: int, groups: int, heads: int, kv_heads: int, head_dim: int,
-                                     max_q: int, max_kv: int, max_prefix: int) -> int:
-    return _shared_workspace_bytes(total_q, batch, groups, heads, kv_heads, head_dim, max_q, max_kv, max_prefix)
+def attention_shared_workspace_bytes(total_q: int, batch: int, groups: int, heads: int, cache: KVCache, max_q: int,
+                                     max_kv: int, max_prefix: int) -> int:
+    return _shared_workspace_bytes(total_q, batch, groups, heads, cache.kv_heads, cache.head_dim, KV_FORMATS[cache.fmt],
+                                   max_q, max_kv, max_prefix)
 
 
 def attention_shared(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, cu_q: torch.Tensor,
@@ -974,7 +978,9 @@ def attention_shared(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor,
 
     Group g is the sequences cu_groups[g] .. cu_groups[g + 1] - 1 (int32 [groups + 1]; sequences outside are of no
     group), whose first prefix_lens[g] (int32 [groups]) keys and values are the same and are read through the table of
-    the first of them that has queries.  max_prefix: about the longest of the prefixes; below 256 nothing is shared.
+    the first of them that has queries.  max_prefix: about the longest of the prefixes, which steers whether they are
+    shared (for few sequences or short prefixes the call is attention_paged; SHARE_ALWAYS: they are) and how the work is
+    split.
     ``workspace``: uint8, at least attention_shared_workspace_bytes (allocated when not given).
     Other arguments as for attention_paged.
     """
@@ -1001,7 +1007,7 @@ def attention_shared(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor,
         _apart(out, "out", cache_k=cache.k, cache_v=cache.v, k_scale=cache.k_scale, v_scale=cache.v_scale)
     out, oh = _out_like(q, out, "out")
     if workspace is None:
-        need = _shared_workspace_bytes(total, batch, groups, heads, cache.kv_heads, d, int(max_q), int(max_kv), int(max_prefix))
+        need = attention_shared_workspace_bytes(total, batch, groups, heads, cache, int(max_q), int(max_kv), int(max_prefix))
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     else:
         _need(workspace, torch.uint8, "workspace")

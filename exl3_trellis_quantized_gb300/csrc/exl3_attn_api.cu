@@ -174,7 +174,7 @@ SharedPlan shared_plan(int64_t total_q, int64_t batch, int64_t groups, int64_t q
     p.ctas = own.ctas;
     cut = 2 * (int64_t)own.ctas * exl3::kTokenRows;
   } else {
-    const int64_t own = max_kv - max_prefix > max_q ? max_kv - max_prefix : max_q;
+    const int64_t rest = max_prefix == EXL3_SHARE_ALWAYS ? max_kv : max_kv - max_prefix, own = rest > max_q ? rest : max_q;
     p.splits = (int)item_parts(exl3::shared_tiles(total_q, batch, per) * kv_heads, own, rows * head_dim);
   }
   const int64_t own = p.token ? rows : p.splits * rows, prefix = (int64_t)p.prefix_ctas * exl3::kPrefixRows;
@@ -182,6 +182,32 @@ SharedPlan shared_plan(int64_t total_q, int64_t batch, int64_t groups, int64_t q
                              groups * (int64_t)sizeof(exl3::SharedGroup), batch * 8, p.token ? (batch + 1) * 8 : 0, 8};
   for (int i = 0; i < 10; ++i) p.at[i + 1] = p.at[i] + (size_t)((bytes[i] + 15) / 16 * 16);
   return p;
+}
+
+// Whether sharing pays: it has two more launches and the parts' join, 12 to 20 us in all.  What a paged call takes for the
+// same prefixes comes out of L2 after the first sequence.
+//   Few rows: 34 keys and key heads a ns (128 values, up to 8 rows).  32 and 8 heads of 128, single tokens, shared and
+// paged us: 8 sequences behind 8192 keys 26.1 and 25.6 (8 bits: 32.6 and 27.0), 16 behind 2048 25.8 and 18.5, 16 behind
+// 8192 28.5 and 41.3 (8 bits: 35.4 and 43.9), 48 behind 2048 25.6 and 44.2; with 16 heads a key head, 16 behind 2048 23.3
+// and 20.9, 16 behind 8192 27.2 and 35.6.
+//   Row tiles: a paged call gives every sequence tiles of its own, 0.43 us for 128 rows and 64 keys; shared, the rows of
+// a group fill them.  8 and 1 tokens of 32 rows: 4 sequences behind 8192 keys 28.7 and 27.1, 12 behind 1024 26.6 and
+// 18.1, 40 behind 1024 38.5 and 45.1, 12 behind 8192 37.5 and 67.1.  Long chunks fill theirs anyway and gain up to a
+// tenth (7 of 33 to 700 tokens behind 16000 4-bit keys 492 and 522) or lose as much where own keys weigh.
+bool worth_sharing(int64_t total_q, int64_t batch, int64_t groups, int64_t q_heads, int64_t kv_heads, int64_t head_dim, bool quant,
+                   int64_t max_q, int64_t max_kv, int64_t max_prefix) {
+  if (max_prefix == EXL3_SHARE_ALWAYS) return groups > 0;
+  if (groups == 0 || batch <= groups || max_prefix < exl3::kLeastPrefix) return false;
+  const int64_t group = q_heads / kv_heads;
+  const double keys = (double)max_prefix * kv_heads * (head_dim / 128.0);
+  if (max_q * group <= exl3::kTokenRows) {
+    const double least = max_q * group <= 8 ? (quant ? 600e3 : 400e3) : (quant ? 360e3 : 240e3);
+    return (double)(batch - groups) * keys >= least;
+  }
+  const int64_t rows = total_q * group / batch;  // of a sequence
+  const int64_t alone = batch * ((rows + 127) / 128), together = (total_q * group + 127) / 128 + groups;
+  if ((double)(alone - together) * keys / 64.0 * 0.43 / kSms >= 6.0) return true;
+  return rows >= 512 && max_prefix >= 8192 && max_prefix >= 8 * (max_kv - max_prefix);
 }
 
 // Checks of a paged call and what the kernels take of it, but for the split; an empty call is not filled in.
@@ -450,11 +476,11 @@ exl3_status_t exl3_attention_paged(const exl3_heads_t* q, exl3_dtype_t dtype, in
 }
 
 size_t exl3_attention_shared_workspace_bytes(int64_t total_q, int32_t batch, int32_t groups, int32_t q_heads,
-                                             int32_t kv_heads, int32_t head_dim, int32_t max_q, int32_t max_kv,
-                                             int32_t max_prefix) {
+                                             int32_t kv_heads, int32_t head_dim, exl3_kv_format_t format, int32_t max_q,
+                                             int32_t max_kv, int32_t max_prefix) {
   if (!valid_rows(total_q) || !valid_rows(batch) || !valid_rows(groups) || !valid_head_counts(q_heads, kv_heads)) return 0;
   if (check_head_dim(head_dim) != EXL3_OK || max_q < 1 || max_kv < 0 || max_prefix < 0 || total_q == 0 || batch == 0) return 0;
-  if (groups == 0 || max_prefix < exl3::kLeastPrefix)
+  if (!worth_sharing(total_q, batch, groups, q_heads, kv_heads, head_dim, exl3::kv_quantised(format), max_q, max_kv, max_prefix))
     return exl3_attention_paged_workspace_bytes(total_q, batch, q_heads, kv_heads, head_dim, max_q, max_kv, 0);
   return shared_plan(total_q, batch, groups, q_heads, kv_heads, head_dim, max_q, max_kv, max_prefix).at[10];
 }
@@ -467,13 +493,13 @@ exl3_status_t exl3_attention_shared(const exl3_heads_t* q, exl3_dtype_t dtype, i
                                     int64_t out_head_stride, void* workspace, size_t workspace_bytes, void* stream) {
   if (!valid_rows(groups) || max_prefix < 0) return EXL3_EINVAL;
   if (groups > 0 && total_q != 0 && batch != 0 && (!aligned4(cu_groups) || !aligned4(prefix_lens))) return EXL3_EINVAL;
-  if (groups == 0 || max_prefix < exl3::kLeastPrefix)
-    return exl3_attention_paged(q, dtype, total_q, q_heads, cache, block_table, table_width, cu_q, kv_lens, batch, max_q, max_kv, 0,
-                                scale, out, out_token_stride, out_head_stride, workspace, workspace_bytes, stream);
   exl3::AttnArgs a = {};
   const exl3_status_t st = paged_args(q, dtype, total_q, q_heads, cache, block_table, table_width, cu_q, kv_lens, batch, max_q, max_kv, 0,
                                       scale, out, out_token_stride, out_head_stride, &a);
   if (st != EXL3_OK || total_q == 0 || batch == 0) return st;
+  if (!worth_sharing(total_q, batch, groups, q_heads, a.kv_heads, a.head_dim, exl3::kv_quantised(a.cache.format), max_q, max_kv, max_prefix))
+    return exl3_attention_paged(q, dtype, total_q, q_heads, cache, block_table, table_width, cu_q, kv_lens, batch, max_q, max_kv, 0,
+                                scale, out, out_token_stride, out_head_stride, workspace, workspace_bytes, stream);
   const SharedPlan plan = shared_plan(total_q, batch, groups, q_heads, a.kv_heads, a.head_dim, max_q, max_kv, max_prefix);
   if (total_q * q_heads > INT32_MAX) return EXL3_EUNSUPPORTED;  // blocks of the join
   if (!aligned16(workspace)) return EXL3_EINVAL;

@@ -11,6 +11,7 @@ from oracle import attention_oracle as A
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
 DT = {"bf16": torch.bfloat16, "f16": torch.float16}
+SHARE = E.SHARE_ALWAYS
 FORMATS = [("bf16", "bf16"), ("f16", "f16"), ("int8", "bf16"), ("int8", "f16"), ("int4", "bf16"), ("int4", "f16")]
 
 
@@ -84,7 +85,7 @@ def shared(sizes, prefixes, q_lens, lens, heads, kv, dim, page, fmt, dtype, skip
     q = wide[:, :heads * dim].view(total, heads, dim)
     out = torch.full((total + 2, heads, dim), 3.0, dtype=DT[dtype], device=DEV)
     groups = i32(skip + np.concatenate([[0], np.cumsum(sizes)]))
-    max_prefix = max(prefixes) if max_prefix is None else max_prefix
+    max_prefix = SHARE if max_prefix is None else max_prefix
     args = (q, cache, table, cu(q_lens), i32(lens), groups, i32(prefixes), max(q_lens), max(lens), max_prefix)
     got = E.attention_shared(*args, scale=scale, out=out[:total])
     torch.cuda.synchronize()
@@ -144,7 +145,7 @@ def test_sequences_before_the_groups(q_len):
 
 
 @pytest.mark.parametrize("q_len", [1, 40])
-@pytest.mark.parametrize("max_prefix", [0, 255, 256, 700, 100000])
+@pytest.mark.parametrize("max_prefix", [0, 255, 700, 100000, 2**31 - 1])
 def test_the_hint_changes_no_more_than_the_order(q_len, max_prefix):
     shared([3], [900], [q_len] * 3, [980, 1000, 941], 8, 2, 128, 64, "int8", "bf16", max_prefix=max_prefix)
 
@@ -168,9 +169,11 @@ def test_no_group_is_the_paged_call():
     args, got = shared([2], [500], [1, 1], [600, 555], 8, 2, 128, 16, "bf16", "bf16")
     q, cache, table, cq, lens, _, _, mq, mk, _ = args
     want = E.attention_paged(q, cache, table, cq, lens, mq, mk)
-    none = E.attention_shared(q, cache, table, cq, lens, i32([0]), i32([]), mq, mk, 500)
+    none = E.attention_shared(q, cache, table, cq, lens, i32([0]), i32([]), mq, mk, SHARE)
     assert torch.equal(none, want)
-    one = E.attention_shared(q, cache, table, cq, lens, i32([0, 1, 2]), i32([500, 500]), mq, mk, 500)
+    few = E.attention_shared(q, cache, table, cq, lens, i32([0, 2]), i32([500]), mq, mk, 500)
+    assert torch.equal(few, want)
+    one = E.attention_shared(q, cache, table, cq, lens, i32([0, 1, 2]), i32([500, 500]), mq, mk, SHARE)
     assert_rows(f64(one), f64(want), 2.0**-7 * np.linalg.norm(f64(want), axis=-1) + 1e-30)
 
 
@@ -179,7 +182,7 @@ def test_no_group_is_the_paged_call():
 def test_in_place_and_a_workspace_of_its_own(fmt, q_len):
     args, got = shared([4], [600], [q_len] * 4, [700, 650, 900, 640], 8, 2, 128, 16, fmt, "bf16")
     q = args[0]
-    need = E.attention_shared_workspace_bytes(q.shape[0], 4, 1, 8, 2, 128, *args[-3:])
+    need = E.attention_shared_workspace_bytes(q.shape[0], 4, 1, 8, args[1], *args[-3:])
     work = torch.full((need,), 0x7F, dtype=torch.uint8, device=DEV)
     mine = q.clone()
     out = E.attention_shared(mine, *args[1:], out=mine, workspace=work)
