@@ -1,13 +1,16 @@
 """An attention layer on quantised weights and a paged, quantised cache.
 
-    python examples/attention_layer.py [--fmt bf16|f16|int8|int4] [--steps N] [--seqs B] [--prompt L]
+    python examples/attention_layer.py [--fmt bf16|f16|int8|int4] [--steps N] [--seqs B] [--prompt L] [--shared S] [--norm]
 
 Prompts of ragged lengths go through the fused q, k, v projection, the rotation
-in place, the cache and prompt attention; then every sequence takes single
-tokens, whose step (projection, rotation into the cache, paged attention, output
-projection) is captured once in a CUDA graph and replayed.  The last step's
-attention is compared with prompt attention over the whole sequences.  Weights
-are random EXL3 layers, activations random.
+(with --norm the norms of query and key heads too) in place, the cache and prompt
+attention; then every sequence takes single tokens, whose step (pages and slots
+from the lengths, projection, rotation into the cache, paged attention, output
+projection) is captured once in a CUDA graph and replayed.  With --shared all
+prompts begin with the same S tokens, which only the first sequence writes: the others
+begin on its pages and read them together.  The last step's attention is compared
+with prompt attention over the whole sequences.  Weights are random EXL3 layers,
+activations random.
 """
 import argparse
 import os
@@ -36,26 +39,28 @@ class Projection:
 
 
 class AttentionLayer:
-    """Sequences 0 .. seqs - 1, each with room for max_len tokens in the cache."""
+    """Sequences 0 .. seqs - 1, each of up to max_len tokens in the cache."""
 
     def __init__(self, hidden, heads, kv_heads, head_dim, seqs, max_len, fmt="int8", page=64, bits=4, window=0,
-                 base=10000.0, seed=1, device="cuda"):
+                 base=10000.0, norm=None, seed=1, device="cuda"):
+        """norm: the rows' type, for norms of query and key heads (random weights); None: no norms."""
         self.heads, self.kv_heads, self.head_dim, self.page, self.window = heads, kv_heads, head_dim, page, window
         self.max_len = max_len
         kv = kv_heads * head_dim
         self.qkv = Projection(hidden, [heads * head_dim, kv, kv], bits, "mcg", seed, device)
         self.out = Projection(heads * head_dim, [hidden], bits, "mcg", seed + 1, device)
         self.phases, self.amplitude = E.rope_phases(head_dim, base=base, device=device)
-        pages = (max_len + page - 1) // page
-        self.cache = E.KVCache.empty(seqs * pages, page, kv_heads, head_dim, fmt, device=device)
-        self.table = torch.randperm(seqs * pages, device=device).to(torch.int32).view(seqs, pages)
-        self.kv_lens = torch.zeros(seqs, dtype=torch.int32, device=device)
-        self.one_each = torch.arange(seqs + 1, dtype=torch.int32, device=device)
-
-    def slots(self, seq, position):
-        """Cache rows of tokens at ``position`` of sequences ``seq``."""
-        at = position.long()
-        return self.table[seq.long(), at // self.page].long() * self.page + at % self.page
+        pages = seqs * ((max_len + page - 1) // page)
+        self.cache = E.KVCache.empty(pages, page, kv_heads, head_dim, fmt, device=device)
+        self.tables = E.KVTables.empty(seqs, max_len, pages, page, device=device)
+        self.one_each = torch.ones(seqs, dtype=torch.int32, device=device)
+        self.q_weight = self.k_weight = self.qk_weight = None
+        if norm is not None:
+            g = torch.Generator(device=device).manual_seed(seed)
+            self.q_weight, self.k_weight = ((1 + 0.2 * torch.randn(head_dim, generator=g, device=device)).to(norm)
+                                            for _ in range(2))
+            self.qk_weight = torch.cat([self.q_weight.expand(heads, -1), self.k_weight.expand(kv_heads, -1)])
+        self.groups, self.prefix, self.max_prefix = None, None, 0
 
     def heads_of(self, y):
         rows = y.view(y.shape[0], -1, self.head_dim)
@@ -65,41 +70,77 @@ class AttentionLayer:
         """Attention of whole prompts [sum(lens), hidden], whose keys and values go into the cache unless not ``keep``."""
         device = x.device
         y = self.qkv(x)
-        cu = torch.tensor([0] + lens, dtype=torch.int32, device=device).cumsum(0, dtype=torch.int32)
-        seq = torch.arange(len(lens), device=device).repeat_interleave(torch.tensor(lens, device=device))
-        position = (torch.arange(x.shape[0], device=device) - cu[seq]).to(torch.int32)
+        new = torch.tensor(lens, dtype=torch.int32, device=device)
+        if keep:
+            cu, position, slots, _ = E.kv_plan(self.tables, new, x.shape[0])
+        else:
+            cu = torch.tensor([0] + lens, dtype=torch.int32, device=device).cumsum(0, dtype=torch.int32)
+            seq = torch.arange(len(lens), device=device).repeat_interleave(new)
+            position = (torch.arange(x.shape[0], device=device) - cu[seq]).to(torch.int32)
         turned = y.view(y.shape[0], -1, self.head_dim)[:, :self.heads + self.kv_heads]  # q and k lie side by side
-        E.rope(turned, position, self.phases, amplitude=self.amplitude, out=turned)
+        E.rope(turned, position, self.phases, amplitude=self.amplitude, out=turned, weight=self.qk_weight)
         q, k, v = self.heads_of(y)
         if keep:
-            E.kv_write(self.cache, k, v, self.slots(seq, position))
-            self.kv_lens.copy_(cu[1:] - cu[:-1])
+            E.kv_write(self.cache, k, v, slots)
         return E.attention_prompt(q, k, v, cu, max(lens), window=self.window)
 
-    def step(self, x):
-        """Attention of the next token of every sequence, x [seqs, hidden]; nothing in here waits for the GPU."""
+    def share(self, tokens, hint=None):
+        """All sequences begin with the first ``tokens`` (whole pages) of sequence 0, on its pages; none but it has any yet.
+        hint: attention_shared's max_prefix, the tokens unless given."""
+        t, pages = self.tables, tokens // self.page
+        t.block_table[1:, :pages] = t.block_table[0, :pages]
+        t.held[1:] = pages
+        t.kv_lens[1:] = tokens
+        self.groups = torch.tensor([0, t.batch], dtype=torch.int32, device=t.kv_lens.device)
+        self.prefix = torch.tensor([tokens], dtype=torch.int32, device=t.kv_lens.device)
+        self.max_prefix = tokens if hint is None else hint
+
+    def step(self, x, new=None, max_new=1):
+        """Attention of the next tokens of every sequence (one each, or new[b] of at most max_new), x [tokens, hidden];
+        nothing in here waits for the GPU."""
         q, k, v = self.heads_of(self.qkv(x))
-        slots = self.slots(self.one_each[:-1], self.kv_lens)
-        q = E.kv_write(self.cache, k, v, slots, q=q, positions=self.kv_lens, phases=self.phases, amplitude=self.amplitude)
-        self.kv_lens += 1
-        return E.attention_paged(q, self.cache, self.table, self.one_each, self.kv_lens, 1, self.max_len,
-                                 window=self.window)
+        cu, position, slots, _ = E.kv_plan(self.tables, self.one_each if new is None else new, x.shape[0])
+        q = E.kv_write(self.cache, k, v, slots, q=q, positions=position, phases=self.phases, amplitude=self.amplitude,
+                       q_weight=self.q_weight, k_weight=self.k_weight)
+        args = (q, self.cache, self.tables.block_table, cu, self.tables.kv_lens)
+        if self.groups is None:
+            return E.attention_paged(*args, max_new, self.max_len, window=self.window)
+        return E.attention_shared(*args, self.groups, self.prefix, max_new, self.max_len, self.max_prefix)
+
+    def end(self, ended):
+        """Sequences end (bool [seqs]): their own pages are free again."""
+        shared = None
+        if self.groups is not None:
+            shared = torch.full_like(self.tables.held, int(self.prefix) // self.page)
+            shared[0] = 0
+        E.kv_release(self.tables, ended, shared)
 
     def project(self, attention):
         return self.out(attention.flatten(1))
 
 
-def run(fmt="int8", steps=32, seqs=8, prompt=500, hidden=2048, heads=16, kv_heads=4, head_dim=128, seed=3):
+def run(fmt="int8", steps=32, seqs=8, prompt=500, hidden=2048, heads=16, kv_heads=4, head_dim=128, seed=3, shared=0,
+        norm=False, hint=None):
     """(the last step's attention, the same by prompt attention, microseconds a step)."""
     device = torch.device("cuda")
     dtype = torch.float16 if fmt == "f16" else torch.bfloat16
     g = torch.Generator(device=device).manual_seed(seed)
     lens = [max(1, prompt - 61 * b) for b in range(seqs)]
-    layer = AttentionLayer(hidden, heads, kv_heads, head_dim, seqs, max(lens) + steps, fmt)
+    page = 64
+    shared = shared // page * page
+    layer = AttentionLayer(hidden, heads, kv_heads, head_dim, seqs, shared + max(lens) + steps, fmt, page=page,
+                           norm=dtype if norm else None)
+    begin = torch.randn((shared, hidden), generator=g, device=device).to(dtype)
     prompts = [torch.randn((n, hidden), generator=g, device=device).to(dtype) for n in lens]
     tokens = torch.randn((steps, seqs, hidden), generator=g, device=device).to(dtype)
 
-    layer.project(layer.prompt(torch.cat(prompts), lens))
+    if shared:
+        layer.prompt(begin, [shared] + [0] * (seqs - 1))
+        layer.share(shared, hint)
+        attention = layer.step(torch.cat(prompts), torch.tensor(lens, dtype=torch.int32, device=device), max(lens))
+        layer.project(attention)
+    else:
+        layer.project(layer.prompt(torch.cat(prompts), lens))
 
     x = tokens[0].clone()
     stream = torch.cuda.Stream()
@@ -112,18 +153,21 @@ def run(fmt="int8", steps=32, seqs=8, prompt=500, hidden=2048, heads=16, kv_head
             attention = layer.step(x)
             layer.project(attention)
     torch.cuda.synchronize()
-    begin = time.perf_counter()
+    start = time.perf_counter()
     with torch.cuda.stream(stream):
         for t in range(1, steps):
             x.copy_(tokens[t])
             graph.replay()
     torch.cuda.synchronize()
-    micros = (time.perf_counter() - begin) * 1e6 / max(1, steps - 1)
+    micros = (time.perf_counter() - start) * 1e6 / max(1, steps - 1)
 
-    whole = [torch.cat([p, tokens[:, b]]) for b, p in enumerate(prompts)]
-    lens = [n + steps for n in lens]
+    whole = [torch.cat([begin, p, tokens[:, b]]) for b, p in enumerate(prompts)]
+    lens = [shared + n + steps for n in lens]
     every = layer.prompt(torch.cat(whole), lens, keep=False)
     last = torch.tensor(lens, device=device).cumsum(0) - 1
+    layer.end(torch.ones(seqs, dtype=torch.bool, device=device))
+    if int(layer.tables.free_count) != layer.cache.num_pages:
+        raise RuntimeError("pages are missing")
     if E.device_status() != 0:
         raise RuntimeError("a kernel gave up waiting")
     return attention, every[last], micros
@@ -135,8 +179,10 @@ def main():
     p.add_argument("--steps", type=int, default=32)
     p.add_argument("--seqs", type=int, default=8)
     p.add_argument("--prompt", type=int, default=500)
+    p.add_argument("--shared", type=int, default=0, help="tokens that all prompts begin with (whole pages of 64)")
+    p.add_argument("--norm", action="store_true", help="norms of query and key heads")
     a = p.parse_args()
-    got, want, micros = run(a.fmt, max(2, a.steps), a.seqs, a.prompt)
+    got, want, micros = run(a.fmt, max(2, a.steps), a.seqs, a.prompt, shared=a.shared, norm=a.norm)
     off = (got.float() - want.float()).norm() / want.float().norm()
     print(f"{a.fmt}: {a.seqs} sequences, {a.steps} steps, {micros:.1f} us a step; "
           f"step against prompt attention: {float(off):.2e} of the norm")

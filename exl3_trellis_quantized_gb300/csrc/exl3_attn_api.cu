@@ -500,8 +500,8 @@ exl3_status_t exl3_attention_shared(const exl3_heads_t* q, exl3_dtype_t dtype, i
   if (!worth_sharing(total_q, batch, groups, q_heads, a.kv_heads, a.head_dim, exl3::kv_quantised(a.cache.format), max_q, max_kv, max_prefix))
     return exl3_attention_paged(q, dtype, total_q, q_heads, cache, block_table, table_width, cu_q, kv_lens, batch, max_q, max_kv, 0,
                                 scale, out, out_token_stride, out_head_stride, workspace, workspace_bytes, stream);
+  if (total_q * q_heads * 16 > INT32_MAX) return EXL3_EUNSUPPORTED;  // CTAs of row tiles in up to 16 parts
   const SharedPlan plan = shared_plan(total_q, batch, groups, q_heads, a.kv_heads, a.head_dim, max_q, max_kv, max_prefix);
-  if (total_q * q_heads > INT32_MAX) return EXL3_EUNSUPPORTED;  // blocks of the join
   if (!aligned16(workspace)) return EXL3_EINVAL;
   if (workspace_bytes < plan.at[10]) return EXL3_EWORKSPACE;
   uint8_t* w = static_cast<uint8_t*>(workspace);
