@@ -129,7 +129,7 @@ def lib() -> ctypes.CDLL:
                                      i64, i64, vp]
     L.exl3_kv_plan.argtypes = [tables, vp, i64] + [vp] * 8
     L.exl3_kv_release.argtypes = [tables] + [vp] * 6
-    L.exl3_attention_shared_workspace_bytes.argtypes = [i64] + [i32] * 5 + [ctypes.c_int] + [i32] * 3
+    L.exl3_attention_shared_workspace_bytes.argtypes = [i64] + [i32] * 5 + [ctypes.c_int] * 2 + [i32] * 3
     L.exl3_attention_shared_workspace_bytes.restype = sz
     L.exl3_attention_shared.argtypes = [heads, ctypes.c_int, i64, i32, cache, vp, i32, vp, vp, i32, vp, vp, i32, i32, i32,
                                         i32, f32, vp, i64, i64, vp, sz, vp]
@@ -964,10 +964,11 @@ def _shared_workspace_bytes(*sizes) -> int:
     return int(lib().exl3_attention_shared_workspace_bytes(*sizes))
 
 
-def attention_shared_workspace_bytes(total_q: int, batch: int, groups: int, heads: int, cache: KVCache, max_q: int,
+def attention_shared_workspace_bytes(total_q: int, batch: int, groups: int, heads: int, dtype, cache: KVCache, max_q: int,
                                      max_kv: int, max_prefix: int) -> int:
-    return _shared_workspace_bytes(total_q, batch, groups, heads, cache.kv_heads, cache.head_dim, KV_FORMATS[cache.fmt],
-                                   max_q, max_kv, max_prefix)
+    """dtype: q's."""
+    return _shared_workspace_bytes(total_q, batch, groups, heads, cache.kv_heads, cache.head_dim,
+                                   _BF16 if dtype is torch.bfloat16 else _F16, KV_FORMATS[cache.fmt], max_q, max_kv, max_prefix)
 
 
 def attention_shared(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, cu_q: torch.Tensor,
@@ -1007,7 +1008,7 @@ def attention_shared(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor,
         _apart(out, "out", cache_k=cache.k, cache_v=cache.v, k_scale=cache.k_scale, v_scale=cache.v_scale)
     out, oh = _out_like(q, out, "out")
     if workspace is None:
-        need = attention_shared_workspace_bytes(total, batch, groups, heads, cache, int(max_q), int(max_kv), int(max_prefix))
+        need = attention_shared_workspace_bytes(total, batch, groups, heads, q.dtype, cache, int(max_q), int(max_kv), int(max_prefix))
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     else:
         _need(workspace, torch.uint8, "workspace")

@@ -194,13 +194,16 @@ SharedPlan shared_plan(int64_t total_q, int64_t batch, int64_t groups, int64_t q
 // a group fill them.  8 and 1 tokens of 32 rows: 4 sequences behind 8192 keys 28.7 and 27.1, 12 behind 1024 26.6 and
 // 18.1, 40 behind 1024 38.5 and 45.1, 12 behind 8192 37.5 and 67.1.  Long chunks fill theirs anyway and gain up to a
 // tenth (7 of 33 to 700 tokens behind 16000 4-bit keys 492 and 522) or lose as much where own keys weigh.
+// And fp16 rows over a quantised cache, where the token kernel holds the rotated q in two terms and the row tiles in one,
+// stay with the former: 17 tokens of 48 heads behind 7791 8-bit keys would have 0.0004 of the result's norm in place of 0.0002.
 bool worth_sharing(int64_t total_q, int64_t batch, int64_t groups, int64_t q_heads, int64_t kv_heads, int64_t head_dim, bool quant,
-                   int64_t max_q, int64_t max_kv, int64_t max_prefix) {
+                   bool bf16, int64_t max_q, int64_t max_kv, int64_t max_prefix) {
   if (max_prefix == EXL3_SHARE_ALWAYS) return groups > 0;
   if (groups == 0 || batch <= groups || max_prefix < exl3::kLeastPrefix) return false;
   const int64_t group = q_heads / kv_heads;
   const double keys = (double)max_prefix * kv_heads * (head_dim / 128.0);
   if (max_q * group <= exl3::kTokenRows) {
+    if (quant && !bf16) return false;
     const double least = max_q * group <= 8 ? (quant ? 600e3 : 400e3) : (quant ? 360e3 : 240e3);
     return (double)(batch - groups) * keys >= least;
   }
@@ -476,11 +479,12 @@ exl3_status_t exl3_attention_paged(const exl3_heads_t* q, exl3_dtype_t dtype, in
 }
 
 size_t exl3_attention_shared_workspace_bytes(int64_t total_q, int32_t batch, int32_t groups, int32_t q_heads,
-                                             int32_t kv_heads, int32_t head_dim, exl3_kv_format_t format, int32_t max_q,
-                                             int32_t max_kv, int32_t max_prefix) {
+                                             int32_t kv_heads, int32_t head_dim, exl3_dtype_t dtype,
+                                             exl3_kv_format_t format, int32_t max_q, int32_t max_kv, int32_t max_prefix) {
   if (!valid_rows(total_q) || !valid_rows(batch) || !valid_rows(groups) || !valid_head_counts(q_heads, kv_heads)) return 0;
   if (check_head_dim(head_dim) != EXL3_OK || max_q < 1 || max_kv < 0 || max_prefix < 0 || total_q == 0 || batch == 0) return 0;
-  if (!worth_sharing(total_q, batch, groups, q_heads, kv_heads, head_dim, exl3::kv_quantised(format), max_q, max_kv, max_prefix))
+  if (!worth_sharing(total_q, batch, groups, q_heads, kv_heads, head_dim, exl3::kv_quantised(format), dtype == EXL3_BF16, max_q,
+                     max_kv, max_prefix))
     return exl3_attention_paged_workspace_bytes(total_q, batch, q_heads, kv_heads, head_dim, max_q, max_kv, 0);
   return shared_plan(total_q, batch, groups, q_heads, kv_heads, head_dim, max_q, max_kv, max_prefix).at[10];
 }
@@ -497,7 +501,8 @@ exl3_status_t exl3_attention_shared(const exl3_heads_t* q, exl3_dtype_t dtype, i
   const exl3_status_t st = paged_args(q, dtype, total_q, q_heads, cache, block_table, table_width, cu_q, kv_lens, batch, max_q, max_kv, 0,
                                       scale, out, out_token_stride, out_head_stride, &a);
   if (st != EXL3_OK || total_q == 0 || batch == 0) return st;
-  if (!worth_sharing(total_q, batch, groups, q_heads, a.kv_heads, a.head_dim, exl3::kv_quantised(a.cache.format), max_q, max_kv, max_prefix))
+  if (!worth_sharing(total_q, batch, groups, q_heads, a.kv_heads, a.head_dim, exl3::kv_quantised(a.cache.format), dtype == EXL3_BF16,
+                     max_q, max_kv, max_prefix))
     return exl3_attention_paged(q, dtype, total_q, q_heads, cache, block_table, table_width, cu_q, kv_lens, batch, max_q, max_kv, 0,
                                 scale, out, out_token_stride, out_head_stride, workspace, workspace_bytes, stream);
   if (total_q * q_heads * 16 > INT32_MAX) return EXL3_EUNSUPPORTED;  // CTAs of row tiles in up to 16 parts

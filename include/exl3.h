@@ -536,8 +536,9 @@ exl3_status_t exl3_attention_paged(const exl3_heads_t* q, exl3_dtype_t dtype, in
  * sequences' tables name the same pages, but copies (of a last page that is filled up differently) will do.
  * Sequences of no group (before cu_groups[0], from cu_groups[groups] on) are as in exl3_attention_paged.
  * Where the sizes say that sharing does not pay (few sequences, short prefixes), the call is exl3_attention_paged.
- * The result is exl3_attention_paged's but for the order of its sums (and, over a quantised cache, the rounding
- * of the rotated q to one fp16 term for prefix keys).  What is shared in fact is whole tiles of 128 keys that every
+ * The result is exl3_attention_paged's but for the order of its sums and, where prefixes of a quantised cache are
+ * shared, the rounding of the rotated q to one fp16 term as in long chunks (so fp16 rows that the paged call
+ * would take in two terms are not shared unless EXL3_SHARE_ALWAYS asks for it).  What is shared in fact is whole tiles of 128 keys that every
  * query of the group sees, from 256 keys on, of groups in which at least two sequences have queries: prefix_lens
  * may be larger than a sequence's length or reach past a query's position.
  *   cu_groups    device, int32 [groups + 1], not falling;  prefix_lens  device, int32 [groups]
@@ -548,8 +549,8 @@ exl3_status_t exl3_attention_paged(const exl3_heads_t* q, exl3_dtype_t dtype, in
  */
 #define EXL3_SHARE_ALWAYS INT32_MAX
 size_t exl3_attention_shared_workspace_bytes(int64_t total_q, int32_t batch, int32_t groups, int32_t q_heads,
-                                             int32_t kv_heads, int32_t head_dim, exl3_kv_format_t format,
-                                             int32_t max_q, int32_t max_kv, int32_t max_prefix);
+                                             int32_t kv_heads, int32_t head_dim, exl3_dtype_t dtype,
+                                             exl3_kv_format_t format, int32_t max_q, int32_t max_kv, int32_t max_prefix);
 exl3_status_t exl3_attention_shared(const exl3_heads_t* q, exl3_dtype_t dtype, int64_t total_q, int32_t q_heads,
                                     const exl3_kv_cache_t* cache, const int32_t* block_table, int32_t table_width,
                                     const int32_t* cu_q, const int32_t* kv_lens, int32_t batch, const int32_t* cu_groups,

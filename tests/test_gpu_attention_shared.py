@@ -182,7 +182,7 @@ def test_no_group_is_the_paged_call():
 def test_in_place_and_a_workspace_of_its_own(fmt, q_len):
     args, got = shared([4], [600], [q_len] * 4, [700, 650, 900, 640], 8, 2, 128, 16, fmt, "bf16")
     q = args[0]
-    need = E.attention_shared_workspace_bytes(q.shape[0], 4, 1, 8, args[1], *args[-3:])
+    need = E.attention_shared_workspace_bytes(q.shape[0], 4, 1, 8, q.dtype, args[1], *args[-3:])
     work = torch.full((need,), 0x7F, dtype=torch.uint8, device=DEV)
     mine = q.clone()
     out = E.attention_shared(mine, *args[1:], out=mine, workspace=work)

@@ -131,7 +131,7 @@ def test_shared_refused(L):  # noqa: F811
     assert call(c=cache(fmt=0)) == call(c=cache(fmt=1), dtype=F16) == EINVAL
     assert call(c=cache(dim=32)) == EUNSUPPORTED
     for mp in (always, 300):  # shared, and the paged call that it else is
-        need = L.exl3_attention_shared_workspace_bytes(4, 4, 1, 8, 2, 128, 3, 1, 64, mp)
+        need = L.exl3_attention_shared_workspace_bytes(4, 4, 1, 8, 2, 128, BF16, 3, 1, 64, mp)
         assert need > 0
         assert call(max_prefix=mp, ws=None) == call(max_prefix=mp, ws=FAKE + 8) == EINVAL
         assert call(max_prefix=mp, ws_bytes=need - 1) == EWORKSPACE
@@ -142,8 +142,8 @@ def test_shared_refused(L):  # noqa: F811
 
 
 def test_shared_workspace_bytes(L):  # noqa: F811
-    def size(total=64, batch=64, groups=1, h=32, kv=8, d=128, fmt=1, max_q=1, max_kv=9000, max_prefix=8192):
-        return L.exl3_attention_shared_workspace_bytes(total, batch, groups, h, kv, d, fmt, max_q, max_kv, max_prefix)
+    def size(total=64, batch=64, groups=1, h=32, kv=8, d=128, dtype=BF16, fmt=1, max_q=1, max_kv=9000, max_prefix=8192):
+        return L.exl3_attention_shared_workspace_bytes(total, batch, groups, h, kv, d, dtype, fmt, max_q, max_kv, max_prefix)
 
     assert size(total=0) == size(batch=0) == size(h=7) == size(d=96) == size(max_q=0) == size(max_prefix=-1) == 0
     paged = L.exl3_attention_paged_workspace_bytes(64, 64, 32, 8, 128, 1, 9000, 0)
@@ -151,6 +151,8 @@ def test_shared_workspace_bytes(L):  # noqa: F811
     few = L.exl3_attention_paged_workspace_bytes(2, 2, 32, 8, 128, 1, 9000, 0)
     assert size(total=2, batch=2) == few            # two sequences behind 8192 keys do not pay
     assert size() > 0 and size() != paged           # 64 do
+    assert size(fmt=2) == size(fmt=3) == size()
+    assert size(dtype=F16, fmt=2) == paged          # but not in one fp16 term where the paged call has two
     assert size(total=2, batch=2, max_prefix=E.SHARE_ALWAYS) > few
     # bounded whatever the lengths: one wave of items, single tokens' own results and two of each CTA
     for kv_len in (1000, 1 << 20, 1 << 30):
