@@ -162,12 +162,14 @@ __global__ void __launch_bounds__(kPrepThreads) shared_prep_kernel(const AttnArg
     if (g < a.groups) {
       const int2 n = sizes(g);
       tiles = n.x > 0 ? (n.y + per - 1) / per : 0;
-      parts = (n.x + unit - 1) / unit;
+      parts = tiles > 0 ? (n.x + unit - 1) / unit : 0;
     }
-    const int64_t before = block_sums((int64_t)tiles * a.kv_heads * parts, part, &items);
+    const int64_t n = (int64_t)tiles * a.kv_heads * parts, before = block_sums(n, part, &items);
     if (g < a.groups) {
-      s.group[g].item = (int)before;
-      s.group[g].parts = parts;
+      // (groups that overlap, which the call does not allow, may be more than there is room for: those have no parts)
+      const bool room_left = before + n <= a.prefix_ctas;
+      s.group[g].item = room_left ? (int)before : 0;
+      s.group[g].parts = room_left ? parts : 0;
     }
   }
   if (tid == 0) {
@@ -243,7 +245,7 @@ __device__ __forceinline__ void finish_row(const AttnArgs& a, const Sum& s, int6
 // The part of row (tok, head) in the first of its prefix items.  The next item's lies kPrefixRows rows on; where the
 // item's rows fill one tile (twice: it has halves with a part each) half of that.
 __device__ __forceinline__ int64_t prefix_row(const AttnArgs& a, const SharedGroup& g, int tok, int h, int head, int group, bool* twice) {
-  const int per = 2 * a.tile_tokens, t = tok - g.q0, tiles = (g.tokens + per - 1) / per, tile = t / per;
+  const int per = 2 * a.tile_tokens, t = max(0, min(tok - g.q0, g.tokens - 1)), tiles = (g.tokens + per - 1) / per, tile = t / per;
   const int64_t item = g.item + ((int64_t)(tiles - 1 - tile) * a.kv_heads + h) * g.parts;  // last tiles come first
   *twice = g.tokens - tile * per <= a.tile_tokens;
   return item * kPrefixRows + (t - tile * per) * group + head;

@@ -91,13 +91,18 @@ def shared(sizes, prefixes, q_lens, lens, heads, kv, dim, page, fmt, dtype, skip
     torch.cuda.synchronize()
     assert E.device_status() == 0
     assert bool((out[total:] == 3.0).all())
-    at = 0
+    at, bounds = 0, shared.bounds
+    bounds.clear()
     for b, (n, m, (k, v)) in enumerate(zip(q_lens, lens, rows)):
         want, tol = bound(f64(q[at:at + n]), k, v, 0, scale, dtype, fmt)
+        bounds.append((want, tol))
         assert_rows(f64(got[at:at + n]), want, tol, f"sequence {b}: {n} queries over {m} keys")
         at += n
     assert torch.equal(E.attention_shared(*args, scale=scale), got)
     return args, got
+
+
+shared.bounds = []  # of each sequence of the last call
 
 
 TOKENS = [
@@ -214,6 +219,22 @@ def test_a_sequence_that_is_not_finite_stays_its_own(q_len):
     out = E.attention_shared(*args)
     assert torch.equal(out[:q_len], got[:q_len]) and torch.equal(out[2 * q_len:], got[2 * q_len:])
     assert torch.isnan(out[q_len:2 * q_len]).any()
+
+
+@pytest.mark.parametrize("q_len", [1, 20])
+@pytest.mark.parametrize("groups", [[0, 9], [-3, 4], [2, 100, 2**31 - 1], [3, 1, 4], [0, 4, 0, 4, 0, 4, 1, 4, 2, 4, 0, 4] * 30])
+def test_groups_that_cannot_be(groups, q_len):
+    """Entries outside the batch are taken as its ends; falling ones give empty groups, or groups that overlap, whose
+    results are undefined: nothing outside the tensors is touched, and the sequence of no group stays within its bound (the
+    sums of its keys may be cut elsewhere)."""
+    args, got = shared([4], [600], [q_len] * 5, [700, 650, 900, 640, 300], 8, 2, 128, 16, "bf16", "bf16")
+    out = torch.full((5 * q_len + 3, 8, 128), 3.0, dtype=torch.bfloat16, device=DEV)
+    prefix = i32([600] * (len(groups) - 1))
+    E.attention_shared(*args[:5], i32(groups), prefix, *args[7:], out=out[:5 * q_len])
+    torch.cuda.synchronize()
+    assert E.device_status() == 0 and bool((out[5 * q_len:] == 3.0).all())
+    if max(groups) <= 4:
+        assert_rows(f64(out[4 * q_len:5 * q_len]), *shared.bounds[4])
 
 
 def test_two_captured_steps():
