@@ -81,29 +81,50 @@ struct SharedCosts {
   float block, joint, fixed, unit, unit_dram;  // us
   int token, per_sm;  // the token kernel takes the own keys, so many CTAs an SM
 };
+// What the lengths say is loaded once, into shared memory as far as that goes (kHeldSeqs sequences, kHeldGroups groups): this
+// block stands before everything else, and its time is its chain of loads (5.3 us with the lengths read where they are used).
+constexpr int kHeldSeqs = 1024, kHeldGroups = 256;
 __global__ void __launch_bounds__(kPrepThreads) shared_prep_kernel(const AttnArgs a, const int32_t* cu_groups,
                                                                    const int32_t* prefix_lens, const SharedState s,
                                                                    const SharedCosts cost) {
-  constexpr int kHeld = 256;  // groups whose sizes shared memory holds
   __shared__ int64_t part[kPrepThreads / 32];
-  __shared__ int2 held[kHeld];  // blocks and tokens
-  __shared__ int longest;
-  __shared__ int unit;
+  __shared__ int h_q[kHeldSeqs + 1], h_kv[kHeldSeqs];  // first query tokens and lengths
+  __shared__ int2 h_seq[kHeldSeqs];                    // what s.seq will hold
+  __shared__ int h_group[kHeldGroups + 1], h_prefix[kHeldGroups];
+  __shared__ int2 h_size[kHeldGroups];                 // blocks and tokens
+  __shared__ int longest, unit;
   pdl_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31;
-  const int per = 2 * a.tile_tokens;
-  for (int b = tid; b < a.batch; b += kPrepThreads) s.seq[b] = make_int2(0, -1);
+  const int per = 2 * a.tile_tokens, room = a.table_width << a.cache.page_shift, total = (int)a.total_q;
+  const bool held = a.batch <= kHeldSeqs;
+  auto clamped = [](int x, int hi) { return max(0, min(x, hi)); };
+  for (int b = tid; b <= min(a.batch, kHeldSeqs); b += kPrepThreads) {
+    h_q[b] = clamped(a.cu_q[b], total);
+    if (b < min(a.batch, kHeldSeqs)) {
+      h_kv[b] = clamped(a.kv_lens[b], room);
+      h_seq[b] = make_int2(0, -1);
+    }
+  }
+  for (int g = tid; g <= min(a.groups, kHeldGroups); g += kPrepThreads) {
+    h_group[g] = clamped(cu_groups[g], a.batch);
+    if (g < min(a.groups, kHeldGroups)) h_prefix[g] = clamped(prefix_lens[g], room);
+  }
+  if (!held)
+    for (int b = tid; b < a.batch; b += kPrepThreads) s.seq[b] = make_int2(0, -1);
   if (tid == 0) longest = 0;
   __syncthreads();
-  const int room = a.table_width << a.cache.page_shift, total = (int)a.total_q;
+  auto first_q = [&](int b) { return held ? h_q[b] : clamped(a.cu_q[b], total); };
+  auto length = [&](int b) { return held ? h_kv[b] : clamped(a.kv_lens[b], room); };
+#pragma unroll 1
   for (int g = tid >> 5; g < a.groups; g += kPrepThreads / 32) {  // one warp a group
-    const int s0 = max(0, min(cu_groups[g], a.batch)), s1 = max(s0, min(cu_groups[g + 1], a.batch));
-    int keys = max(0, min(prefix_lens[g], room)), first = INT32_MAX, queries = 0;
-    const int q0 = max(0, min(a.cu_q[s0], total)), q1 = max(q0, min(a.cu_q[s1], total));
+    const int s0 = g <= kHeldGroups ? h_group[g] : clamped(cu_groups[g], a.batch);
+    const int s1 = max(s0, g < kHeldGroups ? h_group[g + 1] : clamped(cu_groups[g + 1], a.batch));
+    int keys = g < kHeldGroups ? h_prefix[g] : clamped(prefix_lens[g], room), first = INT32_MAX, queries = 0;
+#pragma unroll 1
     for (int b = s0 + lane; b < s1; b += 32) {
-      const int c0 = max(0, a.cu_q[b]), c1 = min(a.cu_q[b + 1], total), kl = max(0, min(a.kv_lens[b], room));
-      if (c1 <= c0) continue;
-      keys = min(keys, max(0, kl - (c1 - c0) + 1));  // what its first query sees
+      const int n = first_q(b + 1) - first_q(b);
+      if (n <= 0) continue;
+      keys = min(keys, max(0, length(b) - n + 1));  // what its first query sees
       first = min(first, b);
       ++queries;
     }
@@ -112,34 +133,45 @@ __global__ void __launch_bounds__(kPrepThreads) shared_prep_kernel(const AttnArg
     queries = __reduce_add_sync(0xffffffffu, queries);
     keys = queries < 2 || keys < kLeastPrefix ? 0 : keys / kPrefixKeys * kPrefixKeys;
     if (keys > 0)
-      for (int b = s0 + lane; b < s1; b += 32) s.seq[b] = make_int2(keys, g);
+      for (int b = s0 + lane; b < s1; b += 32) (held ? h_seq : s.seq)[b] = make_int2(keys, g);
     if (lane == 0) {
+      const int q0 = first_q(s0), q1 = max(q0, first_q(s1));
       s.group[g] = {q0, q1 - q0, keys, keys > 0 ? first : 0, 0, 0};
-      if (g < kHeld) held[g] = make_int2(keys / 64, q1 - q0);
+      if (g < kHeldGroups) h_size[g] = make_int2(keys / 64, q1 - q0);
       atomicMax(&longest, keys / 64);
     }
   }
   __syncthreads();
-  auto sizes = [&](int g) { return g < kHeld ? held[g] : make_int2(s.group[g].keys / 64, s.group[g].tokens); };
+  auto sizes = [&](int g) { return g < kHeldGroups ? h_size[g] : make_int2(s.group[g].keys / 64, s.group[g].tokens); };
   int64_t units = 0;
-  if (cost.token) {
-    for (int b0 = 0; b0 < a.batch; b0 += kPrepThreads) {
-      const int b = b0 + tid;
-      const int64_t before = block_sums(b < a.batch ? load_seq<true>(a, b).weight() : 0, part, &units);
+#pragma unroll 1
+  for (int b0 = 0; b0 < a.batch; b0 += kPrepThreads) {
+    const int b = b0 + tid;
+    int weight = 0;
+    if (b < a.batch) {
+      const int2 seq = held ? h_seq[b] : s.seq[b];
+      if (held) s.seq[b] = seq;
+      // as load_seq has it
+      if (first_q(b + 1) > first_q(b)) weight = max(1, (length(b) - seq.x + kTokenUnit - 1) / kTokenUnit) + kItemUnits;
+    }
+    if (cost.token) {
+      const int64_t before = block_sums(weight, part, &units);
       if (b < a.batch) s.units[b] = before;
     }
-    if (tid == 0) s.units[a.batch] = units;
   }
+  if (cost.token && tid == 0) s.units[a.batch] = units;
   if (tid < 32) {
     // a lane a size
     const int u = max(4, ((longest + lane) / (lane + 1) + 1) & ~1);
     float items = 0.0f, us = 0.0f, one = 0.0f;
+#pragma unroll 1
     for (int g = 0; g < a.groups; ++g) {
       const int2 n = sizes(g);
       if (n.x == 0) continue;
       const float tiles = (float)((n.y + per - 1) / per * a.kv_heads), block = n.y <= a.tile_tokens ? cost.joint : cost.block;
-      items += tiles * (float)((n.x + u - 1) / u);
-      us += tiles * ((float)n.x * block + (float)((n.x + u - 1) / u) * cost.fixed);
+      const float parts = (float)((n.x + u - 1) / u);
+      items += tiles * parts;
+      us += tiles * ((float)n.x * block + parts * cost.fixed);
       one = fmaxf(one, (float)min(n.x, u) * block + cost.fixed);
     }
     const float sms = (float)kSms, all = items <= sms ? one : us / sms + 0.7f * one;
@@ -156,6 +188,7 @@ __global__ void __launch_bounds__(kPrepThreads) shared_prep_kernel(const AttnArg
   }
   __syncthreads();
   int64_t items = 0;
+#pragma unroll 1
   for (int g0 = 0; g0 < a.groups; g0 += kPrepThreads) {
     const int g = g0 + tid;
     int tiles = 0, parts = 0;
