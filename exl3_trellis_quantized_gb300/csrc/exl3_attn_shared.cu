@@ -290,15 +290,16 @@ __device__ __forceinline__ SharedGroup load_group(const SharedGroup* g) {
 // Where a row's parts lie.
 template <bool TOKEN>
 struct Parts {
-  int64_t row, prefix0;  // the row of [total_q][heads]; its place in the first of its prefix items
-  int shared, own;       // parts of the prefix, parts of its own keys
-  int step;              // rows from one part of the prefix to the next
-  int64_t c0, total, first;
-  int ctas, r;
+  // Those of the prefix and those of its own keys: the first, how many, rows from one to the next.
+  int64_t prefix0, own0;
+  int shared, own, step;
+  int64_t own_step;
+  bool cut;  // its own come from ranges that cut the item (token kernel)
+  int64_t c0, total;
+  int ctas;
   // Of row (tok, head); false where there are none.
   __device__ __forceinline__ bool find(const AttnArgs& a, int b, int tok, int head) {
     const int group = a.heads / a.kv_heads, h = head / group;
-    row = (int64_t)tok * a.heads + head;
     const int g = __ldcg(&a.seq[b].y);
     shared = step = 0;
     prefix0 = 0;
@@ -309,34 +310,44 @@ struct Parts {
       shared = twice ? 2 * sg.parts : sg.parts;
       step = twice ? kPrefixRows / 2 : kPrefixRows;
     }
+    own0 = (int64_t)tok * a.heads + head;
     own = a.splits;
+    own_step = a.total_q * a.heads;
+    cut = false;
     if constexpr (TOKEN) {
       const Seq s = load_seq<true>(a, b);
-      r = (tok - (int)s.q0) * group + head - h * group;
+      const int r = (tok - (int)s.q0) * group + head - h * group;
       if (r >= s.q_len * group) return false;  // more tokens than max_q
       ctas = __ldcg(&a.counts->y);
       total = __ldcg(a.units + a.batch) * a.kv_heads;
-      first = __ldcg(a.units + b) * a.kv_heads + (int64_t)h * s.weight() + kItemUnits;
+      const int64_t first = __ldcg(a.units + b) * a.kv_heads + (int64_t)h * s.weight() + kItemUnits;
       // the CTA of a unit is the last whose range begins at or before it
       c0 = ((first + 1) * ctas - 1) / total;
       own = (int)(((first + s.units) * ctas - 1) / total - c0) + 1;
+      cut = own > 1;
+      // two places a CTA, the second for an item that its range does not begin in: the first of the row's CTAs
+      if (cut) own0 = (2 * c0 + 1) * kTokenRows + r, own_step = 2 * kTokenRows;
     }
     return true;
   }
   // Part i's output (null: it has none) and statistics.
   __device__ __forceinline__ const float* at(const AttnArgs& a, int i, int d, const float2** ml) const {
-    const float* o = a.own_o;
-    const float2* l = a.own_ml;
-    int64_t n = (i - shared) * a.total_q * a.heads + row;
+    int64_t n;
     if (i < shared) {
-      o = a.prefix_o, l = a.prefix_ml, n = prefix0 + (int64_t)i * step;
-    } else if (TOKEN && own > 1) {
-      const int64_t c = c0 + i - shared, begin = total * c / ctas;
-      if (begin >= total * (c + 1) / ctas) return nullptr;
-      o = a.cut_o, l = a.cut_ml, n = (2 * c + (begin <= first ? 1 : 0)) * kTokenRows + r;
+      n = prefix0 + (int64_t)i * step;
+      *ml = a.prefix_ml + n;
+      return a.prefix_o + n * d;
     }
-    *ml = l + n;
-    return o + n * d;
+    const int j = i - shared;
+    n = own0 + j * own_step;
+    if (!TOKEN || !cut) {
+      *ml = a.own_ml + n;
+      return a.own_o + n * d;
+    }
+    if (total < ctas && total * (c0 + j) / ctas == total * (c0 + j + 1) / ctas) return nullptr;  // an empty range
+    if (j > 0) n -= kTokenRows;
+    *ml = a.cut_ml + n;
+    return a.cut_o + n * d;
   }
 };
 // The sequence of a token, -1 for none (a whole warp).
@@ -360,14 +371,15 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const AttnArg
   const int lane = threadIdx.x & 31, l = threadIdx.x % LANES;
   const int tok = (int)blockIdx.x;
   const int b = find_sequence(a, tok, lane);
-  pdl_wait();
-  if (b < 0) return;
   // whole warps go round, for the shuffles of the last step
   const int step = gridDim.y * (kJoinThreads / LANES);
-  for (int head0 = blockIdx.y * (kJoinThreads / LANES) + threadIdx.x / 32 * (32 / LANES); head0 < a.heads; head0 += step) {
-    const int head = head0 + lane / LANES;
-    Parts<TOKEN> parts;
-    const bool there = head < a.heads && parts.find(a, b, tok, head);
+  int head = blockIdx.y * (kJoinThreads / LANES) + threadIdx.x / LANES;
+  // (the first kernel of the call is done when the one before this has started: only the parts are waited for)
+  Parts<TOKEN> parts;
+  bool there = b >= 0 && head < a.heads && parts.find(a, b, tok, head);
+  pdl_wait();
+  if (b < 0) return;
+  for (int head0 = head - lane / LANES; head0 < a.heads; head0 += step) {
     Sum sum;
     const int n = there ? parts.shared + parts.own : 0;
     for (int i = 0; i < n; i += kAhead) {
@@ -386,6 +398,8 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const AttnArg
       for (int x = 0; x < kAhead; ++x) sum.add(ml[x], v[x]);
     }
     finish_row<D, QUANT>(a, sum, tok, head, l, there);
+    head += step;
+    there = head < a.heads && parts.find(a, b, tok, head);
   }
 }
 template <int D, bool QUANT, bool TOKEN>
@@ -396,10 +410,10 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_row_kernel(const Att
   const int lane = threadIdx.x & 31, l = threadIdx.x % LANES, team = threadIdx.x / LANES;
   const int tok = (int)blockIdx.x, head = (int)blockIdx.y;
   const int b = find_sequence(a, tok, lane);
-  pdl_wait();
-  if (b < 0) return;
   Parts<TOKEN> parts;
-  if (!parts.find(a, b, tok, head)) return;
+  const bool there = b >= 0 && parts.find(a, b, tok, head);
+  pdl_wait();
+  if (!there) return;
   const int n = parts.shared + parts.own;
   Sum sum;
   for (int i = team; i < n; i += TEAMS) {
