@@ -42,7 +42,7 @@ namespace {
 constexpr int kRopeThreads = 128;
 constexpr int kRopeBlocks = 9;  // blocks an SM: 56 registers a thread (seven blocks of 72: 83 us for 79 below)
 constexpr int kRopeBatch = 4;  // rows a lane group loads before it works on the first
-constexpr int kNormBlocks = 9;  // blocks an SM with norms
+constexpr int kNormBlocks = 9;  // blocks an SM with norms (one less with keys and values: 64 registers, none spilled)
 constexpr int kNormBatch = 2;   // rows at a time with norms, the next ones on their way
 
 __device__ __forceinline__ void unpack8(const uint4& w, bool bf16, float (&v)[8]) {
@@ -415,7 +415,12 @@ __device__ __forceinline__ float square_sum(const float2 (&v)[N]) {
 // all heads of a token: computed once a block, then a row costs a sum of squares and two multiply-adds a value, two
 // values an instruction.  Where heads have weights of their own, P and R are without them.
 //
-// Bound by DRAM as the rotation alone.
+// Bound by DRAM and the issue slots, 63% and 67% busy: 16381 tokens of 32 query and 8 key heads of 128, keys and values
+// into the 16-bit cache 71 us (5680 GB/s), into 4 and 8 bits with the rows read back 103 and 102; 8192 tokens of 48
+// heads, no cache, 38 us (5300 GB/s; the rotation alone 32); one token 2.4 us.  So the type and the layout are chosen
+// when the kernel is compiled (at run time: 77 and 48 us), and rows go two at a time with the next two on their way (one
+// and three at a time: 80 and 108 us; seven and nine blocks an SM in place of eight: 75 and 87).  With the norm, the
+// weights and the rotation one after the other for each row, as the formulas have them, the first case took 97 us.
 // BF16: type of the rows (a choice at run time makes three instructions of every conversion).  PAIRS: interleaved.
 template <int D, bool KV, bool BF16, bool PAIRS>
 __global__ void __launch_bounds__(kRopeThreads, KV ? kNormBlocks - 1 : kNormBlocks) norm_write_kernel(const RopeWriteArgs a, int units_per_block) {
