@@ -260,3 +260,47 @@ def test_two_captured_steps():
             assert torch.equal(out, want)
     torch.cuda.synchronize()
     assert E.device_status() == 0
+
+
+@pytest.mark.parametrize("q_len", [1, 20])
+def test_two_calls_at_once(q_len):
+    """On two streams, each with a workspace of its own: what either gives alone."""
+    calls = [shared([8], [2000], [q_len] * 8, [2100 + 50 * i for i in range(8)], 8, 2, 128, 16, fmt, "bf16", seed=i)
+             for i, fmt in enumerate(("bf16", "int8"))]
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(5):
+        for (args, _), stream, mine in zip(calls, streams, outs):
+            with torch.cuda.stream(stream):
+                mine.append(E.attention_shared(*args))
+    torch.cuda.synchronize()
+    assert E.device_status() == 0
+    for (_, got), mine in zip(calls, outs):
+        assert all(torch.equal(o, got) for o in mine)
+
+
+def test_long_lengths():
+    """Offsets in the cache that pass 32 bits: pages near the end of a cache of more than 2^32 bytes a side."""
+    page, kv, dim, pages = 64, 8, 128, 40000  # 2^32 bytes are 32768 pages
+    cache = E.KVCache(torch.empty((pages, kv, page, dim), dtype=torch.bfloat16, device=DEV),
+                      torch.empty((pages, kv, page, dim), dtype=torch.bfloat16, device=DEV), None, None, "bf16")
+    lens, prefix = [700, 650, 900], 600
+    g = torch.Generator().manual_seed(4)
+    table = torch.arange(pages - 60, pages, dtype=torch.int32, device=DEV).view(3, 20)
+    table[1:, :prefix // page] = table[0, :prefix // page]
+    rows = []
+    for b, n in enumerate(lens):
+        k, v = (torch.randn((n, kv, dim), generator=g).to(torch.bfloat16) for _ in range(2))
+        if b:
+            k[:prefix], v[:prefix] = rows[0][0][:prefix], rows[0][1][:prefix]
+        rows.append((k, v))
+        i = torch.arange(n, device=DEV)
+        E.kv_write(cache, k.to(DEV), v.to(DEV), table[b, i // page].long() * page + i % page)
+    for q_len in (1, 20):
+        q = torch.randn((3 * q_len, 16, dim), generator=g).to(torch.bfloat16).to(DEV)
+        out = E.attention_shared(q, cache, table, cu([q_len] * 3), i32(lens), i32([0, 3]), i32([prefix]), q_len, 900, SHARE)
+        for b in range(3):
+            want, tol = bound(f64(q[b * q_len:(b + 1) * q_len]), *(t.double().numpy() for t in rows[b]), 0, None, "bf16", "bf16")
+            assert_rows(f64(out[b * q_len:(b + 1) * q_len]), want, tol)
+    assert E.device_status() == 0

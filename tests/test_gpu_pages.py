@@ -190,3 +190,17 @@ def test_empty_batch():
     assert cu.tolist() == [0] and positions.tolist() == [0] * 3 and slots.tolist() == [-1] * 3 and granted.numel() == 0
     E.kv_release(tables, torch.zeros(0, dtype=torch.bool, device=DEV))
     assert int(tables.free_count) == 2
+
+
+def test_every_row_of_a_long_prompt():
+    """One request of more rows than the cluster takes at a time, and pages named far beyond 2^31 rows: slots in 64 bits."""
+    total, page = 70001, 256
+    need = (total + page - 1) // page
+    far = 2**31 - 1 - need
+    stack = torch.arange(far, far + need, dtype=torch.int32, device=DEV)
+    tables = E.KVTables(i32(np.full((1, need + 1), -1)), i32([0]), i32([0]), stack, i32([need]), page)
+    cu, positions, slots, granted = E.kv_plan(tables, i32([total]), total)
+    at = torch.arange(total, device=DEV)
+    assert granted.item() and cu.tolist() == [0, total] and torch.equal(positions.long(), at)
+    assert torch.equal(slots, (far + need - 1 - at // page) * page + at % page)
+    assert int(tables.free_count) == 0 and torch.equal(tables.block_table[0, :need], stack.flip(0))
