@@ -621,14 +621,16 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
     float c = a.scale_log2;  // quantised: times the unit of q's row, and a group's times the unit of its keys
     uint32_t tiles = 0;      // quantised: key tiles of the items before
 #ifdef EXL3_ATTN_SHARED
-    // Rotate the half's q where the copy has put it: four lanes a row, chunk 4 x + l of eight values the x-th of lane l, and
+    // Rotate the half's q where the copy has put it: LPQ lanes a row, chunk LPQ x + l of eight values the x-th of lane l, and
     // only rows that there are.  (A thread a row is 1400 instructions in a line, which an item that runs once has to fetch
-    // first; sixteen lanes a row have more than twice the shuffles.)
+    // first.  Of four and eight lanes the better by measurement: 1600 tokens over 16000 8-bit keys 435 and 424 us, 4-bit ones
+    // 438 and 444; heads of 64 356 and 359.)
     auto rotate_q = [&](const Item& x, uint32_t parity) {
       if (!bar_wait(&qraw[i], parity)) return false;
-      constexpr int N = D / 4, RP = 8;  // values a lane; rows a warp takes at a time
+      constexpr int LPQ = D == 128 && SRC == kPaged8 ? 8 : 4;  // lanes of a row
+      constexpr int N = D / LPQ, RP = 32 / LPQ;                // values a lane; rows a warp takes at a time
       const uint32_t at = smem_u32(data + C::kQ) + (uint32_t)i * (kTileRows * D * 2);
-      const int l = lane & 3, rows = min(a.tile_tokens, x.toks - (x.joint ? 0 : i * a.tile_tokens)) * group;
+      const int l = lane % LPQ, rows = min(a.tile_tokens, x.toks - (x.joint ? 0 : i * a.tile_tokens)) * group;
 #pragma unroll 1
       for (int p = 0; p < 32 / RP; ++p) {
         const int first = 32 * (warp & 3) + p * RP;
@@ -639,7 +641,7 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
           uint32_t w[4];
           asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                        : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                       : "r"(at + row_chunk(first + (lane >> 2), 4 * y + l))
+                       : "r"(at + row_chunk(first + lane / LPQ, LPQ * y + l))
                        : "memory");
           if (a.bf16) {
 #pragma unroll
@@ -654,7 +656,7 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
         }
         hadamard_row<N>(v);  // every bit of the place in a chunk and of the lane's chunk
 #pragma unroll
-        for (int st = 1; st < 4; st *= 2)
+        for (int st = 1; st < LPQ; st *= 2)
 #pragma unroll
           for (int y = 0; y < N; ++y) {
             const float o = __shfl_xor_sync(0xffffffffu, v[y], st);
@@ -663,11 +665,11 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
         float top = 0.0f;
 #pragma unroll
         for (int y = 0; y < N; ++y) top = fmaxf(top, fabsf(v[y]));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+#pragma unroll
+        for (int st = 1; st < LPQ; st *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, st));
         // in units of a power of two near its largest value, so that fp16 holds rows of any size alike
         const uint32_t e = unit_exponent(top);
-        const float unit = __shfl_sync(0xffffffffu, power(e), 4 * (lane % RP));
+        const float unit = __shfl_sync(0xffffffffu, power(e), LPQ * (lane % RP));
         if (lane / RP == p) c = a.scale_log2 * (unit * (8.0f / D));  // this thread's row
         const float f = power(254 - e);
 #pragma unroll
@@ -676,7 +678,7 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
 #pragma unroll
           for (int z = 0; z < 4; ++z)
             w[z] = pack2<false>(v[8 * y + column_value<SRC>(2 * z)] * f, v[8 * y + column_value<SRC>(2 * z + 1)] * f);
-          sts128(at + row_chunk(first + (lane >> 2), 4 * y + l), w[0], w[1], w[2], w[3]);
+          sts128(at + row_chunk(first + lane / LPQ, LPQ * y + l), w[0], w[1], w[2], w[3]);
         }
       }
       fence_proxy_async_smem();
@@ -1395,7 +1397,8 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
     constexpr int LPR = C::kRowBytes / 16;  // lanes of a row
     constexpr int RPP = 32 / LPR;           // rows a warp takes at a time
     constexpr int NP = 32 / RPP;            // passes over the warp's 32 rows
-    constexpr int AHEAD = NP < 4 ? NP : 4;  // passes whose codes are read at a time
+    // passes whose codes are read at a time
+    constexpr int AHEAD = kShared && SRC == kPaged4 ? 2 : NP < 4 ? NP : 4;
     const int lw = warp - 12, sub = lane % LPR;
     bool ok = true;
     Item it;
@@ -1455,11 +1458,16 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
           units[s >> 1].k[2 * lw] = ek[0], units[s >> 1].k[2 * lw + 1] = ek[1];
           units[s >> 1].v[2 * lw] = e[0], units[s >> 1].v[2 * lw + 1] = e[1];
         }
+        // behind shared prefixes as a loop: items that run once have to fetch its instructions first, and the softmax's share
+        // their cache (4 bits: 7 chunks over 16000 keys 486 us instead of 490; 8 bits: 39 sequences 67.4 instead of 69.7)
+        constexpr int STEP = kShared ? AHEAD : NP;
+#pragma unroll 1
+        for (int p0 = 0; p0 < NP; p0 += STEP)
 #pragma unroll
-        for (int p = 0; p < NP; ++p) {
-          const int rr = 32 * lw + p * RPP + lane / LPR;
-          if (p > 0 && p % AHEAD == 0) load(p);
-          const uint32_t(&w4)[4] = ww[p % AHEAD];
+        for (int pp = 0; pp < STEP; ++pp) {
+          const int p = p0 + pp, rr = 32 * lw + p * RPP + lane / LPR;
+          if (p > 0 && pp % AHEAD == 0) load(p);
+          const uint32_t(&w4)[4] = ww[pp % AHEAD];
           const uint32_t sh = __shfl_sync(0xffffffffu, mine, rr & 31);
           if constexpr (SRC == kPaged8) {
             uint32_t h[8];
