@@ -300,24 +300,36 @@ __device__ __forceinline__ SharedGroup load_group(const SharedGroup* g) {
 // Where a row's parts lie.
 template <bool TOKEN>
 struct Parts {
+  // Of the token's sequence: its group (keys 0: none) and, with the token kernel, its own items.
+  SharedGroup group;
+  Seq seq;
+  int64_t units, total;
+  int ctas;
   // Those of the prefix and those of its own keys: the first, how many, rows from one to the next.
   int64_t prefix0, own0;
   int shared, own, step;
   int64_t own_step;
   bool cut;  // its own come from ranges that cut the item (token kernel)
-  int64_t c0, total;
-  int ctas;
-  // Of row (tok, head); false where there are none.
-  __device__ __forceinline__ bool find(const AttnArgs& a, int b, int tok, int head) {
-    const int group = a.heads / a.kv_heads, h = head / group;
+  int64_t c0;
+  __device__ __forceinline__ void open(const AttnArgs& a, int b) {
     const int g = __ldcg(&a.seq[b].y);
+    if constexpr (TOKEN) {
+      seq = load_seq<true>(a, b);
+      ctas = __ldcg(&a.counts->y);
+      total = __ldcg(a.units + a.batch) * a.kv_heads;
+      units = __ldcg(a.units + b) * a.kv_heads;
+    }
+    group = g >= 0 ? load_group(a.group + g) : SharedGroup{0, 0, 0, 0, 0, 0};
+  }
+  // Of row (tok, head); false where there are none.
+  __device__ __forceinline__ bool find(const AttnArgs& a, int tok, int head) {
+    const int heads = a.heads / a.kv_heads, h = head / heads;
     shared = step = 0;
     prefix0 = 0;
-    if (g >= 0) {
-      const SharedGroup sg = load_group(a.group + g);
+    if (group.keys > 0) {
       bool twice;
-      prefix0 = prefix_row(a, sg, tok, h, head - h * group, group, &twice);
-      shared = twice ? 2 * sg.parts : sg.parts;
+      prefix0 = prefix_row(a, group, tok, h, head - h * heads, heads, &twice);
+      shared = twice ? 2 * group.parts : group.parts;
       step = twice ? kPrefixRows / 2 : kPrefixRows;
     }
     own0 = (int64_t)tok * a.heads + head;
@@ -325,15 +337,12 @@ struct Parts {
     own_step = a.total_q * a.heads;
     cut = false;
     if constexpr (TOKEN) {
-      const Seq s = load_seq<true>(a, b);
-      const int r = (tok - (int)s.q0) * group + head - h * group;
-      if (r >= s.q_len * group) return false;  // more tokens than max_q
-      ctas = __ldcg(&a.counts->y);
-      total = __ldcg(a.units + a.batch) * a.kv_heads;
-      const int64_t first = __ldcg(a.units + b) * a.kv_heads + (int64_t)h * s.weight() + kItemUnits;
+      const int r = (tok - (int)seq.q0) * heads + head - h * heads;
+      if (r >= seq.q_len * heads) return false;  // more tokens than max_q
+      const int64_t first = units + (int64_t)h * seq.weight() + kItemUnits;
       // the CTA of a unit is the last whose range begins at or before it
       c0 = ((first + 1) * ctas - 1) / total;
-      own = (int)(((first + s.units) * ctas - 1) / total - c0) + 1;
+      own = (int)(((first + seq.units) * ctas - 1) / total - c0) + 1;
       cut = own > 1;
       // two places a CTA, the second for an item that its range does not begin in: the first of the row's CTAs
       if (cut) own0 = (2 * c0 + 1) * kTokenRows + r, own_step = 2 * kTokenRows;
@@ -386,7 +395,8 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const AttnArg
   int head = blockIdx.y * (kJoinThreads / LANES) + threadIdx.x / LANES;
   // (the first kernel of the call is done when the one before this has started: only the parts are waited for)
   Parts<TOKEN> parts;
-  bool there = b >= 0 && head < a.heads && parts.find(a, b, tok, head);
+  if (b >= 0) parts.open(a, b);
+  bool there = b >= 0 && head < a.heads && parts.find(a, tok, head);
   pdl_wait();
   if (b < 0) return;
   for (int head0 = head - lane / LANES; head0 < a.heads; head0 += step) {
@@ -409,7 +419,7 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const AttnArg
     }
     finish_row<D, QUANT>(a, sum, tok, head, l, there);
     head += step;
-    there = head < a.heads && parts.find(a, b, tok, head);
+    there = head < a.heads && parts.find(a, tok, head);
   }
 }
 template <int D, bool QUANT, bool TOKEN>
@@ -421,7 +431,8 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_row_kernel(const Att
   const int tok = (int)blockIdx.x, head = (int)blockIdx.y;
   const int b = find_sequence(a, tok, lane);
   Parts<TOKEN> parts;
-  const bool there = b >= 0 && parts.find(a, b, tok, head);
+  if (b >= 0) parts.open(a, b);
+  const bool there = b >= 0 && parts.find(a, tok, head);
   pdl_wait();
   if (!there) return;
   const int n = parts.shared + parts.own;
