@@ -187,12 +187,12 @@ SharedPlan shared_plan(int64_t total_q, int64_t batch, int64_t groups, int64_t q
 // Whether sharing pays: it has two more launches and the parts' join, 12 to 20 us in all.  What a paged call takes for the
 // same prefixes comes out of L2 after the first sequence.
 //   Few rows: 34 keys and key heads a ns (128 values, up to 8 rows).  32 and 8 heads of 128, single tokens, shared and
-// paged us: 8 sequences behind 8192 keys 26.1 and 25.6 (8 bits: 32.6 and 27.0), 16 behind 2048 25.8 and 18.5, 16 behind
-// 8192 28.5 and 41.3 (8 bits: 35.4 and 43.9), 48 behind 2048 25.6 and 44.2; with 16 heads a key head, 16 behind 2048 23.3
-// and 20.9, 16 behind 8192 27.2 and 35.6.
+// paged us: 8 sequences behind 8192 keys 26.8 and 25.6 (8 bits: 34.2 and 27.0), 16 behind 2048 26.2 and 18.7, 16 behind
+// 8192 29.7 and 41.3 (8 bits: 36.4 and 43.7), 48 behind 2048 24.3 and 44.4; with 16 heads a key head, 16 behind 2048 23.3
+// and 20.8, 16 behind 8192 27.1 and 35.4.
 //   Row tiles: a paged call gives every sequence tiles of its own, 0.43 us for 128 rows and 64 keys; shared, the rows of
-// a group fill them.  8 and 1 tokens of 32 rows: 4 sequences behind 8192 keys 28.7 and 27.1, 12 behind 1024 26.6 and
-// 18.1, 40 behind 1024 38.5 and 45.1, 12 behind 8192 37.5 and 67.1.  Long chunks fill theirs anyway and gain up to a
+// a group fill them.  8 tokens, 32 rows a sequence and key head: 4 sequences behind 8192 keys 28.7 and 27.1, 12 behind 1024
+// 24.9 and 18.0, 40 behind 1024 36.1 and 44.8, 12 behind 8192 35.2 and 66.9.  Long chunks fill theirs anyway and gain up to a
 // tenth (7 of 1 to 700 tokens behind 16000 4-bit keys 480 and 522) or lose as much where own keys weigh.
 // And fp16 rows over a quantised cache, where the token kernel holds the rotated q in two terms and the row tiles in one,
 // stay with the former: 17 tokens of 48 heads behind 7791 8-bit keys would have 0.0004 of the result's norm in place of 0.0002.
@@ -204,12 +204,12 @@ bool worth_sharing(int64_t total_q, int64_t batch, int64_t groups, int64_t q_hea
   const double keys = (double)max_prefix * kv_heads * (head_dim / 128.0);
   if (max_q * group <= exl3::kTokenRows) {
     if (quant && !bf16) return false;
-    const double least = max_q * group <= 8 ? (quant ? 600e3 : 400e3) : (quant ? 360e3 : 240e3);
+    const double least = max_q * group <= 8 ? (quant ? 600e3 : 350e3) : (quant ? 360e3 : 240e3);
     return (double)(batch - groups) * keys >= least;
   }
   const int64_t rows = total_q * group / batch;  // of a sequence
   const int64_t alone = batch * ((rows + 127) / 128), together = (total_q * group + 127) / 128 + groups;
-  if ((double)(alone - together) * keys / 64.0 * 0.43 / kSms >= 6.0) return true;
+  if ((double)(alone - together) * keys / 64.0 * 0.43 / kSms >= 5.0) return true;
   return rows >= 512 && max_prefix >= 8192 && max_prefix >= 8 * (max_kv - max_prefix);
 }
 
