@@ -184,6 +184,9 @@ SharedPlan shared_plan(int64_t total_q, int64_t batch, int64_t groups, int64_t q
   return p;
 }
 
+// Row tiles in up to 16 parts are CTAs of one grid, and counted in 32 bits.
+bool shared_fits(int64_t total_q, int64_t q_heads) { return total_q * q_heads * 16 <= INT32_MAX; }
+
 // Whether sharing pays: it has two more launches and the parts' join, 12 to 20 us in all.  What a paged call takes for the
 // same prefixes comes out of L2 after the first sequence.
 //   Few rows: 34 keys and key heads a ns (128 values, up to 8 rows).  32 and 8 heads of 128, single tokens, shared and
@@ -199,7 +202,7 @@ SharedPlan shared_plan(int64_t total_q, int64_t batch, int64_t groups, int64_t q
 bool worth_sharing(int64_t total_q, int64_t batch, int64_t groups, int64_t q_heads, int64_t kv_heads, int64_t head_dim, bool quant,
                    bool bf16, int64_t max_q, int64_t max_kv, int64_t max_prefix) {
   if (max_prefix == EXL3_SHARE_ALWAYS) return groups > 0;
-  if (groups == 0 || batch <= groups || max_prefix < exl3::kLeastPrefix) return false;
+  if (groups == 0 || batch <= groups || max_prefix < exl3::kLeastPrefix || !shared_fits(total_q, q_heads)) return false;
   const int64_t group = q_heads / kv_heads;
   const double keys = (double)max_prefix * kv_heads * (head_dim / 128.0);
   if (max_q * group <= exl3::kTokenRows) {
@@ -505,7 +508,7 @@ exl3_status_t exl3_attention_shared(const exl3_heads_t* q, exl3_dtype_t dtype, i
                      max_q, max_kv, max_prefix))
     return exl3_attention_paged(q, dtype, total_q, q_heads, cache, block_table, table_width, cu_q, kv_lens, batch, max_q, max_kv, 0,
                                 scale, out, out_token_stride, out_head_stride, workspace, workspace_bytes, stream);
-  if (total_q * q_heads * 16 > INT32_MAX) return EXL3_EUNSUPPORTED;  // CTAs of row tiles in up to 16 parts
+  if (!shared_fits(total_q, q_heads)) return EXL3_EUNSUPPORTED;
   const SharedPlan plan = shared_plan(total_q, batch, groups, q_heads, a.kv_heads, a.head_dim, max_q, max_kv, max_prefix);
   if (!aligned16(workspace)) return EXL3_EINVAL;
   if (workspace_bytes < plan.at[10]) return EXL3_EWORKSPACE;
