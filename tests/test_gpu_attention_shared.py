@@ -304,3 +304,18 @@ def test_long_lengths():
             want, tol = bound(f64(q[b * q_len:(b + 1) * q_len]), *(t.double().numpy() for t in rows[b]), 0, None, "bf16", "bf16")
             assert_rows(f64(out[b * q_len:(b + 1) * q_len]), want, tol)
     assert E.device_status() == 0
+
+
+@pytest.mark.parametrize("q_len", [1, 20])
+@pytest.mark.parametrize("fmt", ["bf16", "int4"])
+def test_rows_of_no_sequence_keep_their_output(fmt, q_len):
+    """A captured step's padding behind the last sequence, and rows before the first: as they were."""
+    args, got = shared([3], [600], [q_len] * 3, [700, 650, 900], 8, 2, 128, 16, fmt, "bf16")
+    n = 3 * q_len
+    q = torch.full((n + 7, 8, 128), float("nan"), dtype=torch.bfloat16, device=DEV)
+    q[2:n + 2] = args[0]
+    out = torch.full_like(q, 5.0)
+    E.attention_shared(q, *args[1:3], args[3] + 2, *args[4:], out=out)
+    assert torch.equal(out[2:n + 2], got)
+    assert bool((out[:2] == 5.0).all()) and bool((out[n + 2:] == 5.0).all())
+    assert E.device_status() == 0
