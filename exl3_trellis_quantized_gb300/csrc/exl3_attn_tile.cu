@@ -1060,6 +1060,9 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kIssueRegs));
     if (warp == 8 || warp == 10) {
       // ---------------- MMA issue: a warp a half ----------------
+      // Looking at a barrier over and over takes issue slots, which the conversion of codes wants (1600 tokens over 16000
+      // 4-bit keys, shared: 426 us with it and 418 without; 16-bit ones 340 and 358).
+      constexpr bool SPIN = !(kShared && C::kQuant);
       // The MMAs' descriptors are taken from uniform registers.  What comes out of shared memory is the same in every
       // lane but not known to be: it goes through a warp reduction, whose result is.
       constexpr uint32_t kIdS = idesc(BF16, 128, kBlock, false);
@@ -1097,7 +1100,7 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
           for (; ok && kt < upto; ++kt, ++vt) {
 #pragma unroll
             for (int value = 0; value < 2; ++value) {
-              ok = bar_wait<true>(&kvfull[slot[value]], sph[value]) && ok;
+              ok = bar_wait<SPIN>(&kvfull[slot[value]], sph[value]) && ok;
               if (one) mbar_arrive(&kvempty[slot[value]]);
               if (value && mend_values(vt, tail, lead)) fph ^= 1u << slot[1];
               next_slot(value);
@@ -1107,7 +1110,7 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
         };
         skip(b0 < b1 ? b0 >> 1 : jhi);
         if (b0 < b1) {
-          ok = bar_wait<true>(&qfull[i], qph) && ok;
+          ok = bar_wait<SPIN>(&qfull[i], qph) && ok;
           qph ^= 1u;
         }
         // Scores run a block ahead of weights times values: turn b has the scores of block b and the values of the one
@@ -1116,7 +1119,7 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
         for (int b = b0; b < b1 + step && b0 < b1; b += step) {
           if (b < b1) {
             const uint32_t s = slot[0], buf = blocks & 1u;
-            ok = bar_wait<true>(&kvfull[s], sph[0]) && ok;
+            ok = bar_wait<SPIN>(&kvfull[s], sph[0]) && ok;
             tc_fence_after();
             const uint64_t kd = kd0 + (uint64_t)(s * (C::kSlot >> 4) + (b & 1) * (kBlock * 128 >> 4));
 #pragma unroll
@@ -1138,14 +1141,14 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
           if (b > b0) {
             const int pb = b - step;
             const uint32_t s = slot[1], g = blocks - 1, buf = g & 1u;
-            ok = bar_wait<true>(&kvfull[s], sph[1]) && ok;
-            if (!C::kQuant && mend_values(vt, tail, lead)) ok = bar_wait<true>(&vfix[s], fph >> s & 1u) && ok;
+            ok = bar_wait<SPIN>(&kvfull[s], sph[1]) && ok;
+            if (!C::kQuant && mend_values(vt, tail, lead)) ok = bar_wait<SPIN>(&vfix[s], fph >> s & 1u) && ok;
             // keys past the length take no part: whole steps of 16 are left out
             const int steps = (min(kBlock, keys - pb * kBlock) + 15) >> 4;
             const uint64_t vd = vd0 + (uint64_t)(s * (C::kSlot >> 4) + (pb & 1) * (kBlock * 128 >> 4));
             const uint32_t pd = tm + kBlock * buf;
             const bool held = pb > b0;
-            ok = bar_wait<true>(&pfull[2 * i + buf], g >> 1 & 1u) && ok;
+            ok = bar_wait<SPIN>(&pfull[2 * i + buf], g >> 1 & 1u) && ok;
             tc_fence_after();
             if (steps == 4) {
 #pragma unroll
@@ -1185,7 +1188,7 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
         // what was issued must be done before the CTA's memory goes
         if (one) tc_commit(&mdrain[i]);
         __syncwarp();
-        bar_wait<true>(&mdrain[i], 0u);
+        bar_wait<SPIN>(&mdrain[i], 0u);
       }
       tc_fence_before();
     } else if (warp == 9) {
