@@ -27,7 +27,8 @@ constexpr int kPer = 2;          // requests a thread
 constexpr int kThreads = 1024;   // at most
 constexpr int kChunk = kPer * kThreads;
 
-__device__ __forceinline__ int sat_add(int a, int b) { return min(a + b, kMost); }  // of 0 .. 2^30 each: below 2^31
+// Of 0 .. 2^30 each.  Two that are saturated make 2^31, which only the unsigned sum holds.
+__device__ __forceinline__ int sat_add(int a, int b) { return (int)min((uint32_t)a + (uint32_t)b, (uint32_t)kMost); }
 __device__ __forceinline__ int clamped(int x, int hi) { return max(0, min(x, hi)); }
 
 __device__ __forceinline__ uint32_t cluster_rank() {

@@ -145,6 +145,37 @@ def test_state_out_of_range_is_clamped():
     assert table[2].tolist() == [3, 2, 1] and tables.kv_lens.tolist() == [2, 48, 42, 3]
 
 
+@pytest.mark.parametrize("batch", [2048, 2049, 6000])
+def test_rows_far_beyond_32_bits(batch):
+    """Requests of 2^31 - 1 new tokens each, so that sums of sums pass 2^31: the first that fits is served, the rest wait."""
+    page, width, total = 16, 8, 1 << 20
+    tables = E.KVTables(i32(np.full((batch, width), -1)), i32([3] * batch), i32([0] * batch), i32(np.arange(64)), i32([64]), page)
+    new = [5] + [2**31 - 1] * (batch - 2) + [0]
+    cu, positions, slots, granted = E.kv_plan(tables, i32(new), total)
+    assert cu.tolist() == [0, 5] + [total] * (batch - 1)
+    assert granted.tolist() == [True] + [False] * (batch - 1)
+    want = 3 + torch.cat([torch.arange(5), torch.arange(total - 5)])
+    assert torch.equal(positions.cpu().long(), want)
+    assert slots[:5].tolist() == [63 * page + 3 + i for i in range(5)] and bool((slots[5:] == -1).all())
+    assert int(tables.free_count) == 63 and tables.held.tolist() == [1] + [0] * (batch - 1)
+    assert tables.kv_lens.tolist() == [8] + [3] * (batch - 1)
+
+
+def test_pages_far_beyond_32_bits():
+    """Requests that lack 2^26 pages each, so that the needs of the batch pass 2^31: none is granted, and none behind them."""
+    batch, page, width = 70, 16, 1 << 26
+    table = torch.empty(batch, width, dtype=torch.int32, device=DEV)  # held 0: nothing of it is read
+    table[:, 0] = -3
+    lens = [4] + [2**30 - 1] * (batch - 2) + [4]
+    tables = E.KVTables(table, i32(lens), i32([0] * batch), i32(np.arange(64)), i32([64]), page)
+    cu, positions, slots, granted = E.kv_plan(tables, i32([1] * batch), batch)
+    assert cu.tolist() == list(range(batch + 1)) and positions.tolist() == lens
+    assert granted.tolist() == [True] + [False] * (batch - 1)
+    assert slots.tolist() == [63 * page + 4] + [-1] * (batch - 1)
+    assert int(tables.free_count) == 63 and tables.held.tolist() == [1] + [0] * (batch - 1)
+    assert tables.kv_lens.tolist() == [5] + lens[1:] and table[:, 0].tolist() == [63] + [-3] * (batch - 1)
+
+
 def test_into_leaves_the_state():
     tables, model, rng = make(300, 700, 32, 400, 8)
     keep = [t.clone() for t in (tables.kv_lens, tables.held, tables.free_count, tables.free_pages)]
