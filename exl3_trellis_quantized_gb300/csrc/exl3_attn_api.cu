@@ -196,7 +196,7 @@ bool shared_fits(int64_t total_q, int64_t q_heads) { return total_q * q_heads * 
 //   Row tiles: a paged call gives every sequence tiles of its own, 0.43 us for 128 rows and 64 keys; shared, the rows of
 // a group fill them.  8 tokens, 32 rows a sequence and key head: 4 sequences behind 8192 keys 28.7 and 27.1, 12 behind 1024
 // 24.9 and 18.0, 40 behind 1024 36.1 and 44.8, 12 behind 8192 35.2 and 66.9.  Long chunks fill theirs anyway and gain up to a
-// tenth (7 of 1 to 700 tokens behind 16000 4-bit keys 480 and 522) or lose as much where own keys weigh.
+// tenth (7 of 1 to 700 tokens behind 16000 4-bit keys 479 and 522) or lose as much where own keys weigh.
 // And fp16 rows over a quantised cache, where the token kernel holds the rotated q in two terms and the row tiles in one,
 // stay with the former: 17 tokens of 48 heads behind 7791 8-bit keys would have 0.0004 of the result's norm in place of 0.0002.
 bool worth_sharing(int64_t total_q, int64_t batch, int64_t groups, int64_t q_heads, int64_t kv_heads, int64_t head_dim, bool quant,

@@ -18,7 +18,7 @@
 //   64 sequences, 1 to 2000 own keys behind 8192, one token, 32 and 8 heads of 128, 16 bits
 //     68.2 us (a paged call 160): 317 MB, 4640 GB/s; lengths 5 us, then prefix 50 and own keys 47 beside each other, join 6
 //   24 and 9 sequences behind 6011 and 30000, 6 alone, 1 to 3 tokens, 40 and 8 heads, 8 bits   68.0 us (187)
-//   7 chunks of 1 to 700 tokens behind 16000, 32 and 8 heads, 4 bits   480 us (522), 990 TFLOP/s
+//   7 chunks of 1 to 700 tokens behind 16000, 32 and 8 heads, 4 bits   479 us (522), 992 TFLOP/s
 // Halves of a row tile that take blocks in turn leave a part each: meeting in shared memory, as a paged call's do, costs
 // an item 2 us.  A row's parts are found before the wait for them (found after it 71.7 us in the second case), from a
 // group and sequence read once a token (once a head: 486 us in the third).

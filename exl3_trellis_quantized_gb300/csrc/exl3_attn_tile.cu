@@ -623,8 +623,9 @@ __global__ void __launch_bounds__(TileCfg<D, SRC>::kThreads, 1)
 #ifdef EXL3_ATTN_SHARED
     // Rotate the half's q where the copy has put it: LPQ lanes a row, chunk LPQ x + l of eight values the x-th of lane l, and
     // only rows that there are.  (A thread a row is 1400 instructions in a line, which an item that runs once has to fetch
-    // first.  Of four and eight lanes the better by measurement: 1600 tokens over 16000 8-bit keys 435 and 424 us, 4-bit ones
-    // 438 and 444; heads of 64 356 and 359.)
+    // first.  Of four and eight lanes the better by measurement, with issuing warps that looked at their barriers over and
+    // over: 1600 tokens over 16000 8-bit keys 435 and 424 us, 4-bit ones 438 and 444; heads of 64 356 and 359.  Without that
+    // the ones taken are 415, 418 us.)
     auto rotate_q = [&](const Item& x, uint32_t parity) {
       if (!bar_wait(&qraw[i], parity)) return false;
       constexpr int LPQ = D == 128 && SRC == kPaged8 ? 8 : 4;  // lanes of a row
