@@ -770,8 +770,8 @@ class KVTables:
         _alike(kv_lens, torch.int32, (batch,), "kv_lens")
         _alike(held, torch.int32, (batch,), "held")
         _need(free_pages, torch.int32, "free_pages")
-        if free_pages.dim() != 1 or free_pages.numel() < 1:
-            raise ValueError("free_pages must be [capacity]")
+        if free_pages.dim() != 1 or not 1 <= free_pages.numel() < 1 << 30:
+            raise ValueError("free_pages must be [capacity], below 2^30")
         _alike(free_count, torch.int32, (1,), "free_count")
         _one_device(block_table, kv_lens, held, free_pages, free_count)
         if page_size not in (16, 32, 64, 128, 256) or width * page_size > 1 << 30:

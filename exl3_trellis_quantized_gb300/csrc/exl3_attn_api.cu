@@ -69,7 +69,8 @@ int page_shift(int32_t page_size) {
 exl3_status_t check_tables(const exl3_kv_tables_t* t, exl3::KvTables* out) {
   if (t == nullptr || !valid_rows(t->batch) || t->table_width < 1 || t->capacity < 1) return EXL3_EINVAL;
   const int shift = page_shift(t->page_size);
-  if (shift < 0 || ((int64_t)t->table_width << shift) > (int64_t(1) << 30) || t->capacity > (1 << 30)) return EXL3_EINVAL;
+  if (shift < 0 || ((int64_t)t->table_width << shift) > (int64_t(1) << 30)) return EXL3_EINVAL;
+  if (t->capacity >= (1 << 30)) return EXL3_EINVAL;  // where sums of pages saturate: one that has is above every stack
   if (!aligned4(t->free_pages) || !aligned4(t->free_count)) return EXL3_EINVAL;
   if (t->batch > 0 && (!aligned4(t->block_table) || !aligned4(t->kv_lens) || !aligned4(t->held))) return EXL3_EINVAL;
   *out = {t->block_table, t->kv_lens, t->held, t->free_pages, t->free_count, t->batch, t->table_width, shift, t->capacity};

@@ -6,7 +6,8 @@
 // page) - held_b), and it takes them from the top of the stack of free pages,
 // after the needs of the requests before it: two prefix sums, then one
 // search and one lookup a token.  The sums saturate at 2^30 (min(a + b, 2^30) of
-// numbers from 0 to 2^30 is associative), so they stay in 32 bits whatever the lengths.
+// numbers from 0 to 2^30 is associative), so they stay in 32 bits whatever the lengths;
+// rows and stacks are fewer, so what has saturated never fits.
 //
 // Bound by latency: a step's few hundred KB at the most are nothing, the chain launch,
 // lengths, two sums of a block, search, table, store is what counts.  So it is one

@@ -427,7 +427,7 @@ exl3_status_t exl3_kv_read(const exl3_kv_cache_t* cache, const int64_t* slots, i
  * cached tokens fill: a length may be set back, when drafted tokens are refused, without giving pages back).
  *   block_table  device, int32 [batch][table_width];  table_width * page_size at most 2^30
  *   kv_lens, held  device, int32 [batch]
- *   free_pages   device, int32 [capacity]: the free pages are its first free_count[0] entries;  capacity at most 2^30
+ *   free_pages   device, int32 [capacity]: the free pages are its first free_count[0] entries;  capacity below 2^30
  *   page_size    as for the cache
  * What lies outside its range (a length above table_width * page_size, a count above capacity) is taken as the
  * nearest that does not.

@@ -1,0 +1,26 @@
+"""The ends of what the calls of a serving step accept, without a GPU."""
+import pytest
+
+import exl3_trellis_quantized_gb300 as E  # noqa: F401
+from exl3_trellis_quantized_gb300 import binding as B
+from test_attention_abi import EINVAL, FAKE, L  # noqa: F401
+from test_serving_abi import ints, on_cpu, tables  # noqa: F401
+
+
+def test_stacks_stay_below_where_sums_saturate(L):  # noqa: F811
+    """A sum of pages that saturates (2^30) must not look like one that the stack holds, so no stack holds 2^30."""
+    full = tables(capacity=1 << 30)
+    assert L.exl3_kv_plan(full, FAKE, 5, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, None) == EINVAL
+    assert L.exl3_kv_release(full, FAKE, FAKE, FAKE, FAKE, FAKE, None) == EINVAL
+
+
+def test_tables_refuse_such_a_stack(on_cpu, monkeypatch):  # noqa: F811
+    monkeypatch.setattr(B, "_apart", lambda *args, **others: None)  # tensors without memory all lie at 0
+
+    def made(capacity):
+        return B.KVTables(ints(3, 4, device="meta"), ints(3, device="meta"), ints(3, device="meta"),
+                          ints(capacity, device="meta"), ints(1, device="meta"), 16)
+
+    assert made((1 << 30) - 1).free_pages.numel() == (1 << 30) - 1
+    with pytest.raises(ValueError, match="free_pages"):
+        made(1 << 30)
