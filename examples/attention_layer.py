@@ -61,6 +61,7 @@ class AttentionLayer:
                                             for _ in range(2))
             self.qk_weight = torch.cat([self.q_weight.expand(heads, -1), self.k_weight.expand(kv_heads, -1)])
         self.groups, self.prefix, self.max_prefix = None, None, 0
+        self.shared_pages, self.running = 0, torch.ones(seqs, dtype=torch.bool)  # of shared prefixes, on the host
 
     def heads_of(self, y):
         rows = y.view(y.shape[0], -1, self.head_dim)
@@ -91,13 +92,15 @@ class AttentionLayer:
         t.block_table[1:, :pages] = t.block_table[0, :pages]
         t.held[1:] = pages
         t.kv_lens[1:] = tokens
+        self.shared_pages = pages
         self.groups = torch.tensor([0, t.batch], dtype=torch.int32, device=t.kv_lens.device)
         self.prefix = torch.tensor([tokens], dtype=torch.int32, device=t.kv_lens.device)
         self.max_prefix = tokens if hint is None else hint
 
     def step(self, x, new=None, max_new=1):
         """Attention of the next tokens of every sequence (one each, or new[b] of at most max_new), x [tokens, hidden];
-        nothing in here waits for the GPU."""
+        nothing in here waits for the GPU.  Behind a shared beginning sequences that have ended take none: their rows
+        are not in x, and their new[b] is 0."""
         q, k, v = self.heads_of(self.qkv(x))
         cu, position, slots, _ = E.kv_plan(self.tables, self.one_each if new is None else new, x.shape[0])
         q = E.kv_write(self.cache, k, v, slots, q=q, positions=position, phases=self.phases, amplitude=self.amplitude,
@@ -108,11 +111,20 @@ class AttentionLayer:
         return E.attention_shared(*args, self.groups, self.prefix, max_new, self.max_len, self.max_prefix)
 
     def end(self, ended):
-        """Sequences end (bool [seqs]): their own pages are free again."""
+        """Sequences end (bool [seqs]): their own pages are free again.  Those of a shared beginning are when the last of
+        its sequences ends, and only then may sequences begin anew."""
         shared = None
         if self.groups is not None:
-            shared = torch.full_like(self.tables.held, int(self.prefix) // self.page)
-            shared[0] = 0
+            now = ended.cpu() & self.running
+            self.running &= ~now
+            shared = torch.full_like(self.tables.held, self.shared_pages)
+            if self.running.any():
+                self.one_each.masked_fill_(ended, 0)
+            else:
+                shared[int(now.int().argmax())] = 0
+                self.one_each.fill_(1)
+                self.running.fill_(True)
+                self.groups, self.prefix, self.max_prefix = None, None, 0
         E.kv_release(self.tables, ended, shared)
 
     def project(self, attention):
