@@ -88,6 +88,8 @@ class AttentionLayer:
     def share(self, tokens, hint=None):
         """All sequences begin with the first ``tokens`` (whole pages) of sequence 0, on its pages; none but it has any yet.
         hint: attention_shared's max_prefix, the tokens unless given."""
+        if self.window > 0:
+            raise ValueError("attention behind a shared beginning has no window")
         t, pages = self.tables, tokens // self.page
         t.block_table[1:, :pages] = t.block_table[0, :pages]
         t.held[1:] = pages

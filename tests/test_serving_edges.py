@@ -1,10 +1,13 @@
 """The ends of what the calls of a serving step accept, without a GPU."""
+import os
+import sys
+
 import pytest
 
 import exl3_trellis_quantized_gb300 as E  # noqa: F401
 from exl3_trellis_quantized_gb300 import binding as B
 from test_attention_abi import EINVAL, FAKE, L  # noqa: F401
-from test_serving_abi import ints, on_cpu, tables  # noqa: F401
+from test_serving_abi import ints, on_cpu, some_tables, tables  # noqa: F401
 
 
 def test_stacks_stay_below_where_sums_saturate(L):  # noqa: F811
@@ -24,3 +27,19 @@ def test_tables_refuse_such_a_stack(on_cpu, monkeypatch):  # noqa: F811
     assert made((1 << 30) - 1).free_pages.numel() == (1 << 30) - 1
     with pytest.raises(ValueError, match="free_pages"):
         made(1 << 30)
+
+
+def example_layer(**attributes):
+    """The example's layer without tensors on a GPU."""
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    from attention_layer import AttentionLayer
+
+    layer = object.__new__(AttentionLayer)
+    layer.__dict__.update(dict(window=0, page=16, groups=None, tables=some_tables()), **attributes)
+    return layer
+
+
+def test_a_layer_with_a_window_shares_nothing(on_cpu):  # noqa: F811
+    """Attention behind shared prefixes has no window: a layer that has one must not lose it."""
+    with pytest.raises(ValueError, match="window"):
+        example_layer(window=100).share(32)
