@@ -69,6 +69,8 @@ class AttentionLayer:
 
     def prompt(self, x, lens, keep=True):
         """Attention of whole prompts [sum(lens), hidden], whose keys and values go into the cache unless not ``keep``."""
+        if keep and self.groups is not None:
+            raise ValueError("tokens behind a shared beginning go through step")
         device = x.device
         y = self.qkv(x)
         new = torch.tensor(lens, dtype=torch.int32, device=device)
@@ -90,6 +92,8 @@ class AttentionLayer:
         hint: attention_shared's max_prefix, the tokens unless given."""
         if self.window > 0:
             raise ValueError("attention behind a shared beginning has no window")
+        if tokens < 1 or tokens % self.page:
+            raise ValueError("a shared beginning is whole pages")
         t, pages = self.tables, tokens // self.page
         t.block_table[1:, :pages] = t.block_table[0, :pages]
         t.held[1:] = pages

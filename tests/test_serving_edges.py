@@ -7,7 +7,7 @@ import pytest
 import exl3_trellis_quantized_gb300 as E  # noqa: F401
 from exl3_trellis_quantized_gb300 import binding as B
 from test_attention_abi import EINVAL, FAKE, L  # noqa: F401
-from test_serving_abi import ints, on_cpu, some_tables, tables  # noqa: F401
+from test_serving_abi import ints, on_cpu, rows, some_tables, tables  # noqa: F401
 
 
 def test_stacks_stay_below_where_sums_saturate(L):  # noqa: F811
@@ -43,3 +43,15 @@ def test_a_layer_with_a_window_shares_nothing(on_cpu):  # noqa: F811
     """Attention behind shared prefixes has no window: a layer that has one must not lose it."""
     with pytest.raises(ValueError, match="window"):
         example_layer(window=100).share(32)
+
+
+def test_a_layer_shares_whole_pages(on_cpu):  # noqa: F811
+    for tokens in (40, 0, -16):
+        with pytest.raises(ValueError, match="pages"):
+            example_layer().share(tokens)
+
+
+def test_no_whole_prompts_behind_a_shared_beginning(on_cpu):  # noqa: F811
+    """Prompt attention sees the new rows only."""
+    with pytest.raises(ValueError, match="step"):
+        example_layer(groups=ints(2)).prompt(rows(), [1, 1, 0])
