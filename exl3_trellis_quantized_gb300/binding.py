@@ -598,9 +598,9 @@ def _norm_args(weight: Optional[torch.Tensor], eps: float, dtype, heads: int, d:
     return _Norm(weight.data_ptr(), 0 if one else d, float(eps))
 
 
-def rope(x: torch.Tensor, positions: torch.Tensor, phases: torch.Tensor, layout: str = "half", amplitude: float = 1.0,
-         out: Optional[torch.Tensor] = None, axes: Optional[torch.Tensor] = None, weight: Optional[torch.Tensor] = None,
-         eps: float = 1e-6) -> torch.Tensor:
+def rope(x: torch.Tensor, positions: Optional[torch.Tensor] = None, phases: Optional[torch.Tensor] = None,
+         layout: str = "half", amplitude: float = 1.0, out: Optional[torch.Tensor] = None,
+         axes: Optional[torch.Tensor] = None, weight: Optional[torch.Tensor] = None, eps: float = 1e-6) -> torch.Tensor:
     """Rotary positions on the heads of x [tokens, heads, head_dim] (a view of a fused projection will do).
 
     The first 2 * phases.numel() values of every head turn.  ``out`` may be x itself.
@@ -608,12 +608,16 @@ def rope(x: torch.Tensor, positions: torch.Tensor, phases: torch.Tensor, layout:
     axes (uint8 [phases.numel()]): positions are int32 [number of axes, tokens], and pair i turns by the row axes[i] of
     them (time, height and width of images and video).  weight ([head_dim], or [heads, head_dim], of x's type): every
     head is first divided by sqrt(mean of its squares + eps) and multiplied by the weight, in the same pass and without
-    a rounding in between.
+    a rounding in between; with a weight there need be no positions and phases, and nothing turns.
     """
     dt = _type(x, "x")
     xh = _heads(x, x.dtype, "x")
     tokens, heads, d = x.shape
-    r = _rope_args(positions, phases, layout, amplitude, tokens, axes)
+    r = None
+    if positions is not None and phases is not None:
+        r = _rope_args(positions, phases, layout, amplitude, tokens, axes)
+    elif weight is None or positions is not None or phases is not None or axes is not None:
+        raise ValueError("x is only taken to be rotated or normed: it needs positions and phases, or a weight alone")
     norm = _norm_args(weight, eps, x.dtype, heads, d, "weight")
     _one_device(x, positions, phases, out, axes, weight)
     if out is not None and weight is not None:

@@ -1,11 +1,27 @@
-"""Rows without a norm beside rows with one in the pass that rotates and writes."""
+"""Norms of heads without a rotation (against the FP64 oracle), and rows without a norm beside rows with one."""
 import pytest
 import torch
 
 import exl3_trellis_quantized_gb300 as E
-from test_gpu_norm_rope import DEV, DT, inputs, weights
+from test_gpu_norm_rope import DEV, DT, assert_normed, f64, inputs, weights
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("tokens,heads,dim", [(1, 1, 64), (7, 5, 128), (130, 3, 64), (33, 41, 128), (700, 6, 128)])
+@pytest.mark.parametrize("each", [False, True])
+def test_norm_without_a_rotation(layout, dtype, tokens, heads, dim, each):
+    x = inputs(tokens, heads + 1, dim, dtype, 11)
+    view = x[:, :heads * dim].view(tokens, heads, dim)
+    w = weights((heads, dim) if each else (dim,), dtype, 5)
+    keep = x.clone()
+    out = E.rope(view, layout=layout, weight=w, eps=1e-5)
+    assert torch.equal(x, keep)
+    assert_normed(f64(out), f64(view), f64(w), 1e-5, None, None, None, layout, 1.0, dtype)
+    E.rope(view, layout=layout, out=view, weight=w, eps=1e-5)
+    assert torch.equal(view, out) and torch.equal(x[:, heads * dim:], keep[:, heads * dim:])
 
 
 @pytest.mark.parametrize("layout", ["half", "interleaved"])

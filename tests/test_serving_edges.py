@@ -3,8 +3,9 @@ import os
 import sys
 
 import pytest
+import torch
 
-import exl3_trellis_quantized_gb300 as E  # noqa: F401
+import exl3_trellis_quantized_gb300 as E
 from exl3_trellis_quantized_gb300 import binding as B
 from test_attention_abi import EINVAL, FAKE, L  # noqa: F401
 from test_serving_abi import ints, on_cpu, rows, some_tables, tables  # noqa: F401
@@ -27,6 +28,21 @@ def test_tables_refuse_such_a_stack(on_cpu, monkeypatch):  # noqa: F811
     assert made((1 << 30) - 1).free_pages.numel() == (1 << 30) - 1
     with pytest.raises(ValueError, match="free_pages"):
         made(1 << 30)
+
+
+def test_norm_alone_checks(on_cpu):  # noqa: F811
+    """With a weight the rows need no positions; half of a rotation is refused."""
+    positions, phases, w = ints(2), ints(16, dtype=torch.int64), torch.zeros(64, dtype=torch.bfloat16)
+    E.rope(rows(), weight=w)
+    E.rope(rows(), weight=w.expand(2, 64))
+    assert on_cpu == ["exl3_norm_rope"] * 2
+    on_cpu.clear()
+    for bad in (dict(), dict(positions=positions), dict(phases=phases), dict(positions=positions, weight=w),
+                dict(phases=phases, weight=w), dict(axes=ints(16, dtype=torch.uint8), weight=w), dict(weight=w[:32]),
+                dict(weight=w.to("meta"))):
+        with pytest.raises(ValueError):
+            E.rope(rows(), **bad)
+    assert not on_cpu
 
 
 def example_layer(**attributes):
