@@ -133,13 +133,13 @@ struct AttnArgs {
   float* part_o;
   float2* part_ml;
   // Attention behind shared prefixes (else zeros).  prefix_o and prefix_ml: the parts of the prefixes' items, in order of
-  // the CTAs that make them, kPrefixRows rows each; own_*: the parts of the sequences' own keys, [splits][total_q][heads]
-  // (token kernel: one, of whole items; cut_*: of items that its ranges cut).
+  // the CTAs that make them, kPrefixRows rows each; own_*: the parts of the sequences' own keys, [splits][total_q][heads],
+  // of which each sequence has as many as its own keys take (token kernel: one, of whole items; cut_*: of items that its ranges cut).
   int groups, prefix_ctas;
   const SharedGroup* group;  // [groups] made by shared_prep_kernel, as what follows
   const int2* seq;           // [batch] first key that is a sequence's own, and its group
   const int64_t* units;      // [batch + 1] units of the sequences before each (token kernel)
-  const int2* counts;        // [1] items of all prefixes, CTAs of the token kernel that take part
+  const int4* counts;        // [1] items of all prefixes, CTAs of the token kernel that take part, blocks of 64 own keys a part at the most
   float *prefix_o, *own_o, *cut_o;
   float2 *prefix_ml, *own_ml, *cut_ml;
 };

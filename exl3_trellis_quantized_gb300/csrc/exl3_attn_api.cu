@@ -161,7 +161,7 @@ struct SharedPlan {
   size_t at[11];  // where in the workspace each array begins, and the end
 };
 SharedPlan shared_plan(int64_t total_q, int64_t batch, int64_t groups, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
-                       int64_t max_q, int64_t max_kv, int64_t max_prefix) {
+                       int64_t max_q, int64_t max_kv) {
   SharedPlan p = {};
   const int64_t group = q_heads / kv_heads, per = 2 * (exl3::kTileTokenRows / group), rows = total_q * q_heads;
   p.token = max_q * group <= exl3::kTokenRows;
@@ -175,12 +175,12 @@ SharedPlan shared_plan(int64_t total_q, int64_t batch, int64_t groups, int64_t q
     p.ctas = own.ctas;
     cut = 2 * (int64_t)own.ctas * exl3::kTokenRows;
   } else {
-    const int64_t rest = max_prefix == EXL3_SHARE_ALWAYS ? max_kv : max_kv - max_prefix, own = rest > max_q ? rest : max_q;
-    p.splits = (int)item_parts(exl3::shared_tiles(total_q, batch, per) * kv_heads, own, rows * head_dim);
+    // room for the parts of sequences that share nothing and are as long as any; of how many parts each is the GPU says
+    p.splits = (int)item_parts(exl3::shared_tiles(total_q, batch, per) * kv_heads, max_kv > max_q ? max_kv : max_q, rows * head_dim);
   }
   const int64_t own = p.token ? rows : p.splits * rows, prefix = (int64_t)p.prefix_ctas * exl3::kPrefixRows;
   const int64_t bytes[10] = {prefix * head_dim * 4, prefix * 8, own * head_dim * 4, own * 8, cut * head_dim * 4, cut * 8,
-                             groups * (int64_t)sizeof(exl3::SharedGroup), batch * 8, p.token ? (batch + 1) * 8 : 0, 8};
+                             groups * (int64_t)sizeof(exl3::SharedGroup), batch * 8, p.token ? (batch + 1) * 8 : 0, 16};
   for (int i = 0; i < 10; ++i) p.at[i + 1] = p.at[i] + (size_t)((bytes[i] + 15) / 16 * 16);
   return p;
 }
@@ -490,7 +490,7 @@ size_t exl3_attention_shared_workspace_bytes(int64_t total_q, int32_t batch, int
   if (!worth_sharing(total_q, batch, groups, q_heads, kv_heads, head_dim, exl3::kv_quantised(format), dtype == EXL3_BF16, max_q,
                      max_kv, max_prefix))
     return exl3_attention_paged_workspace_bytes(total_q, batch, q_heads, kv_heads, head_dim, max_q, max_kv, 0);
-  return shared_plan(total_q, batch, groups, q_heads, kv_heads, head_dim, max_q, max_kv, max_prefix).at[10];
+  return shared_plan(total_q, batch, groups, q_heads, kv_heads, head_dim, max_q, max_kv).at[10];
 }
 
 exl3_status_t exl3_attention_shared(const exl3_heads_t* q, exl3_dtype_t dtype, int64_t total_q, int32_t q_heads,
@@ -510,7 +510,7 @@ exl3_status_t exl3_attention_shared(const exl3_heads_t* q, exl3_dtype_t dtype, i
     return exl3_attention_paged(q, dtype, total_q, q_heads, cache, block_table, table_width, cu_q, kv_lens, batch, max_q, max_kv, 0,
                                 scale, out, out_token_stride, out_head_stride, workspace, workspace_bytes, stream);
   if (!shared_fits(total_q, q_heads)) return EXL3_EUNSUPPORTED;
-  const SharedPlan plan = shared_plan(total_q, batch, groups, q_heads, a.kv_heads, a.head_dim, max_q, max_kv, max_prefix);
+  const SharedPlan plan = shared_plan(total_q, batch, groups, q_heads, a.kv_heads, a.head_dim, max_q, max_kv);
   if (!aligned16(workspace)) return EXL3_EINVAL;
   if (workspace_bytes < plan.at[10]) return EXL3_EWORKSPACE;
   uint8_t* w = static_cast<uint8_t*>(workspace);
@@ -527,7 +527,7 @@ exl3_status_t exl3_attention_shared(const exl3_heads_t* q, exl3_dtype_t dtype, i
   a.group = reinterpret_cast<const exl3::SharedGroup*>(w + plan.at[6]);
   a.seq = reinterpret_cast<const int2*>(w + plan.at[7]);
   a.units = reinterpret_cast<const int64_t*>(w + plan.at[8]);
-  a.counts = reinterpret_cast<const int2*>(w + plan.at[9]);
+  a.counts = reinterpret_cast<const int4*>(w + plan.at[9]);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = exl3::launch_shared_prep(a, cu_groups, prefix_lens, plan.token, s);
   if (e == cudaSuccess) e = exl3::launch_attn_tile_shared(a, !plan.token, s);

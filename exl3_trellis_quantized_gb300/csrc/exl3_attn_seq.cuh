@@ -40,5 +40,12 @@ __device__ __forceinline__ Seq load_seq(const AttnArgs& a, int b) {
   return s;
 }
 
+// Parts of a sequence's own keys in row tiles behind shared prefixes, `unit` blocks of 64 at the most.
+__device__ __forceinline__ int shared_own_parts(const AttnArgs& a, int b, int unit) {
+  if (a.splits <= 1) return 1;
+  const int keys = max(0, min(a.kv_lens[b], a.table_width << a.cache.page_shift)) - __ldcg(&a.seq[b].x);
+  return max(1, ((max(0, keys) + 63) / 64 + unit - 1) / unit);
+}
+
 }  // namespace
 }  // namespace exl3

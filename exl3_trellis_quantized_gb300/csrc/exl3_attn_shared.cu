@@ -45,7 +45,7 @@ struct SharedState {
   SharedGroup* group;
   int2* seq;
   int64_t* units;
-  int2* counts;
+  int4* counts;
 };
 
 // Sums before each thread's value, in thread order, after those that came before (`carry`, which moves on).
@@ -86,6 +86,9 @@ __device__ __forceinline__ int64_t block_sums(int64_t v, int64_t* part, int64_t*
 // 81 and (one after the other) 80 us with the prefix in 2, 3, 5, 6, 8, 12 and 16 parts.
 //   Without, up to 152 items the longest counts; more are taken up in turn: all of them by 152, and 0.7 of the last.
 // And every item's rows are written and joined, at 4 TB/s.
+//   Own keys in row tiles are of a few parts too where the call has few items (the host says how many at the most, for a
+// sequence that shares nothing), each sequence by its own length: 36 tokens alone over 31510 keys 29 us and 240 in one part
+// (a paged call 28), 74 groups of one or two behind 8000 to 16000 8-bit keys, 24 rows a sequence, 151 and 290 us (212).
 constexpr int kPrepThreads = 256;
 constexpr int kSms = 152, kMostBeside = 128;
 struct SharedCosts {
@@ -103,7 +106,7 @@ __global__ void __launch_bounds__(kPrepThreads) shared_prep_kernel(const AttnArg
   __shared__ int2 h_seq[kHeldSeqs];                    // what s.seq will hold
   __shared__ int h_group[kHeldGroups + 1], h_prefix[kHeldGroups];
   __shared__ int2 h_size[kHeldGroups];                 // blocks and tokens
-  __shared__ int longest, unit;
+  __shared__ int longest, longest_own, unit;
   pdl_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31;
   const int per = 2 * a.tile_tokens, room = a.table_width << a.cache.page_shift, total = (int)a.total_q;
@@ -122,7 +125,7 @@ __global__ void __launch_bounds__(kPrepThreads) shared_prep_kernel(const AttnArg
   }
   if (!held)
     for (int b = tid; b < a.batch; b += kPrepThreads) s.seq[b] = make_int2(0, -1);
-  if (tid == 0) longest = 0;
+  if (tid == 0) longest = longest_own = 0;
   __syncthreads();
   auto first_q = [&](int b) { return held ? h_q[b] : clamped(a.cu_q[b], total); };
   auto length = [&](int b) { return held ? h_kv[b] : clamped(a.kv_lens[b], room); };
@@ -165,6 +168,7 @@ __global__ void __launch_bounds__(kPrepThreads) shared_prep_kernel(const AttnArg
       // as load_seq has it
       if (first_q(b + 1) > first_q(b)) weight = max(1, (length(b) - seq.x + kTokenUnit - 1) / kTokenUnit) + kItemUnits;
     }
+    if (a.splits > 1 && weight > 0) atomicMax(&longest_own, weight - kItemUnits);
     if (cost.token) {
       const int64_t before = block_sums(weight, part, &units);
       if (b < a.batch) s.units[b] = before;
@@ -219,7 +223,9 @@ __global__ void __launch_bounds__(kPrepThreads) shared_prep_kernel(const AttnArg
   if (tid == 0) {
     const int n = (int)min(items, (int64_t)a.prefix_ctas);
     const int beside = n <= kMostBeside ? (kSms - n) * cost.per_sm : kSms * cost.per_sm;
-    s.counts[0] = make_int2(n, min(a.ctas, beside));
+    // (row tiles: parts of own keys, no shorter than those of prefixes, beside which they run)
+    const int own = a.splits > 1 ? max(max(8, unit), (longest_own + a.splits - 1) / a.splits) : INT32_MAX / 2;
+    s.counts[0] = make_int4(n, min(a.ctas, beside), own, 0);
   }
 }
 
@@ -308,7 +314,7 @@ struct Parts {
   int ctas;
   // Those of the prefix and those of its own keys: the first, how many, rows from one to the next.
   int64_t prefix0, own0;
-  int shared, own, step;
+  int shared, own, step, own_parts;
   int64_t own_step;
   bool cut;  // its own come from ranges that cut the item (token kernel)
   int64_t c0;
@@ -319,6 +325,8 @@ struct Parts {
       ctas = __ldcg(&a.counts->y);
       total = __ldcg(a.units + a.batch) * a.kv_heads;
       units = __ldcg(a.units + b) * a.kv_heads;
+    } else {
+      own_parts = shared_own_parts(a, b, __ldcg(a.counts).z);
     }
     group = g >= 0 ? load_group(a.group + g) : SharedGroup{0, 0, 0, 0, 0, 0};
   }
@@ -334,7 +342,7 @@ struct Parts {
       step = twice ? kPrefixRows / 2 : kPrefixRows;
     }
     own0 = (int64_t)tok * a.heads + head;
-    own = a.splits;
+    own = own_parts;
     own_step = a.total_q * a.heads;
     cut = false;
     if constexpr (TOKEN) {
@@ -467,7 +475,7 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_row_kernel(const Att
 cudaError_t launch_shared_prep(const AttnArgs& a, const int32_t* cu_groups, const int32_t* prefix_lens, bool token,
                                cudaStream_t stream) {
   const SharedState s = {const_cast<SharedGroup*>(a.group), const_cast<int2*>(a.seq), const_cast<int64_t*>(a.units),
-                         const_cast<int2*>(a.counts)};
+                         const_cast<int4*>(a.counts)};
   const bool quant = kv_quantised(a.cache.format), few = a.max_q * (a.heads / a.kv_heads) <= 8;
   const float wide = (float)a.head_dim / 128.0f;
   SharedCosts cost = {};

@@ -72,6 +72,7 @@
 #include <mutex>
 
 #include "exl3_attn.h"
+#include "exl3_attn_seq.cuh"
 #include "exl3_sm100.cuh"
 
 namespace exl3 {
@@ -361,7 +362,8 @@ __device__ Span half_span(const AttnArgs& a, const Item& it, int n0, int n1, int
 template <int SRC>
 __device__ bool find_item(const AttnArgs& a, int lane, int64_t idx, Item* it) {
   const int per = 2 * a.tile_tokens, group = a.heads / a.kv_heads;
-  const int prefix_items = __ldcg(&a.counts->x);
+  const int4 counts = __ldcg(a.counts);
+  const int prefix_items = counts.x;
   const bool prefix = idx < prefix_items;
   if (!prefix && a.splits == 0) return false;  // own keys go through the token kernel
   // Items come in lists, one a group or (own keys) a sequence: of each its row tiles, of each its key heads, of each its
@@ -371,7 +373,7 @@ __device__ bool find_item(const AttnArgs& a, int lane, int64_t idx, Item* it) {
 #pragma unroll 1
   for (int b0 = 0; b0 < lists; b0 += 32) {
     const int b = b0 + lane;
-    int c0 = 0, n = 0, keys = 0, seq = b, parts = a.splits;
+    int c0 = 0, n = 0, keys = 0, seq = b, parts = 1;
     if (b < lists) {
       if (prefix) {
         const SharedGroup* g = a.group + b;
@@ -381,6 +383,7 @@ __device__ bool find_item(const AttnArgs& a, int lane, int64_t idx, Item* it) {
         c0 = max(0, min(a.cu_q[b], total));
         n = max(0, min(a.cu_q[b + 1], total) - c0);
         keys = max(0, min(a.kv_lens[b], a.table_width << a.cache.page_shift));
+        parts = shared_own_parts(a, b, counts.z);
       }
     }
     const int tiles = (n + per - 1) / per, here = tiles * a.kv_heads * parts;

@@ -99,3 +99,16 @@ def test_alone_before_and_behind_many_groups(q_len):
     prefixes = [256 + 3 * (i % 50) for i in range(300)]
     q, lens = lengths([5] + sizes + [700], [0] + prefixes + [10], {3, 304, 900}, q_len, 8)
     shared(sizes, prefixes, q, lens, 2, 1, 64, 16, "int8", "bf16", skip=5)
+
+
+@pytest.mark.parametrize("fmt,dtype", [("bf16", "bf16"), ("int8", "f16"), ("int4", "bf16")])
+@pytest.mark.parametrize("sizes,prefixes,q_lens,lens,heads,kv", [
+    ([2], [600], [20, 20, 20, 20], [640, 700, 9000, 300], 8, 1),     # alone and long beside a short prefix
+    ([1, 2], [8000, 300], [33, 17, 40], [8100, 400, 350], 4, 2),     # a group of one: nothing is shared of its prefix
+    ([3], [5000], [20, 1, 30, 64], [5020, 5100, 5030, 5200], 12, 2),
+    ([2], [700], [40, 40, 0, 40], [760, 777, 8000, 40], 4, 1),       # long, without queries
+])
+def test_long_own_keys_in_row_tiles(fmt, dtype, sizes, prefixes, q_lens, lens, heads, kv):
+    """Own keys far longer than the rest behind a prefix: parts by each sequence's own length."""
+    for max_prefix in (SHARE, max(prefixes)):
+        shared(sizes, prefixes, q_lens, lens, heads, kv, 128, 64, fmt, dtype, max_prefix=max_prefix)
