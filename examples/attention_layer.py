@@ -114,7 +114,8 @@ class AttentionLayer:
         args = (q, self.cache, self.tables.block_table, cu, self.tables.kv_lens)
         if self.groups is None:
             return E.attention_paged(*args, max_new, self.max_len, window=self.window)
-        return E.attention_shared(*args, self.groups, self.prefix, max_new, self.max_len, self.max_prefix)
+        return E.attention_shared(*args, self.groups, self.prefix, max_new, self.max_len, self.max_prefix,
+                                  sharers=int(self.running.sum()))
 
     def end(self, ended):
         """Sequences end (bool [seqs]): their own pages are free again.  Those of a shared beginning are when the last of

@@ -131,6 +131,8 @@ def lib() -> ctypes.CDLL:
     L.exl3_kv_release.argtypes = [tables] + [vp] * 6
     L.exl3_attention_shared_workspace_bytes.argtypes = [i64] + [i32] * 5 + [ctypes.c_int] * 2 + [i32] * 3
     L.exl3_attention_shared_workspace_bytes.restype = sz
+    L.exl3_attention_shared_pays.argtypes = [i64] + [i32] * 6 + [ctypes.c_int] * 2 + [i32] * 2
+    L.exl3_attention_shared_pays.restype = ctypes.c_int
     L.exl3_attention_shared.argtypes = [heads, ctypes.c_int, i64, i32, cache, vp, i32, vp, vp, i32, vp, vp, i32, i32, i32,
                                         i32, f32, vp, i64, i64, vp, sz, vp]
     for name in ("exl3_norm_rope", "exl3_norm_kv_write", "exl3_kv_plan", "exl3_kv_release", "exl3_attention_shared"):
@@ -968,9 +970,29 @@ def _shared_workspace_bytes(*sizes) -> int:
     return int(lib().exl3_attention_shared_workspace_bytes(*sizes))
 
 
+@functools.lru_cache(maxsize=1024)
+def _sharing_pays(*sizes) -> bool:
+    return bool(lib().exl3_attention_shared_pays(*sizes))
+
+
+def _steer(total_q: int, batch: int, sharers: Optional[int], groups: int, heads: int, dtype, cache: KVCache, max_q: int,
+           max_prefix: int) -> int:
+    """max_prefix, or 0 (not shared) where sharing does not pay for so many of the sequences."""
+    if sharers is None:
+        return max_prefix
+    if not 0 <= sharers <= batch:
+        raise ValueError("sharers must be a number of the call's sequences")
+    if max_prefix == SHARE_ALWAYS or _sharing_pays(total_q, batch, sharers, groups, heads, cache.kv_heads, cache.head_dim,
+                                                   _BF16 if dtype is torch.bfloat16 else _F16, KV_FORMATS[cache.fmt],
+                                                   max_q, max_prefix):
+        return max_prefix
+    return 0
+
+
 def attention_shared_workspace_bytes(total_q: int, batch: int, groups: int, heads: int, dtype, cache: KVCache, max_q: int,
-                                     max_kv: int, max_prefix: int) -> int:
+                                     max_kv: int, max_prefix: int, sharers: Optional[int] = None) -> int:
     """dtype: q's."""
+    max_prefix = _steer(total_q, batch, sharers, groups, heads, dtype, cache, max_q, max_prefix)
     return _shared_workspace_bytes(total_q, batch, groups, heads, cache.kv_heads, cache.head_dim,
                                    _BF16 if dtype is torch.bfloat16 else _F16, KV_FORMATS[cache.fmt], max_q, max_kv, max_prefix)
 
@@ -978,14 +1000,15 @@ def attention_shared_workspace_bytes(total_q: int, batch: int, groups: int, head
 def attention_shared(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, cu_q: torch.Tensor,
                      kv_lens: torch.Tensor, cu_groups: torch.Tensor, prefix_lens: torch.Tensor, max_q: int, max_kv: int,
                      max_prefix: int, scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
-                     workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+                     workspace: Optional[torch.Tensor] = None, sharers: Optional[int] = None) -> torch.Tensor:
     """attention_paged for sequences that begin with the same cached tokens, which are read once for all of them.
 
     Group g is the sequences cu_groups[g] .. cu_groups[g + 1] - 1 (int32 [groups + 1]; sequences outside are of no
     group), whose first prefix_lens[g] (int32 [groups]) keys and values are the same and are read through the table of
     the first of them that has queries.  max_prefix: about the longest of the prefixes, which steers whether they are
-    shared (for few sequences or short prefixes the call is attention_paged; SHARE_ALWAYS: they are) and how the work is
-    split.
+    shared (for few sequences or short prefixes the call is attention_paged; SHARE_ALWAYS: they are; 0: they are not) and
+    how the work is split.  sharers: how many sequences the groups hold, all unless given; where they are fewer, sharing
+    must pay for those.
     ``workspace``: uint8, at least attention_shared_workspace_bytes (allocated when not given).
     Other arguments as for attention_paged.
     """
@@ -1011,6 +1034,7 @@ def attention_shared(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor,
     if out is not None:
         _apart(out, "out", cache_k=cache.k, cache_v=cache.v, k_scale=cache.k_scale, v_scale=cache.v_scale)
     out, oh = _out_like(q, out, "out")
+    max_prefix = _steer(total, batch, sharers, groups, heads, q.dtype, cache, int(max_q), int(max_prefix))
     if workspace is None:
         need = attention_shared_workspace_bytes(total, batch, groups, heads, q.dtype, cache, int(max_q), int(max_kv), int(max_prefix))
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)

@@ -188,33 +188,62 @@ SharedPlan shared_plan(int64_t total_q, int64_t batch, int64_t groups, int64_t q
 // Row tiles in up to 16 parts are CTAs of one grid, and counted in 32 bits.
 bool shared_fits(int64_t total_q, int64_t q_heads) { return total_q * q_heads * 16 <= INT32_MAX; }
 
-// Whether sharing pays: it has two more launches and the parts' join, 12 to 20 us in all.  What a paged call takes for the
-// same prefixes comes out of L2 after the first sequence.
-//   Few rows: 34 keys and key heads a ns (128 values, up to 8 rows).  32 and 8 heads of 128, single tokens, shared and
-// paged us: 8 sequences behind 8192 keys 26.8 and 25.6 (8 bits: 34.2 and 27.0), 16 behind 2048 26.2 and 18.7, 16 behind
-// 8192 29.7 and 41.3 (8 bits: 36.4 and 43.7), 48 behind 2048 24.3 and 44.4; with 16 heads a key head, 16 behind 2048 23.3
-// and 20.8, 16 behind 8192 27.1 and 35.4.
-//   Row tiles: a paged call gives every sequence tiles of its own, 0.43 us for 128 rows and 64 keys; shared, the rows of
-// a group fill them.  8 tokens, 32 rows a sequence and key head: 4 sequences behind 8192 keys 28.7 and 27.1, 12 behind 1024
-// 24.9 and 18.0, 40 behind 1024 36.1 and 44.8, 12 behind 8192 35.2 and 66.9.  Long chunks fill theirs anyway and gain up to a
-// tenth (7 of 1 to 700 tokens behind 16000 4-bit keys 479 and 522) or lose as much where own keys weigh.
-// And fp16 rows over a quantised cache, where the token kernel holds the rotated q in two terms and the row tiles in one,
-// stay with the former: 17 tokens of 48 heads behind 7791 8-bit keys would have 0.0004 of the result's norm in place of 0.0002.
-bool worth_sharing(int64_t total_q, int64_t batch, int64_t groups, int64_t q_heads, int64_t kv_heads, int64_t head_dim, bool quant,
-                   bool bf16, int64_t max_q, int64_t max_kv, int64_t max_prefix) {
+// Whether sharing pays, for groups that hold `sharers` of the call's sequences: what the prefixes take when every sequence
+// reads them for itself, less what they take when they are read once, against what the call has in addition (two launches,
+// the lengths, the join).  Each time is a sum of SM time by measured rates, so the sides are those of the sizes at hand: how
+// many groups, how long, how wide.  All prefixes count as the longest, and sequences and groups as equally large.
+//   Row tiles take `joint` or `full` us for 64 keys, by whether the rows fill one tile of 128, and `fixed` us an item.  Many
+// more rows than an item holds leave the last item of each list half empty, or a little more.
+//   Few rows go through the token kernel: 34 keys and key heads a ns (128 values; 24 where a key head has more than 8
+// rows), or DRAM, which gives a prefix to every sequence where those of the groups do not stay in L2 together.  Its
+// join looks through all sequences for each of them.  The lengths take 0.17 us a group and 0.04 a sequence.
+//   us of a layer by the paged call and shared, layers in turn whose caches are larger than L2 together; 32 and 8 heads of
+// 128, 16 bits but where it says codes:
+//     single tokens of one group: 8 sequences behind 8192 keys 27 and 28 (codes 27 and 33), 16 behind 4096 28 and 30 (29 and
+//       35), 16 behind 8192 44 and 32 (45 and 37), 32 behind 1024 25 and 24, 64 behind 512 33 and 28
+//     pairs: 16 behind 4096 82 and 67 (codes 53 and 83), 64 behind 4096 353 and 233 (203 and 290), 250 behind 512 401 and
+//       320 (335 and 354); 64 groups of four behind 512 160 and 122 (135 and 131)
+//     2, 8 and 32 of 62 to 64 behind 8192, the others alone: 102 and 117, 109 and 116, 108 and 81
+//     8 tokens each (32 rows): 4 sequences behind 4096 21 and 24, 8 behind 4096 30 and 24, 40 behind 1024 50 and 41
+//     30 tokens each (120 rows): 4 behind 2048 20 and 29, 8 behind 4096 42 and 37, 16 behind 8192 72 and 79 (codes 120
+//       and 104)
+//     chunks of about 100 tokens, 16 sequences: behind 4000 119 and 140, 8000 213 and 192, 16000 408 and 349; of about 1500,
+//       2 sequences: behind 8000 341 and 355, 16000 640 and 666, 32000 1250 and 1296 (waves of items move single sizes by
+//       tenths either way, which no sum of times sees)
+// Over 2550 sizes, two thirds of them drawn, the side chosen takes 1.6% more than the better one on average (always the
+// paged call: 34%); where it is the shared one, 29% more at the most, and more than a tenth at 34 sizes.
+// Rows of fp16 over codes, where the token kernel holds the rotated q in two terms and the row tiles in one, stay with the
+// former: 17 tokens of 48 heads behind 7791 8-bit keys would have 0.0004 of the result's norm in place of 0.0002.
+bool worth_sharing(int64_t total_q, int64_t batch, int64_t sharers, int64_t groups, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                   int format, bool bf16, int64_t max_q, int64_t max_prefix) {
   if (max_prefix == EXL3_SHARE_ALWAYS) return groups > 0;
-  if (groups == 0 || batch <= groups || max_prefix < exl3::kLeastPrefix || !shared_fits(total_q, q_heads)) return false;
-  const int64_t group = q_heads / kv_heads;
-  const double keys = (double)max_prefix * kv_heads * (head_dim / 128.0);
-  if (max_q * group <= exl3::kTokenRows) {
-    if (quant && !bf16) return false;
-    const double least = max_q * group <= 8 ? (quant ? 600e3 : 350e3) : (quant ? 360e3 : 240e3);
-    return (double)(batch - groups) * keys >= least;
+  if (groups == 0 || sharers <= groups || max_prefix < exl3::kLeastPrefix || !shared_fits(total_q, q_heads)) return false;
+  const bool quant = exl3::kv_quantised(format);
+  const int64_t each = max_q * (q_heads / kv_heads);
+  const bool token = each <= exl3::kTokenRows;
+  if (token && quant && !bf16) return false;
+  const double wide = head_dim / 128.0, blocks = max_prefix / 64.0 * wide;
+  const double joint = quant ? 0.82 : 0.72, full = 0.9, fixed = token ? 14.0 : quant ? 6.0 : 5.0;
+  // of row tiles over the prefix, `lists` times `rows` rows
+  auto items = [&](double lists, double rows) { return (rows <= 256.0 ? lists : lists * (rows / 256.0 + 0.55)) * kv_heads / kSms; };
+  auto tiles = [&](double lists, double rows) { return items(lists, rows) * (fixed + blocks * (rows <= 128.0 ? joint : full)); };
+  const double own = (double)total_q * (q_heads / kv_heads) / batch, all = own * sharers / groups;  // rows of a sequence and of a group
+  const bool some = sharers < batch;
+  double alone, together, more = 0.17 * groups + 0.04 * batch;
+  if (token) {
+    const double bytes = (double)max_prefix * kv_heads * 2 * exl3::kv_row_bytes(format, (int)head_dim);
+    auto dram = [&](double times) { return times * bytes / 6.8e6; };
+    alone = fmax((double)sharers * max_prefix * kv_heads * wide / (each <= 8 ? 34e3 : 24e3), dram(groups * bytes > 80e6 ? sharers : groups)) +
+            0.0008 * batch * batch * (q_heads * max_q / 32.0);
+    together = fmax(tiles(groups, all), dram(groups));
+    more += total_q * q_heads <= 4 * kSms ? 16.0 : some ? 13.0 : quant ? 9.0 : 7.0;
+  } else {
+    // (the sequences' own keys are items of their own, and every row has parts to be joined)
+    alone = tiles(sharers, own);
+    together = tiles(groups, all);
+    more += (quant ? 4.0 : 7.5) + (some ? 7.5 : 0.0) + 6.5 * items(batch, own) + 0.0115 * total_q * q_heads / 32.0 * wide;
   }
-  const int64_t rows = total_q * group / batch;  // of a sequence
-  const int64_t alone = batch * ((rows + 127) / 128), together = (total_q * group + 127) / 128 + groups;
-  if ((double)(alone - together) * keys / 64.0 * 0.43 / kSms >= 5.0) return true;
-  return rows >= 512 && max_prefix >= 8192 && max_prefix >= 8 * (max_kv - max_prefix);
+  return alone - together > more;
 }
 
 // Checks of a paged call and what the kernels take of it, but for the split; an empty call is not filled in.
@@ -487,10 +516,17 @@ size_t exl3_attention_shared_workspace_bytes(int64_t total_q, int32_t batch, int
                                              exl3_kv_format_t format, int32_t max_q, int32_t max_kv, int32_t max_prefix) {
   if (!valid_rows(total_q) || !valid_rows(batch) || !valid_rows(groups) || !valid_head_counts(q_heads, kv_heads)) return 0;
   if (check_head_dim(head_dim) != EXL3_OK || max_q < 1 || max_kv < 0 || max_prefix < 0 || total_q == 0 || batch == 0) return 0;
-  if (!worth_sharing(total_q, batch, groups, q_heads, kv_heads, head_dim, exl3::kv_quantised(format), dtype == EXL3_BF16, max_q,
-                     max_kv, max_prefix))
+  if (!worth_sharing(total_q, batch, batch, groups, q_heads, kv_heads, head_dim, format, dtype == EXL3_BF16, max_q, max_prefix))
     return exl3_attention_paged_workspace_bytes(total_q, batch, q_heads, kv_heads, head_dim, max_q, max_kv, 0);
   return shared_plan(total_q, batch, groups, q_heads, kv_heads, head_dim, max_q, max_kv).at[10];
+}
+
+int32_t exl3_attention_shared_pays(int64_t total_q, int32_t batch, int32_t sharers, int32_t groups, int32_t q_heads,
+                                   int32_t kv_heads, int32_t head_dim, exl3_dtype_t dtype, exl3_kv_format_t format,
+                                   int32_t max_q, int32_t max_prefix) {
+  if (!valid_rows(total_q) || !valid_rows(batch) || !valid_rows(groups) || !valid_head_counts(q_heads, kv_heads)) return 0;
+  if (check_head_dim(head_dim) != EXL3_OK || max_q < 1 || max_prefix < 0 || total_q == 0 || batch == 0 || sharers < 0 || sharers > batch) return 0;
+  return worth_sharing(total_q, batch, sharers, groups, q_heads, kv_heads, head_dim, format, dtype == EXL3_BF16, max_q, max_prefix) ? 1 : 0;
 }
 
 exl3_status_t exl3_attention_shared(const exl3_heads_t* q, exl3_dtype_t dtype, int64_t total_q, int32_t q_heads,
@@ -505,8 +541,7 @@ exl3_status_t exl3_attention_shared(const exl3_heads_t* q, exl3_dtype_t dtype, i
   const exl3_status_t st = paged_args(q, dtype, total_q, q_heads, cache, block_table, table_width, cu_q, kv_lens, batch, max_q, max_kv, 0,
                                       scale, out, out_token_stride, out_head_stride, &a);
   if (st != EXL3_OK || total_q == 0 || batch == 0) return st;
-  if (!worth_sharing(total_q, batch, groups, q_heads, a.kv_heads, a.head_dim, exl3::kv_quantised(a.cache.format), dtype == EXL3_BF16,
-                     max_q, max_kv, max_prefix))
+  if (!worth_sharing(total_q, batch, batch, groups, q_heads, a.kv_heads, a.head_dim, a.cache.format, dtype == EXL3_BF16, max_q, max_prefix))
     return exl3_attention_paged(q, dtype, total_q, q_heads, cache, block_table, table_width, cu_q, kv_lens, batch, max_q, max_kv, 0,
                                 scale, out, out_token_stride, out_head_stride, workspace, workspace_bytes, stream);
   if (!shared_fits(total_q, q_heads)) return EXL3_EUNSUPPORTED;

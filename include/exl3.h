@@ -543,7 +543,8 @@ exl3_status_t exl3_attention_paged(const exl3_heads_t* q, exl3_dtype_t dtype, in
  * may be larger than a sequence's length or reach past a query's position.
  *   cu_groups    device, int32 [groups + 1], not falling;  prefix_lens  device, int32 [groups]
  *   max_prefix   HOST: about the longest prefix; it steers whether prefixes are shared and how the work is split.
- *                EXL3_SHARE_ALWAYS: they are, whatever the sizes say
+ *                EXL3_SHARE_ALWAYS: they are, whatever the sizes say; 0: they are not.  The sizes are weighed as if
+ *                every sequence were of a group: where the groups hold fewer, ask exl3_attention_shared_pays
  *   workspace    as for exl3_attention_paged, at least exl3_attention_shared_workspace_bytes of the same sizes
  *   other arguments and limits as for exl3_attention_paged
  */
@@ -551,6 +552,11 @@ exl3_status_t exl3_attention_paged(const exl3_heads_t* q, exl3_dtype_t dtype, in
 size_t exl3_attention_shared_workspace_bytes(int64_t total_q, int32_t batch, int32_t groups, int32_t q_heads,
                                              int32_t kv_heads, int32_t head_dim, exl3_dtype_t dtype,
                                              exl3_kv_format_t format, int32_t max_q, int32_t max_kv, int32_t max_prefix);
+/* 1 where the sizes say that sharing pays for groups that hold `sharers` of the batch's sequences, else 0 (also for sizes
+ * that the call refuses).  Where it is 0, pass max_prefix 0. */
+int32_t exl3_attention_shared_pays(int64_t total_q, int32_t batch, int32_t sharers, int32_t groups, int32_t q_heads,
+                                   int32_t kv_heads, int32_t head_dim, exl3_dtype_t dtype, exl3_kv_format_t format,
+                                   int32_t max_q, int32_t max_prefix);
 exl3_status_t exl3_attention_shared(const exl3_heads_t* q, exl3_dtype_t dtype, int64_t total_q, int32_t q_heads,
                                     const exl3_kv_cache_t* cache, const int32_t* block_table, int32_t table_width,
                                     const int32_t* cu_q, const int32_t* kv_lens, int32_t batch, const int32_t* cu_groups,
