@@ -833,7 +833,7 @@ def kv_plan(tables: KVTables, new_lens: torch.Tensor, total: int, into: Optional
     tables' lengths, rows and stack move on, or with ``into`` (a KVTables over the same block_table and free_pages) the
     new lengths, held pages and count go there.  A request whose pages are not to be had (or whose tokens do not fit
     into total, or pages into the table) is not granted: its state stays and its slots are -1; none after it gets
-    pages that it waits for.  The four outputs are new tensors unless given.
+    pages that it waits for.  Attention's outputs for its rows mean nothing.  The four outputs are new tensors unless given.
     """
     total, batch = int(total), tables.batch
     device = tables.kv_lens.device
@@ -1005,10 +1005,11 @@ def attention_shared(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor,
 
     Group g is the sequences cu_groups[g] .. cu_groups[g + 1] - 1 (int32 [groups + 1]; sequences outside are of no
     group), whose first prefix_lens[g] (int32 [groups]) keys and values are the same and are read through the table of
-    the first of them that has queries.  max_prefix: about the longest of the prefixes, which steers whether they are
-    shared (for few sequences or short prefixes the call is attention_paged; SHARE_ALWAYS: they are; 0: they are not) and
-    how the work is split.  sharers: how many sequences the groups hold, all unless given; where they are fewer, sharing
-    must pay for those.
+    the first of them that has queries.  Shared are the keys that every query of the group sees (rows that kv_plan did
+    not grant see fewer).  Over a quantised cache the rows, keys and values of the prefix are rounded as in long chunks.
+    max_prefix: about the longest of the prefixes, which steers whether they are shared (for few sequences or short
+    prefixes the call is attention_paged; SHARE_ALWAYS: they are; 0: they are not).  sharers: how many sequences the
+    groups hold, all unless given; where they are fewer, sharing must pay for those.
     ``workspace``: uint8, at least attention_shared_workspace_bytes (allocated when not given).
     Other arguments as for attention_paged.
     """

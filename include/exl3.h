@@ -453,6 +453,8 @@ typedef struct {
  * kv_lens + n, held_out = held + need.  Row cu_q[b] + i has position kv_lens[b] + i and the slot of that position.
  * Not granted: length, pages and table stay; its rows have positions as above and the slot -1, which exl3_kv_write
  * skips.  Rows from cu_q[batch] to total (padding of a captured step): position 0, slot -1.
+ * Attention over the new state takes the rows of a request that was not granted for the last tokens of its old
+ * length: what it gives for them means nothing.
  *   new_lens  device, int32 [batch]
  *   kv_lens_out, held_out, free_count_out  device (outputs): the new state; may be the tables' own (updated in place)
  *   cu_q      device, int32 [batch + 1];  positions  int32 [total];  slots  int64 [total];  granted  uint8 [batch], 0 or 1
@@ -537,12 +539,15 @@ exl3_status_t exl3_attention_paged(const exl3_heads_t* q, exl3_dtype_t dtype, in
  * Sequences of no group (before cu_groups[0], from cu_groups[groups] on) are as in exl3_attention_paged.
  * Where the sizes say that sharing does not pay (few sequences, short prefixes), the call is exl3_attention_paged.
  * The result is exl3_attention_paged's but for the order of its sums and, where prefixes of a quantised cache are
- * shared, the rounding of the rotated q to one fp16 term as in long chunks (so fp16 rows that the paged call
- * would take in two terms are not shared unless EXL3_SHARE_ALWAYS asks for it).  What is shared in fact is whole tiles of 128 keys that every
- * query of the group sees, from 256 keys on, of groups in which at least two sequences have queries: prefix_lens
- * may be larger than a sequence's length or reach past a query's position.
+ * shared, the roundings that it has in long chunks: the rotated q is one fp16 term, and every key and value of the
+ * prefix (code times scale) an fp16 number.  (For few rows the paged call takes codes as they are, scales in fp32 and
+ * q of fp16 rows in two terms; such fp16 rows are not shared unless EXL3_SHARE_ALWAYS asks for it.)
+ * What is shared in fact is whole tiles of 128 keys that every query of the group sees, from 256 keys on, of groups
+ * in which at least two sequences have queries: prefix_lens may be larger than a sequence's length or reach past a
+ * query's position.  So the sequence that sees least says how much its group shares: n rows that exl3_kv_plan did
+ * not grant, behind a prefix that is all that is cached, take n - 1 keys off it, or all.
  *   cu_groups    device, int32 [groups + 1], not falling;  prefix_lens  device, int32 [groups]
- *   max_prefix   HOST: about the longest prefix; it steers whether prefixes are shared and how the work is split.
+ *   max_prefix   HOST: about the longest prefix; it steers whether prefixes are shared.
  *                EXL3_SHARE_ALWAYS: they are, whatever the sizes say; 0: they are not.  The sizes are weighed as if
  *                every sequence were of a group: where the groups hold fewer, ask exl3_attention_shared_pays
  *   workspace    as for exl3_attention_paged, at least exl3_attention_shared_workspace_bytes of the same sizes
