@@ -980,6 +980,7 @@ def _steer(total_q: int, batch: int, sharers: Optional[int], groups: int, heads:
     """max_prefix, or 0 (not shared) where sharing does not pay for so many of the sequences."""
     if sharers is None:
         return max_prefix
+    sharers = int(sharers)
     if not 0 <= sharers <= batch:
         raise ValueError("sharers must be a number of the call's sequences")
     if max_prefix == SHARE_ALWAYS or _sharing_pays(total_q, batch, sharers, groups, heads, cache.kv_heads, cache.head_dim,
