@@ -66,7 +66,7 @@ def test_sharing_pays_where_it_was_measured_to(L):  # noqa: F811
              dict(n=32, prefix=8192, groups=16, fmt=2), dict(n=500, prefix=2048, groups=250, fmt=2),
              dict(n=2, alone=60, prefix=8192), dict(n=2, alone=60, prefix=8192, fmt=2), dict(n=8, alone=56, prefix=8192, fmt=2),
              dict(n=4, alone=60, prefix=32768, fmt=2), dict(n=4, prefix=4096, q=8), dict(n=16, prefix=512, q=8),
-             dict(n=4, prefix=2048, q=30), dict(n=16, prefix=2048, q=30), dict(n=16, prefix=4000, q=100), dict(n=2, prefix=8000, q=1500)]
+             dict(n=4, prefix=2048, q=30), dict(n=16, prefix=2048, q=30), dict(n=16, prefix=4000, q=100)]
     for args in shared:
         assert pays(L, **args) == 1, args
     for args in paged:
